@@ -409,6 +409,122 @@ int mm_moe_ep_barrier(void* const* peer_flags, int N, int rank, uint32_t epoch, 
 int mm_moe_ep_barrier_ranks(void* const* peer_flags, int N, uint32_t epoch, unsigned timeout_ms, uint64_t absent,
                             int32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the expert layer: the router's top-k, tokens sorted by
+ * expert and back, 4-bit quantisation and product.  Each enqueues its kernels
+ * on `stream`; none allocates or synchronises.  Element types of rows: */
+#define MM_MOE_DTYPE_F32 0
+#define MM_MOE_DTYPE_BF16 1
+#define MM_MOE_DTYPE_F16 2
+
+#define MM_MOE_SCORE_SOFTMAX 0
+#define MM_MOE_SCORE_SIGMOID 1
+
+/* Top-k of each token's expert logits, and their weights.
+ *   logits [T, E] of `dtype`, `row_stride` elements between rows (>= E)
+ *   key    logit, or with bias (fp32 [E], sigmoid only) sigmoid(logit) + bias: the K
+ *          largest in descending order, equal keys by ascending expert.  -inf and
+ *          NaN logits are never chosen: a row with fewer than K others ends in
+ *          topk_idx = -1, topk_w = 0.
+ *   p      softmax over the row's E logits, or sigmoid of each
+ *   topk_w scale * p / z (fp32 [T, K]); z = 1, or with renorm the sum of the chosen
+ *          p (sigmoid: plus 1e-20).  The bias moves the choice only.  A logit of
+ *          +inf makes its row's softmax weights NaN.
+ * topk_idx int32 [T, K] and topk_w are what mm_moe_forward and mm_moe_dispatch
+ * take.  1 <= K <= 16, K <= E <= 1024. */
+int mm_moe_route(const void* logits, int dtype, int64_t row_stride, int T, int E, int K, const float* bias, int score,
+                 int renorm, float scale, int32_t* topk_idx, float* topk_w, void* stream);
+
+/* Gradient of mm_moe_route's weights with respect to the logits (the choice is a
+ * constant).  topk_idx as mm_moe_route wrote it: distinct experts, -1 for none;
+ * d_topk_w fp32 [T, K]; score, renorm and scale as in the forward call.
+ * d_logits [T, E] of `dtype` is fully overwritten. */
+int mm_moe_route_backward(const void* logits, int dtype, int64_t row_stride, const int32_t* topk_idx,
+                          const float* d_topk_w, int T, int E, int K, int score, int renorm, float scale,
+                          void* d_logits, int64_t d_row_stride, void* stream);
+
+/* Tokens into the pool of a routing (mm_moe_dispatch's slot, src and blk_off of
+ * the same T, K, E, block_m): rows[slot[t*K + k]] = x[t]; every other row of the
+ * num_rows is zero (padding, and rows past the last block).  x [T, H],
+ * row_stride elements between rows; rows [num_rows, H] contiguous.  H >= 1 of
+ * any size; accesses are as wide as addresses and row pitches are aligned.
+ * num_rows at least mm_moe_dispatch's src_capacity rule for these sizes; src
+ * holds num_rows entries. */
+int mm_moe_permute(const void* x, int dtype, int64_t row_stride, int T, int H, int K, int E, int block_m,
+                   const int32_t* slot, const int32_t* src, const int32_t* blk_off, void* rows, int64_t num_rows,
+                   void* stream);
+
+/* The pool back to the tokens: out[t] = sum over k of w[t, k] * rows[slot[t*K + k]],
+ * masked slots left out, the sum in fp32 in k order, rounded once.  w fp32
+ * [T, K], or null for ones (then this is also mm_moe_permute's gradient).
+ * out [T, H], out_stride elements between rows. */
+int mm_moe_unpermute(const void* rows, int dtype, int64_t num_rows, int T, int H, int K, const int32_t* slot,
+                     const float* w, void* out, int64_t out_stride, void* stream);
+
+/* Gradients of mm_moe_unpermute: d_rows[slot[t*K + k]] = w[t, k] * d_out[t], zero in
+ * every other row; d_w[t, k] = <d_out[t], rows[slot[t*K + k]]> in fp32, 0 where
+ * masked.  w null: ones.  d_w null: not computed, and rows is not read. */
+int mm_moe_unpermute_backward(const void* d_out, int dtype, int64_t d_stride, const void* rows, int T, int H, int K,
+                              int E, int block_m, const int32_t* slot, const int32_t* src, const int32_t* blk_off,
+                              const float* w, void* d_rows, int64_t num_rows, float* d_w, void* stream);
+
+/* Bytes of one scale region in the order the 4-bit product reads, for `rows` rows
+ * and a contraction of C elements: [ceil(rows/128)][2 ceil(C/256)][512]. */
+int mm_moe_mx_scale_size(int64_t rows, int C, size_t* bytes);
+
+/* Rows into microscaled 4-bit: e2m1 codes (two per byte, low nibble = even
+ * column) and one UE8M0 byte per 32 elements.  The scale is 2^e, e the smallest
+ * integer with 6 * 2^e >= max(amax, 1e-10), the byte e + 127; codes round to
+ * nearest, ties to the even code.  A block with a NaN or an infinity gets byte
+ * 255 and zero codes (it stands for NaN).
+ *   x      [R, C] of `dtype`, row_stride elements between rows; C >= 1, the last
+ *          block padded with zeros
+ *   codes  [rows, 16 * ceil(C/32)] bytes, 16-byte aligned
+ *   sf     chunks = 0: [rows, ceil(C/32)], the canonical weight scales of
+ *          mm_moe_prepare_weights and mm_moe_mx_prepare; chunks = 1: the product's
+ *          order, mm_moe_mx_scale_size(rows, C) bytes, 16-byte aligned
+ *   slot   null: rows = R.  Else int32 [R, K]: row r goes to rows slot[r*K + k] of
+ *          num_rows (-1: nowhere), and rows that no slot names are left as they are. */
+int mm_moe_mx_quantize(const void* x, int dtype, int64_t row_stride, int64_t R, int C, const int32_t* slot, int K,
+                       int64_t num_rows, void* codes, void* sf, int chunks, void* stream);
+
+/* The values codes and row-major scales stand for: out [R, C] of `dtype` (bf16 and
+ * fp32 hold them exactly), out_stride elements between rows. */
+int mm_moe_mx_dequantize(const void* codes, const void* sf, int64_t R, int C, int dtype, void* out, int64_t out_stride,
+                         void* stream);
+
+/* Scales of 4-bit weights [E, N, ceil(C/32)] into the product's order, once: sfp has E
+ * times mm_moe_mx_scale_size(N, C) bytes, 16-byte aligned. */
+int mm_moe_mx_prepare(const void* sf, int E, int N, int C, void* sfp, void* stream);
+
+/* out[r, n] = sum over c of a[r, c] * w[e, n, c] over 4-bit operands (tcgen05
+ * kind::mxf4), fp32 sums rounded once to `dtype`.
+ *   codes, sf  activations [rows, C/2] and their scales in chunks (mm_moe_mx_quantize)
+ *   w, w_sfp   weights [E, N, C/2] and their prepared scales; C % 32 == 0, codes and w
+ *              16-byte aligned
+ *   cnt, blk_off  null: a dense product, E = 1.  Else the routing of mm_moe_dispatch
+ *              with block_m = 128: the rows of expert e's blocks take w[e], and only its
+ *              cnt[e] rows are written; other rows of out are left as they are.
+ *   out        [rows, N], out_stride elements between rows
+ *   status     device int32[4], zeroed by the caller: a wait past timeout_ms (0: 2000)
+ *              leaves MM_MOE_ERR_TIMEOUT there and out undefined */
+int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, const void* w, const void* w_sfp, int E,
+                      int N, const int32_t* cnt, const int32_t* blk_off, int dtype, void* out, int64_t out_stride,
+                      int32_t* status, unsigned timeout_ms, void* stream);
+
+/* mm_moe_mx_quantize into a workspace and mm_moe_mx_product from it, with the
+ * product's setup and first weight loads overlapping the quantiser.
+ *   x      [T, C] of `dtype` (also out's), row_stride elements between rows
+ *   slot   null: dense (E = 1, num_rows = T).  Else int32 [T, K] with cnt and blk_off of
+ *          mm_moe_dispatch with block_m = 128, rows sorted by expert on the way.
+ *   workspace  mm_moe_mx_linear_workspace(num_rows, C) bytes, 256-byte aligned; its
+ *          status word is read by mm_moe_sync_status. */
+int mm_moe_mx_linear_workspace(int64_t num_rows, int C, size_t* bytes);
+int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C, const void* w, const void* w_sfp,
+                     int E, int N, const int32_t* slot, int K, const int32_t* cnt, const int32_t* blk_off,
+                     int64_t num_rows, void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                     unsigned timeout_ms, void* stream);
+
 /* Human-readable name of a return code. */
 const char* mm_moe_status_string(int code);
 

@@ -25,6 +25,11 @@ MM_MOE_ERR_WORKSPACE_TOO_SMALL = 6
 MM_MOE_VARIANT_MX = 0
 MM_MOE_VARIANT_F8 = 1
 MM_MOE_NUM_TIMING_EVENTS = 6
+MM_MOE_DTYPE_F32 = 0
+MM_MOE_DTYPE_BF16 = 1
+MM_MOE_DTYPE_F16 = 2
+MM_MOE_SCORE_SOFTMAX = 0
+MM_MOE_SCORE_SIGMOID = 1
 STAGES = ["dispatch", "gather", "l1", "l2", "combine"]
 
 # every symbol include/mm_moe.h declares
@@ -33,7 +38,10 @@ EXPORTS = ["mm_moe_default_options", "mm_moe_workspace_size", "mm_moe_weight_sf_
            "mm_moe_sync_status", "mm_moe_status_string", "mm_moe_workspace_region",
            "mm_moe_dispatch_noalloc", "mm_moe_ep_count", "mm_moe_ep_plan", "mm_moe_ep_push_meta", "mm_moe_ep_pull",
            "mm_moe_ep_combine", "mm_moe_ep_push_out", "mm_moe_ep_combine_local", "mm_moe_ep_recv_capacity",
-           "mm_moe_ep_barrier", "mm_moe_ep_barrier_ranks"]
+           "mm_moe_ep_barrier", "mm_moe_ep_barrier_ranks",
+           "mm_moe_route", "mm_moe_route_backward", "mm_moe_permute", "mm_moe_unpermute", "mm_moe_unpermute_backward",
+           "mm_moe_mx_scale_size", "mm_moe_mx_quantize", "mm_moe_mx_dequantize", "mm_moe_mx_prepare",
+           "mm_moe_mx_product", "mm_moe_mx_linear_workspace", "mm_moe_mx_linear"]
 
 
 class mm_moe_options(ctypes.Structure):
@@ -93,6 +101,21 @@ def lib() -> ctypes.CDLL:
             "mm_moe_ep_recv_capacity": (_I, [_I, _I, _I, _I, ctypes.POINTER(_I64)]),
             "mm_moe_ep_barrier": (_I, [_P, _I, _I, ctypes.c_uint32, ctypes.c_uint, _P, _P]),
             "mm_moe_ep_barrier_ranks": (_I, [_P, _I, ctypes.c_uint32, ctypes.c_uint, ctypes.c_uint64, _P, _P]),
+            # the operators around the layer (tensor forms in ops.py)
+            "mm_moe_route": (_I, [_P, _I, _I64, _I, _I, _I, _P, _I, _I, ctypes.c_float, _P, _P, _P]),
+            "mm_moe_route_backward": (_I, [_P, _I, _I64, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P, _I64, _P]),
+            "mm_moe_permute": (_I, [_P, _I, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I64, _P]),
+            "mm_moe_unpermute": (_I, [_P, _I, _I64, _I, _I, _I, _P, _P, _P, _I64, _P]),
+            "mm_moe_unpermute_backward": (_I, [_P, _I, _I64, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I64, _P,
+                                               _P]),
+            "mm_moe_mx_scale_size": (_I, [_I64, _I, ctypes.POINTER(_SZ)]),
+            "mm_moe_mx_quantize": (_I, [_P, _I, _I64, _I64, _I, _P, _I, _I64, _P, _P, _I, _P]),
+            "mm_moe_mx_dequantize": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _P]),
+            "mm_moe_mx_prepare": (_I, [_P, _I, _I, _I, _P, _P]),
+            "mm_moe_mx_product": (_I, [_P, _P, _I64, _I, _P, _P, _I, _I, _P, _P, _I, _P, _I64, _P, ctypes.c_uint, _P]),
+            "mm_moe_mx_linear_workspace": (_I, [_I64, _I, ctypes.POINTER(_SZ)]),
+            "mm_moe_mx_linear": (_I, [_P, _I, _I64, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _I64, _P, _I64, _P, _SZ,
+                                      ctypes.c_uint, _P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -358,3 +381,64 @@ def mm_moe_ep_barrier(peer_flags, N, rank, epoch, timeout_ms, status, stream) ->
 
 def mm_moe_ep_barrier_ranks(peer_flags, N, epoch, timeout_ms, absent, status, stream) -> int:
     return lib().mm_moe_ep_barrier_ranks(peer_flags, N, epoch, timeout_ms, absent, status, stream)
+
+
+# ------------------------------------------------------------------ operators around the layer (tensor forms: ops.py)
+def mm_moe_route(logits, dtype, row_stride, T, E, K, bias, score, renorm, scale, topk_idx, topk_w, stream) -> int:
+    return lib().mm_moe_route(logits, dtype, row_stride, T, E, K, bias, score, renorm, scale, topk_idx, topk_w, stream)
+
+
+def mm_moe_route_backward(logits, dtype, row_stride, topk_idx, d_topk_w, T, E, K, score, renorm, scale, d_logits,
+                          d_row_stride, stream) -> int:
+    return lib().mm_moe_route_backward(logits, dtype, row_stride, topk_idx, d_topk_w, T, E, K, score, renorm, scale,
+                                       d_logits, d_row_stride, stream)
+
+
+def mm_moe_permute(x, dtype, row_stride, T, H, K, E, block_m, slot, src, blk_off, rows, num_rows, stream) -> int:
+    return lib().mm_moe_permute(x, dtype, row_stride, T, H, K, E, block_m, slot, src, blk_off, rows, num_rows, stream)
+
+
+def mm_moe_unpermute(rows, dtype, num_rows, T, H, K, slot, w, out, out_stride, stream) -> int:
+    return lib().mm_moe_unpermute(rows, dtype, num_rows, T, H, K, slot, w, out, out_stride, stream)
+
+
+def mm_moe_unpermute_backward(d_out, dtype, d_stride, rows, T, H, K, E, block_m, slot, src, blk_off, w, d_rows,
+                              num_rows, d_w, stream) -> int:
+    return lib().mm_moe_unpermute_backward(d_out, dtype, d_stride, rows, T, H, K, E, block_m, slot, src, blk_off, w,
+                                           d_rows, num_rows, d_w, stream)
+
+
+def mm_moe_mx_scale_size(rows, C) -> int:
+    n = _SZ(0)
+    _check(lib().mm_moe_mx_scale_size(rows, C, ctypes.byref(n)), "mm_moe_mx_scale_size")
+    return n.value
+
+
+def mm_moe_mx_quantize(x, dtype, row_stride, R, C, slot, K, num_rows, codes, sf, chunks, stream) -> int:
+    return lib().mm_moe_mx_quantize(x, dtype, row_stride, R, C, slot, K, num_rows, codes, sf, chunks, stream)
+
+
+def mm_moe_mx_dequantize(codes, sf, R, C, dtype, out, out_stride, stream) -> int:
+    return lib().mm_moe_mx_dequantize(codes, sf, R, C, dtype, out, out_stride, stream)
+
+
+def mm_moe_mx_prepare(sf, E, N, C, sfp, stream) -> int:
+    return lib().mm_moe_mx_prepare(sf, E, N, C, sfp, stream)
+
+
+def mm_moe_mx_product(codes, sf, rows, C, w, w_sfp, E, N, cnt, blk_off, dtype, out, out_stride, status, timeout_ms,
+                      stream) -> int:
+    return lib().mm_moe_mx_product(codes, sf, rows, C, w, w_sfp, E, N, cnt, blk_off, dtype, out, out_stride, status,
+                                   timeout_ms, stream)
+
+
+def mm_moe_mx_linear_workspace(num_rows, C) -> int:
+    n = _SZ(0)
+    _check(lib().mm_moe_mx_linear_workspace(num_rows, C, ctypes.byref(n)), "mm_moe_mx_linear_workspace")
+    return n.value
+
+
+def mm_moe_mx_linear(x, dtype, row_stride, T, C, w, w_sfp, E, N, slot, K, cnt, blk_off, num_rows, out, out_stride,
+                     workspace, ws_bytes, timeout_ms, stream) -> int:
+    return lib().mm_moe_mx_linear(x, dtype, row_stride, T, C, w, w_sfp, E, N, slot, K, cnt, blk_off, num_rows, out,
+                                  out_stride, workspace, ws_bytes, timeout_ms, stream)

@@ -174,6 +174,40 @@ struct GemmLaunchF8 {
 cudaError_t launch_gemm_f8_l1(const GemmLaunchF8& g, cudaStream_t s);
 cudaError_t launch_gemm_f8_l2(const GemmLaunchF8& g, cudaStream_t s);
 
+// The router (route.cu); weights and gradients are fp32, logits any dtype.
+struct RouteArgs {
+  const void* logits;
+  int dtype;
+  int64_t stride;            // elements between rows
+  int T, E, K;
+  const float* bias;         // [E] or null (sigmoid only)
+  int score, renorm;
+  float scale;
+  int32_t* topk_idx;
+  float* topk_w;
+};
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_route_backward(const RouteArgs& a, const int32_t* topk_idx, const float* d_w, void* d_logits,
+                                  int64_t d_stride, cudaStream_t s);
+
+// Rows sorted by expert and back (rows.cu), over the routing of launch_dispatch.
+struct RowsArgs {
+  int dtype;
+  int64_t T;
+  int H, K, E, block_m;
+  int64_t num_rows;          // pool rows
+  const int32_t* slot;
+  const int32_t* src;
+  const int32_t* blk_off;
+};
+cudaError_t launch_permute(const RowsArgs& a, const void* x, int64_t x_stride, void* rows, cudaStream_t s);
+// w: weights per pair, or null (ones)
+cudaError_t launch_unpermute(const RowsArgs& a, const void* rows, const float* w, void* out, int64_t out_stride,
+                             cudaStream_t s);
+// d_w: null leaves the weights' gradient out
+cudaError_t launch_unpermute_backward(const RowsArgs& a, const void* d_out, int64_t d_stride, const void* rows,
+                                      const float* w, void* d_rows, float* d_w, cudaStream_t s);
+
 // TMA descriptor creation through the driver entry point.
 CUresult encode_tmap(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
                      const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swz);

@@ -1,0 +1,304 @@
+// Tokens sorted by expert and back.  The routing kernels give every (token, k)
+// pair a row (slot, -1 where masked) of a pool whose segments are padded to
+// whole blocks, and every pool row its pair (src, -1 on padding).
+//   permute            rows[slot[t,k]] = x[t]; padding rows = 0
+//   unpermute          y[t] = sum_k w[t,k] rows[slot[t,k]]
+//   unpermute backward d_rows[slot[t,k]] = w[t,k] dy[t], padding rows = 0;
+//                      dw[t,k] = <dy[t], rows[slot[t,k]]>
+// (permute's gradient is unpermute without weights: dx[t] = sum_k d_rows[slot[t,k]].)
+// Sums are fp32 in ascending k (a dot: fp32 in a fixed tree), rounded once.
+//
+// All three move bytes and nothing else: a token's row is read once and its K
+// pool rows are written (permute), or K rows are read and one written.  Each
+// token belongs to a group of threads as wide as its row has 16-byte words (8
+// to 256), so short rows share a CTA and long rows get all of it; the pool
+// rows of a token are independent loads in flight together.
+#include "rowtypes.cuh"
+
+namespace mm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPadRows = 32;                 // pool rows a padding CTA looks at
+constexpr int kMaxGroups = kThreads / 8;     // tokens of one CTA at most
+
+// Zeroes the padding among pool rows [g * 32, g * 32 + 32): rows whose src is
+// -1, and rows past the last block, whose src the routing never wrote.
+template <int B>
+__device__ __forceinline__ void zero_padding(const int32_t* __restrict__ src, const int32_t* __restrict__ blk_off, int E,
+                                             int block_m, char* __restrict__ rows, int64_t num_rows, int64_t pitch,
+                                             int64_t g) {
+  using V = Vec<char, B>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r0 = g * kPadRows;
+  const int64_t end = static_cast<int64_t>(__ldg(blk_off + E)) * block_m;
+  const int64_t r = r0 + lane;
+  const bool pad = r < num_rows && (r >= end || __ldg(src + r) < 0);
+  unsigned m = __ballot_sync(0xffffffffu, pad);
+  const int n = static_cast<int>(pitch / B);
+  V zero;
+#pragma unroll
+  for (int i = 0; i < B; ++i) zero.v[i] = 0;
+  for (int seen = 0; m; m &= m - 1, ++seen) {
+    if ((seen & (kThreads / 32 - 1)) != warp) continue;
+    V* d = reinterpret_cast<V*>(rows + (r0 + __ffs(m) - 1) * pitch);
+    for (int i = lane; i < n; i += 32) d[i] = zero;
+  }
+}
+
+// The pool rows and weights of a CTA's tokens in shared memory.
+struct TokenRows {
+  int32_t row[kMaxGroups * kMaxK];
+  float w[kMaxGroups * kMaxK];
+};
+__device__ __forceinline__ void load_token_rows(TokenRows& s, const int32_t* __restrict__ slot,
+                                                const float* __restrict__ w, int64_t t0, int tokens, int64_t T, int K,
+                                                int64_t num_rows) {
+  for (int i = threadIdx.x; i < tokens * K; i += kThreads) {
+    const int64_t p = t0 * K + i;
+    int r = -1;
+    float wv = 1.f;
+    if (p < T * K) {
+      r = __ldg(slot + p);
+      if (r >= num_rows) r = -1;
+      if (w) wv = __ldg(w + p);
+    }
+    s.row[i] = r;
+    s.w[i] = wv;
+  }
+  __syncthreads();
+}
+
+template <int B>
+__global__ void __launch_bounds__(kThreads)
+    permute_kernel(const char* __restrict__ x, int64_t x_pitch, int64_t T, int64_t pitch, int lanes, int token_ctas,
+                   const int32_t* __restrict__ slot, int K, const int32_t* __restrict__ src,
+                   const int32_t* __restrict__ blk_off, int E, int block_m, char* __restrict__ rows,
+                   int64_t num_rows) {
+  using V = Vec<char, B>;
+  if (static_cast<int>(blockIdx.x) >= token_ctas) {
+    zero_padding<B>(src, blk_off, E, block_m, rows, num_rows, pitch, blockIdx.x - token_ctas);
+    return;
+  }
+  __shared__ TokenRows s;
+  const int tokens = kThreads / lanes;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  load_token_rows(s, slot, nullptr, t0, tokens, T, K, num_rows);
+  const int sub = threadIdx.x / lanes, l = threadIdx.x % lanes;
+  const int64_t t = t0 + sub;
+  if (t >= T) return;
+  const V* xr = reinterpret_cast<const V*>(x + t * x_pitch);
+  const int32_t* my = s.row + sub * K;
+  const int n = static_cast<int>(pitch / B);
+  for (int i = l; i < n; i += lanes) {
+    const V v = xr[i];
+#pragma unroll 4
+    for (int k = 0; k < K; ++k) {
+      const int64_t r = my[k];
+      if (r >= 0) reinterpret_cast<V*>(rows + r * pitch)[i] = v;
+    }
+  }
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads)
+    unpermute_kernel(const T* __restrict__ rows, int64_t num_rows, int H, int64_t tokens_total, int lanes,
+                     const int32_t* __restrict__ slot, const float* __restrict__ w, int K, T* __restrict__ out,
+                     int64_t out_stride) {
+  using V = Vec<T, N>;
+  __shared__ TokenRows s;
+  const int tokens = kThreads / lanes;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  load_token_rows(s, slot, w, t0, tokens, tokens_total, K, num_rows);
+  const int sub = threadIdx.x / lanes, l = threadIdx.x % lanes;
+  const int64_t t = t0 + sub;
+  if (t >= tokens_total) return;
+  const int32_t* my = s.row + sub * K;
+  const float* mw = s.w + sub * K;
+  const int n = H / N;
+  for (int i = l; i < n; i += lanes) {
+    float acc[N];
+#pragma unroll
+    for (int c = 0; c < N; ++c) acc[c] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < K; ++k) {
+      const int64_t r = my[k];
+      if (r >= 0) {
+        const V v = reinterpret_cast<const V*>(rows + r * H)[i];
+        const float wk = mw[k];
+#pragma unroll
+        for (int c = 0; c < N; ++c) acc[c] = fmaf(wk, to_float(v.v[c]), acc[c]);
+      }
+    }
+    V o;
+#pragma unroll
+    for (int c = 0; c < N; ++c) o.v[c] = from_float<T>(acc[c]);
+    reinterpret_cast<V*>(out + t * out_stride)[i] = o;
+  }
+}
+
+// KT >= K: the dots of a token live in registers.
+template <typename T, int N, int KT>
+__global__ void __launch_bounds__(kThreads)
+    unpermute_backward_kernel(const T* __restrict__ d_out, int64_t d_stride, const T* __restrict__ rows, int H,
+                              int64_t tokens_total, int lanes, int token_ctas, const int32_t* __restrict__ slot,
+                              const float* __restrict__ w, int K, const int32_t* __restrict__ src,
+                              const int32_t* __restrict__ blk_off, int E, int block_m, T* __restrict__ d_rows,
+                              int64_t num_rows, float* __restrict__ d_w) {
+  using V = Vec<T, N>;
+  if (static_cast<int>(blockIdx.x) >= token_ctas) {
+    zero_padding<N * sizeof(T)>(src, blk_off, E, block_m, reinterpret_cast<char*>(d_rows), num_rows,
+                                static_cast<int64_t>(H) * sizeof(T), blockIdx.x - token_ctas);
+    return;
+  }
+  __shared__ TokenRows s;
+  __shared__ float s_dot[kThreads / 32][KT];
+  const int tokens = kThreads / lanes;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  load_token_rows(s, slot, w, t0, tokens, tokens_total, K, num_rows);
+  const int sub = threadIdx.x / lanes, l = threadIdx.x % lanes;
+  const int64_t t = t0 + sub;
+  float dot[KT];
+#pragma unroll
+  for (int k = 0; k < KT; ++k) dot[k] = 0.f;
+  if (t < tokens_total) {
+    const V* dr = reinterpret_cast<const V*>(d_out + t * d_stride);
+    const int32_t* my = s.row + sub * K;
+    const float* mw = s.w + sub * K;
+    const int n = H / N;
+    for (int i = l; i < n; i += lanes) {
+      const V dv = dr[i];
+      float d[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) d[c] = to_float(dv.v[c]);
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const int64_t r = k < K ? my[k] : -1;
+        if (r >= 0) {
+          if (d_w) {
+            const V v = reinterpret_cast<const V*>(rows + r * H)[i];
+#pragma unroll
+            for (int c = 0; c < N; ++c) dot[k] = fmaf(to_float(v.v[c]), d[c], dot[k]);
+          }
+          const float wk = mw[k];
+          V o;
+#pragma unroll
+          for (int c = 0; c < N; ++c) o.v[c] = from_float<T>(wk * d[c]);
+          reinterpret_cast<V*>(d_rows + r * H)[i] = o;
+        }
+      }
+    }
+  }
+  if (!d_w) return;
+  // sum over the token's threads: lanes of a warp, then (rows wider than a warp) its warps in order
+  const int width = lanes < 32 ? lanes : 32;
+#pragma unroll
+  for (int k = 0; k < KT; ++k)
+    for (int o = width / 2; o > 0; o >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], o);
+  if (lanes <= 32) {
+    if (l == 0 && t < tokens_total)
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+        if (k < K) d_w[t * K + k] = dot[k];
+    return;
+  }
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < KT; ++k) s_dot[threadIdx.x >> 5][k] = dot[k];
+  __syncthreads();
+  if (l < K && t < tokens_total) {
+    float v = 0.f;
+    for (int i = 0; i < lanes / 32; ++i) v += s_dot[sub * (lanes / 32) + i][l];
+    d_w[t * K + l] = v;
+  }
+}
+
+// Threads of a token's group: its accesses rounded up to a power of two, 8 to 256.
+int group_lanes(int64_t accesses) {
+  int l = 8;
+  while (l < kThreads && l < accesses) l *= 2;
+  return l;
+}
+
+uint64_t bits_of(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+
+// f with the number of elements a B-byte access holds
+template <typename T, typename F>
+cudaError_t with_access(int B, F f) {
+  if (B == 16) return f(std::integral_constant<int, 16 / sizeof(T)>{});
+  if (B == 8) return f(std::integral_constant<int, 8 / sizeof(T)>{});
+  if constexpr (sizeof(T) == 2) {
+    if (B == 4) return f(std::integral_constant<int, 2>{});
+  }
+  return f(std::integral_constant<int, 1>{});
+}
+
+}  // namespace
+
+cudaError_t launch_permute(const RowsArgs& a, const void* x, int64_t x_stride, void* rows, cudaStream_t s) {
+  const int es = dtype_size(a.dtype);
+  const int64_t pitch = static_cast<int64_t>(a.H) * es, x_pitch = x_stride * es;
+  const int B = access_bytes(bits_of(x) | bits_of(rows) | pitch | x_pitch);
+  const int lanes = group_lanes(pitch / B);
+  const int64_t ctas = (a.T + kThreads / lanes - 1) / (kThreads / lanes);
+  const int64_t grid = ctas + (a.num_rows + kPadRows - 1) / kPadRows;
+  if (grid == 0) return cudaSuccess;
+  auto go = [&](auto b) {
+    permute_kernel<decltype(b)::value><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(
+        static_cast<const char*>(x), x_pitch, a.T, pitch, lanes, static_cast<int>(ctas), a.slot, a.K, a.src, a.blk_off,
+        a.E, a.block_m, static_cast<char*>(rows), a.num_rows);
+    return cudaGetLastError();
+  };
+  if (B == 16) return go(std::integral_constant<int, 16>{});
+  if (B == 8) return go(std::integral_constant<int, 8>{});
+  if (B == 4) return go(std::integral_constant<int, 4>{});
+  return go(std::integral_constant<int, 2>{});
+}
+
+cudaError_t launch_unpermute(const RowsArgs& a, const void* rows, const float* w, void* out, int64_t out_stride,
+                             cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  const int es = dtype_size(a.dtype);
+  const int B = access_bytes(bits_of(rows) | bits_of(out) | static_cast<uint64_t>(a.H) * es |
+                             static_cast<uint64_t>(out_stride) * es);
+  return with_dtype(a.dtype, [&](auto tag) {
+    using T = decltype(tag);
+    return with_access<T>(B, [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      const int lanes = group_lanes(a.H / N);
+      const int64_t ctas = (a.T + kThreads / lanes - 1) / (kThreads / lanes);
+      unpermute_kernel<T, N><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(
+          static_cast<const T*>(rows), a.num_rows, a.H, a.T, lanes, a.slot, w, a.K, static_cast<T*>(out), out_stride);
+      return cudaGetLastError();
+    });
+  });
+}
+
+cudaError_t launch_unpermute_backward(const RowsArgs& a, const void* d_out, int64_t d_stride, const void* rows,
+                                      const float* w, void* d_rows, float* d_w, cudaStream_t s) {
+  const int es = dtype_size(a.dtype);
+  const int B = access_bytes(bits_of(rows) | bits_of(d_out) | bits_of(d_rows) | static_cast<uint64_t>(a.H) * es |
+                             static_cast<uint64_t>(d_stride) * es);
+  return with_dtype(a.dtype, [&](auto tag) {
+    using T = decltype(tag);
+    return with_access<T>(B, [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      const int lanes = group_lanes(a.H / N);
+      const int64_t ctas = (a.T + kThreads / lanes - 1) / (kThreads / lanes);
+      const int64_t grid = ctas + (a.num_rows + kPadRows - 1) / kPadRows;
+      if (grid == 0) return cudaSuccess;
+      auto go = [&](auto kt) {
+        unpermute_backward_kernel<T, N, decltype(kt)::value><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(
+            static_cast<const T*>(d_out), d_stride, static_cast<const T*>(rows), a.H, a.T, lanes,
+            static_cast<int>(ctas), a.slot, w, a.K, a.src, a.blk_off, a.E, a.block_m, static_cast<T*>(d_rows),
+            a.num_rows, d_w);
+        return cudaGetLastError();
+      };
+      if (a.K <= 4) return go(std::integral_constant<int, 4>{});
+      if (a.K <= 8) return go(std::integral_constant<int, 8>{});
+      return go(std::integral_constant<int, 16>{});
+    });
+  });
+}
+
+}  // namespace mm
