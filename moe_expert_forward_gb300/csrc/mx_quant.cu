@@ -5,22 +5,26 @@
 // A block that holds a NaN or an infinity gets the scale byte 255 (NaN) and
 // zero codes, so everything computed from it is NaN.
 //
-// The quantiser is bound by its reads (R * C elements in, 17/32 byte per
-// element out).  A lane takes 8 elements, four lanes a block: reads of 16 bytes
-// a lane and code stores of 4 are contiguous over the warp, and a block's amax
-// is two shuffles away.  kBatch octets' loads are in flight per thread.
+// Both directions are bound by memory (R * C elements on one side, 17/32 byte per
+// element on the other).  A lane takes 16 elements, two lanes a block: 16-bit
+// rows are read and written 32 bytes a lane and codes 8, contiguous over the
+// warp, and a block's amax is one shuffle away.  The amax is taken on the packed
+// 16-bit words, and every thread steps its (row, group) pair instead of dividing.
 #include "mx_linear.h"
 #include "ptx.cuh"
 #include "rowtypes.cuh"
+
+#include <cstring>
+#include <type_traits>
 
 namespace mm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;
+constexpr int kBatch = 2;            // groups of 16 elements a thread has in flight
 
 // 8 fp32 values -> 8 e2m1 codes, value 0 in the lowest nibble
-__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v) {
   uint32_t r;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -41,135 +45,207 @@ __device__ __forceinline__ int e2m1_exponent(uint32_t amax_bits) {
   return static_cast<int>(b >> 23) - 126 - 3 + ((b & 0x7FFFFF) > 0x400000 ? 1 : 0);
 }
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void load8(const T* __restrict__ row, int c, int C, float (&f)[8]) {
-  if (kVec) {
-    if (c < C) {
-      if constexpr (sizeof(T) == 2) {
-        const Vec<T, 8> v = *reinterpret_cast<const Vec<T, 8>*>(row + c);
+// Sixteen consecutive elements of a row as they sit in memory.
+template <typename T>
+struct Group {
+  static constexpr int kWords = 16 * sizeof(T) / 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = to_float(v.v[i]);
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // elements c .. c+15 of `row`, zeros past C
+  template <bool kVec>
+  __device__ __forceinline__ void load(const T* __restrict__ row, int c, int C) {
+    if (kVec) {                       // C is a multiple of 16, rows 32-byte aligned
+      if (c < C) {
+#pragma unroll
+        for (int h = 0; h < kWords / 8; ++h)
+          asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                       : "=r"(w[8 * h]), "=r"(w[8 * h + 1]), "=r"(w[8 * h + 2]), "=r"(w[8 * h + 3]),
+                         "=r"(w[8 * h + 4]), "=r"(w[8 * h + 5]), "=r"(w[8 * h + 6]), "=r"(w[8 * h + 7])
+                       : "l"(row + c + h * (32 / sizeof(T))));
       } else {
-        const Vec<T, 4> v0 = *reinterpret_cast<const Vec<T, 4>*>(row + c);
-        const Vec<T, 4> v1 = *reinterpret_cast<const Vec<T, 4>*>(row + c + 4);
+        clear();
+      }
+    } else {
+      T v[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[i] = to_float(v0.v[i]);
-          f[i + 4] = to_float(v1.v[i]);
-        }
+      for (int i = 0; i < 16; ++i) v[i] = c + i < C ? row[c + i] : from_float<T>(0.f);
+      memcpy(w, v, sizeof(v));
+    }
+  }
+  // the largest |element| as fp32 bits; at least 0x7F800000 where one is not finite
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    if constexpr (sizeof(T) == 4) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+      return m;
+    } else {
+      // magnitudes of 16-bit floats order like their bits, NaN above infinity
+      uint32_t hi = 0, lo = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        hi = max(hi, w[i] & 0x7FFF0000u);
+        lo = max(lo, w[i] & 0x00007FFFu);
+      }
+      const uint32_t m = max(hi >> 16, lo);
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) return m << 16;
+      else return m >= 0x7C00u ? 0x7F800000u : __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+    }
+  }
+  __device__ __forceinline__ void floats(float (&f)[16]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        __half2 h;
+        memcpy(&h, &w[i], 4);
+        const float2 p = __half22float2(h);
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+      }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < C ? to_float(row[c + i]) : 0.f;
   }
-}
+};
 
-// Octet o of row r, over all rows; thread i takes octets i, i + step, ...  A row
-// has `opr` octets (a multiple of 4); step = d_row * opr + d_oct.
-template <typename T, bool kVec>
+// The position of a thread in [rows][groups of 16], stepped by a fixed number of groups.
+struct Walk {
+  int64_t r;
+  int g;
+  __device__ __forceinline__ Walk(int64_t i, int groups) : r(i / groups), g(static_cast<int>(i - r * groups)) {}
+  __device__ __forceinline__ void step(int d_row, int d_group, int groups) {
+    r += d_row;
+    g += d_group;
+    if (g >= groups) {
+      g -= groups;
+      ++r;
+    }
+  }
+};
+
+// step = gridDim * kThreads groups = d_row rows and d_group groups; `groups` (of a row) is even.
+template <typename T, bool kVec, bool kChunks, bool kSlots>
 __global__ void __launch_bounds__(kThreads)
-    quantize_kernel(const MxQuantArgs a, int opr, int d_row, int d_oct) {
+    quantize_kernel(const MxQuantArgs a, int groups, int d_row, int d_group) {
   pdl_trigger();                      // the product may set itself up meanwhile
   const T* x = static_cast<const T*>(a.x);
   if (a.status && blockIdx.x == 0 && threadIdx.x < 4) a.status[threadIdx.x] = 0;
-  const int code_octs = (a.C + 31) / 32 * 4;          // octets a row of codes holds
+  const int code_groups = (a.C + 31) / 32 * 2;        // groups a row of codes holds
   const int KB = mx_chunks(a.C);
-  const int64_t total = a.R * opr;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  int64_t r = i0 / opr;
-  int o = static_cast<int>(i0 - r * opr);
-  // the last lanes of a warp may be past the end: they take part in the shuffles with zeros
-  for (int64_t base = i0 - (threadIdx.x & 31); base < total; base += kBatch * step) {
-    float f[kBatch][8];
+  Walk at(i0, groups);
+  // a warp runs while any of its lanes has a row, so the shuffles see all of it
+  while (__any_sync(0xffffffffu, at.r < a.R)) {
+    Group<T> v[kBatch];
     int64_t rr[kBatch];
-    int oo[kBatch];
+    int gg[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      rr[u] = r;
-      oo[u] = o;
-      if (r < a.R) {
-        load8<T, kVec>(x + r * a.stride, o * 8, a.C, f[u]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
-      }
-      r += d_row;
-      o += d_oct;
-      if (o >= opr) {
-        o -= opr;
-        ++r;
-      }
+      rr[u] = at.r;
+      gg[u] = at.g;
+      if (at.r < a.R) v[u].template load<kVec>(x + at.r * a.stride, at.g * 16, a.C);
+      else v[u].clear();
+      at.step(d_row, d_group, groups);
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      uint32_t am = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(f[u][i]) & 0x7FFFFFFFu);
+      uint32_t am = v[u].amax_bits();
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
       const bool bad = am >= 0x7F800000u;
       const int e = bad ? 128 : e2m1_exponent(am);
-      const float scale = __uint_as_float(bad ? 0u : static_cast<uint32_t>(127 - e) << 23);   // 2^-e
+      const float scale = __uint_as_float(static_cast<uint32_t>(bad ? 0 : 127 - e) << 23);   // 2^-e
+      float f[16];
+      v[u].floats(f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[u][i] = bad ? 0.f : f[u][i] * scale;
-      const uint32_t codes = cvt_e2m1x8(f[u]);
-      if (rr[u] >= a.R) continue;
-      const uint8_t sf = static_cast<uint8_t>(e + 127);
-      const int K = a.slot ? a.K : 1;
-      for (int k = 0; k < K; ++k) {
-        int64_t d = rr[u];
-        if (a.slot) {
-          d = __ldg(a.slot + rr[u] * K + k);
-          if (d < 0 || d >= a.num_rows) continue;
-        }
-        if (oo[u] < code_octs) *reinterpret_cast<uint32_t*>(a.codes + (d * code_octs + oo[u]) * 4) = codes;
-        if ((oo[u] & 3) == 0) {
-          const int b = oo[u] >> 2;
-          if (a.chunks) a.sf[mx_sf_word(d, b >> 2, KB) + (b & 3)] = sf;
-          else a.sf[d * (code_octs / 4) + b] = sf;
+      for (int i = 0; i < 16; ++i) f[i] = f[i] * scale;
+      uint2 codes = make_uint2(cvt_e2m1x8(f), cvt_e2m1x8(f + 8));
+      if (bad) codes = make_uint2(0, 0);
+      if (rr[u] < a.R) {
+        const uint8_t sf = static_cast<uint8_t>(e + 127);
+        const int K = kSlots ? a.K : 1;
+        for (int k = 0; k < K; ++k) {
+          int64_t d = rr[u];
+          if (kSlots) {
+            d = __ldg(a.slot + rr[u] * K + k);
+            if (d < 0 || d >= a.num_rows) continue;
+          }
+          if (!kChunks || gg[u] < code_groups) reinterpret_cast<uint2*>(a.codes)[d * code_groups + gg[u]] = codes;
+          if ((gg[u] & 1) == 0) {
+            const int b = gg[u] >> 1;
+            if (kChunks) a.sf[mx_sf_word(d, b >> 2, KB) + (b & 3)] = sf;
+            else a.sf[d * (code_groups / 2) + b] = sf;
+          }
         }
       }
     }
+  }
+}
+
+// Four e2m1 codes (the low 16 bits of c) times 2^126 * s, s = 2^(sf - 127): the code's three magnitude bits
+// placed at the top of an fp32 mantissa and exponent are its value times 2^-126, the subnormal 0.5 included.
+__device__ __forceinline__ void decode4(uint32_t c, float s, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t n = c >> (4 * i);
+    f[i] = __uint_as_float((n & 7u) << 22 | (n & 8u) << 28) * 0x1p126f * s;
   }
 }
 
 // Values of codes [R, ceil(C/32) * 16 bytes] with row-major scales.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads)
-    dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ sf, int64_t R, int C,
-                      T* __restrict__ out, int64_t out_stride) {
-  const int octs = (C + 31) / 32 * 4;
-  const int64_t total = R * octs;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t r = i / octs;
-    const int o = static_cast<int>(i - r * octs);
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-    const uint32_t b = __ldg(sf + (i >> 2));
-    const float scale = b == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(b ? b << 23 : 0x00400000u);
-    T* d = out + r * out_stride + o * 8;
-    Vec<T, 8> v;
+    dequantize_kernel(const uint2* __restrict__ codes, const uint8_t* __restrict__ sf, int64_t R, int C,
+                      T* __restrict__ out, int64_t out_stride, int groups, int d_row, int d_group) {
+  int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads, total = R * groups;
+  Walk at(i, groups);
+  while (i < total) {
+    uint2 w[kBatch];
+    uint32_t b[kBatch];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      // sign, then the magnitude (2-bit exponent, 1-bit mantissa; 0 and 0.5 are its subnormals)
-      const uint32_t n = (w >> (4 * q)) & 15u, ex = (n >> 1) & 3u, m = n & 1u;
-      const float mag = ex ? __uint_as_float((ex + 126u) << 23 | m << 22) : 0.5f * m;
-      v.v[q] = from_float<T>(scale * (n & 8u ? -mag : mag));
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t j = i + u * step;
+      w[u] = j < total ? __ldg(codes + j) : make_uint2(0, 0);
+      b[u] = j < total ? __ldg(sf + (j >> 1)) : 0;
     }
-    if (kVec && o * 8 + 8 <= C) {
-      constexpr int N = 16 / sizeof(T);
 #pragma unroll
-      for (int h = 0; h < 8 / N; ++h)
-        reinterpret_cast<Vec<T, N>*>(d)[h] = reinterpret_cast<const Vec<T, N>*>(&v)[h];
-    } else {
+    for (int u = 0; u < kBatch; ++u) {
+      if (i < total) {
+        const float s = __uint_as_float(b[u] == 255 ? 0x7FC00000u : (b[u] ? b[u] << 23 : 0x00400000u));
+        float f[16];
+        decode4(w[u].x, s, f);
+        decode4(w[u].x >> 16, s, f + 4);
+        decode4(w[u].y, s, f + 8);
+        decode4(w[u].y >> 16, s, f + 12);
+        T* d = out + at.r * out_stride + at.g * 16;
+        const int left = C - at.g * 16;
+        if (kVec && left >= 16) {
+          T v[16];
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (o * 8 + q < C) d[q] = v.v[q];
+          for (int q = 0; q < 16; ++q) v[q] = from_float<T>(f[q]);
+          uint32_t o[Group<T>::kWords];
+          memcpy(o, v, sizeof(v));
+#pragma unroll
+          for (int h = 0; h < Group<T>::kWords / 8; ++h) st_global_v8(reinterpret_cast<float*>(d) + 8 * h, o + 8 * h);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            if (q < left) d[q] = from_float<T>(f[q]);
+        }
+      }
+      i += step;
+      at.step(d_row, d_group, groups);
     }
   }
 }
@@ -206,36 +282,46 @@ int blocks_for(int64_t threads, int per_sm) {
   return static_cast<int>(b < 1 ? 1 : (b > cap ? cap : b));
 }
 
-bool wide(const void* p, int64_t pitch_bytes) {
-  return access_bytes(reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(pitch_bytes)) == 16;
+// rows of whole 16-element groups on 32-byte boundaries
+bool wide(const void* p, int64_t pitch_bytes, int C) {
+  return (reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(pitch_bytes)) % 32 == 0 && C % 16 == 0;
 }
 
 }  // namespace
 
 cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t s) {
-  const int opr = a.chunks ? mx_chunks(a.C) * 16 : (a.C + 31) / 32 * 4;
-  const int grid = blocks_for((a.R * opr + kBatch - 1) / kBatch, 8);
+  const int groups = a.chunks ? mx_chunks(a.C) * 8 : (a.C + 31) / 32 * 2;
+  const int grid = blocks_for((a.R * groups + kBatch - 1) / kBatch, 8);
   const int64_t step = static_cast<int64_t>(grid) * kThreads;
-  const int d_row = static_cast<int>(step / opr), d_oct = static_cast<int>(step % opr);
+  const int d_row = static_cast<int>(step / groups), d_group = static_cast<int>(step % groups);
   return with_dtype(a.dtype, [&](auto tag) {
     using T = decltype(tag);
-    if (wide(a.x, a.stride * sizeof(T)) && a.C % 8 == 0)
-      quantize_kernel<T, true><<<grid, kThreads, 0, s>>>(a, opr, d_row, d_oct);
-    else
-      quantize_kernel<T, false><<<grid, kThreads, 0, s>>>(a, opr, d_row, d_oct);
-    return cudaGetLastError();
+    auto go = [&](auto vec) {
+      constexpr bool V = decltype(vec)::value;
+      if (a.slot && a.chunks) quantize_kernel<T, V, true, true><<<grid, kThreads, 0, s>>>(a, groups, d_row, d_group);
+      else if (a.slot) quantize_kernel<T, V, false, true><<<grid, kThreads, 0, s>>>(a, groups, d_row, d_group);
+      else if (a.chunks) quantize_kernel<T, V, true, false><<<grid, kThreads, 0, s>>>(a, groups, d_row, d_group);
+      else quantize_kernel<T, V, false, false><<<grid, kThreads, 0, s>>>(a, groups, d_row, d_group);
+      return cudaGetLastError();
+    };
+    return wide(a.x, a.stride * sizeof(T), a.C) ? go(std::true_type{}) : go(std::false_type{});
   });
 }
 
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* sf, int64_t R, int C, int dtype, void* out,
                                  int64_t out_stride, cudaStream_t s) {
-  const int grid = blocks_for(R * ((C + 31) / 32 * 4), 16);
+  const int groups = (C + 31) / 32 * 2;
+  const int grid = blocks_for((R * groups + kBatch - 1) / kBatch, 8);
+  const int64_t step = static_cast<int64_t>(grid) * kThreads;
+  const int d_row = static_cast<int>(step / groups), d_group = static_cast<int>(step % groups);
+  const uint2* c = reinterpret_cast<const uint2*>(codes);
   return with_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
-    if (wide(out, out_stride * sizeof(T)))
-      dequantize_kernel<T, true><<<grid, kThreads, 0, s>>>(codes, sf, R, C, static_cast<T*>(out), out_stride);
+    T* o = static_cast<T*>(out);
+    if (wide(out, out_stride * sizeof(T), C))
+      dequantize_kernel<T, true><<<grid, kThreads, 0, s>>>(c, sf, R, C, o, out_stride, groups, d_row, d_group);
     else
-      dequantize_kernel<T, false><<<grid, kThreads, 0, s>>>(codes, sf, R, C, static_cast<T*>(out), out_stride);
+      dequantize_kernel<T, false><<<grid, kThreads, 0, s>>>(c, sf, R, C, o, out_stride, groups, d_row, d_group);
     return cudaGetLastError();
   });
 }
