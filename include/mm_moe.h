@@ -443,13 +443,23 @@ int mm_moe_route_backward(const void* logits, int dtype, int64_t row_stride, con
                           const float* d_topk_w, int T, int E, int K, int score, int renorm, float scale,
                           void* d_logits, int64_t d_row_stride, void* stream);
 
-/* Tokens into the pool of a routing (mm_moe_dispatch's slot, src and blk_off of
+/* mm_moe_dispatch's results (cnt [E], blk_off [E+1], slot [T*K], src [src_capacity])
+ * for rows that are sorted outside mm_moe_forward: one launch up to 2^18 pairs, and
+ * `status` (device int32[4]) is cleared by the call instead of the caller, so status[0]
+ * is this call's MM_MOE_OK or MM_MOE_ERR_BAD_ROUTING.  scratch: mm_moe_sort_scratch_size
+ * bytes, 4-byte aligned (0 bytes, and null allowed, where one launch does it). */
+int mm_moe_sort_scratch_size(int T, int K, int E, size_t* bytes);
+int mm_moe_sort(const int32_t* topk_idx, int T, int K, int E, int block_m, int32_t* cnt, int32_t* blk_off,
+                int32_t* slot, int32_t* src, int64_t src_capacity, void* scratch, size_t scratch_bytes,
+                int32_t* status, void* stream);
+
+/* Tokens into the pool of a routing (mm_moe_sort's or mm_moe_dispatch's slot, src and blk_off of
  * the same T, K, E, block_m): rows[slot[t*K + k]] = x[t]; every other row of the
  * num_rows is zero (padding, and rows past the last block).  x [T, H],
  * row_stride elements between rows; rows [num_rows, H] contiguous.  H >= 1 of
  * any size; accesses are as wide as addresses and row pitches are aligned.
- * num_rows at least mm_moe_dispatch's src_capacity rule for these sizes; src
- * holds num_rows entries. */
+ * num_rows at least T*K + min(T*K, E) * (block_m - 1); src holds
+ * num_rows entries. */
 int mm_moe_permute(const void* x, int dtype, int64_t row_stride, int T, int H, int K, int E, int block_m,
                    const int32_t* slot, const int32_t* src, const int32_t* blk_off, void* rows, int64_t num_rows,
                    void* stream);
@@ -489,7 +499,7 @@ int mm_moe_mx_quantize(const void* x, int dtype, int64_t row_stride, int64_t R, 
                        int64_t num_rows, void* codes, void* sf, int chunks, void* stream);
 
 /* The values codes and row-major scales stand for: out [R, C] of `dtype` (bf16 and
- * fp32 hold them exactly), out_stride elements between rows. */
+ * fp32 hold them exactly), out_stride elements between rows; codes 16-byte aligned. */
 int mm_moe_mx_dequantize(const void* codes, const void* sf, int64_t R, int C, int dtype, void* out, int64_t out_stride,
                          void* stream);
 

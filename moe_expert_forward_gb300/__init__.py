@@ -39,7 +39,7 @@ EXPORTS = ["mm_moe_default_options", "mm_moe_workspace_size", "mm_moe_weight_sf_
            "mm_moe_dispatch_noalloc", "mm_moe_ep_count", "mm_moe_ep_plan", "mm_moe_ep_push_meta", "mm_moe_ep_pull",
            "mm_moe_ep_combine", "mm_moe_ep_push_out", "mm_moe_ep_combine_local", "mm_moe_ep_recv_capacity",
            "mm_moe_ep_barrier", "mm_moe_ep_barrier_ranks",
-           "mm_moe_route", "mm_moe_route_backward", "mm_moe_permute", "mm_moe_unpermute", "mm_moe_unpermute_backward",
+           "mm_moe_route", "mm_moe_route_backward", "mm_moe_sort_scratch_size", "mm_moe_sort", "mm_moe_permute", "mm_moe_unpermute", "mm_moe_unpermute_backward",
            "mm_moe_mx_scale_size", "mm_moe_mx_quantize", "mm_moe_mx_dequantize", "mm_moe_mx_prepare",
            "mm_moe_mx_product", "mm_moe_mx_linear_workspace", "mm_moe_mx_linear"]
 
@@ -104,6 +104,8 @@ def lib() -> ctypes.CDLL:
             # the operators around the layer (tensor forms in ops.py)
             "mm_moe_route": (_I, [_P, _I, _I64, _I, _I, _I, _P, _I, _I, ctypes.c_float, _P, _P, _P]),
             "mm_moe_route_backward": (_I, [_P, _I, _I64, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P, _I64, _P]),
+            "mm_moe_sort_scratch_size": (_I, [_I, _I, _I, ctypes.POINTER(_SZ)]),
+            "mm_moe_sort": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _I64, _P, _SZ, _P, _P]),
             "mm_moe_permute": (_I, [_P, _I, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I64, _P]),
             "mm_moe_unpermute": (_I, [_P, _I, _I64, _I, _I, _I, _P, _P, _P, _I64, _P]),
             "mm_moe_unpermute_backward": (_I, [_P, _I, _I64, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I64, _P,
@@ -392,6 +394,18 @@ def mm_moe_route_backward(logits, dtype, row_stride, topk_idx, d_topk_w, T, E, K
                           d_row_stride, stream) -> int:
     return lib().mm_moe_route_backward(logits, dtype, row_stride, topk_idx, d_topk_w, T, E, K, score, renorm, scale,
                                        d_logits, d_row_stride, stream)
+
+
+def mm_moe_sort_scratch_size(T, K, E) -> int:
+    n = _SZ(0)
+    _check(lib().mm_moe_sort_scratch_size(T, K, E, ctypes.byref(n)), "mm_moe_sort_scratch_size")
+    return n.value
+
+
+def mm_moe_sort(topk_idx, T, K, E, block_m, cnt, blk_off, slot, src, src_capacity, scratch, scratch_bytes, status,
+                stream) -> int:
+    return lib().mm_moe_sort(topk_idx, T, K, E, block_m, cnt, blk_off, slot, src, src_capacity, scratch,
+                             scratch_bytes, status, stream)
 
 
 def mm_moe_permute(x, dtype, row_stride, T, H, K, E, block_m, slot, src, blk_off, rows, num_rows, stream) -> int:

@@ -93,6 +93,28 @@ int mm_moe_route_backward(const void* logits, int dtype, int64_t row_stride, con
   return done(launch_route_backward(a, topk_idx, d_topk_w, d_logits, d_row_stride, static_cast<cudaStream_t>(stream)));
 }
 
+int mm_moe_sort_scratch_size(int T, int K, int E, size_t* bytes) {
+  if (!bytes || T < 0 || K < 1 || K > kMaxK || E < 1 || E > kMaxE || K > E) return MM_MOE_ERR_INVALID_ARG;
+  const int64_t pairs = static_cast<int64_t>(T) * K;
+  if (pairs > kMaxPairs) return MM_MOE_ERR_INVALID_ARG;
+  *bytes = sort_in_one_launch(pairs) ? 0 : sizeof(int32_t) * static_cast<size_t>(kDispatchMaxCtas) * E;
+  return MM_MOE_OK;
+}
+
+int mm_moe_sort(const int32_t* topk_idx, int T, int K, int E, int block_m, int32_t* cnt, int32_t* blk_off,
+                int32_t* slot, int32_t* src, int64_t src_capacity, void* scratch, size_t scratch_bytes,
+                int32_t* status, void* stream) {
+  size_t need = 0;
+  if (int r = mm_moe_sort_scratch_size(T, K, E, &need)) return r;
+  if (int r = check_pool(T, K, E, block_m, src_capacity)) return r;
+  if (!cnt || !blk_off || !status || (T > 0 && (!topk_idx || !slot || !src))) return MM_MOE_ERR_INVALID_ARG;
+  if (need && (!scratch || !aligned(scratch, 4))) return MM_MOE_ERR_INVALID_ARG;
+  if (scratch_bytes < need) return MM_MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
+  return done(launch_sort(topk_idx, T, K, E, block_m, cnt, blk_off, slot, src, status, static_cast<int32_t*>(scratch),
+                          static_cast<int64_t>(scratch_bytes / 4), static_cast<cudaStream_t>(stream)));
+}
+
 int mm_moe_permute(const void* x, int dtype, int64_t row_stride, int T, int H, int K, int E, int block_m,
                    const int32_t* slot, const int32_t* src, const int32_t* blk_off, void* rows, int64_t num_rows,
                    void* stream) {
@@ -162,7 +184,7 @@ int mm_moe_mx_dequantize(const void* codes, const void* sf, int64_t R, int C, in
   if (!dtype_known(dtype) || R < 0 || R > kMaxRows || C < 1 || C > (1 << 30) || out_stride < C)
     return MM_MOE_ERR_INVALID_ARG;
   if (R == 0) return MM_MOE_OK;
-  if (!codes || !sf || !out || !aligned(codes, 4) || !aligned(out, dtype_size(dtype))) return MM_MOE_ERR_INVALID_ARG;
+  if (!codes || !sf || !out || !aligned(codes, 16) || !aligned(out, dtype_size(dtype))) return MM_MOE_ERR_INVALID_ARG;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   return done(launch_mx_dequantize(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(sf), R, C, dtype,
                                    out, out_stride, static_cast<cudaStream_t>(stream)));

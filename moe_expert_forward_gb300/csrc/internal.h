@@ -190,6 +190,14 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_route_backward(const RouteArgs& a, const int32_t* topk_idx, const float* d_w, void* d_logits,
                                   int64_t d_stride, cudaStream_t s);
 
+// The routing in one launch up to so many pairs (sort.cu), by launch_dispatch above;
+// status is cleared first.  `scratch` is launch_dispatch's, unused in one launch.
+constexpr int64_t kSortOneLaunchPairs = int64_t(1) << 18;
+bool sort_in_one_launch(int64_t pairs);
+cudaError_t launch_sort(const int32_t* topk_idx, int T, int K, int E, int block_m, int32_t* cnt, int32_t* blk_off,
+                        int32_t* slot, int32_t* src, int32_t* status, int32_t* scratch, int64_t scratch_ints,
+                        cudaStream_t s);
+
 // Rows sorted by expert and back (rows.cu), over the routing of launch_dispatch.
 struct RowsArgs {
   int dtype;

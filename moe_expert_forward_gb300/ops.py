@@ -29,18 +29,51 @@ _SCORES = {"softmax": MM_MOE_SCORE_SOFTMAX, "sigmoid": MM_MOE_SCORE_SIGMOID}
 PRODUCT_BLOCK = 128      # rows of a routed block the 4-bit product reads
 
 
-class Routing(NamedTuple):
-    """Where every (token, k) pair of a batch sits in a pool sorted by expert."""
-    cnt: torch.Tensor      # int32 [E]: rows of each expert
-    blk_off: torch.Tensor  # int32 [E + 1]: first block of each expert
-    slot: torch.Tensor     # int32 [T, K]: pool row of each pair, -1 where masked
-    src: torch.Tensor      # int32 [rows]: pair of each pool row, -1 on padding (undefined past the last block)
-    status: torch.Tensor   # int32 [4]: [0] = MM_MOE_ERR_BAD_ROUTING where topk_idx held other ids
-    T: int
-    K: int
-    E: int
-    block_m: int
-    rows: int              # pool rows that any routing of these sizes fits
+class Routing:
+    """Where every (token, k) pair of a batch sits in a pool sorted by expert.
+
+    T, K, E, block_m: of the batch; rows: pool rows that any routing of these sizes
+    fits.  The tensors are views of one buffer:
+      cnt      int32 [E]      rows of each expert
+      blk_off  int32 [E + 1]  first block of each expert
+      slot     int32 [T, K]   pool row of each pair, -1 where masked
+      src      int32 [rows]   pair of each pool row, -1 on padding (undefined past the last block)
+      status   int32 [4]      [0] = MM_MOE_ERR_BAD_ROUTING where topk_idx held other ids
+    """
+    __slots__ = ("T", "K", "E", "block_m", "rows", "_buf", "_status", "_cnt", "_blk", "_slot", "_src")
+
+    def __init__(self, T: int, K: int, E: int, block_m: int, rows: int, device, scratch_ints: int):
+        self.T, self.K, self.E, self.block_m, self.rows = T, K, E, block_m, rows
+        self._buf = torch.empty(4 + 2 * E + 1 + T * K + rows + scratch_ints, dtype=torch.int32, device=device)
+        self._status = self._buf.data_ptr()          # addresses, for the calls
+        self._cnt = self._status + 16
+        self._blk = self._cnt + 4 * E
+        self._slot = self._blk + 4 * (E + 1)
+        self._src = self._slot + 4 * T * K
+
+    def _view(self, address: int, n: int):
+        at = (address - self._status) // 4
+        return self._buf[at:at + n]
+
+    @property
+    def status(self):
+        return self._view(self._status, 4)
+
+    @property
+    def cnt(self):
+        return self._view(self._cnt, self.E)
+
+    @property
+    def blk_off(self):
+        return self._view(self._blk, self.E + 1)
+
+    @property
+    def slot(self):
+        return self._view(self._slot, self.T * self.K).view(self.T, self.K)
+
+    @property
+    def src(self):
+        return self._view(self._src, self.rows)
 
 
 class MxWeights(NamedTuple):
@@ -147,22 +180,14 @@ def sort_tokens(topk_idx, E: int, block_m: int = 16, stream=None) -> Routing:
     T, K = topk_idx.shape
     ip = _whole(topk_idx, "sort_tokens", "topk_idx", (T, K), torch.int32)
     n = ctypes.c_size_t(0)
-    _check(lib().mm_moe_dispatch_scratch_size(T, K, E, ctypes.byref(n)), "mm_moe_dispatch_scratch_size")
+    _check(lib().mm_moe_sort_scratch_size(T, K, E, ctypes.byref(n)), "mm_moe_sort_scratch_size")
+    if block_m < 1:
+        _bad("sort_tokens", f"block_m must be 16 to 256, got {block_m}")
     rows = pool_rows(T, K, E, block_m)
-    # one allocation: status (zeroed), counts, block offsets, slots, sources, scratch
-    sizes = (4, E, E + 1, T * K, rows, n.value // 4)
-    buf = torch.empty(sum(sizes), dtype=torch.int32, device=topk_idx.device)
-    status, cnt, blk_off, slot, src, scratch = torch.split(buf, sizes)
-    s = _stream(stream)
-    if stream is None:
-        status.zero_()
-    else:
-        with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
-            status.zero_()
-    _check(lib().mm_moe_dispatch(ip, T, K, E, block_m, cnt.data_ptr(), blk_off.data_ptr(), slot.data_ptr(),
-                                 src.data_ptr(), rows, scratch.data_ptr(), n.value, status.data_ptr(), s),
-           "mm_moe_dispatch")
-    return Routing(cnt, blk_off, slot.view(T, K), src, status, T, K, E, block_m, rows)
+    r = Routing(T, K, E, block_m, rows, topk_idx.device, n.value // 4)
+    _check(lib().mm_moe_sort(ip, T, K, E, block_m, r._cnt, r._blk, r._slot, r._src, rows, r._src + 4 * rows, n.value,
+                             r._status, _stream(stream)), "mm_moe_sort")
+    return r
 
 
 def permute(x, routing: Routing, stream=None):
@@ -173,8 +198,8 @@ def permute(x, routing: Routing, stream=None):
     if T != r.T:
         _bad("permute", f"x has {T} tokens, the routing {r.T}")
     rows = torch.empty((r.rows, H), dtype=x.dtype, device=x.device)
-    _check(lib().mm_moe_permute(x.data_ptr(), code, _pitch(x), T, H, r.K, r.E, r.block_m, r.slot.data_ptr(),
-                                r.src.data_ptr(), r.blk_off.data_ptr(), rows.data_ptr(), r.rows, _stream(stream)),
+    _check(lib().mm_moe_permute(x.data_ptr(), code, _pitch(x), T, H, r.K, r.E, r.block_m, r._slot,
+                                r._src, r._blk, rows.data_ptr(), r.rows, _stream(stream)),
            "mm_moe_permute")
     return rows
 
@@ -189,7 +214,7 @@ def unpermute(rows, routing: Routing, topk_w=None, stream=None):
         _bad("unpermute", f"rows must be contiguous [{r.rows}, H], got {tuple(rows.shape)}")
     wp = None if topk_w is None else _whole(topk_w, "unpermute", "topk_w", (r.T, r.K), torch.float32)
     out = torch.empty((r.T, H), dtype=rows.dtype, device=rows.device)
-    _check(lib().mm_moe_unpermute(rows.data_ptr(), code, r.rows, r.T, H, r.K, r.slot.data_ptr(), wp, out.data_ptr(), H,
+    _check(lib().mm_moe_unpermute(rows.data_ptr(), code, r.rows, r.T, H, r.K, r._slot, wp, out.data_ptr(), H,
                                   _stream(stream)), "mm_moe_unpermute")
     return out
 
@@ -214,7 +239,7 @@ def unpermute_backward(d_out, rows, routing: Routing, topk_w=None, stream=None):
         d_w = torch.empty((T, r.K), dtype=torch.float32, device=d_out.device)
     d_rows = torch.empty((r.rows, H), dtype=d_out.dtype, device=d_out.device)
     _check(lib().mm_moe_unpermute_backward(d_out.data_ptr(), code, _pitch(d_out), rp, T, H, r.K, r.E, r.block_m,
-                                           r.slot.data_ptr(), r.src.data_ptr(), r.blk_off.data_ptr(), wp,
+                                           r._slot, r._src, r._blk, wp,
                                            d_rows.data_ptr(), r.rows, None if d_w is None else d_w.data_ptr(),
                                            _stream(stream)), "mm_moe_unpermute_backward")
     return d_rows, d_w
@@ -239,7 +264,7 @@ def mx_quantize(x, routing: Optional[Routing] = None, chunks: bool = False, stre
     if routing is not None:
         if routing.T != R:
             _bad("mx_quantize", f"x has {R} tokens, the routing {routing.T}")
-        rows, slot, K = routing.rows, routing.slot.data_ptr(), routing.K
+        rows, slot, K = routing.rows, routing._slot, routing.K
     nb = -(-C // 32)
     codes = torch.empty((rows, 16 * nb), dtype=torch.uint8, device=x.device)
     sf = torch.empty(_scale_bytes(rows, C) if chunks else (rows, nb), dtype=torch.uint8, device=x.device)
@@ -288,7 +313,7 @@ def _product_args(what: str, weights: MxWeights, routing: Optional[Routing], row
         if routing.block_m != PRODUCT_BLOCK or routing.E != weights.E:
             _bad(what, f"the routing must have blocks of {PRODUCT_BLOCK} and {weights.E} experts, got "
                        f"{routing.block_m} and {routing.E}")
-        cnt, blk = routing.cnt.data_ptr(), routing.blk_off.data_ptr()
+        cnt, blk = routing._cnt, routing._blk
     if out is None:
         out = torch.empty((rows, weights.N), dtype=dtype, device=device)
     else:
@@ -344,7 +369,7 @@ def mx_linear(x, weights: MxWeights, routing: Optional[Routing] = None, out=None
     if routing is not None:
         if routing.T != T:
             _bad("mx_linear", f"x has {T} tokens, the routing {routing.T}")
-        rows, slot, K = routing.rows, routing.slot.data_ptr(), routing.K
+        rows, slot, K = routing.rows, routing._slot, routing.K
     out, cnt, blk = _product_args("mx_linear", weights, routing, rows, x.dtype, x.device, out)
     if workspace is None:
         workspace = torch.empty(_linear_bytes(rows, C), dtype=torch.uint8, device=x.device)

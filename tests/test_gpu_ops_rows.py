@@ -93,6 +93,24 @@ def test_blocks(ops, block):
     check(ops, 200, 40, 7, 2, block=block, seed=block)
 
 
+@pytest.mark.parametrize("T,K,E,block", [(512, 4, 9, 16), (513, 4, 300, 32), (3000, 3, 384, 16), (8192, 6, 384, 16),
+                                         (16384, 16, 1024, 64), (16385, 16, 1024, 64), (50000, 8, 256, 128)])
+def test_sorts_of_every_size(ops, T, K, E, block):
+    """One CTA, clusters of 2 to 8, and (from 2^18 pairs) the two launches."""
+    rng = np.random.default_rng(T)
+    idx = rng.integers(0, E, (T, K)).astype(np.int32)
+    idx[rng.random(idx.shape) < 0.05] = -1
+    r = ops.sort_tokens(torch.from_numpy(idx).cuda(), E, block)
+    ref = O.route(idx, E, block)
+    assert int(r.status[0]) == 0
+    assert np.array_equal(r.cnt.cpu().numpy(), ref["cnt"]) and np.array_equal(r.blk_off.cpu().numpy(), ref["blk_off"])
+    assert np.array_equal(r.slot.cpu().numpy(), ref["slot"])
+    assert np.array_equal(r.src.cpu().numpy()[:len(ref["src"])], ref["src"])
+    bad = idx.copy()
+    bad[T // 2, 0] = E
+    assert int(ops.sort_tokens(torch.from_numpy(bad).cuda(), E, block).status[0]) == 5
+
+
 def test_every_slot_masked(ops):
     check(ops, 33, 64, 4, 2, idx=np.full((33, 2), -1, np.int32))
 

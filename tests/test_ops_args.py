@@ -33,6 +33,18 @@ def test_route_backward(M):
     assert call(T=0, logits=None, idx=None, g=None, d=None) == M.MM_MOE_OK
 
 
+def test_sort(M):
+    def sort(idx=A, T=4, K=2, E=4, bm=16, cnt=A, blk=A, slot=A, src=A, cap=8 + 4 * 15, scr=None, n=0, status=A):
+        return M.mm_moe_sort(idx, T, K, E, bm, cnt, blk, slot, src, cap, scr, n, status, None)
+    for kw in (dict(idx=None), dict(T=-1), dict(K=0), dict(K=5), dict(E=0), dict(E=1025), dict(bm=8), dict(bm=20),
+               dict(cnt=None), dict(blk=None), dict(slot=None), dict(src=None), dict(cap=67), dict(status=None),
+               dict(T=1 << 20, cap=1 << 24)):                       # two launches need scratch
+        assert sort(**kw) == M.MM_MOE_ERR_INVALID_ARG, kw
+    need = M.mm_moe_sort_scratch_size(1 << 20, 2, 4)
+    assert need > 0 and M.mm_moe_sort_scratch_size(4, 2, 4) == 0
+    assert sort(T=1 << 20, cap=1 << 24, scr=A, n=need - 1) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL
+
+
 def test_rows(M):
     def permute(x=A, dtype=0, stride=8, T=4, H=8, K=2, E=4, bm=16, slot=A, src=A, blk=A, rows=A, n=8 + 4 * 15):
         return M.mm_moe_permute(x, dtype, stride, T, H, K, E, bm, slot, src, blk, rows, n, None)
