@@ -1,0 +1,137 @@
+// Device pieces shared by the 4-bit products (mx_linear.cu, mx_linear_pair.cu).
+#pragma once
+
+#include "mx_linear.h"
+#include "ptx.cuh"
+#include "rowtypes.cuh"
+
+namespace mm {
+
+constexpr int kMxRows = 128;                     // rows of a block
+constexpr int kMxStageK = 256;                   // contraction elements per stage
+constexpr int kMxStageBytes = kMxStageK / 2;     // of one row's codes: one 128-byte swizzle atom
+constexpr int kMxTileBytes = kMxRows * kMxStageBytes;
+constexpr int kMxSfBytes = 2 * kSFChunk;         // the two scale chunks of 128 rows and one stage
+
+struct MxArgs {
+  int rows, C, E, N;
+  int KS, KB;                // 256-wide stages, scale chunks along the contraction
+  int NB, NT;                // 128-row scale blocks and weight tiles of one expert
+  int nblk;                  // row blocks of a dense product
+  const uint8_t* sf;
+  const uint8_t* w_sf;
+  const int* cnt;
+  const int* blk_off;
+  char* out;
+  int64_t out_pitch;         // bytes
+  int wide;                  // out rows and base are 32-byte aligned
+  int wait_prior;            // launched programmatically: activations come from the kernel before
+  int* status;
+  uint64_t timeout_ns;
+};
+
+// Instruction descriptor of kind::mxf4: A and B e2m1 (1) in [9:7] and [11:10],
+// both K-major, N >> 3 in [22:17], UE8M0 scales (bit 23), M >> 7 in [28:27];
+// the scale bytes a 64-wide MMA takes from each 32-bit word: 0 (bytes 0, 1) or 2
+// (bytes 2, 3) in [30:29] for A and [5:4] for B.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int n, int m, int half) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(m >> 7) << 27) | (static_cast<uint32_t>(2 * half) << 29) |
+         (static_cast<uint32_t>(2 * half) << 4);
+}
+
+// The last i < n with a[i] <= v; a[0] <= v.
+__device__ __forceinline__ int last_not_above(const int* a, int n, int v) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a[mid] <= v) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Two accumulators as one 32-bit word of 16-bit elements.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
+  Vec<T, 2> h;
+  h.v[0] = from_float<T>(__uint_as_float(a));
+  h.v[1] = from_float<T>(__uint_as_float(b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One row's accumulator columns [col, col + kCols) of TMEM, the first `cols` of them stored at p (p null: none).
+// `release` is called as soon as the accumulator has been read: 16-bit results are packed into registers first
+// and stored after it, fp32 ones are stored 32 columns at a time and it follows the last read.
+template <typename T, int kCols, typename F>
+__device__ __forceinline__ void store_accumulator(uint32_t col, T* p, int cols, bool wide, F release) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t w[kCols / 2];
+#pragma unroll
+    for (int c = 0; c < kCols; c += 32) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(col + c, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[c / 2 + i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+    }
+    release();
+    if (!p) return;
+#pragma unroll
+    for (int c = 0; c < kCols; c += 16) {
+      if (wide && cols >= c + 16) {
+        st_global_v8(reinterpret_cast<float*>(p + c), w + c / 2);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const Vec<T, 2> h = *reinterpret_cast<const Vec<T, 2>*>(&w[c / 2 + i]);
+          if (c + 2 * i < cols) p[c + 2 * i] = h.v[0];
+          if (c + 2 * i + 1 < cols) p[c + 2 * i + 1] = h.v[1];
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kCols; c += 32) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(col + c, v);
+      tmem_ld_wait();
+      if (c + 32 == kCols) release();
+      if (!p) continue;
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        if (wide && cols >= c + i + 8) {
+          st_global_v8(reinterpret_cast<float*>(p + c + i), v + i);
+        } else {
+#pragma unroll
+          for (int j = i; j < i + 8; ++j)
+            if (c + j < cols) p[c + j] = __uint_as_float(v[j]);
+        }
+      }
+    }
+  }
+}
+
+// Arguments and tensor maps that do not depend on the kernel's tiles.
+inline MxArgs mx_args(const MxProductArgs& p, int elem, int tile_n) {
+  MxArgs a{};
+  a.rows = static_cast<int>(p.rows);
+  a.C = p.C; a.E = p.E; a.N = p.N;
+  a.KB = mx_chunks(p.C); a.KS = a.KB / 2;
+  a.NB = (p.N + 127) / 128; a.NT = (p.N + tile_n - 1) / tile_n;
+  a.nblk = static_cast<int>((p.rows + kMxRows - 1) / kMxRows);
+  a.sf = p.sf; a.w_sf = p.w_sf; a.cnt = p.cnt; a.blk_off = p.blk_off;
+  a.out = static_cast<char*>(p.out);
+  a.out_pitch = p.out_stride * static_cast<int64_t>(elem);
+  a.wide = (reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(a.out_pitch)) % 32 == 0;
+  a.wait_prior = p.after_quantize;
+  a.status = p.status; a.timeout_ns = p.timeout_ns;
+  return a;
+}
+// codes of `rows` rows as [rows, C/2] bytes in boxes of one stage x box_rows
+inline CUresult mx_codes_map(CUtensorMap* m, const void* codes, int64_t rows, int C, int box_rows) {
+  const uint64_t pitch = static_cast<uint64_t>(C) / 2;
+  return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, pitch, static_cast<uint64_t>(rows), pitch,
+                        kMxStageBytes, static_cast<uint32_t>(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace mm

@@ -57,5 +57,7 @@ struct MxProductArgs {
   bool after_quantize;       // launched programmatically behind the quantiser
 };
 cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t s);
+// on CTA pairs: two 128-row blocks a task
+cudaError_t launch_mx_product_pair(const MxProductArgs& a, cudaStream_t s);
 
 }  // namespace mm

@@ -9,8 +9,8 @@
 // warp then ranks its pairs.  The order inside an expert is ascending pair.
 // What bounds it is latency, a chain of a few barriers: the two dispatch kernels
 // spread over many SMs instead, and take over where a warp's run gets long.
+#include "cluster.cuh"
 #include "internal.h"
-#include "rowtypes.cuh"
 
 namespace mm {
 namespace {
@@ -28,30 +28,6 @@ struct SortArgs {
   int32_t *cnt, *blk_off, *slot, *src, *status;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// the int at the same shared address in CTA `rank` of the cluster
-__device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
-  uint32_t a;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-               : "=r"(a)
-               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-
 __global__ void __launch_bounds__(kThreads, 1) sort_kernel(const SortArgs a) {
   extern __shared__ int sm[];
   const int E = a.E;
@@ -62,7 +38,7 @@ __global__ void __launch_bounds__(kThreads, 1) sort_kernel(const SortArgs a) {
   int* s_blk = s_cnt + E;             // [E + 1]: first blocks
   __shared__ int s_warp[kWarps];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  const uint32_t rank = cluster_ctarank(), ctas = cluster_nctarank();
   const int gw = static_cast<int>(rank) * kWarps + w;
 
   for (int i = tid; i < kWarps * E; i += kThreads) wc[i] = 0;
@@ -92,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, 1) sort_kernel(const SortArgs a) {
     }
     s_tot[e] = run;
   }
-  cluster_sync();
+  cluster_barrier();
   // totals over the cluster; E <= kThreads: one expert a thread, and a scan of its blocks
   int base = 0, tot = 0;
   if (tid < E)
@@ -140,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) sort_kernel(const SortArgs a) {
       for (uint32_t c = 0; c < ctas; ++c) code |= peer_int(s_tot + E, c);
     a.status[tid] = code ? MM_MOE_ERR_BAD_ROUTING : 0;
   }
-  cluster_sync();                     // the totals were read: a CTA may leave; and s_start is there
+  cluster_barrier();                     // the totals were read: a CTA may leave; and s_start is there
 
   for (int64_t p0 = beg; p0 < end; p0 += 32) {
     const int64_t p = p0 + lane;
