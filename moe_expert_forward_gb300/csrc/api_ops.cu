@@ -243,11 +243,12 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int32_t* status = reinterpret_cast<int32_t*>(ws);
   const MxQuantArgs q{x, dtype, row_stride, T, C, ws + L.codes, ws + L.sf, 1, slot, K, num_rows, status};
-  cudaError_t e = launch_mx_quantize(q, s);
-  if (e != cudaSuccess) return done(e);
   const MxProductArgs p{ws + L.codes, ws + L.sf, num_rows, C, static_cast<const uint8_t*>(w),
                         static_cast<const uint8_t*>(w_sfp), E, N, cnt, blk_off, dtype, out, out_stride, status,
                         timeout_ns(timeout_ms), true};
+  if (mx_few_rows(T, C, routed, static_cast<int64_t>(T) * K)) return done(launch_mx_few(q, p, s));
+  cudaError_t e = launch_mx_quantize(q, s);
+  if (e != cudaSuccess) return done(e);
   return done(launch_mx_product(p, s));
 }
 

@@ -60,4 +60,11 @@ cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t s);
 // on CTA pairs: two 128-row blocks a task
 cudaError_t launch_mx_product_pair(const MxProductArgs& a, cudaStream_t s);
 
+// Both steps of a linear in one launch for a few rows (mx_few.cu).
+constexpr int kMxFewTokens = 4;      // rows of a dense linear
+constexpr int kMxFewPairs = 16;      // (token, k) pairs of a routed one
+constexpr int kMxFewSmem = 160 * 1024;
+bool mx_few_rows(int T, int C, bool routed, int64_t pairs);
+cudaError_t launch_mx_few(const MxQuantArgs& q, const MxProductArgs& p, cudaStream_t s);
+
 }  // namespace mm
