@@ -527,9 +527,12 @@ int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, co
  *   x      [T, C] of `dtype` (also out's), row_stride elements between rows
  *   slot   null: dense (E = 1, num_rows = T).  Else int32 [T, K] with cnt and blk_off of
  *          mm_moe_dispatch with block_m = 128, rows sorted by expert on the way.
- *   workspace  mm_moe_mx_linear_workspace(num_rows, C) bytes, 256-byte aligned; its
- *          status word is read by mm_moe_sync_status. */
-int mm_moe_mx_linear_workspace(int64_t num_rows, int C, size_t* bytes);
+ *   workspace  mm_moe_mx_linear_workspace bytes (K = 0: dense), 256-byte aligned; its
+ *          status word is read by mm_moe_sync_status.  Up to 4 tokens of a dense linear, or
+ *          16 pairs of a routed one, run in one launch where rows * N * C is small, and need
+ *          none (0 bytes, null allowed; a workspace of 16 bytes or more gets its status
+ *          word cleared). */
+int mm_moe_mx_linear_workspace(int T, int C, int N, int K, int64_t num_rows, size_t* bytes);
 int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C, const void* w, const void* w_sfp,
                      int E, int N, const int32_t* slot, int K, const int32_t* cnt, const int32_t* blk_off,
                      int64_t num_rows, void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,

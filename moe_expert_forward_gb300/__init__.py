@@ -115,7 +115,7 @@ def lib() -> ctypes.CDLL:
             "mm_moe_mx_dequantize": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _P]),
             "mm_moe_mx_prepare": (_I, [_P, _I, _I, _I, _P, _P]),
             "mm_moe_mx_product": (_I, [_P, _P, _I64, _I, _P, _P, _I, _I, _P, _P, _I, _P, _I64, _P, ctypes.c_uint, _P]),
-            "mm_moe_mx_linear_workspace": (_I, [_I64, _I, ctypes.POINTER(_SZ)]),
+            "mm_moe_mx_linear_workspace": (_I, [_I, _I, _I, _I, _I64, ctypes.POINTER(_SZ)]),
             "mm_moe_mx_linear": (_I, [_P, _I, _I64, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _I64, _P, _I64, _P, _SZ,
                                       ctypes.c_uint, _P]),
         }
@@ -446,9 +446,9 @@ def mm_moe_mx_product(codes, sf, rows, C, w, w_sfp, E, N, cnt, blk_off, dtype, o
                                    timeout_ms, stream)
 
 
-def mm_moe_mx_linear_workspace(num_rows, C) -> int:
+def mm_moe_mx_linear_workspace(T, C, N, K, num_rows) -> int:
     n = _SZ(0)
-    _check(lib().mm_moe_mx_linear_workspace(num_rows, C, ctypes.byref(n)), "mm_moe_mx_linear_workspace")
+    _check(lib().mm_moe_mx_linear_workspace(T, C, N, K, num_rows, ctypes.byref(n)), "mm_moe_mx_linear_workspace")
     return n.value
 
 

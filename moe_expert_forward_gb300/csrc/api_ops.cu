@@ -214,9 +214,11 @@ int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, co
   return done(launch_mx_product(a, static_cast<cudaStream_t>(stream)));
 }
 
-int mm_moe_mx_linear_workspace(int64_t num_rows, int C, size_t* bytes) {
-  if (!bytes || num_rows < 0 || num_rows > kMaxRows || C < 32 || C % 32 || C > (1 << 30)) return MM_MOE_ERR_INVALID_ARG;
-  *bytes = linear_layout(num_rows, C).total;
+int mm_moe_mx_linear_workspace(int T, int C, int N, int K, int64_t num_rows, size_t* bytes) {
+  if (!bytes || T < 0 || N < 1 || K < 0 || K > kMaxK || num_rows < 0 || num_rows > kMaxRows || C < 32 || C % 32 || C > (1 << 30))
+    return MM_MOE_ERR_INVALID_ARG;
+  if (K == 0 && num_rows != T) return MM_MOE_ERR_INVALID_ARG;
+  *bytes = mx_few_rows(T, C, N, K) ? 0 : linear_layout(num_rows, C).total;
   return MM_MOE_OK;
 }
 
@@ -233,11 +235,12 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
     if (int r = check_pool(T, K, E, 128, num_rows)) return r;
   }
   const LinearLayout L = linear_layout(num_rows, C);
-  if (!workspace || !aligned(workspace, 256)) return MM_MOE_ERR_INVALID_ARG;
-  if (workspace_bytes < L.total) return MM_MOE_ERR_WORKSPACE_TOO_SMALL;
+  const bool few = mx_few_rows(T, C, N, routed ? K : 0);
+  if ((!few && !workspace) || !aligned(workspace, 256)) return MM_MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < (few ? (workspace ? 16 : 0) : L.total)) return MM_MOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T == 0)   // nothing to compute; leave a clean status word for mm_moe_sync_status
-    return done(cudaMemsetAsync(workspace, 0, 16, s));
+    return workspace ? done(cudaMemsetAsync(workspace, 0, 16, s)) : MM_MOE_OK;
   if (!x || !aligned(x, dtype_size(dtype))) return MM_MOE_ERR_INVALID_ARG;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -246,7 +249,7 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
   const MxProductArgs p{ws + L.codes, ws + L.sf, num_rows, C, static_cast<const uint8_t*>(w),
                         static_cast<const uint8_t*>(w_sfp), E, N, cnt, blk_off, dtype, out, out_stride, status,
                         timeout_ns(timeout_ms), true};
-  if (mx_few_rows(T, C, routed, static_cast<int64_t>(T) * K)) return done(launch_mx_few(q, p, s));
+  if (few) return done(launch_mx_few(q, p, s));
   cudaError_t e = launch_mx_quantize(q, s);
   if (e != cudaSuccess) return done(e);
   return done(launch_mx_product(p, s));

@@ -32,6 +32,15 @@ __device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_shared(p, rank)) : "memory");
   return v;
 }
+// four floats at the same shared address in CTA `rank`
+__device__ __forceinline__ float4 peer_float4(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(map_shared(p, rank))
+               : "memory");
+  return v;
+}
 // arrive on an mbarrier of any CTA of the cluster, releasing at cluster scope
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");

@@ -10,8 +10,9 @@
 //
 // What bounds it is latency, then the weights' bytes. A warp takes two weight
 // rows and a lane one block of 32 (16 bytes) of each per step; the first steps'
-// loads are issued before x is quantised. The sixteen rows of a CTA are chosen so
-// that their scales (mx_sf_word) fill whole 32-byte sectors.
+// loads are issued before x is quantised. A CTA takes sets of sixteen rows, chosen
+// so that their scales (mx_sf_word) fill whole 32-byte sectors, and quantises x once
+// for all of its sets.
 #include "mx_quant.cuh"
 
 namespace mm {
@@ -56,7 +57,7 @@ __device__ __forceinline__ uint2 twice_values(uint32_t w) {
 
 // NT rows of x at most per CTA (one where routed).
 template <typename T, int NT, bool kVec>
-__global__ void __launch_bounds__(kThreads) few_kernel(const FewArgs a, int rows) {
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) few_kernel(const FewArgs a, int rows, int sets) {
   extern __shared__ uint8_t smem[];
   const int n32 = a.C / 32;
   // per row of x: the first and second 16 int8 of every block, then every block's scale
@@ -74,102 +75,108 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewArgs a, int rows
     token0 = blockIdx.y / a.K;
     if (row0 < 0 || row0 >= a.num_rows) return;      // the same for the whole CTA
     const int b = static_cast<int>(row0 >> 7);
+    if (threadIdx.x == 0) s_expert = -1;
+    __syncthreads();
     for (int i = threadIdx.x; i < a.E; i += kThreads)
       if (__ldg(a.blk_off + i) <= b && b < __ldg(a.blk_off + i + 1)) s_expert = i;
     __syncthreads();
     e = s_expert;
+    if (e < 0) return;                               // a row of no expert's block
   }
-  // the warp's two weight rows: n and n + 1
-  const int n = static_cast<int>(blockIdx.x >> 3) * 128 + static_cast<int>(blockIdx.x & 7) * 4 + (warp & 1) * 2 +
-                (warp >> 1) * 32;
-  const uint4* wr[2];
-  const uint8_t* sr[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int m = min(n + r, a.N - 1);               // past the last row: its values again, not stored
-    wr[r] = reinterpret_cast<const uint4*>(a.w + (static_cast<int64_t>(e) * a.N + m) * (a.C / 2));
-    sr[r] = a.w_sf + static_cast<size_t>(e) * a.NB * a.KB * kSFChunk + mx_sf_word(m, 0, a.KB);
-  }
-  uint4 wv[kAhead][2];
-  uint32_t sv[kAhead][2];
-  auto load = [&](int u, int b) {
+  for (int set = blockIdx.x; set < sets; set += gridDim.x) {
+    // the warp's two weight rows: n and n + 1
+    const int n = (set >> 3) * 128 + (set & 7) * 4 + (warp & 1) * 2 + (warp >> 1) * 32;
+    const uint4* wr[2];
+    const uint8_t* sr[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      wv[u][r] = b < n32 ? __ldg(wr[r] + b) : make_uint4(0, 0, 0, 0);
-      sv[u][r] = b < n32 ? __ldg(sr[r] + static_cast<size_t>(b >> 2) * kSFChunk + (b & 3)) : 0u;
+      const int m = min(n + r, a.N - 1);               // past the last row: its values again, not stored
+      wr[r] = reinterpret_cast<const uint4*>(a.w + (static_cast<int64_t>(e) * a.N + m) * (a.C / 2));
+      sr[r] = a.w_sf + static_cast<size_t>(e) * a.NB * a.KB * kSFChunk + mx_sf_word(m, 0, a.KB);
     }
-  };
+    uint4 wv[kAhead][2];
+    uint32_t sv[kAhead][2];
+    auto load = [&](int u, int b) {
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) load(u, u * 32 + lane);
+      for (int r = 0; r < 2; ++r) {
+        wv[u][r] = b < n32 ? __ldg(wr[r] + b) : make_uint4(0, 0, 0, 0);
+        sv[u][r] = b < n32 ? __ldg(sr[r] + static_cast<size_t>(b >> 2) * kSFChunk + (b & 3)) : 0u;
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load(u, u * 32 + lane);
 
-  // x: two lanes a block
-  const T* x = static_cast<const T*>(a.x) + token0 * a.stride;
-  const int groups = NT * n32 * 2;
-  for (int g0 = 0; g0 < groups; g0 += kThreads) {
-    const int g = g0 + threadIdx.x;
-    const int t = g / (n32 * 2), q = g - t * n32 * 2;
-    Group<T> v;
-    if (g < groups && t < rows) v.template load<kVec>(x + t * a.stride, q * 16, a.C);
-    else v.clear();
-    uint2 codes;
-    const uint32_t byte = quantize_group(v, codes);
-    if (g < groups) {
-      const uint2 v0 = twice_values(codes.x), v1 = twice_values(codes.y);
-      const int b = t * n32 + (q >> 1);
-      ((q & 1) ? s_hi : s_lo)[b] = make_uint4(v0.x, v0.y, v1.x, v1.y);
-      if ((q & 1) == 0) s_sc[b] = ue8m0_value(byte) * 0.25f;
-    }
-  }
-  __syncthreads();
-
-  float acc[2][NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = 0.f;
-  for (int b0 = 0; b0 < n32; b0 += 32 * kAhead) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int b = b0 + u * 32 + lane;
-      if (b < n32) {
-        uint2 d[2][4];
-        float sc[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          d[r][0] = twice_values(wv[u][r].x);
-          d[r][1] = twice_values(wv[u][r].y);
-          d[r][2] = twice_values(wv[u][r].z);
-          d[r][3] = twice_values(wv[u][r].w);
-          sc[r] = ue8m0_value(sv[u][r]);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const uint4 lo = s_lo[t * n32 + b], hi = s_hi[t * n32 + b];
-          const float sx = s_sc[t * n32 + b];
-          const uint32_t xs[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            int dot = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              dot = __dp4a(static_cast<int>(d[r][i].x), static_cast<int>(xs[2 * i]), dot);
-              dot = __dp4a(static_cast<int>(d[r][i].y), static_cast<int>(xs[2 * i + 1]), dot);
-            }
-            acc[r][t] += static_cast<float>(dot) * sx * sc[r];
-          }
+    if (set == static_cast<int>(blockIdx.x)) {
+      // x: two lanes a block
+      const T* x = static_cast<const T*>(a.x) + token0 * a.stride;
+      const int groups = NT * n32 * 2;
+      for (int g0 = 0; g0 < groups; g0 += kThreads) {
+        const int g = g0 + threadIdx.x;
+        const int t = g / (n32 * 2), q = g - t * n32 * 2;
+        Group<T> v;
+        if (g < groups && t < rows) v.template load<kVec>(x + t * a.stride, q * 16, a.C);
+        else v.clear();
+        uint2 codes;
+        const uint32_t byte = quantize_group(v, codes);
+        if (g < groups) {
+          const uint2 v0 = twice_values(codes.x), v1 = twice_values(codes.y);
+          const int b = t * n32 + (q >> 1);
+          ((q & 1) ? s_hi : s_lo)[b] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+          if ((q & 1) == 0) s_sc[b] = ue8m0_value(byte) * 0.25f;
         }
       }
-      load(u, b + 32 * kAhead);
+      __syncthreads();
     }
+
+    float acc[2][NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = 0.f;
+    for (int b0 = 0; b0 < n32; b0 += 32 * kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int b = b0 + u * 32 + lane;
+        if (b < n32) {
+          uint2 d[2][4];
+          float sc[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            d[r][0] = twice_values(wv[u][r].x);
+            d[r][1] = twice_values(wv[u][r].y);
+            d[r][2] = twice_values(wv[u][r].z);
+            d[r][3] = twice_values(wv[u][r].w);
+            sc[r] = ue8m0_value(sv[u][r]);
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const uint4 lo = s_lo[t * n32 + b], hi = s_hi[t * n32 + b];
+            const float sx = s_sc[t * n32 + b];
+            const uint32_t xs[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              int dot = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                dot = __dp4a(static_cast<int>(d[r][i].x), static_cast<int>(xs[2 * i]), dot);
+                dot = __dp4a(static_cast<int>(d[r][i].y), static_cast<int>(xs[2 * i + 1]), dot);
+              }
+              acc[r][t] += static_cast<float>(dot) * sx * sc[r];
+            }
+          }
+        }
+        load(u, b + 32 * kAhead);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float v = acc[r][t];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0 && n + r < a.N && t < rows)
+          reinterpret_cast<T*>(a.out)[(row0 + t) * a.out_stride + n + r] = from_float<T>(v);
+      }
   }
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float v = acc[r][t];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0 && n + r < a.N && t < rows)
-        reinterpret_cast<T*>(a.out)[(row0 + t) * a.out_stride + n + r] = from_float<T>(v);
-    }
 }
 
 template <typename T, int NT>
@@ -178,16 +185,25 @@ cudaError_t launch_few(const FewArgs& a, int rows, int64_t groups, cudaStream_t 
   auto kernel = vec ? few_kernel<T, NT, true> : few_kernel<T, NT, false>;
   const int smem = NT * (a.C / 32) * 36;
   if (cudaError_t e = configure_kernel(reinterpret_cast<const void*>(kernel), 0, kMxFewSmem)) return e;
-  const dim3 grid(static_cast<unsigned>((a.N + 127) / 128 * 8), static_cast<unsigned>(groups));
-  kernel<<<grid, kThreads, smem, s>>>(a, rows);
+  // as many CTAs as the SMs hold, spread over the groups
+  const int sets = (a.N + 127) / 128 * 8;
+  const int64_t room = static_cast<int64_t>(dev_info().sms) * (NT <= 2 ? 3 : 2) / groups;
+  const dim3 grid(static_cast<unsigned>(sets < room ? sets : (room < 1 ? 1 : room)), static_cast<unsigned>(groups));
+  kernel<<<grid, kThreads, smem, s>>>(a, rows, sets);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-bool mx_few_rows(int T, int C, bool routed, int64_t pairs) {
-  const int tokens = routed ? 1 : (T <= 1 ? 1 : (T <= 2 ? 2 : 4));
-  return (routed ? pairs <= kMxFewPairs : T <= kMxFewTokens) && static_cast<int64_t>(tokens) * (C / 32) * 36 <= kMxFewSmem;
+// Where one launch is the faster: its time grows with rows * N * C, the tensor-core kernels' (up to 128 rows) hardly
+// with the rows. Measured (us, this kernel / the others): 1 row, 8192x4096 8.4 / 10.5, 16384x8192 21.6 / 18.8; 2 rows,
+// 4096x4096 6.1 / 7.9, 8192x4096 10.1 / 10.4, 16384x8192 25.6 / 18.8; 4 rows, 4096x4096 7.7 / 7.9, 8192x4096
+// 13.1 / 10.5; 4 pairs 4096x4096 16.2 / 20.3, 8 pairs 24.5 / 19.9.
+bool mx_few_rows(int T, int C, int N, int K) {
+  const int64_t rows = K ? static_cast<int64_t>(T) * K : (T <= 1 ? 1 : (T <= 2 ? 2 : 4));
+  if (K ? rows > kMxFewPairs : T > kMxFewTokens) return false;
+  const int64_t smem = (K ? 1 : rows) * (C / 32) * 36;     // codes and scales of x
+  return rows * N <= kMxFewWork / C && smem <= kMxFewSmem;
 }
 
 cudaError_t launch_mx_few(const MxQuantArgs& q, const MxProductArgs& p, cudaStream_t s) {

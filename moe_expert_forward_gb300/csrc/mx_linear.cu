@@ -13,6 +13,7 @@
 // Warps: 4 or 8 epilogue warps (one or two per TMEM lane quadrant), one that
 // issues scale copies and MMAs, and one TMA producer per stage.
 // Every wait is bounded; on a timeout each role winds down what it issued.
+#include "cluster.cuh"
 #include "mx_linear.cuh"
 
 namespace mm {
@@ -42,6 +43,8 @@ struct Cfg {
   static constexpr int nbars = 2 * kStages + 2 * kAccBufs + 1;   // full, empty, tfull, tempty, drain
   static constexpr int meta = bars + nbars * 8 + 16;             // blk_off[E + 1], cnt[E]
   static int total(int E) { return meta + (2 * E + 1) * 4 + 1024; }
+  static constexpr int kPartPitch = BN + 4;                      // floats of a row of partial sums
+  static_assert(kMxRows * kPartPitch * 4 <= sft, "partial sums fit the stages");
   static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
   static_assert(meta + (2 * kMaxE + 1) * 4 + 1024 <= 232448, "shared memory");
 };
@@ -80,7 +83,8 @@ __device__ __forceinline__ Task task_at(int i, const MxArgs& a, const int* s_blk
   return t;
 }
 
-template <int BN, typename T>
+// kSplit: a cluster takes one task, each CTA a range of its stages; the partial accumulators meet in shared memory.
+template <int BN, typename T, bool kSplit>
 __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
     mx_product_kernel(const __grid_constant__ Maps maps, const MxArgs args) {
   using C = Cfg<BN>;
@@ -129,6 +133,13 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
   const uint32_t tmem = *s_tmem;
   const int ntasks = (args.blk_off ? min(s_blk[args.E], args.rows / kMxRows) : args.nblk) * args.NT;
 
+  // this CTA's tasks, and its stages [k0, k0 + nks) of each
+  const int part = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
+  const int parts = kSplit ? static_cast<int>(cluster_nctarank()) : 1;
+  const int first = static_cast<int>(blockIdx.x) / parts, stride = static_cast<int>(gridDim.x) / parts;
+  const int k0 = kSplit ? args.KS * part / parts : 0;
+  const int nks = kSplit ? args.KS * (part + 1) / parts - k0 : args.KS;
+
   if (warp > C::kEpiWarps) {
     // ------------------------------------------------------------------ TMA producers, one per stage
     if (lane == 0) {
@@ -141,7 +152,7 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
       int step = 0;                              // stages of this CTA's tasks so far
       bool armed = false, waited = args.wait_prior == 0;
       uint32_t armed_parity = 0;
-      for (int i = blockIdx.x; i < ntasks && !*s_abort; i += gridDim.x) {
+      for (int i = first; i < ntasks && !*s_abort; i += stride) {
         const Task t = task_at(i, args, s_blk, s_cnt);
         const int box = t.valid > 64 ? 2 : (t.valid > 32 ? 1 : 0);
         const int n0 = t.n * BN;
@@ -149,25 +160,25 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
         const int nbs = min(C::kWgtBlocks, args.NB - nb0);
         const uint32_t bytes = (32u << box) * kMxStageBytes + C::kWgtBytes + (1 + nbs) * kMxSfBytes;
         int ks = ((p - step) % S + S) % S;
-        for (; ks < args.KS; ks += S) {
+        for (; ks < nks; ks += S) {
           const uint32_t phase = ((step + ks) / S) & 1;
           if (!mbar_wait(&empty[p], phase ^ 1, st, s_abort, kSiteEmpty)) break;
           mbar_arrive_expect_tx(&full[p], bytes);
           armed = true;
           armed_parity = phase;
-          tma_load_2d(wt, &maps.w, &full[p], ks * kMxStageBytes, t.e * args.N + n0, pol);
+          tma_load_2d(wt, &maps.w, &full[p], (k0 + ks) * kMxStageBytes, t.e * args.N + n0, pol);
           for (int j = 0; j < nbs; ++j)
             bulk_load(sw + j * kMxSfBytes,
-                      args.w_sf + ((static_cast<size_t>(t.e) * args.NB + nb0 + j) * args.KB + 2 * ks) * kSFChunk,
+                      args.w_sf + ((static_cast<size_t>(t.e) * args.NB + nb0 + j) * args.KB + 2 * (k0 + ks)) * kSFChunk,
                       kMxSfBytes, &full[p]);
           if (!waited) {                         // the weights do not depend on the kernel before; the rows do
             pdl_wait();
             waited = true;
           }
-          tma_load_2d(tk, &maps.a[box], &full[p], ks * kMxStageBytes, t.b * kMxRows, pol);
-          bulk_load(sa, args.sf + (static_cast<size_t>(t.b) * args.KB + 2 * ks) * kSFChunk, kMxSfBytes, &full[p]);
+          tma_load_2d(tk, &maps.a[box], &full[p], (k0 + ks) * kMxStageBytes, t.b * kMxRows, pol);
+          bulk_load(sa, args.sf + (static_cast<size_t>(t.b) * args.KB + 2 * (k0 + ks)) * kSFChunk, kMxSfBytes, &full[p]);
         }
-        step += args.KS;
+        step += nks;
       }
       if (armed) mbar_wait_drain(&full[p], armed_parity, st, kSiteDrainCopies);
     }
@@ -179,10 +190,10 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
       const uint64_t dsft = make_smem_desc(smem_u32(smem + C::sft), 0, 128, 0);
       const uint64_t dsfw = make_smem_desc(smem_u32(smem + C::sfw), 0, 128, 0);
       uint32_t phase = 0;
-      int it = 0, ks = 0, task = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x);
+      int it = 0, ks = 0, task = first - stride;
       uint32_t acc = 0, sfw_shift = 0;
       auto start_task = [&]() -> bool {
-        task += gridDim.x;
+        task += stride;
         if (task >= ntasks || *s_abort) return false;
         const int buf = it % C::kAccBufs;
         acc = tmem + buf * BN;
@@ -218,7 +229,7 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
                 tc_mma_mxf4(acc, da + 2 * kk, db + 2 * kk, idesc_mxf4(BN, kMxRows, kk & 1), sfa + 4 * (kk >> 1),
                             sfb + (kk >> 1) * 4 * C::kWgtBlocks + sfw_shift, (ks | kk) != 0);
               tc_commit(&empty[s]);
-              if (++ks == args.KS) {
+              if (++ks == nks) {
                 tc_commit(&tfull[it % C::kAccBufs]);
                 ks = 0;
                 ++it;
@@ -239,13 +250,27 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
     const int quad = warp & 3;
     const int c0 = C::kEpiWarps == 8 ? (warp >> 2) * kCols : 0;
     int it = 0;
-    for (int i = blockIdx.x; i < ntasks; i += gridDim.x, ++it) {
+    for (int i = first; i < ntasks; i += stride, ++it) {
       const Task t = task_at(i, args, s_blk, s_cnt);
       const int buf = it % C::kAccBufs;
       if (!mbar_wait(&tfull[buf], (it / C::kAccBufs) & 1, st, s_abort, kSiteTmemFull)) break;
       tc_fence_after();
       const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * BN + c0;
       const int row = quad * 32 + lane;
+      if constexpr (kSplit) {                    // every MMA of the task has completed: the stages' memory is free
+        float* d = reinterpret_cast<float*>(smem) + row * C::kPartPitch + c0;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(src + c, v);
+          tmem_ld_wait();
+          if (row < t.valid)
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<uint4*>(d + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+        continue;
+      }
       const int n = t.n * BN + c0;
       T* dst = reinterpret_cast<T*>(args.out + (static_cast<int64_t>(t.b) * kMxRows + row) * args.out_pitch) + n;
       store_accumulator<T, kCols>(src, row < t.valid ? dst : nullptr, args.N - n, args.wide != 0, [&] {
@@ -255,6 +280,37 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
       });
     }
   }
+  if constexpr (kSplit) {
+    // every CTA adds up its share of the columns, the parts in order
+    cluster_barrier();
+    if (first < ntasks) {
+      const Task t = task_at(first, args, s_blk, s_cnt);
+      const int quads = BN / 4 / parts;          // groups of four columns
+      for (int i = threadIdx.x; i < t.valid * quads; i += C::kThreads) {
+        const int row = i / quads;
+        const int c = part * (BN / parts) + (i - row * quads) * 4;
+        const float* src = reinterpret_cast<const float*>(smem) + row * C::kPartPitch + c;
+        float4 sum = peer_float4(src, 0);
+        for (int s = 1; s < parts; ++s) {
+          const float4 v = peer_float4(src, s);
+          sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+        }
+        Vec<T, 4> o;
+        o.v[0] = from_float<T>(sum.x); o.v[1] = from_float<T>(sum.y);
+        o.v[2] = from_float<T>(sum.z); o.v[3] = from_float<T>(sum.w);
+        const int n = t.n * BN + c;
+        T* dst = reinterpret_cast<T*>(args.out + (static_cast<int64_t>(t.b) * kMxRows + row) * args.out_pitch) + n;
+        if (args.wide && n + 4 <= args.N) {
+          *reinterpret_cast<Vec<T, 4>*>(dst) = o;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n + j < args.N) dst[j] = o.v[j];
+        }
+      }
+    }
+    cluster_barrier();                           // the others have read this CTA's part
+  }
   __syncthreads();
   if (warp == C::kEpiWarps) {
     tc_fence_after();
@@ -262,45 +318,88 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
   }
 }
 
-template <int BN, typename T>
-cudaError_t launch_impl(const MxProductArgs& p, cudaStream_t s) {
+template <int BN, typename T, bool kSplit>
+cudaError_t launch_impl(const MxProductArgs& p, int parts, cudaStream_t s) {
   using C = Cfg<BN>;
   Maps maps;
   const MxArgs a = mx_args(p, sizeof(T), BN);
   if (mx_codes_map(&maps.w, p.w, static_cast<int64_t>(p.E) * p.N, p.C, BN) != CUDA_SUCCESS) return cudaErrorInvalidValue;
   for (int i = 0; i < 3; ++i)
     if (mx_codes_map(&maps.a[i], p.codes, p.rows, p.C, 32 << i) != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  auto kernel = mx_product_kernel<BN, T>;
+  auto kernel = mx_product_kernel<BN, T, kSplit>;
   if (cudaError_t e = configure_kernel(reinterpret_cast<const void*>(kernel), 0, C::total(kMaxE))) return e;
   const int64_t tasks = static_cast<int64_t>(a.nblk) * a.NT;
   const int sms = dev_info().sms;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tasks < sms ? tasks : sms));
+  cfg.gridDim = dim3(static_cast<unsigned>(kSplit ? tasks * parts : (tasks < sms ? tasks : sms)));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::total(p.blk_off ? p.E : 0);
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.after_quantize ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  if (p.after_quantize) {
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (kSplit) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = parts; attr[na].val.clusterDim.y = 1; attr[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
+}
+
+// Weight rows of a tile and CTAs that share a task's contraction.
+struct Tile {
+  int bn, parts;
+};
+
+// The cheapest of the tile widths and splits by a model in SM cycles: a stage costs 560 and 1.75 per weight row;
+// splitting costs 1500, a quarter cycle per partial sum of a CTA, and 36 per CTA for launching clusters. Measured
+// (rows x N x C, us with the quantiser): 512x4096x4096 at 128/1 12.8, 256/1 14.1, 256/2 15.1, 64/1 19.1;
+// 128x4096x7168 at 128/4 13.0, 128/1 15.8, 256/4 14.1, 64/1 16.6; 64x1000x4096 at 64/4 7.8, 256/1 27.2, 64/1 14.3.
+// Clusters of 8 gain nothing over 4: too few of them fit a GPC.
+Tile choose_tile(int64_t blocks, int rows, int N, int KS, int sms) {
+  Tile best{256, 1};
+  int64_t least = INT64_MAX;
+  for (int bn = 256; bn >= 64; bn /= 2) {
+    const int64_t tasks = blocks * ((N + bn - 1) / bn);
+    for (int parts = 1; parts <= 4 && parts <= KS; parts *= 2) {
+      if (parts > 1 && tasks * parts > sms) break;
+      const int64_t waves = (tasks * parts + sms - 1) / sms;
+      const int64_t split = parts > 1 ? 1500 + static_cast<int64_t>(rows) * bn / 4 + 36 * tasks * parts : 0;
+      const int64_t cost = waves * ((KS + parts - 1) / parts) * (560 + 7 * bn / 4) + split;
+      if (cost < least) {
+        least = cost;
+        best = {bn, parts};
+      }
+    }
+  }
+  return best;
+}
+
+template <typename T, bool kSplit>
+cudaError_t launch_tile(const MxProductArgs& p, const Tile& t, cudaStream_t s) {
+  if (t.bn == 256) return launch_impl<256, T, kSplit>(p, t.parts, s);
+  if (t.bn == 128) return launch_impl<128, T, kSplit>(p, t.parts, s);
+  return launch_impl<64, T, kSplit>(p, t.parts, s);
 }
 
 }  // namespace
 
 cudaError_t launch_mx_product(const MxProductArgs& p, cudaStream_t s) {
   if (p.rows == 0) return cudaSuccess;
-  // pairs where every pair of SMs has a whole task of full blocks; else the widest weight tile that still gives every SM one
   const int64_t blocks = (p.rows + kMxRows - 1) / kMxRows;
   const int sms = dev_info().sms;
+  // pairs where every pair of SMs has a whole task of full blocks
   const int64_t full_pairs = p.blk_off ? 0 : p.rows / (2 * kMxRows);
   if (full_pairs * ((p.N + 255) / 256) >= sms / 2) return launch_mx_product_pair(p, s);
+  const Tile t = choose_tile(blocks, p.rows < kMxRows ? static_cast<int>(p.rows) : kMxRows, p.N, mx_chunks(p.C) / 2, sms);
   return with_dtype(p.dtype, [&](auto tag) {
     using T = decltype(tag);
-    if (blocks * ((p.N + 255) / 256) >= sms) return launch_impl<256, T>(p, s);
-    if (blocks * ((p.N + 127) / 128) >= sms) return launch_impl<128, T>(p, s);
-    return launch_impl<64, T>(p, s);
+    return t.parts > 1 ? launch_tile<T, true>(p, t, s) : launch_tile<T, false>(p, t, s);
   });
 }
 

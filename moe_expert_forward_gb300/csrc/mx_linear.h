@@ -63,8 +63,9 @@ cudaError_t launch_mx_product_pair(const MxProductArgs& a, cudaStream_t s);
 // Both steps of a linear in one launch for a few rows (mx_few.cu).
 constexpr int kMxFewTokens = 4;      // rows of a dense linear
 constexpr int kMxFewPairs = 16;      // (token, k) pairs of a routed one
+constexpr int64_t kMxFewWork = int64_t(1) << 26;   // rows * N * C
 constexpr int kMxFewSmem = 160 * 1024;
-bool mx_few_rows(int T, int C, bool routed, int64_t pairs);
+bool mx_few_rows(int T, int C, int N, int K);   // K = 0: dense
 cudaError_t launch_mx_few(const MxQuantArgs& q, const MxProductArgs& p, cudaStream_t s);
 
 }  // namespace mm

@@ -89,29 +89,35 @@ def _bad(what: str, why: str):
     raise MMError(MM_MOE_ERR_INVALID_ARG, f"{what}: {why}")
 
 
+_device = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # absent in builds of torch without CUDA
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _here(t, what: str, name: str):
     """A tensor on the current CUDA device."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != torch.cuda.current_device():
+    if not isinstance(t, torch.Tensor) or t.get_device() != _device():
         _bad(what, f"{name} must be a tensor on the current CUDA device")
 
 
 def _rows(t, what: str, name: str, cols: Optional[int] = None, dtype=None) -> int:
-    """dtype code of a 2-D tensor with unit column stride."""
+    """dtype code of a 2-D tensor with unit column stride and rows that do not overlap."""
     _here(t, what, name)
     code = _DTYPES.get(t.dtype)
     if code is None or (dtype is not None and t.dtype != dtype):
         _bad(what, f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (cols is not None and t.shape[1] != cols):
-        _bad(what, f"{name} must be [rows, {'columns' if cols is None else cols}] with contiguous columns, "
-                   f"got {tuple(t.shape)} strides {t.stride()}")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        _bad(what, f"{name}'s rows overlap: strides {t.stride()}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        _bad(what, f"{name} must be [rows, {'columns' if cols is None else cols}], got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        R, C = t.shape
+        if (C > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < C):
+            _bad(what, f"{name} must have contiguous columns and rows that do not overlap, got {tuple(t.shape)} "
+                       f"strides {t.stride()}")
     return code
 
 
@@ -347,6 +353,9 @@ def mx_product(codes, sf, weights: MxWeights, routing: Optional[Routing] = None,
     return out
 
 
+FEW_TOKENS, FEW_PAIRS, FEW_WORK, FEW_BYTES = 4, 16, 1 << 26, 160 * 1024   # mm_moe_mx_linear_workspace's rule
+
+
 def mx_linear_workspace(num_rows: int, C: int, device="cuda"):
     """A workspace of mx_linear for num_rows rows (T, or a routing's rows)."""
     return torch.empty(_linear_bytes(num_rows, C), dtype=torch.uint8, device=device)
@@ -356,10 +365,19 @@ def _linear_bytes(rows: int, C: int) -> int:
     return (256 + rows * (C // 2) + 255) // 256 * 256 + _scale_bytes(rows, C)
 
 
+def _few(T: int, C: int, N: int, K: int) -> bool:
+    """Whether mx_linear of these sizes needs no workspace (K = 0: dense)."""
+    rows = T * K if K else 1 if T < 2 else 2 if T == 2 else 4
+    if (rows > FEW_PAIRS) if K else (T > FEW_TOKENS):
+        return False
+    return rows * N <= FEW_WORK // C and (1 if K else rows) * (C // 32) * 36 <= FEW_BYTES
+
+
 def mx_linear(x, weights: MxWeights, routing: Optional[Routing] = None, out=None, workspace=None, stream=None):
     """x [T, C] through 4-bit weights: x quantised to 4 bits, then the product, in x's type.
 
-    Dense: [T, N].  With a routing (block_m = 128): [routing.rows, N], every token's
+    A few tokens (up to FEW_TOKENS, or FEW_PAIRS routed pairs) run in one launch without
+    a workspace.  Dense: [T, N].  With a routing (block_m = 128): [routing.rows, N], every token's
     row through its experts' matrices, rows of padding left as they are.  With a
     workspace of the caller's (mx_linear_workspace), sync_status(workspace) of the
     package reports a device wait that timed out."""
@@ -371,15 +389,16 @@ def mx_linear(x, weights: MxWeights, routing: Optional[Routing] = None, out=None
             _bad("mx_linear", f"x has {T} tokens, the routing {routing.T}")
         rows, slot, K = routing.rows, routing._slot, routing.K
     out, cnt, blk = _product_args("mx_linear", weights, routing, rows, x.dtype, x.device, out)
-    if workspace is None:
-        workspace = torch.empty(_linear_bytes(rows, C), dtype=torch.uint8, device=x.device)
-    else:
-        _here(workspace, "mx_linear", "workspace")
-        if not workspace.is_contiguous():
-            _bad("mx_linear", "workspace must be contiguous")
+    ws, ws_bytes = None, 0
+    if workspace is not None or not _few(T, C, weights.N, K):
+        if workspace is None:
+            workspace = torch.empty(_linear_bytes(rows, C), dtype=torch.uint8, device=x.device)
+        else:
+            _here(workspace, "mx_linear", "workspace")
+            if not workspace.is_contiguous():
+                _bad("mx_linear", "workspace must be contiguous")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(lib().mm_moe_mx_linear(x.data_ptr(), code, _pitch(x), T, C, weights.codes.data_ptr(),
                                   weights.sfp.data_ptr(), weights.E, weights.N, slot, K, cnt, blk, rows,
-                                  out.data_ptr(), _pitch(out), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), 0, _stream(stream)),
-           "mm_moe_mx_linear")
+                                  out.data_ptr(), _pitch(out), ws, ws_bytes, 0, _stream(stream)), "mm_moe_mx_linear")
     return out

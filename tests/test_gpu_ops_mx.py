@@ -178,6 +178,20 @@ def test_linear_few_rows(ops, T, N, C, dt):
     assert torch.equal(ops.mx_linear(wide.cuda()[:, 1:C + 1], wt), y)          # rows on no 32-byte boundary
 
 
+@pytest.mark.parametrize("T,N,C", [(5, 300, 2080), (64, 1000, 4096), (128, 520, 2048), (128, 2048, 3104), (200, 70, 7168),
+                                   (300, 1030, 1280), (2, 16400, 4128)])
+def test_linear_split_contraction(ops, T, N, C):
+    """Few tiles: clusters of CTAs share a tile's contraction, unevenly where it has an odd number of stages."""
+    codes, sf, w = weights(1, N, C, N)
+    x = torch.randn(T, C, generator=torch.Generator().manual_seed(T))
+    wt = ops.mx_weights(codes.cuda(), sf.cuda())
+    y = ops.mx_linear(x.cuda(), wt)
+    close(y, plain_quantise(x.double().numpy())[0], w[0], "f32")
+    assert torch.equal(ops.mx_linear(x.cuda(), wt), y)
+    half = ops.mx_linear(x.cuda().bfloat16(), wt)
+    close(half, plain_quantise(x.bfloat16().double().numpy())[0], w[0], "bf16")
+
+
 def run_routed(ops, T, N, C, E, K, masked=0.0, seed=0, idx=None, dt="f32"):
     rng = np.random.default_rng(seed)
     if idx is None:
@@ -295,7 +309,7 @@ def test_refusals(ops):
                  lambda: ops.mx_linear(x, two, routing=r3), lambda: ops.mx_linear(x[:3], two, routing=r128),
                  lambda: ops.mx_linear(x, one, out=torch.zeros(4, 63, device="cuda")),
                  lambda: ops.mx_linear(x, one, out=torch.zeros(4, 64, device="cuda", dtype=torch.bfloat16)),
-                 lambda: ops.mx_linear(x, one, workspace=torch.empty(256, dtype=torch.uint8, device="cuda")),
+                 lambda: ops.mx_linear(x.repeat(2, 1), one, workspace=torch.empty(256, dtype=torch.uint8, device="cuda")),
                  lambda: ops.mx_weights(codes[:, :, :8], sf), lambda: ops.mx_weights(codes, sf[:, :, :1]),
                  lambda: ops.mx_weights(codes.cpu(), sf), lambda: ops.mx_quantize(x.int()),
                  lambda: ops.mx_quantize(x[:, :0]), lambda: ops.mx_quantize(x, routing=ops.sort_tokens(idx[:2], 2, 128)),

@@ -92,9 +92,9 @@ def test_product(M):
 
 
 def test_linear(M):
-    need = M.mm_moe_mx_linear_workspace(4, 64)
+    need = M.mm_moe_mx_linear_workspace(8, 64, 8, 0, 8)
 
-    def lin(x=A, dtype=1, stride=64, T=4, C=64, w=A, E=1, N=8, slot=None, K=0, cnt=None, blk=None, n=4, out=A, ws=A,
+    def lin(x=A, dtype=1, stride=64, T=8, C=64, w=A, E=1, N=8, slot=None, K=0, cnt=None, blk=None, n=8, out=A, ws=A,
             size=need):
         return M.mm_moe_mx_linear(x, dtype, stride, T, C, w, A, E, N, slot, K, cnt, blk, n, out, N, ws, size, 0, None)
     for kw in (dict(x=None), dict(x=A + 1), dict(dtype=7), dict(stride=63), dict(T=-1, n=-1), dict(C=63), dict(w=None),
@@ -103,5 +103,21 @@ def test_linear(M):
                dict(slot=A, K=0, cnt=A, blk=A, E=4, n=1024)):
         assert lin(**kw) == M.MM_MOE_ERR_INVALID_ARG, kw
     assert lin(size=need - 1) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL
-    with pytest.raises(M.MMError):
-        M.mm_moe_mx_linear_workspace(4, 100)
+    assert lin(T=4, n=4, size=8) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL      # given, it holds a status word
+    assert lin(T=4, n=4, x=None, ws=None, size=0) == M.MM_MOE_ERR_INVALID_ARG
+    for bad in ((4, 100, 8, 0, 4), (4, 64, 8, 0, 5), (-1, 64, 8, 0, -1), (4, 64, 8, 17, 512), (4, 64, 0, 0, 4)):
+        with pytest.raises(M.MMError):
+            M.mm_moe_mx_linear_workspace(*bad)
+
+
+def test_binding_sizes_agree_with_the_library(M):
+    from moe_expert_forward_gb300 import ops
+    for rows, C in ((1, 32), (129, 96), (1000, 4096)):
+        assert M.mm_moe_mx_scale_size(rows, C) == ops._scale_bytes(rows, C)
+    for T in (0, 1, 2, 3, 4, 5, 100):
+        for K in (0, 1, 3, 4, 8):
+            for C in (32, 4096, 36384, 65536, 145632, 200000 // 32 * 32):
+                for N in (1, 300, 2048, 4096, 8192, 16384):
+                    rows = T if K == 0 else ops.pool_rows(T, K, 16, 128)
+                    want = 0 if ops._few(T, C, N, K) else ops._linear_bytes(rows, C)
+                    assert M.mm_moe_mx_linear_workspace(T, C, N, K, rows) == want, (T, K, C, N)
