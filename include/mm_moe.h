@@ -444,7 +444,7 @@ int mm_moe_route_backward(const void* logits, int dtype, int64_t row_stride, con
                           void* d_logits, int64_t d_row_stride, void* stream);
 
 /* mm_moe_dispatch's results (cnt [E], blk_off [E+1], slot [T*K], src [src_capacity])
- * for rows that are sorted outside mm_moe_forward: one launch up to 2^18 pairs, and
+ * for rows that are sorted outside mm_moe_forward: one launch up to 196608 pairs, and
  * `status` (device int32[4]) is cleared by the call instead of the caller, so status[0]
  * is this call's MM_MOE_OK or MM_MOE_ERR_BAD_ROUTING.  scratch: mm_moe_sort_scratch_size
  * bytes, 4-byte aligned (0 bytes, and null allowed, where one launch does it). */

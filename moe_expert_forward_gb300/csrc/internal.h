@@ -192,7 +192,7 @@ cudaError_t launch_route_backward(const RouteArgs& a, const int32_t* topk_idx, c
 
 // The routing in one launch up to so many pairs (sort.cu), by launch_dispatch above;
 // status is cleared first.  `scratch` is launch_dispatch's, unused in one launch.
-constexpr int64_t kSortOneLaunchPairs = int64_t(1) << 18;
+constexpr int64_t kSortOneLaunchPairs = int64_t(3) << 16;
 bool sort_in_one_launch(int64_t pairs);
 cudaError_t launch_sort(const int32_t* topk_idx, int T, int K, int E, int block_m, int32_t* cnt, int32_t* blk_off,
                         int32_t* slot, int32_t* src, int32_t* status, int32_t* scratch, int64_t scratch_ints,

@@ -42,7 +42,7 @@ __device__ __forceinline__ void zero_padding(const int32_t* __restrict__ src, co
   for (int seen = 0; m; m &= m - 1, ++seen) {
     if ((seen & (kThreads / 32 - 1)) != warp) continue;
     V* d = reinterpret_cast<V*>(rows + (r0 + __ffs(m) - 1) * pitch);
-    for (int i = lane; i < n; i += 32) d[i] = zero;
+    for (int i = lane; i < n; i += 32) store_once(d + i, zero);
   }
 }
 
@@ -91,11 +91,11 @@ __global__ void __launch_bounds__(kThreads)
   const int32_t* my = s.row + sub * K;
   const int n = static_cast<int>(pitch / B);
   for (int i = l; i < n; i += lanes) {
-    const V v = xr[i];
+    const V v = load_once(xr + i);
 #pragma unroll 4
     for (int k = 0; k < K; ++k) {
       const int64_t r = my[k];
-      if (r >= 0) reinterpret_cast<V*>(rows + r * pitch)[i] = v;
+      if (r >= 0) store_once(reinterpret_cast<V*>(rows + r * pitch) + i, v);
     }
   }
 }
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int k = 0; k < K; ++k) {
       const int64_t r = my[k];
       if (r >= 0) {
-        const V v = reinterpret_cast<const V*>(rows + r * H)[i];
+        const V v = load_once(reinterpret_cast<const V*>(rows + r * H) + i);
         const float wk = mw[k];
 #pragma unroll
         for (int c = 0; c < N; ++c) acc[c] = fmaf(wk, to_float(v.v[c]), acc[c]);
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads)
     V o;
 #pragma unroll
     for (int c = 0; c < N; ++c) o.v[c] = from_float<T>(acc[c]);
-    reinterpret_cast<V*>(out + t * out_stride)[i] = o;
+    store_once(reinterpret_cast<V*>(out + t * out_stride) + i, o);
   }
 }
 
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads)
     const float* mw = s.w + sub * K;
     const int n = H / N;
     for (int i = l; i < n; i += lanes) {
-      const V dv = dr[i];
+      const V dv = load_once(dr + i);
       float d[N];
 #pragma unroll
       for (int c = 0; c < N; ++c) d[c] = to_float(dv.v[c]);
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads)
         const int64_t r = k < K ? my[k] : -1;
         if (r >= 0) {
           if (d_w) {
-            const V v = reinterpret_cast<const V*>(rows + r * H)[i];
+            const V v = load_once(reinterpret_cast<const V*>(rows + r * H) + i);
 #pragma unroll
             for (int c = 0; c < N; ++c) dot[k] = fmaf(to_float(v.v[c]), d[c], dot[k]);
           }
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads)
           V o;
 #pragma unroll
           for (int c = 0; c < N; ++c) o.v[c] = from_float<T>(wk * d[c]);
-          reinterpret_cast<V*>(d_rows + r * H)[i] = o;
+          store_once(reinterpret_cast<V*>(d_rows + r * H) + i, o);
         }
       }
     }
@@ -213,10 +213,13 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Threads of a token's group: its accesses rounded up to a power of two, 8 to 256.
+// Threads of a token's group: its accesses rounded up to a power of two, 8 to 256, then halved (not below
+// 64) while that leaves fewer lanes idle in the last step: 448 accesses take 7 steps of 64, not 2 of 256.
 int group_lanes(int64_t accesses) {
   int l = 8;
   while (l < kThreads && l < accesses) l *= 2;
+  auto idle = [&](int w) { return (accesses + w - 1) / w * w - accesses; };
+  while (l > 64 && idle(l / 2) < idle(l)) l /= 2;
   return l;
 }
 
@@ -225,6 +228,7 @@ uint64_t bits_of(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 // f with the number of elements a B-byte access holds
 template <typename T, typename F>
 cudaError_t with_access(int B, F f) {
+  if (B == 32) return f(std::integral_constant<int, 32 / sizeof(T)>{});
   if (B == 16) return f(std::integral_constant<int, 16 / sizeof(T)>{});
   if (B == 8) return f(std::integral_constant<int, 8 / sizeof(T)>{});
   if constexpr (sizeof(T) == 2) {
@@ -249,6 +253,7 @@ cudaError_t launch_permute(const RowsArgs& a, const void* x, int64_t x_stride, v
         a.E, a.block_m, static_cast<char*>(rows), a.num_rows);
     return cudaGetLastError();
   };
+  if (B == 32) return go(std::integral_constant<int, 32>{});
   if (B == 16) return go(std::integral_constant<int, 16>{});
   if (B == 8) return go(std::integral_constant<int, 8>{});
   if (B == 4) return go(std::integral_constant<int, 4>{});

@@ -2,13 +2,16 @@
 // every (token, k) pair and the pair of every pool row, with the results of the
 // two dispatch kernels (kernels_misc.cu) bit for bit.
 //
-// One cluster of up to 8 CTAs takes the pairs, every warp a contiguous run of
+// One cluster of up to 16 CTAs takes the pairs, every warp a contiguous run of
 // them.  Each warp counts its experts in shared memory (equal experts of 32
-// pairs found with one match), a CTA turns its warps' counts into offsets, the
+// pairs found with votes), a CTA turns its warps' counts into offsets, the
 // CTAs read one another's totals through distributed shared memory, and every
 // warp then ranks its pairs.  The order inside an expert is ascending pair.
-// What bounds it is latency, a chain of a few barriers: the two dispatch kernels
-// spread over many SMs instead, and take over where a warp's run gets long.
+// What bounds it is latency, a chain of a few barriers, then each SM's scattered
+// stores; the two dispatch kernels spread over all SMs and take over where a warp's
+// run gets long. Measured (us, this kernel / the two): 1024 pairs over 256 experts
+// 6.3 / 12.3, 49152 over 384 9.9 / 20.5, 65536 over 256 10.5 / 17.6, 262144 over 256
+// 25.6 / 22.6.
 #include "cluster.cuh"
 #include "internal.h"
 
@@ -17,7 +20,8 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;       // more than 8 is an opt-in of the kernel
+constexpr int kBatch = 8;             // a lane's index loads in flight
 constexpr unsigned kAll = 0xffffffffu;
 
 struct SortArgs {
@@ -27,6 +31,19 @@ struct SortArgs {
   int E, block_m;
   int32_t *cnt, *blk_off, *slot, *src, *status;
 };
+
+// The valid lanes whose expert is this lane's (any mask where this one is not valid): a vote per bit of the ids.
+// (__match_any_sync took 2000 cycles for the 32 warps of a CTA, these votes a few hundred.)
+__device__ __forceinline__ unsigned same_expert(int e, bool valid, int bits) {
+  unsigned m = __ballot_sync(kAll, valid);
+#pragma unroll 2
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (e >> b) & 1;
+    const unsigned v = __ballot_sync(kAll, one);
+    m &= one ? v : ~v;
+  }
+  return m;
+}
 
 __global__ void __launch_bounds__(kThreads, 1) sort_kernel(const SortArgs a) {
   extern __shared__ int sm[];
@@ -41,20 +58,30 @@ __global__ void __launch_bounds__(kThreads, 1) sort_kernel(const SortArgs a) {
   const uint32_t rank = cluster_ctarank(), ctas = cluster_nctarank();
   const int gw = static_cast<int>(rank) * kWarps + w;
 
+  const int bits = 32 - __clz(E - 1);  // of an id; 0 for one expert
   for (int i = tid; i < kWarps * E; i += kThreads) wc[i] = 0;
   __syncthreads();
   const int64_t beg = gw * a.per;
   const int64_t end = beg + a.per < a.pairs ? beg + a.per : a.pairs;
   int* my = wc + w * E;
   bool bad = false;
-  for (int64_t p0 = beg; p0 < end; p0 += 32) {
-    const int64_t p = p0 + lane;
-    const int e = p < end ? __ldg(a.idx + p) : -1;
-    const bool valid = e >= 0 && e < E;
-    bad |= e < -1 || e >= E;
-    const unsigned m = __match_any_sync(kAll, valid ? e : -1);
-    if (valid && lane == __ffs(m) - 1) my[e] += __popc(m);
-    __syncwarp();
+  for (int64_t p0 = beg; p0 < end; p0 += 32 * kBatch) {
+    int ev[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int64_t p = p0 + j * 32 + lane;
+      ev[j] = p < end ? __ldg(a.idx + p) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (p0 + j * 32 >= end) break;  // the same for the warp
+      const int e = ev[j];
+      const bool valid = e >= 0 && e < E;
+      bad |= e < -1 || e >= E;
+      const unsigned m = same_expert(e, valid, bits);
+      if (valid && lane == __ffs(m) - 1) my[e] += __popc(m);
+      __syncwarp();
+    }
   }
   const int any_bad = __syncthreads_or(bad);
   if (tid == 0) s_tot[E] = any_bad;
@@ -118,23 +145,33 @@ __global__ void __launch_bounds__(kThreads, 1) sort_kernel(const SortArgs a) {
   }
   cluster_barrier();                     // the totals were read: a CTA may leave; and s_start is there
 
-  for (int64_t p0 = beg; p0 < end; p0 += 32) {
-    const int64_t p = p0 + lane;
-    const int e = p < end ? __ldg(a.idx + p) : -1;
-    const bool valid = e >= 0 && e < E;
-    const unsigned m = __match_any_sync(kAll, valid ? e : -1);
-    int before = 0;
-    if (valid) before = my[e];
-    __syncwarp();
-    if (valid) {
-      const int row = s_start[e] + before + __popc(m & ((1u << lane) - 1u));
-      a.slot[p] = row;
-      a.src[row] = static_cast<int32_t>(p);
-      if (lane == __ffs(m) - 1) my[e] = before + __popc(m);
-    } else if (p < end) {
-      a.slot[p] = -1;
+  for (int64_t p0 = beg; p0 < end; p0 += 32 * kBatch) {
+    int ev[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int64_t p = p0 + j * 32 + lane;
+      ev[j] = p < end ? __ldg(a.idx + p) : -1;
     }
-    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (p0 + j * 32 >= end) break;
+      const int64_t p = p0 + j * 32 + lane;
+      const int e = ev[j];
+      const bool valid = e >= 0 && e < E;
+      const unsigned m = same_expert(e, valid, bits);
+      int before = 0;
+      if (valid) before = my[e];
+      __syncwarp();
+      if (valid) {
+        const int row = s_start[e] + before + __popc(m & ((1u << lane) - 1u));
+        a.slot[p] = row;
+        a.src[row] = static_cast<int32_t>(p);
+        if (lane == __ffs(m) - 1) my[e] = before + __popc(m);
+      } else if (p < end) {
+        a.slot[p] = -1;
+      }
+      __syncwarp();
+    }
   }
   for (int e = gw; e < E; e += static_cast<int>(ctas) * kWarps) {
     const int64_t hi = static_cast<int64_t>(s_blk[e + 1]) * a.block_m;
@@ -155,14 +192,18 @@ cudaError_t launch_sort(const int32_t* topk_idx, int T, int K, int E, int block_
     if (e != cudaSuccess) return e;
     return launch_dispatch(topk_idx, T, K, E, block_m, cnt, blk_off, slot, src, status, scratch, scratch_ints, s);
   }
-  // as many CTAs as keep a warp's run at 64 pairs, then longer runs
-  int ctas = 1;
-  while (ctas < kMaxCluster && pairs > static_cast<int64_t>(ctas) * kWarps * 64) ctas *= 2;
+  // as many CTAs as keep a warp's run at 32 pairs, then longer runs; 4 at least, for the padding rows (1024 pairs
+  // over 256 experts: 1 CTA 8.3 us, 4 CTAs 6.3)
+  int ctas = 4;
+  while (ctas < kMaxCluster && pairs > static_cast<int64_t>(ctas) * kWarps * 32) ctas *= 2;
   int64_t per = (pairs + ctas * kWarps - 1) / (ctas * kWarps);
   per = (per + 31) / 32 * 32;
   const SortArgs a{topk_idx, pairs, per, E, block_m, cnt, blk_off, slot, src, status};
   auto smem = [](int e) { return static_cast<int>(((kWarps + 4) * e + 2) * sizeof(int)); };
-  if (cudaError_t e = configure_kernel(reinterpret_cast<const void*>(sort_kernel), 0, smem(kMaxE))) return e;
+  const void* fn = reinterpret_cast<const void*>(sort_kernel);
+  if (cudaError_t e = configure_kernel(fn, 0, smem(kMaxE))) return e;
+  if (ctas > 8)
+    if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);

@@ -94,9 +94,9 @@ def test_blocks(ops, block):
 
 
 @pytest.mark.parametrize("T,K,E,block", [(512, 4, 9, 16), (513, 4, 300, 32), (3000, 3, 384, 16), (8192, 6, 384, 16),
-                                         (16384, 16, 1024, 64), (16385, 16, 1024, 64), (50000, 8, 256, 128)])
+                                         (12288, 16, 1024, 64), (12289, 16, 1024, 64), (50000, 8, 256, 128)])
 def test_sorts_of_every_size(ops, T, K, E, block):
-    """One CTA, clusters of 2 to 8, and (from 2^18 pairs) the two launches."""
+    """Clusters of 4 to 16 CTAs, and (past 196608 pairs) the two launches."""
     rng = np.random.default_rng(T)
     idx = rng.integers(0, E, (T, K)).astype(np.int32)
     idx[rng.random(idx.shape) < 0.05] = -1
