@@ -14,13 +14,17 @@
 //   e is not chosen.  Under softmax with renorm the p cancel to q_k = exp(l_k - m) / sum of the
 //   chosen: dl_k = q_k (g_k - sum_j g_j q_j), and every other expert's gradient is zero.
 //
-// One warp takes one row and keeps its logits in registers, expert e in lane
-// e % 32, so a row is read once.  A round of the choice is the largest key of the
-// lane, one reduction over the warp for the key and one for the lowest expert
-// that holds it; where the logits have 16 bits and there is no bias, key and
-// expert fit one word and one reduction does both.  What bounds it is the issue of
-// these instructions (65536 rows of 160 read 21 MB, 3 us), so nothing is kept or
-// computed for more than the ceil(E / 32) logits a lane has.
+// A group of G lanes takes a row and keeps its logits in registers, P consecutive
+// ones per access, so a row is read once.  A round of the choice is the largest key
+// of the lane, a reduction over the group for the key and one for the lowest
+// expert that holds it; where the logits have 16 bits and there is no bias, key and
+// expert fit one word, all words differ, one reduction does both, and a round takes
+// the largest word below the last choice, one add-and-max per logit: of differences
+// k - last mod 2^32, those of words below `last` are the larger ones.  Two forms:
+//   G = 32, P = 1  a warp a row: few rows, where the latency of one row counts
+//   G = 8, P = 2   four rows a warp: many rows, where the issue of instructions
+//                  bounds it (65536 rows of 160 read 21 MB, 3 us) and the reductions
+//                  and the work at a row's end are shared by four
 //
 // The softmax takes exp as 2^(x log2 e) by the fast unit, a few units in the last
 // place of fp32 off for the arguments (<= 0) that matter; the sigmoid, whose sums
@@ -35,11 +39,22 @@ namespace {
 constexpr int kRouteWarps = 4;
 constexpr unsigned kAll = 0xffffffffu;
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Reductions over each group of G consecutive lanes; the whole warp takes part.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (G == 32) return __reduce_max_sync(kAll, v);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) { return ~group_max<G>(~v); }
 
 // Unsigned integers in the order of the floats (-0 counts as +0); -inf and NaN, never chosen, are 0.
 __device__ __forceinline__ uint32_t ordered(float f) {
@@ -50,23 +65,26 @@ __device__ __forceinline__ uint32_t ordered(float f) {
 __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float((o >> 31) ? (o ^ 0x80000000u) : ~o);
 }
-__device__ __forceinline__ float warp_max(float v) {
-  const uint32_t o = __reduce_max_sync(kAll, ordered(v));
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+  const uint32_t o = group_max<G>(ordered(v));
   return o ? unordered(o) : -INFINITY;
 }
 
 // Key and expert of a 16-bit logit in one word: the float's bits in order on top, 0xFFFF - e below, so that the
-// larger of two equal logits' words is the lower expert's; 0 where it is never chosen.
+// larger of two equal logits' words is the lower expert's. v is no NaN and no -0 (clean).
 template <typename T>
-__device__ __forceinline__ uint32_t packed_key(T v, int e) {
-  const float f = to_float(v);
-  if (!(f > -INFINITY)) return 0u;
-  uint32_t b;
-  if constexpr (std::is_same<T, __half>::value) b = __half_as_ushort(v);
-  else b = __bfloat16_as_ushort(v);
-  b = b == 0x8000u ? 0u : b;
-  b = (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
-  return b << 16 | static_cast<uint32_t>(0xFFFF - e);
+__device__ __forceinline__ uint32_t packed_key(T v, uint32_t rest) {
+  uint32_t u;
+  if constexpr (std::is_same<T, __half>::value) u = static_cast<uint32_t>(__half_as_ushort(v)) << 16;
+  else u = static_cast<uint32_t>(__bfloat16_as_ushort(v)) << 16;
+  const uint32_t o = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return (o & 0xFFFF0000u) | rest;
+}
+// words of -inf, which is never chosen, are below this
+template <typename T>
+__device__ __forceinline__ uint32_t first_packed() {
+  return std::is_same<T, __half>::value ? 0x04000000u : 0x00800000u;
 }
 template <typename T>
 __device__ __forceinline__ float packed_value(uint32_t key) {
@@ -75,6 +93,36 @@ __device__ __forceinline__ float packed_value(uint32_t key) {
   if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
   else return __uint_as_float(b << 16);
 }
+// NaN -> -inf, -0 -> +0
+template <typename T>
+__device__ __forceinline__ T clean(T v) {
+  if constexpr (sizeof(T) == 4) return fmaxf(v + 0.0f, -INFINITY);
+  else return __hmax(__hadd(v, from_float<T>(0.f)), from_float<T>(-INFINITY));
+}
+template <typename T>
+__device__ __forceinline__ void clean2(T* v) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 r = __hmax2(__hadd2(__halves2half2(v[0], v[1]), __float2half2_rn(0.f)), __float2half2_rn(-INFINITY));
+    v[0] = __low2half(r);
+    v[1] = __high2half(r);
+  } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const __nv_bfloat162 r = __hmax2(__hadd2(__halves2bfloat162(v[0], v[1]), __float2bfloat162_rn(0.f)),
+                                     __float2bfloat162_rn(-INFINITY));
+    v[0] = __low2bfloat16(r);
+    v[1] = __high2bfloat16(r);
+  } else {
+    v[0] = clean(v[0]);
+    v[1] = clean(v[1]);
+  }
+}
+
+// 2^y by the fast unit; results below fp32's normal range are 0
+__device__ __forceinline__ float exp2_fast(float y) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
+}
+constexpr float kLog2e = 1.44269504f;
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
 
@@ -84,50 +132,76 @@ __device__ __forceinline__ float load_logit(const T* row, int e, int E) {
   return x == x ? x : -INFINITY;
 }
 
-template <typename T, int VPL, bool kBias>
+// A lane's V accesses of P logits: value i of access j is expert (j G + lane) P + i. E is a multiple of P.
+template <typename T, int V, int G, int P>
+__device__ __forceinline__ void load_row(const T* row, int lane, int E, T (&v)[V * P]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int c = (j * G + lane) * P;
+    Vec<T, P> a;
+#pragma unroll
+    for (int i = 0; i < P; ++i) a.v[i] = from_float<T>(-INFINITY);
+    if (c < E) a = *reinterpret_cast<const Vec<T, P>*>(row + c);
+    if constexpr (P == 2) clean2(a.v);
+    else a.v[0] = clean(a.v[0]);
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[j * P + i] = a.v[i];
+  }
+}
+
+template <typename T, int V, int G, int P, bool kBias>
 __global__ void __launch_bounds__(32 * kRouteWarps)
     route_kernel(const T* __restrict__ logits, int64_t stride, int T_, int E, int K, const float* __restrict__ bias,
                  int score, int renorm, float scale, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
   constexpr bool kPacked = sizeof(T) == 2 && !kBias;
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
-  if (t >= T_) return;
+  constexpr int N = V * P;
+  const int lane = threadIdx.x % G;
+  const int t0 = blockIdx.x * (32 * kRouteWarps / G) + threadIdx.x / G;
+  if (G == 32 && t0 >= T_) return;
+  const int t = min(t0, T_ - 1);                  // a group past the last row repeats it and stores nothing
   const T* row = logits + t * stride;
   const bool all = score == MM_MOE_SCORE_SOFTMAX && !renorm;   // the sum runs over every expert
-  float x[VPL];
-  uint32_t key[VPL];
+  T v[N];
+  load_row<T, V, G, P>(row, lane, E, v);
+  uint32_t key[N];
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int e = j * 32 + lane;
-    x[j] = load_logit(row, e, E);
-    if constexpr (kPacked) key[j] = e < E ? packed_key(row[e], e) : 0u;
-    else if constexpr (kBias) key[j] = x[j] == -INFINITY ? 0u : ordered(sigmoid(x[j]) + __ldg(bias + (e < E ? e : 0)));
-    else key[j] = ordered(x[j]);
+  for (int n = 0; n < N; ++n) {
+    const int e = (n / P * G + lane) * P + n % P;
+    if constexpr (kPacked) key[n] = packed_key(v[n], static_cast<uint32_t>(0xFFFF - e));
+    else if constexpr (kBias)
+      key[n] = to_float(v[n]) > -INFINITY ? ordered(sigmoid(to_float(v[n])) + __ldg(bias + (e < E ? e : 0))) : 0u;
+    else key[n] = ordered(to_float(v[n]));
   }
   // lane k ends up with the k-th choice
   int my_e = -1;
-  uint32_t my_key = 0, first = 0;
+  uint32_t my_key = 0, first = 0, last = 0;
   for (int k = 0; k < K; ++k) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
-    const uint32_t top = __reduce_max_sync(kAll, best);
-    if (top == 0) break;
-    if (k == 0) first = top;
+    uint32_t top = 0;
     unsigned at;
     if constexpr (kPacked) {
-      at = 0xFFFFu - (top & 0xFFFFu);
+      uint32_t best = 0;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) key[j] = key[j] == top ? 0u : key[j];
+      for (int n = 0; n < N; ++n) best = __viaddmax_u32(key[n], 0u - last, best);
+      top = group_max<G>(best) + last;
+      last = top;
+      if (top < first_packed<T>()) top = 0;         // and from here on every round ends here: all words below are -inf's
+      at = 0xFFFFu - (top & 0xFFFFu);
     } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) top = max(top, key[n]);
+      top = group_max<G>(top);
       at = 0xffffffffu;
 #pragma unroll
-      for (int j = VPL - 1; j >= 0; --j) at = key[j] == top ? static_cast<unsigned>(j * 32 + lane) : at;
-      at = __reduce_min_sync(kAll, at);
+      for (int n = N - 1; n >= 0; --n)
+        at = key[n] == top ? static_cast<unsigned>((n / P * G + lane) * P + n % P) : at;
+      at = group_min<G>(at);
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) key[j] = at == static_cast<unsigned>(j * 32 + lane) ? 0u : key[j];
+      for (int n = 0; n < N; ++n)
+        key[n] = at == static_cast<unsigned>((n / P * G + lane) * P + n % P) ? 0u : key[n];
     }
-    if (lane == k) {
+    if (k == 0) first = top;
+    if (G == 32 && top == 0) break;
+    if (lane == k && top != 0) {
       my_e = static_cast<int>(at);
       my_key = top;
     }
@@ -136,43 +210,40 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   auto value = [&](uint32_t k) { return kPacked ? packed_value<T>(k) : unordered(k); };
   float p = 0.f;
   if (score == MM_MOE_SCORE_SOFTMAX) {
-    const float m = value(first);                 // the first choice is the row's largest logit
-    if (my_e >= 0) p = __expf(value(my_key) - m);
+    const float m = first ? value(first) : 0.f;   // the first choice is the row's largest logit
+    if (my_e >= 0) p = exp2_fast((value(my_key) - m) * kLog2e);
     if (all) {
       float z = 0.f;
-      if (first) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) z += __expf(x[j] - m);
-      }
-      z = warp_sum(z);
+      for (int n = 0; n < N; ++n) z += exp2_fast((to_float(v[n]) - m) * kLog2e);
+      z = group_sum<G>(z);
       if (my_e >= 0) p = __fdiv_rn(p, z);
     }
   } else if (my_e >= 0) {
     p = sigmoid(kBias ? to_float(row[my_e]) : value(my_key));
   }
-  if (renorm) p = __fdiv_rn(p, warp_sum(p) + 1e-20f);
-  if (lane < K) {
+  if (renorm) p = __fdiv_rn(p, group_sum<G>(p) + 1e-20f);
+  if (lane < K && t0 < T_) {
     topk_idx[static_cast<int64_t>(t) * K + lane] = my_e;
     topk_w[static_cast<int64_t>(t) * K + lane] = p * scale;
   }
 }
 
-template <typename T, int VPL>
+template <typename T, int V, int G, int P>
 __global__ void __launch_bounds__(32 * kRouteWarps)
     route_backward_kernel(const T* __restrict__ logits, int64_t stride, const int32_t* __restrict__ topk_idx,
                           const float* __restrict__ d_w, int T_, int E, int K, int score, int renorm, float scale,
                           T* __restrict__ d_logits, int64_t d_stride) {
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
-  if (t >= T_) return;
+  constexpr int N = V * P;
+  const int lane = threadIdx.x % G;
+  const int t0 = blockIdx.x * (32 * kRouteWarps / G) + threadIdx.x / G;
+  if (G == 32 && t0 >= T_) return;
+  const int t = min(t0, T_ - 1);
   const T* row = logits + t * stride;
   T* d_row = d_logits + t * d_stride;
   const bool all = score == MM_MOE_SCORE_SOFTMAX && !renorm;
-  float v[VPL];
-  if (all) {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) v[j] = load_logit(row, j * 32 + lane, E);
-  }
+  T raw[N];
+  if (all) load_row<T, V, G, P>(row, lane, E, raw);
   int e = -1;
   float g = 0.f, x = -INFINITY;
   if (lane < K) {
@@ -184,82 +255,108 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     }
   }
   float d;                                          // lane k: the gradient of choice k's logit
+  float v[N], r = 0.f;                              // the others': v r
   if (all) {
-    float m = v[0], z = 0.f;
+    float m = -INFINITY, z = 0.f;
 #pragma unroll
-    for (int j = 1; j < VPL; ++j) m = fmaxf(m, v[j]);
-    m = warp_max(m);
+    for (int n = 0; n < N; ++n) {
+      v[n] = to_float(raw[n]);
+      m = fmaxf(m, v[n]);
+    }
+    m = group_max<G>(m);
     if (m == -INFINITY) m = 0.f;                    // a row without logits: every exp is 0
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      v[j] = __expf(v[j] - m);
-      z += v[j];
+    for (int n = 0; n < N; ++n) {
+      v[n] = exp2_fast((v[n] - m) * kLog2e);
+      z += v[n];
     }
-    z = warp_sum(z);
+    z = group_sum<G>(z);
     const float rz = z == 0.f ? 0.f : __fdiv_rn(1.0f, z);
-    const float p = e >= 0 ? __expf(x - m) * rz : 0.f;
-    const float s = warp_sum(g * p);
+    const float p = e >= 0 ? exp2_fast((x - m) * kLog2e) * rz : 0.f;
+    const float s = group_sum<G>(g * p);
     d = p * (g - s);
-    const float r = -rz * s;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int c = j * 32 + lane;
-      if (c < E) d_row[c] = from_float<T>(v[j] * r);
-    }
+    r = -rz * s;
   } else {
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = 0.f;
     if (score == MM_MOE_SCORE_SOFTMAX) {
-      const float m = warp_max(x);
-      const float q0 = e >= 0 ? __expf(x - m) : 0.f;
-      const float z = warp_sum(q0);
+      const float m = group_max<G>(x);
+      const float q0 = e >= 0 ? exp2_fast((x - m) * kLog2e) : 0.f;
+      const float z = group_sum<G>(q0);
       const float q = e >= 0 ? __fdiv_rn(q0, z) : 0.f;
-      d = q * (g - warp_sum(g * q));
+      d = q * (g - group_sum<G>(g * q));
     } else {
       const float p = e >= 0 ? sigmoid(x) : 0.f;
       float dp = g;
       if (renorm) {
-        const float z = warp_sum(p) + 1e-20f;
-        dp = __fdiv_rn(g - warp_sum(g * __fdiv_rn(p, z)), z);
+        const float z = group_sum<G>(p) + 1e-20f;
+        dp = __fdiv_rn(g - group_sum<G>(g * __fdiv_rn(p, z)), z);
       }
       d = dp * p * (1.0f - p);
     }
+  }
+  if (t0 < T_) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int c = j * 32 + lane;
-      if (c < E) d_row[c] = from_float<T>(0.f);
+    for (int j = 0; j < V; ++j) {
+      const int c = (j * G + lane) * P;
+      Vec<T, P> o;
+#pragma unroll
+      for (int i = 0; i < P; ++i) o.v[i] = from_float<T>(v[j * P + i] * r);
+      if (c < E) *reinterpret_cast<Vec<T, P>*>(d_row + c) = o;
     }
   }
   __syncwarp();                                     // the row's other entries first, then the chosen ones over them
-  if (e >= 0) d_row[e] = from_float<T>(d);
+  if (e >= 0 && t0 < T_) d_row[e] = from_float<T>(d);
 }
 
-// f with the logits a lane holds, ceil(E / 32) rounded up to a width that is built
-template <typename F>
-cudaError_t with_width(int E, F f) {
+template <int V, int G, int P>
+struct Form {
+  static constexpr int v = V, g = G, p = P;
+  static unsigned grid(int T) { return static_cast<unsigned>((T + 32 * kRouteWarps / G - 1) / (32 * kRouteWarps / G)); }
+};
+
+// Four rows a warp from so many rows on; below, the rows do not fill the SMs' warps. Measured, us forward, four rows a
+// warp / a warp a row, bf16: 65521x160 top-4 12.2 / 19.4, 16384x256 top-8 7.6 / 8.7, 8192x160 3.3 / 3.8, 2048x160
+// 2.3 / 2.2; fp32: 65521x160 20.9 / 28.8, 16384x160 6.4 / 8.2, 8192x256 top-8 9.4 / 8.3.
+template <typename T>
+constexpr int kManyRows = sizeof(T) == 2 ? 8192 : 16384;
+
+// f with the form that takes E logits a row; `bits` are the row pitches' and addresses' in bytes, or-ed.
+template <typename T, typename F>
+cudaError_t with_form(int rows, int E, int K, uint64_t bits, F f) {
+  if (rows >= kManyRows<T> && K <= 8 && E <= 256 && E % 2 == 0 && bits % (2 * sizeof(T)) == 0) {
+    const int n = (E + 15) / 16;
+    if (n <= 2) return f(Form<2, 8, 2>{});
+    if (n <= 4) return f(Form<4, 8, 2>{});
+    if (n <= 6) return f(Form<6, 8, 2>{});
+    if (n <= 8) return f(Form<8, 8, 2>{});
+    if (n <= 10) return f(Form<10, 8, 2>{});
+    if (n <= 12) return f(Form<12, 8, 2>{});
+    return f(Form<16, 8, 2>{});
+  }
   const int n = (E + 31) / 32;
-  if (n <= 1) return f(std::integral_constant<int, 1>{});
-  if (n <= 2) return f(std::integral_constant<int, 2>{});
-  if (n <= 3) return f(std::integral_constant<int, 3>{});
-  if (n <= 4) return f(std::integral_constant<int, 4>{});
-  if (n <= 5) return f(std::integral_constant<int, 5>{});
-  if (n <= 6) return f(std::integral_constant<int, 6>{});
-  if (n <= 8) return f(std::integral_constant<int, 8>{});
-  if (n <= 12) return f(std::integral_constant<int, 12>{});
-  if (n <= 16) return f(std::integral_constant<int, 16>{});
-  if (n <= 24) return f(std::integral_constant<int, 24>{});
-  return f(std::integral_constant<int, 32>{});
+  if (n <= 1) return f(Form<1, 32, 1>{});
+  if (n <= 2) return f(Form<2, 32, 1>{});
+  if (n <= 4) return f(Form<4, 32, 1>{});
+  if (n <= 6) return f(Form<6, 32, 1>{});
+  if (n <= 8) return f(Form<8, 32, 1>{});
+  if (n <= 12) return f(Form<12, 32, 1>{});
+  if (n <= 16) return f(Form<16, 32, 1>{});
+  if (n <= 24) return f(Form<24, 32, 1>{});
+  return f(Form<32, 32, 1>{});
 }
 
 }  // namespace
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((a.T + kRouteWarps - 1) / kRouteWarps);
   return with_dtype(a.dtype, [&](auto tag) {
     using T = decltype(tag);
-    return with_width(a.E, [&](auto w) {
-      constexpr int W = decltype(w)::value;
-      auto kernel = a.bias ? route_kernel<T, W, true> : route_kernel<T, W, false>;
-      kernel<<<grid, 32 * kRouteWarps, 0, s>>>(static_cast<const T*>(a.logits), a.stride, a.T, a.E, a.K, a.bias,
-                                               a.score, a.renorm, a.scale, a.topk_idx, a.topk_w);
+    const uint64_t bits = reinterpret_cast<uintptr_t>(a.logits) | static_cast<uint64_t>(a.stride) * sizeof(T);
+    return with_form<T>(a.T, a.E, a.K, bits, [&](auto form) {
+      using W = decltype(form);
+      auto kernel = a.bias ? route_kernel<T, W::v, W::g, W::p, true> : route_kernel<T, W::v, W::g, W::p, false>;
+      kernel<<<W::grid(a.T), 32 * kRouteWarps, 0, s>>>(static_cast<const T*>(a.logits), a.stride, a.T, a.E, a.K,
+                                                       a.bias, a.score, a.renorm, a.scale, a.topk_idx, a.topk_w);
       return cudaGetLastError();
     });
   });
@@ -267,11 +364,13 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
 
 cudaError_t launch_route_backward(const RouteArgs& a, const int32_t* topk_idx, const float* d_w, void* d_logits,
                                   int64_t d_stride, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((a.T + kRouteWarps - 1) / kRouteWarps);
   return with_dtype(a.dtype, [&](auto tag) {
     using T = decltype(tag);
-    return with_width(a.E, [&](auto w) {
-      route_backward_kernel<T, decltype(w)::value><<<grid, 32 * kRouteWarps, 0, s>>>(
+    const uint64_t bits = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(d_logits) |
+                          static_cast<uint64_t>(a.stride | d_stride) * sizeof(T);
+    return with_form<T>(a.T, a.E, a.K, bits, [&](auto form) {
+      using W = decltype(form);
+      route_backward_kernel<T, W::v, W::g, W::p><<<W::grid(a.T), 32 * kRouteWarps, 0, s>>>(
           static_cast<const T*>(a.logits), a.stride, topk_idx, d_w, a.T, a.E, a.K, a.score, a.renorm, a.scale,
           static_cast<T*>(d_logits), d_stride);
       return cudaGetLastError();

@@ -102,6 +102,28 @@ def test_sixteen_bit_logits_with_ties(ops, dt, score, renorm):
     check(ops, x, 8, score=score, renorm=renorm, dt=dt)
 
 
+@pytest.mark.parametrize("E,K,dt", [(8, 2, "f32"), (62, 8, "bf16"), (160, 4, "bf16"), (160, 4, "f16"), (256, 8, "f32"),
+                                    (250, 1, "bf16"), (161, 4, "bf16"), (64, 9, "f32")])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_many_rows(ops, E, K, dt, score, renorm):
+    """Four of many rows share a warp (up to 256 experts, an even number, and 8 choices): the same as those rows in
+    small batches, which take a warp each."""
+    g = torch.Generator().manual_seed(E + K)
+    x = (torch.randn(16387, E, generator=g) * 2).to(DT[dt])
+    x[torch.rand(x.shape, generator=g) < 0.3] = -float("inf")
+    x[5], x[6, 1:] = -float("inf"), float("nan")
+    x, dw = x.cuda(), torch.randn(16387, K, generator=g).cuda()
+    bias = torch.randn(E, generator=g).cuda() if score == "sigmoid" and E != 160 else None
+    idx, w = ops.route(x, K, bias=bias, score=score, renorm=renorm)
+    d = ops.route_backward(x, idx, dw, score=score, renorm=renorm)
+    parts = [slice(0, 6000), slice(6000, 12000), slice(12000, 16387)]
+    i2, w2 = zip(*[ops.route(x[p], K, bias=bias, score=score, renorm=renorm) for p in parts])
+    assert torch.equal(idx, torch.cat(i2))
+    assert (w - torch.cat(w2)).abs().max() <= W_TOL
+    d2 = torch.cat([ops.route_backward(x[p], idx[p], dw[p], score=score, renorm=renorm) for p in parts]).float()
+    assert ((d.float() - d2).abs() <= 2 * W_TOL * dw.abs().max() + 2 * ROUND[dt] * d2.abs() + (1e-7 if dt == "f16" else 0)).all()
+
+
 def test_bias_moves_the_choice_only(ops):
     g = torch.Generator().manual_seed(9)
     x = torch.randn(300, 64, generator=g)
