@@ -16,7 +16,8 @@ namespace mm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 2;            // groups of 16 elements a thread has in flight
+constexpr int kBatch = 4;            // groups of 16 elements a thread has in flight
+constexpr int kOutBatch = 2;         // coming back from 4 bits
 
 // The position of a thread in [rows][groups of 16], stepped by a fixed number of groups.
 struct Walk {
@@ -81,13 +82,24 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Four e2m1 codes (the low 16 bits of c) times 2^126 * s, s = 2^(sf - 127): the code's three magnitude bits
-// placed at the top of an fp32 mantissa and exponent are its value times 2^-126, the subnormal 0.5 included.
-__device__ __forceinline__ void decode4(uint32_t c, float s, float* f) {
+// Eight e2m1 codes times s.
+__device__ __forceinline__ void decode8(uint32_t c, float s, float* f) {
+  uint32_t h[4];                      // pairs of fp16, exact
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(c));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t n = c >> (4 * i);
-    f[i] = __uint_as_float((n & 7u) << 22 | (n & 8u) << 28) * 0x1p126f * s;
+    __half2 p;
+    memcpy(&p, &h[i], 4);
+    const float2 v = __half22float2(p);
+    f[2 * i] = v.x * s;
+    f[2 * i + 1] = v.y * s;
   }
 }
 
@@ -100,23 +112,21 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads, total = R * groups;
   Walk at(i, groups);
   while (i < total) {
-    uint2 w[kBatch];
-    uint32_t b[kBatch];
+    uint2 w[kOutBatch];
+    uint32_t b[kOutBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
+    for (int u = 0; u < kOutBatch; ++u) {
       const int64_t j = i + u * step;
       w[u] = j < total ? __ldg(codes + j) : make_uint2(0, 0);
       b[u] = j < total ? __ldg(sf + (j >> 1)) : 0;
     }
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
+    for (int u = 0; u < kOutBatch; ++u) {
       if (i < total) {
         const float s = ue8m0_value(b[u]);
         float f[16];
-        decode4(w[u].x, s, f);
-        decode4(w[u].x >> 16, s, f + 4);
-        decode4(w[u].y, s, f + 8);
-        decode4(w[u].y >> 16, s, f + 12);
+        decode8(w[u].x, s, f);
+        decode8(w[u].y, s, f + 8);
         T* d = out + at.r * out_stride + at.g * 16;
         const int left = C - at.g * 16;
         if (kVec && left >= 16) {
@@ -200,7 +210,7 @@ cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t s) {
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* sf, int64_t R, int C, int dtype, void* out,
                                  int64_t out_stride, cudaStream_t s) {
   const int groups = (C + 31) / 32 * 2;
-  const int grid = blocks_for((R * groups + kBatch - 1) / kBatch, 8);
+  const int grid = blocks_for((R * groups + kOutBatch - 1) / kOutBatch, 8);
   const int64_t step = static_cast<int64_t>(grid) * kThreads;
   const int d_row = static_cast<int>(step / groups), d_group = static_cast<int>(step % groups);
   const uint2* c = reinterpret_cast<const uint2*>(codes);

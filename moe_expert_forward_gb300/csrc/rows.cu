@@ -18,30 +18,29 @@
 namespace mm {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPadRows = 32;                 // pool rows a padding CTA looks at
+constexpr int kThreads = 256;                // permute, unpermute
+constexpr int kBackThreads = 128;            // the gradients (8192x4096 top-8: 190 us, with 256 threads 205)
+constexpr int kPadRows = 8;                  // pool rows a padding CTA looks at
 constexpr int kMaxGroups = kThreads / 8;     // tokens of one CTA at most
 
-// Zeroes the padding among pool rows [g * 32, g * 32 + 32): rows whose src is
-// -1, and rows past the last block, whose src the routing never wrote.
+// Zeroes the padding among the 8 pool rows from 8 g on: rows whose src is -1, and rows past the last block, whose
+// src the routing never wrote. The CTAs that do this come first in the grid and are many and small: the rows past the
+// last block lie together, and in CTAs of 32 rows at the grid's end they were its tail (permute 8192x7168: 152 us,
+// without any padding 132).
 template <int B>
 __device__ __forceinline__ void zero_padding(const int32_t* __restrict__ src, const int32_t* __restrict__ blk_off, int E,
                                              int block_m, char* __restrict__ rows, int64_t num_rows, int64_t pitch,
                                              int64_t g) {
   using V = Vec<char, B>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t r0 = g * kPadRows;
+  const int lane = threadIdx.x & 31;
   const int64_t end = static_cast<int64_t>(__ldg(blk_off + E)) * block_m;
-  const int64_t r = r0 + lane;
-  const bool pad = r < num_rows && (r >= end || __ldg(src + r) < 0);
-  unsigned m = __ballot_sync(0xffffffffu, pad);
   const int n = static_cast<int>(pitch / B);
   V zero;
 #pragma unroll
   for (int i = 0; i < B; ++i) zero.v[i] = 0;
-  for (int seen = 0; m; m &= m - 1, ++seen) {
-    if ((seen & (kThreads / 32 - 1)) != warp) continue;
-    V* d = reinterpret_cast<V*>(rows + (r0 + __ffs(m) - 1) * pitch);
+  for (int64_t r = g * kPadRows + (threadIdx.x >> 5); r < (g + 1) * kPadRows && r < num_rows; r += blockDim.x / 32) {
+    if (r < end && __ldg(src + r) >= 0) continue;
+    V* d = reinterpret_cast<V*>(rows + r * pitch);
     for (int i = lane; i < n; i += 32) store_once(d + i, zero);
   }
 }
@@ -54,7 +53,7 @@ struct TokenRows {
 __device__ __forceinline__ void load_token_rows(TokenRows& s, const int32_t* __restrict__ slot,
                                                 const float* __restrict__ w, int64_t t0, int tokens, int64_t T, int K,
                                                 int64_t num_rows) {
-  for (int i = threadIdx.x; i < tokens * K; i += kThreads) {
+  for (int i = threadIdx.x; i < tokens * K; i += blockDim.x) {
     const int64_t p = t0 * K + i;
     int r = -1;
     float wv = 1.f;
@@ -71,18 +70,18 @@ __device__ __forceinline__ void load_token_rows(TokenRows& s, const int32_t* __r
 
 template <int B>
 __global__ void __launch_bounds__(kThreads)
-    permute_kernel(const char* __restrict__ x, int64_t x_pitch, int64_t T, int64_t pitch, int lanes, int token_ctas,
+    permute_kernel(const char* __restrict__ x, int64_t x_pitch, int64_t T, int64_t pitch, int lanes, unsigned pad_ctas,
                    const int32_t* __restrict__ slot, int K, const int32_t* __restrict__ src,
                    const int32_t* __restrict__ blk_off, int E, int block_m, char* __restrict__ rows,
                    int64_t num_rows) {
   using V = Vec<char, B>;
-  if (static_cast<int>(blockIdx.x) >= token_ctas) {
-    zero_padding<B>(src, blk_off, E, block_m, rows, num_rows, pitch, blockIdx.x - token_ctas);
+  if (blockIdx.x < pad_ctas) {
+    zero_padding<B>(src, blk_off, E, block_m, rows, num_rows, pitch, blockIdx.x);
     return;
   }
   __shared__ TokenRows s;
   const int tokens = kThreads / lanes;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x - pad_ctas) * tokens;
   load_token_rows(s, slot, nullptr, t0, tokens, T, K, num_rows);
   const int sub = threadIdx.x / lanes, l = threadIdx.x % lanes;
   const int64_t t = t0 + sub;
@@ -139,22 +138,22 @@ __global__ void __launch_bounds__(kThreads)
 
 // KT >= K: the dots of a token live in registers.
 template <typename T, int N, int KT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kBackThreads)
     unpermute_backward_kernel(const T* __restrict__ d_out, int64_t d_stride, const T* __restrict__ rows, int H,
-                              int64_t tokens_total, int lanes, int token_ctas, const int32_t* __restrict__ slot,
+                              int64_t tokens_total, int lanes, unsigned pad_ctas, const int32_t* __restrict__ slot,
                               const float* __restrict__ w, int K, const int32_t* __restrict__ src,
                               const int32_t* __restrict__ blk_off, int E, int block_m, T* __restrict__ d_rows,
                               int64_t num_rows, float* __restrict__ d_w) {
   using V = Vec<T, N>;
-  if (static_cast<int>(blockIdx.x) >= token_ctas) {
+  if (blockIdx.x < pad_ctas) {
     zero_padding<N * sizeof(T)>(src, blk_off, E, block_m, reinterpret_cast<char*>(d_rows), num_rows,
-                                static_cast<int64_t>(H) * sizeof(T), blockIdx.x - token_ctas);
+                                static_cast<int64_t>(H) * sizeof(T), blockIdx.x);
     return;
   }
   __shared__ TokenRows s;
-  __shared__ float s_dot[kThreads / 32][KT];
-  const int tokens = kThreads / lanes;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  __shared__ float s_dot[kBackThreads / 32][KT];
+  const int tokens = kBackThreads / lanes;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x - pad_ctas) * tokens;
   load_token_rows(s, slot, w, t0, tokens, tokens_total, K, num_rows);
   const int sub = threadIdx.x / lanes, l = threadIdx.x % lanes;
   const int64_t t = t0 + sub;
@@ -213,13 +212,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Threads of a token's group: its accesses rounded up to a power of two, 8 to 256, then halved (not below
-// 64) while that leaves fewer lanes idle in the last step: 448 accesses take 7 steps of 64, not 2 of 256.
-int group_lanes(int64_t accesses) {
+// Threads of a token's group: its accesses rounded up to a power of two, 8 to the CTA's threads.
+int group_lanes(int64_t accesses, int threads) {
   int l = 8;
-  while (l < kThreads && l < accesses) l *= 2;
-  auto idle = [&](int w) { return (accesses + w - 1) / w * w - accesses; };
-  while (l > 64 && idle(l / 2) < idle(l)) l /= 2;
+  while (l < threads && l < accesses) l *= 2;
   return l;
 }
 
@@ -243,13 +239,13 @@ cudaError_t launch_permute(const RowsArgs& a, const void* x, int64_t x_stride, v
   const int es = dtype_size(a.dtype);
   const int64_t pitch = static_cast<int64_t>(a.H) * es, x_pitch = x_stride * es;
   const int B = access_bytes(bits_of(x) | bits_of(rows) | pitch | x_pitch);
-  const int lanes = group_lanes(pitch / B);
+  const int lanes = group_lanes(pitch / B, kThreads);
   const int64_t ctas = (a.T + kThreads / lanes - 1) / (kThreads / lanes);
-  const int64_t grid = ctas + (a.num_rows + kPadRows - 1) / kPadRows;
+  const int64_t pad = (a.num_rows + kPadRows - 1) / kPadRows, grid = pad + ctas;
   if (grid == 0) return cudaSuccess;
   auto go = [&](auto b) {
     permute_kernel<decltype(b)::value><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(
-        static_cast<const char*>(x), x_pitch, a.T, pitch, lanes, static_cast<int>(ctas), a.slot, a.K, a.src, a.blk_off,
+        static_cast<const char*>(x), x_pitch, a.T, pitch, lanes, static_cast<unsigned>(pad), a.slot, a.K, a.src, a.blk_off,
         a.E, a.block_m, static_cast<char*>(rows), a.num_rows);
     return cudaGetLastError();
   };
@@ -270,7 +266,7 @@ cudaError_t launch_unpermute(const RowsArgs& a, const void* rows, const float* w
     using T = decltype(tag);
     return with_access<T>(B, [&](auto n) {
       constexpr int N = decltype(n)::value;
-      const int lanes = group_lanes(a.H / N);
+      const int lanes = group_lanes(a.H / N, kThreads);
       const int64_t ctas = (a.T + kThreads / lanes - 1) / (kThreads / lanes);
       unpermute_kernel<T, N><<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(
           static_cast<const T*>(rows), a.num_rows, a.H, a.T, lanes, a.slot, w, a.K, static_cast<T*>(out), out_stride);
@@ -288,14 +284,14 @@ cudaError_t launch_unpermute_backward(const RowsArgs& a, const void* d_out, int6
     using T = decltype(tag);
     return with_access<T>(B, [&](auto n) {
       constexpr int N = decltype(n)::value;
-      const int lanes = group_lanes(a.H / N);
-      const int64_t ctas = (a.T + kThreads / lanes - 1) / (kThreads / lanes);
-      const int64_t grid = ctas + (a.num_rows + kPadRows - 1) / kPadRows;
+      const int lanes = group_lanes(a.H / N, kBackThreads);
+      const int64_t ctas = (a.T + kBackThreads / lanes - 1) / (kBackThreads / lanes);
+      const int64_t pad = (a.num_rows + kPadRows - 1) / kPadRows, grid = pad + ctas;
       if (grid == 0) return cudaSuccess;
       auto go = [&](auto kt) {
-        unpermute_backward_kernel<T, N, decltype(kt)::value><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(
+        unpermute_backward_kernel<T, N, decltype(kt)::value><<<static_cast<unsigned>(grid), kBackThreads, 0, s>>>(
             static_cast<const T*>(d_out), d_stride, static_cast<const T*>(rows), a.H, a.T, lanes,
-            static_cast<int>(ctas), a.slot, w, a.K, a.src, a.blk_off, a.E, a.block_m, static_cast<T*>(d_rows),
+            static_cast<unsigned>(pad), a.slot, w, a.K, a.src, a.blk_off, a.E, a.block_m, static_cast<T*>(d_rows),
             a.num_rows, d_w);
         return cudaGetLastError();
       };
