@@ -16,8 +16,7 @@ namespace mm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;            // groups of 16 elements a thread has in flight
-constexpr int kOutBatch = 2;         // coming back from 4 bits
+constexpr int kBatch = 2;            // groups of 16 elements a thread has in flight
 
 // The position of a thread in [rows][groups of 16], stepped by a fixed number of groups.
 struct Walk {
@@ -112,16 +111,16 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads, total = R * groups;
   Walk at(i, groups);
   while (i < total) {
-    uint2 w[kOutBatch];
-    uint32_t b[kOutBatch];
+    uint2 w[kBatch];
+    uint32_t b[kBatch];
 #pragma unroll
-    for (int u = 0; u < kOutBatch; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
       const int64_t j = i + u * step;
       w[u] = j < total ? __ldg(codes + j) : make_uint2(0, 0);
       b[u] = j < total ? __ldg(sf + (j >> 1)) : 0;
     }
 #pragma unroll
-    for (int u = 0; u < kOutBatch; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
       if (i < total) {
         const float s = ue8m0_value(b[u]);
         float f[16];
@@ -175,6 +174,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// Per SM: as many CTAs as one pass over the data takes. 65536x4096 bf16, into 4 bits and back: 97 and 98 us (6.7 TB/s),
+// with 8 CTAs an SM that step through the data 104 and 114.
+constexpr int kOnePass = 1 << 20;
+
 int blocks_for(int64_t threads, int per_sm) {
   int64_t b = (threads + kThreads - 1) / kThreads;
   const int64_t cap = static_cast<int64_t>(dev_info().sms) * per_sm;
@@ -190,7 +193,7 @@ bool wide(const void* p, int64_t pitch_bytes, int C) {
 
 cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t s) {
   const int groups = a.chunks ? mx_chunks(a.C) * 8 : (a.C + 31) / 32 * 2;
-  const int grid = blocks_for((a.R * groups + kBatch - 1) / kBatch, 8);
+  const int grid = blocks_for((a.R * groups + kBatch - 1) / kBatch, kOnePass);
   const int64_t step = static_cast<int64_t>(grid) * kThreads;
   const int d_row = static_cast<int>(step / groups), d_group = static_cast<int>(step % groups);
   return with_dtype(a.dtype, [&](auto tag) {
@@ -210,7 +213,7 @@ cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t s) {
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* sf, int64_t R, int C, int dtype, void* out,
                                  int64_t out_stride, cudaStream_t s) {
   const int groups = (C + 31) / 32 * 2;
-  const int grid = blocks_for((R * groups + kOutBatch - 1) / kOutBatch, 8);
+  const int grid = blocks_for((R * groups + kBatch - 1) / kBatch, kOnePass);
   const int64_t step = static_cast<int64_t>(grid) * kThreads;
   const int d_row = static_cast<int>(step / groups), d_group = static_cast<int>(step % groups);
   const uint2* c = reinterpret_cast<const uint2*>(codes);
