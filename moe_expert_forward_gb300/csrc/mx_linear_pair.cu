@@ -1,20 +1,28 @@
-// The 4-bit product (mx_linear.cu) on CTA pairs, for many rows: a task is two
-// 128-row blocks of one expert times 256 weight rows, 4-bit codes streamed in
-// stages of 256 elements, M = 256, N = 256 tcgen05 cta_group::2 MMAs.
+// The dense 4-bit product (mx_linear.cu) on CTA pairs, for many rows: a task is two
+// 128-row blocks times 256 weight rows, 4-bit codes streamed in stages of 256
+// elements, M = 256, N = 256 tcgen05 cta_group::2 MMAs.  (Routed rows stay with the
+// single-CTA kernel: an expert's last odd block would leave half a pair idle, and
+// from 256 to 2048 rows an expert pairs measured between 9 % slower and 3 % faster.)
 //
 // Why pairs: what bounds the product is how fast the L2 feeds the SMs, not the
 // tensor cores. CTA r holds row block r and weight rows [128 r, 128 r + 128) of
 // the tile, so an SM fetches 35 KB a stage where a 128 x 256 tile of its own
 // takes 51 KB, and six stages fit instead of four.
 //
-// Every copy of both CTAs completes on the leader's stage barrier, so its MMA
-// thread waits once a stage, then issues the scale copies (both CTAs' chunks, 6
-// instructions) and 4 MMAs: 513 cycles a stage measured alone, the MMAs' own
-// time. (A relay of per-CTA barriers through cluster-scope arrivals instead took
-// 1650 cycles a stage.)
+// Every copy of both CTAs completes on the leader's stage barrier. One leader
+// thread waits for it and copies the scales of both CTAs into tensor memory (6
+// instructions), another waits for that and issues 4 MMAs: with the copies, the
+// commits and one wait in one thread a stage measured 724 cycles alone, apart 513,
+// the MMAs' own time. The epilogue packs 16-bit results into registers and hands
+// the accumulator back before it stores them.
 //
-// Warps per CTA: 8 epilogue, 1 MMA (the leader's issues; both allocate TMEM), 6
-// producers (one a stage). Every wait is bounded.
+// Measured: 8192 x 7168 x 4096 in 85 us, 5.7 PFLOP/s, 830 cycles a stage; with the
+// copies but no MMAs 72 us, with MMAs at their own rate it would be 52. (A relay of
+// per-CTA barriers through cluster-scope arrivals took 1650 cycles a stage, scales
+// stored to tensor memory by warps 1725, one thread for copies and MMAs 1190.)
+//
+// Warps per CTA: 8 epilogue, 1 MMA and 1 scale-copy (the leader's issue; both
+// CTAs' MMA warps allocate TMEM), 6 producers (one a stage). Every wait is bounded.
 #include "cluster.cuh"
 #include "mx_linear.cuh"
 
@@ -42,10 +50,9 @@ struct Smem {
   static constexpr int bars = sfb + kStages * 2 * kMxSfBytes;
   static constexpr int nbars = 3 * kStages + 4;  // full, ready, empty, tfull, tempty, 2 drains
   static constexpr int exit = bars + nbars * 8 + 16;   // per stage: phases the leader armed, phases the peer loaded
-  static constexpr int meta = exit + 2 * kStages * 4;  // pairs before each expert [E + 1], cnt [E], first blocks [E]
-  static int total(int E) { return meta + (3 * E + 1) * 4 + 1024; }
+  static constexpr int total = exit + 2 * kStages * 4 + 1024;
 };
-static_assert(Smem::meta + (3 * kMaxE + 1) * 4 + 1024 <= 232448, "shared memory");
+static_assert(Smem::total <= 232448, "shared memory");
 
 enum : int {
   kSiteEmpty = 171, kSiteFull = 172, kSiteReady = 173, kSiteTmemEmpty = 174, kSiteTmemFull = 175,
@@ -96,25 +103,14 @@ __device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d, uint64_t adesc, uin
 // This CTA's share of pair task i: its row block and the rows of it that exist (0: a ghost, which
 // computes the pair's first block again and stores nothing).
 struct Task {
-  int b, n, e, valid;
+  int b, n, valid;
 };
-__device__ __forceinline__ Task task_at(int i, uint32_t rank, const MxArgs& a, const int* s_pair, const int* s_cnt,
-                                        const int* s_first) {
+__device__ __forceinline__ Task task_at(int i, uint32_t rank, const MxArgs& a) {
   Task t;
   const int pb = i / a.NT;
   t.n = i - pb * a.NT;
-  int rows_left;
-  if (a.blk_off) {
-    t.e = last_not_above(s_pair, a.E, pb);
-    const int in = 2 * (pb - s_pair[t.e]);       // the pair's first block inside the expert
-    t.b = s_first[t.e] + in;
-    rows_left = s_cnt[t.e] - in * kMxRows;
-  } else {
-    t.e = 0;
-    t.b = 2 * pb;
-    rows_left = a.rows - t.b * kMxRows;
-  }
-  t.valid = min(kMxRows, rows_left - static_cast<int>(rank) * kMxRows);
+  t.b = 2 * pb;
+  t.valid = min(kMxRows, a.rows - (t.b + static_cast<int>(rank)) * kMxRows);
   if (t.valid > 0) t.b += static_cast<int>(rank);
   else t.valid = 0;
   return t;
@@ -135,9 +131,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_armed = reinterpret_cast<int*>(smem + Smem::exit);
   int* s_peer = s_armed + kStages;
-  int* s_pair = reinterpret_cast<int*>(smem + Smem::meta);
-  int* s_cnt = s_pair + args.E + 1;
-  int* s_first = s_cnt + args.E;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -160,35 +153,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc_pair(s_tmem, kTmemCols);
-  if (args.blk_off) {
-    for (int i = threadIdx.x; i < args.E; i += kThreads) {
-      s_cnt[i] = args.cnt[i];
-      s_first[i] = args.blk_off[i];
-    }
-    if (warp == 0) {                             // pairs before each expert: a scan by one warp
-      int before = 0;
-      for (int e0 = 0; e0 < args.E; e0 += 32) {
-        const int e = e0 + lane;
-        int incl = e < args.E ? (args.blk_off[e + 1] - args.blk_off[e] + 1) / 2 : 0;
-        const int own = incl;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        if (e < args.E) s_pair[e] = before + incl - own;
-        before += __shfl_sync(0xffffffffu, incl, 31);
-      }
-      if (lane == 0) s_pair[args.E] = before;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   cluster_barrier();                             // both CTAs' barriers exist before anything targets them
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const int pairs = args.blk_off ? s_pair[args.E] : (args.nblk + 1) / 2;
-  const int ntasks = pairs * args.NT;
+  const int ntasks = (args.nblk + 1) / 2 * args.NT;
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
   if (warp >= kProducer0) {
@@ -205,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int loaded = 0;                            // phases of this stage loaded
       bool waited = args.wait_prior == 0;
       for (int i = first; i < ntasks && !*s_abort; i += stride) {
-        const Task t = task_at(i, rank, args, s_pair, s_cnt, s_first);
+        const Task t = task_at(i, rank, args);
         int ks = ((p - step) % kStages + kStages) % kStages;
         for (; ks < args.KS; ks += kStages) {
           const uint32_t phase = ((step + ks) / kStages) & 1;
@@ -213,8 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&full[p], 2 * kCtaBytes);
           ++loaded;
           tma_load_2d_pair(wt, &maps.w, bar, ks * kMxStageBytes,
-                           t.e * args.N + t.n * kTileN + static_cast<int>(rank) * 128, pol);
-          tma_load_3d_pair(sb, &maps.w_sf, bar, 0, 4 * ks, t.e * args.NB + 2 * t.n, pol);
+                           t.n * kTileN + static_cast<int>(rank) * 128, pol);
+          tma_load_3d_pair(sb, &maps.w_sf, bar, 0, 4 * ks, 2 * t.n, pol);
           if (!waited) {                         // the weights do not depend on the kernel before; the rows do
             pdl_wait();
             waited = true;
@@ -322,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
     int it = 0;
     for (int i = first; i < ntasks; i += stride, ++it) {
-      const Task t = task_at(i, rank, args, s_pair, s_cnt, s_first);
+      const Task t = task_at(i, rank, args);
       if (!mbar_wait(tfull, it & 1, st, s_abort, kSiteTmemFull)) break;
       tc_fence_after();
       const int n = t.n * kTileN + c0;
@@ -361,32 +331,31 @@ cudaError_t launch_mx_product_pair(const MxProductArgs& p, cudaStream_t s) {
     using T = decltype(tag);
     const MxArgs a = mx_args(p, sizeof(T), kTileN);
     Maps maps;
-    if (mx_codes_map(&maps.w, p.w, static_cast<int64_t>(p.E) * p.N, p.C, 128) != CUDA_SUCCESS ||
+    if (mx_codes_map(&maps.w, p.w, p.N, p.C, 128) != CUDA_SUCCESS ||
         mx_codes_map(&maps.a, p.codes, p.rows, p.C, kMxRows) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
-    // a stage's two chunks of two weight row blocks (past the last one: the next expert's, or zeros, in columns
-    // that are not stored), and of one activation block
+    // a stage's two chunks of two weight row blocks (past the last one: zeros, in columns that are not stored), and
+    // of one activation block
     auto scales_map = [&](CUtensorMap* m, const uint8_t* sf, int64_t row_blocks, uint32_t box) {
       const uint64_t dims[3] = {256, static_cast<uint64_t>(a.KB) * 2, static_cast<uint64_t>(row_blocks)};
       const uint64_t strides[2] = {256, static_cast<uint64_t>(a.KB) * kSFChunk};
       const uint32_t boxes[3] = {256, 4, box};
       return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, sf, dims, strides, boxes, CU_TENSOR_MAP_SWIZZLE_NONE);
     };
-    if (scales_map(&maps.w_sf, p.w_sf, static_cast<int64_t>(p.E) * a.NB, 2) != CUDA_SUCCESS ||
+    if (scales_map(&maps.w_sf, p.w_sf, a.NB, 2) != CUDA_SUCCESS ||
         scales_map(&maps.sf, p.sf, a.nblk, 1) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
     auto kernel = mx_product_pair_kernel<T>;
     const void* fn = reinterpret_cast<const void*>(kernel);
-    if (cudaError_t e = configure_kernel(fn, 0, Smem::total(kMaxE))) return e;
+    if (cudaError_t e = configure_kernel(fn, 0, Smem::total)) return e;
     int clusters = 0;
-    if (cudaError_t e = max_pair_clusters(fn, kThreads, Smem::total(kMaxE), &clusters)) return e;
+    if (cudaError_t e = max_pair_clusters(fn, kThreads, Smem::total, &clusters)) return e;
     if (clusters < 1) return cudaErrorInvalidConfiguration;
-    // a routed pool of nblk blocks has at most as many pairs as blocks
-    const int64_t tasks = (p.blk_off ? static_cast<int64_t>(a.nblk) : (a.nblk + 1) / 2) * a.NT;
+    const int64_t tasks = static_cast<int64_t>((a.nblk + 1) / 2) * a.NT;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * static_cast<unsigned>(tasks < clusters ? tasks : clusters));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Smem::total(p.blk_off ? p.E : 0);
+    cfg.dynamicSmemBytes = Smem::total;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
