@@ -517,10 +517,11 @@ int mm_moe_mx_prepare(const void* sf, int E, int N, int C, void* sfp, void* stre
  *              cnt[e] rows are written; other rows of out are left as they are.
  *   out        [rows, N], out_stride elements between rows
  *   status     device int32[4], zeroed by the caller: a wait past timeout_ms (0: 2000)
- *              leaves MM_MOE_ERR_TIMEOUT there and out undefined */
+ *              leaves MM_MOE_ERR_TIMEOUT there and out undefined
+ *   debug_flags  0; bit 0 leaves one stage of each CTA unloaded, so that its wait runs out */
 int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, const void* w, const void* w_sfp, int E,
                       int N, const int32_t* cnt, const int32_t* blk_off, int dtype, void* out, int64_t out_stride,
-                      int32_t* status, unsigned timeout_ms, void* stream);
+                      int32_t* status, unsigned timeout_ms, int debug_flags, void* stream);
 
 /* mm_moe_mx_quantize into a workspace and mm_moe_mx_product from it, with the
  * product's setup and first weight loads overlapping the quantiser.

@@ -114,7 +114,7 @@ def lib() -> ctypes.CDLL:
             "mm_moe_mx_quantize": (_I, [_P, _I, _I64, _I64, _I, _P, _I, _I64, _P, _P, _I, _P]),
             "mm_moe_mx_dequantize": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _P]),
             "mm_moe_mx_prepare": (_I, [_P, _I, _I, _I, _P, _P]),
-            "mm_moe_mx_product": (_I, [_P, _P, _I64, _I, _P, _P, _I, _I, _P, _P, _I, _P, _I64, _P, ctypes.c_uint, _P]),
+            "mm_moe_mx_product": (_I, [_P, _P, _I64, _I, _P, _P, _I, _I, _P, _P, _I, _P, _I64, _P, ctypes.c_uint, _I, _P]),
             "mm_moe_mx_linear_workspace": (_I, [_I, _I, _I, _I, _I64, ctypes.POINTER(_SZ)]),
             "mm_moe_mx_linear": (_I, [_P, _I, _I64, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _I64, _P, _I64, _P, _SZ,
                                       ctypes.c_uint, _P]),
@@ -441,9 +441,9 @@ def mm_moe_mx_prepare(sf, E, N, C, sfp, stream) -> int:
 
 
 def mm_moe_mx_product(codes, sf, rows, C, w, w_sfp, E, N, cnt, blk_off, dtype, out, out_stride, status, timeout_ms,
-                      stream) -> int:
+                      debug_flags, stream) -> int:
     return lib().mm_moe_mx_product(codes, sf, rows, C, w, w_sfp, E, N, cnt, blk_off, dtype, out, out_stride, status,
-                                   timeout_ms, stream)
+                                   timeout_ms, debug_flags, stream)
 
 
 def mm_moe_mx_linear_workspace(T, C, N, K, num_rows) -> int:

@@ -201,7 +201,7 @@ int mm_moe_mx_prepare(const void* sf, int E, int N, int C, void* sfp, void* stre
 
 int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, const void* w, const void* w_sfp, int E,
                       int N, const int32_t* cnt, const int32_t* blk_off, int dtype, void* out, int64_t out_stride,
-                      int32_t* status, unsigned timeout_ms, void* stream) {
+                      int32_t* status, unsigned timeout_ms, int debug_flags, void* stream) {
   if (!cnt != !blk_off) return MM_MOE_ERR_INVALID_ARG;
   if (int r = check_product(rows, C, w, w_sfp, E, N, blk_off != nullptr, dtype, out, out_stride)) return r;
   if (rows == 0) return MM_MOE_OK;
@@ -210,7 +210,7 @@ int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, co
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   const MxProductArgs a{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(sf), rows, C,
                         static_cast<const uint8_t*>(w), static_cast<const uint8_t*>(w_sfp), E, N, cnt, blk_off, dtype,
-                        out, out_stride, status, timeout_ns(timeout_ms), false};
+                        out, out_stride, status, timeout_ns(timeout_ms), false, (debug_flags & 1) != 0};
   return done(launch_mx_product(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -248,7 +248,7 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
   const MxQuantArgs q{x, dtype, row_stride, T, C, ws + L.codes, ws + L.sf, 1, slot, K, num_rows, status};
   const MxProductArgs p{ws + L.codes, ws + L.sf, num_rows, C, static_cast<const uint8_t*>(w),
                         static_cast<const uint8_t*>(w_sfp), E, N, cnt, blk_off, dtype, out, out_stride, status,
-                        timeout_ns(timeout_ms), true};
+                        timeout_ns(timeout_ms), true, false};
   if (few) return done(launch_mx_few(q, p, s));
   cudaError_t e = launch_mx_quantize(q, s);
   if (e != cudaSuccess) return done(e);

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
         int ks = ((p - step) % S + S) % S;
         for (; ks < nks; ks += S) {
           const uint32_t phase = ((step + ks) / S) & 1;
+          if (args.unreachable && i + stride >= ntasks && ks == nks - 1) break;
           if (!mbar_wait(&empty[p], phase ^ 1, st, s_abort, kSiteEmpty)) break;
           mbar_arrive_expect_tx(&full[p], bytes);
           armed = true;

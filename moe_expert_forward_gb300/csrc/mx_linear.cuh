@@ -26,6 +26,7 @@ struct MxArgs {
   int64_t out_pitch;         // bytes
   int wide;                  // out rows and base are 32-byte aligned
   int wait_prior;            // launched programmatically: activations come from the kernel before
+  int unreachable;           // leave the last stage of the CTA's last task out
   int* status;
   uint64_t timeout_ns;
 };
@@ -124,6 +125,7 @@ inline MxArgs mx_args(const MxProductArgs& p, int elem, int tile_n) {
   a.out_pitch = p.out_stride * static_cast<int64_t>(elem);
   a.wide = (reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(a.out_pitch)) % 32 == 0;
   a.wait_prior = p.after_quantize;
+  a.unreachable = p.unreachable;
   a.status = p.status; a.timeout_ns = p.timeout_ns;
   return a;
 }

@@ -55,6 +55,7 @@ struct MxProductArgs {
   int32_t* status;
   uint64_t timeout_ns;
   bool after_quantize;       // launched programmatically behind the quantiser
+  bool unreachable;          // the last stage of each CTA's last task is never loaded (a test of the bounded waits)
 };
 cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t s);
 // on CTA pairs: two 128-row blocks a task

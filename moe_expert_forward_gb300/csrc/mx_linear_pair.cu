@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ks = ((p - step) % kStages + kStages) % kStages;
         for (; ks < args.KS; ks += kStages) {
           const uint32_t phase = ((step + ks) / kStages) & 1;
+          if (args.unreachable && i + stride >= ntasks && ks == args.KS - 1) break;
           if (!mbar_wait(&empty[p], phase ^ 1, st, s_abort, kSiteEmpty)) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[p], 2 * kCtaBytes);
           ++loaded;

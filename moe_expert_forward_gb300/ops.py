@@ -348,7 +348,7 @@ def mx_product(codes, sf, weights: MxWeights, routing: Optional[Routing] = None,
         status = torch.zeros(4, dtype=torch.int32, device=codes.device)
     st = _whole(status, "mx_product", "status", (4,), torch.int32)
     _check(lib().mm_moe_mx_product(cp, sp, rows, weights.C, weights.codes.data_ptr(), weights.sfp.data_ptr(), weights.E,
-                                   weights.N, cnt, blk, _DTYPES[dtype], out.data_ptr(), _pitch(out), st, 0,
+                                   weights.N, cnt, blk, _DTYPES[dtype], out.data_ptr(), _pitch(out), st, 0, 0,
                                    _stream(stream)), "mm_moe_mx_product")
     return out
 

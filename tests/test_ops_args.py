@@ -83,7 +83,7 @@ def test_quantise(M):
 
 def test_product(M):
     def p(codes=A, sf=A, rows=128, C=64, w=A, w_sf=A, E=1, N=8, cnt=None, blk=None, dtype=1, out=A, stride=8, status=A):
-        return M.mm_moe_mx_product(codes, sf, rows, C, w, w_sf, E, N, cnt, blk, dtype, out, stride, status, 0, None)
+        return M.mm_moe_mx_product(codes, sf, rows, C, w, w_sf, E, N, cnt, blk, dtype, out, stride, status, 0, 0, None)
     for kw in (dict(codes=None), dict(codes=A + 8), dict(sf=None), dict(rows=-1), dict(C=48), dict(C=0), dict(w=None),
                dict(w=A + 8), dict(w_sf=None), dict(E=2), dict(N=0), dict(cnt=A), dict(blk=A), dict(dtype=4),
                dict(out=None), dict(out=A + 1), dict(stride=7), dict(status=None), dict(rows=100, cnt=A, blk=A)):
