@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
         continue;
       }
       const int n = t.n * BN + c0;
-      T* dst = reinterpret_cast<T*>(args.out + (static_cast<int64_t>(t.b) * kMxRows + row) * args.out_pitch) + n;
-      store_accumulator<T, kCols>(src, row < t.valid ? dst : nullptr, args.N - n, args.wide != 0, [&] {
+      char* dst = args.out + (static_cast<int64_t>(t.b) * kMxRows + quad * 32) * args.out_pitch + n * sizeof(T);
+      store_accumulator<T, kCols>(src, dst, args.out_pitch, t.valid - quad * 32, args.N - n, args.wide != 0, lane, [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[buf]);

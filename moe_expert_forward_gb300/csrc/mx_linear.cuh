@@ -60,33 +60,60 @@ __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One row's accumulator columns [col, col + kCols) of TMEM, the first `cols` of them stored at p (p null: none).
-// `release` is called as soon as the accumulator has been read: 16-bit results are packed into registers first
-// and stored after it, fp32 ones are stored 32 columns at a time and it follows the last read.
+// Exchanges 32-byte pieces among each 4 lanes: lane j's piece i becomes piece j of what lane i held.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[32], int lane) {
+#pragma unroll
+  for (int step = 1; step <= 2; step *= 2) {
+    const bool up = (lane & step) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & step) continue;                    // pieces i and i + step change places with lane ^ step
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t& lo = w[8 * i + c];
+        uint32_t& hi = w[8 * (i + step) + c];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, step);
+        if (up) lo = got; else hi = got;
+      }
+    }
+  }
+}
+
+// A warp's 32 rows of accumulator columns [col, col + kCols) of TMEM, lane = row, stored from `out` on (row 0, first
+// column) `pitch` bytes a row: the first `rows` rows and the first `cols` columns. `release` is called as soon as the
+// accumulator has been read: 16-bit results are packed into registers first and stored after it, fp32 ones are
+// stored 32 columns at a time and it follows the last read. Where rows are aligned (wide), 16-bit results change
+// lanes so that an instruction stores whole 128-byte lines of 8 rows instead of 32 bytes of 32.
 template <typename T, int kCols, typename F>
-__device__ __forceinline__ void store_accumulator(uint32_t col, T* p, int cols, bool wide, F release) {
+__device__ __forceinline__ void store_accumulator(uint32_t col, char* out, int64_t pitch, int rows, int cols, bool wide,
+                                                  int lane, F release) {
+  T* p = reinterpret_cast<T*>(out + lane * pitch);
   if constexpr (sizeof(T) == 2) {
-    uint32_t w[kCols / 2];
+    uint32_t w[kCols / 64][32];
 #pragma unroll
     for (int c = 0; c < kCols; c += 32) {
       uint32_t v[32];
       tmem_ld_32x32b_x32(col + c, v);
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[c / 2 + i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < 16; ++i) w[c / 64][c % 64 / 2 + i] = pack2<T>(v[2 * i], v[2 * i + 1]);
     }
     release();
-    if (!p) return;
 #pragma unroll
-    for (int c = 0; c < kCols; c += 16) {
-      if (wide && cols >= c + 16) {
-        st_global_v8(reinterpret_cast<float*>(p + c), w + c / 2);
-      } else {
+    for (int h = 0; h < kCols / 64; ++h) {
+      if (wide && cols >= 64 * (h + 1)) {
+        transpose4(w[h], lane);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const Vec<T, 2> h = *reinterpret_cast<const Vec<T, 2>*>(&w[c / 2 + i]);
-          if (c + 2 * i < cols) p[c + 2 * i] = h.v[0];
-          if (c + 2 * i + 1 < cols) p[c + 2 * i + 1] = h.v[1];
+        for (int i = 0; i < 4; ++i) {
+          const int r = (lane & ~3) + i;
+          if (r < rows) st_global_v8(reinterpret_cast<float*>(out + r * pitch + h * 128 + (lane & 3) * 32), w[h] + 8 * i);
+        }
+      } else if (lane < rows) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const Vec<T, 2> e = *reinterpret_cast<const Vec<T, 2>*>(&w[h][i]);
+          if (64 * h + 2 * i < cols) p[64 * h + 2 * i] = e.v[0];
+          if (64 * h + 2 * i + 1 < cols) p[64 * h + 2 * i + 1] = e.v[1];
         }
       }
     }
@@ -97,7 +124,7 @@ __device__ __forceinline__ void store_accumulator(uint32_t col, T* p, int cols, 
       tmem_ld_32x32b_x32(col + c, v);
       tmem_ld_wait();
       if (c + 32 == kCols) release();
-      if (!p) continue;
+      if (lane >= rows) continue;
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
         if (wide && cols >= c + i + 8) {

@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ epilogue
     constexpr int kCols = kTileN / 2;            // columns of one warp
     const int c0 = (warp >> 2) * kCols;
-    const int row = (warp & 3) * 32 + lane;
     const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
     int it = 0;
     for (int i = first; i < ntasks; i += stride, ++it) {
@@ -297,8 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait(tfull, it & 1, st, s_abort, kSiteTmemFull)) break;
       tc_fence_after();
       const int n = t.n * kTileN + c0;
-      T* dst = reinterpret_cast<T*>(args.out + (static_cast<int64_t>(t.b) * kMxRows + row) * args.out_pitch) + n;
-      store_accumulator<T, kCols>(src, row < t.valid ? dst : nullptr, args.N - n, args.wide != 0, [&] {
+      const int row0 = (warp & 3) * 32;
+      char* dst = args.out + (static_cast<int64_t>(t.b) * kMxRows + row0) * args.out_pitch + n * sizeof(T);
+      store_accumulator<T, kCols>(src, dst, args.out_pitch, t.valid - row0, args.N - n, args.wide != 0, lane, [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(map_shared(tempty, 0));

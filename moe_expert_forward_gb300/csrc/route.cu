@@ -48,10 +48,13 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 template <int G>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  if constexpr (G == 32) return __reduce_max_sync(kAll, v);
+  if constexpr (G == 32) {
+    return __reduce_max_sync(kAll, v);
+  } else {
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+    for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+  }
 }
 template <int G>
 __device__ __forceinline__ uint32_t group_min(uint32_t v) { return ~group_max<G>(~v); }
