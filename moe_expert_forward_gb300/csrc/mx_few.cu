@@ -19,7 +19,6 @@ namespace mm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;            // steps of 1024 elements whose weights are loaded before x is there
 
 struct FewArgs {

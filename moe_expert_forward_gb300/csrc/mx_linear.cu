@@ -84,7 +84,8 @@ __device__ __forceinline__ Task task_at(int i, const MxArgs& a, const int* s_blk
 }
 
 // kSplit: a cluster takes one task, each CTA a range of its stages; the partial accumulators meet in shared memory.
-template <int BN, typename T, bool kSplit>
+// kLines: see store_accumulator.
+template <int BN, typename T, bool kSplit, bool kLines>
 __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
     mx_product_kernel(const __grid_constant__ Maps maps, const MxArgs args) {
   using C = Cfg<BN>;
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
       }
       const int n = t.n * BN + c0;
       char* dst = args.out + (static_cast<int64_t>(t.b) * kMxRows + quad * 32) * args.out_pitch + n * sizeof(T);
-      store_accumulator<T, kCols>(src, dst, args.out_pitch, t.valid - quad * 32, args.N - n, args.wide != 0, lane, [&] {
+      store_accumulator<T, kCols, kLines>(src, dst, args.out_pitch, t.valid - quad * 32, args.N - n, lane, [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[buf]);
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
         o.v[2] = from_float<T>(sum.z); o.v[3] = from_float<T>(sum.w);
         const int n = t.n * BN + c;
         T* dst = reinterpret_cast<T*>(args.out + (static_cast<int64_t>(t.b) * kMxRows + row) * args.out_pitch) + n;
-        if (args.wide && n + 4 <= args.N) {
+        if (kLines && n + 4 <= args.N) {
           *reinterpret_cast<Vec<T, 4>*>(dst) = o;
         } else {
 #pragma unroll
@@ -327,7 +328,7 @@ cudaError_t launch_impl(const MxProductArgs& p, int parts, cudaStream_t s) {
   if (mx_codes_map(&maps.w, p.w, static_cast<int64_t>(p.E) * p.N, p.C, BN) != CUDA_SUCCESS) return cudaErrorInvalidValue;
   for (int i = 0; i < 3; ++i)
     if (mx_codes_map(&maps.a[i], p.codes, p.rows, p.C, 32 << i) != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  auto kernel = mx_product_kernel<BN, T, kSplit>;
+  auto kernel = a.lines ? mx_product_kernel<BN, T, kSplit, true> : mx_product_kernel<BN, T, kSplit, false>;
   if (cudaError_t e = configure_kernel(reinterpret_cast<const void*>(kernel), 0, C::total(kMaxE))) return e;
   const int64_t tasks = static_cast<int64_t>(a.nblk) * a.NT;
   const int sms = dev_info().sms;

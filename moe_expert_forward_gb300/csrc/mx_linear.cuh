@@ -24,7 +24,7 @@ struct MxArgs {
   const int* blk_off;
   char* out;
   int64_t out_pitch;         // bytes
-  int wide;                  // out rows and base are 32-byte aligned
+  int lines;                 // out and its rows are 32-byte aligned
   int wait_prior;            // launched programmatically: activations come from the kernel before
   int unreachable;           // leave the last stage of the CTA's last task out
   int* status;
@@ -79,42 +79,98 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[32], int lane) {
   }
 }
 
+// Word i of lane j becomes word j of lane i.
+__device__ __forceinline__ void transpose32(uint32_t (&w)[32], int lane) {
+#pragma unroll
+  for (int step = 1; step <= 16; step *= 2) {
+    const bool up = (lane & step) != 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i & step) continue;
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + step], step);
+      if (up) w[i] = got; else w[i + step] = got;
+    }
+  }
+}
+
 // A warp's 32 rows of accumulator columns [col, col + kCols) of TMEM, lane = row, stored from `out` on (row 0, first
 // column) `pitch` bytes a row: the first `rows` rows and the first `cols` columns. `release` is called as soon as the
-// accumulator has been read: 16-bit results are packed into registers first and stored after it, fp32 ones are
-// stored 32 columns at a time and it follows the last read. Where rows are aligned (wide), 16-bit results change
-// lanes so that an instruction stores whole 128-byte lines of 8 rows instead of 32 bytes of 32.
-template <typename T, int kCols, typename F>
-__device__ __forceinline__ void store_accumulator(uint32_t col, char* out, int64_t pitch, int rows, int cols, bool wide,
+// accumulator has been read: with kLines 16-bit results are packed into registers first and stored after it, others are
+// stored 32 or 64 columns at a time and it follows the last read.
+//
+// kLines: `out` and its rows are 32-byte aligned. 16-bit results change lanes so that an instruction stores whole
+// 128-byte lines of 8 rows instead of 32 bytes of 32 rows (8192x7168x4096: 87 us, 90 without).
+// Otherwise the warp transposes 32 words and stores one row at a time, consecutive lanes consecutive words, as words
+// where rows are 4-byte aligned (8192x4096x4095 bf16: 309 us with a row per lane).
+template <typename T, int kCols, bool kLines, typename F>
+__device__ __forceinline__ void store_accumulator(uint32_t col, char* out, int64_t pitch, int rows, int cols,
                                                   int lane, F release) {
-  T* p = reinterpret_cast<T*>(out + lane * pitch);
-  if constexpr (sizeof(T) == 2) {
-    uint32_t w[kCols / 64][32];
+  // 64 columns as 32 words of two 16-bit elements
+  auto load64 = [&](int c, uint32_t (&w)[32]) {
 #pragma unroll
-    for (int c = 0; c < kCols; c += 32) {
+    for (int h = 0; h < 2; ++h) {
       uint32_t v[32];
-      tmem_ld_32x32b_x32(col + c, v);
+      tmem_ld_32x32b_x32(col + c + 32 * h, v);
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[c / 64][c % 64 / 2 + i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < 16; ++i) w[16 * h + i] = pack2<T>(v[2 * i], v[2 * i + 1]);
     }
+  };
+  if constexpr (sizeof(T) == 2 && kLines) {
+    uint32_t w[kCols / 64][32];
+#pragma unroll
+    for (int h = 0; h < kCols / 64; ++h) load64(64 * h, w[h]);
     release();
+    T* p = reinterpret_cast<T*>(out + lane * pitch);
 #pragma unroll
     for (int h = 0; h < kCols / 64; ++h) {
-      if (wide && cols >= 64 * (h + 1)) {
+      if (cols >= 64 * (h + 1)) {
         transpose4(w[h], lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = (lane & ~3) + i;
-          if (r < rows) st_global_v8(reinterpret_cast<float*>(out + r * pitch + h * 128 + (lane & 3) * 32), w[h] + 8 * i);
+          if (r < rows)
+            st_global_v8(reinterpret_cast<float*>(out + r * pitch + h * 128 + (lane & 3) * 32), w[h] + 8 * i);
         }
-      } else if (lane < rows) {
+      } else if (lane < rows) {                  // the last columns: 32 bytes of a row, then element by element
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const Vec<T, 2> e = *reinterpret_cast<const Vec<T, 2>*>(&w[h][i]);
-          if (64 * h + 2 * i < cols) p[64 * h + 2 * i] = e.v[0];
-          if (64 * h + 2 * i + 1 < cols) p[64 * h + 2 * i + 1] = e.v[1];
+        for (int c = 0; c < 64; c += 16) {
+          if (cols >= 64 * h + c + 16) {
+            st_global_v8(reinterpret_cast<float*>(p + 64 * h + c), w[h] + c / 2);
+          } else {
+#pragma unroll
+            for (int i = c / 2; i < c / 2 + 8; ++i) {
+              const Vec<T, 2> e = *reinterpret_cast<const Vec<T, 2>*>(&w[h][i]);
+              if (64 * h + 2 * i < cols) p[64 * h + 2 * i] = e.v[0];
+              if (64 * h + 2 * i + 1 < cols) p[64 * h + 2 * i + 1] = e.v[1];
+            }
+          }
         }
+      }
+    }
+  } else if constexpr (sizeof(T) == 2) {
+    const bool words = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(pitch)) & 3) == 0;
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 64) {
+      uint32_t w[32];
+      load64(c, w);
+      if (c + 64 == kCols) release();
+      if (cols <= c) continue;
+      transpose32(w, lane);
+      const int left = cols - c - 2 * lane;      // columns from this lane's two on
+      char* q = out + (c + 2 * lane) * 2;
+      if (words && left >= 2) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r, q += pitch)
+          if (r < rows) *reinterpret_cast<uint32_t*>(q) = w[r];
+      } else if (left >= 1) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r, q += pitch)
+          if (r < rows) {
+            const Vec<T, 2> e = *reinterpret_cast<const Vec<T, 2>*>(&w[r]);
+            reinterpret_cast<T*>(q)[0] = e.v[0];
+            if (left >= 2) reinterpret_cast<T*>(q)[1] = e.v[1];
+          }
       }
     }
   } else {
@@ -124,15 +180,19 @@ __device__ __forceinline__ void store_accumulator(uint32_t col, char* out, int64
       tmem_ld_32x32b_x32(col + c, v);
       tmem_ld_wait();
       if (c + 32 == kCols) release();
-      if (lane >= rows) continue;
+      if (kLines && cols >= c + 32) {
+        if (lane < rows) {
+          float* p = reinterpret_cast<float*>(out + lane * pitch) + c;
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        if (wide && cols >= c + i + 8) {
-          st_global_v8(reinterpret_cast<float*>(p + c + i), v + i);
-        } else {
+          for (int i = 0; i < 32; i += 8) st_global_v8(p + i, v + i);
+        }
+      } else if (cols > c) {
+        transpose32(v, lane);
+        char* q = out + (c + lane) * 4;
+        if (c + lane < cols) {
 #pragma unroll
-          for (int j = i; j < i + 8; ++j)
-            if (c + j < cols) p[c + j] = __uint_as_float(v[j]);
+          for (int r = 0; r < 32; ++r, q += pitch)
+            if (r < rows) *reinterpret_cast<uint32_t*>(q) = v[r];
         }
       }
     }
@@ -150,7 +210,7 @@ inline MxArgs mx_args(const MxProductArgs& p, int elem, int tile_n) {
   a.sf = p.sf; a.w_sf = p.w_sf; a.cnt = p.cnt; a.blk_off = p.blk_off;
   a.out = static_cast<char*>(p.out);
   a.out_pitch = p.out_stride * static_cast<int64_t>(elem);
-  a.wide = (reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(a.out_pitch)) % 32 == 0;
+  a.lines = (reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(a.out_pitch)) % 32 == 0;
   a.wait_prior = p.after_quantize;
   a.unreachable = p.unreachable;
   a.status = p.status; a.timeout_ns = p.timeout_ns;

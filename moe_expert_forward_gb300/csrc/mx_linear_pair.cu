@@ -116,7 +116,7 @@ __device__ __forceinline__ Task task_at(int i, uint32_t rank, const MxArgs& a) {
   return t;
 }
 
-template <typename T>
+template <typename T, bool kLines>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_product_pair_kernel(const __grid_constant__ Maps maps, const MxArgs args) {
   extern __shared__ uint8_t smem_raw[];
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = t.n * kTileN + c0;
       const int row0 = (warp & 3) * 32;
       char* dst = args.out + (static_cast<int64_t>(t.b) * kMxRows + row0) * args.out_pitch + n * sizeof(T);
-      store_accumulator<T, kCols>(src, dst, args.out_pitch, t.valid - row0, args.N - n, args.wide != 0, lane, [&] {
+      store_accumulator<T, kCols, kLines>(src, dst, args.out_pitch, t.valid - row0, args.N - n, lane, [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(map_shared(tempty, 0));
@@ -346,7 +346,7 @@ cudaError_t launch_mx_product_pair(const MxProductArgs& p, cudaStream_t s) {
     if (scales_map(&maps.w_sf, p.w_sf, a.NB, 2) != CUDA_SUCCESS ||
         scales_map(&maps.sf, p.sf, a.nblk, 1) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
-    auto kernel = mx_product_pair_kernel<T>;
+    auto kernel = a.lines ? mx_product_pair_kernel<T, true> : mx_product_pair_kernel<T, false>;
     const void* fn = reinterpret_cast<const void*>(kernel);
     if (cudaError_t e = configure_kernel(fn, 0, Smem::total)) return e;
     int clusters = 0;
