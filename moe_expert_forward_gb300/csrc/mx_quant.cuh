@@ -58,10 +58,24 @@ struct Group {
         clear();
       }
     } else {
-      T v[16];
+      constexpr int N = 16 / sizeof(T);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = c + i < C ? row[c + i] : from_float<T>(0.f);
-      memcpy(w, v, sizeof(v));
+      for (int h = 0; h < kWords / 4; ++h) {
+        const int n = C - (c + h * N);               // elements from here on
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (n > 0) q = load16_any(row + c + h * N, (n < N ? n : N) * static_cast<int>(sizeof(T)));
+        w[4 * h] = q.x; w[4 * h + 1] = q.y; w[4 * h + 2] = q.z; w[4 * h + 3] = q.w;
+        if (n < N) {                                 // what lies past the row
+          if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[4 * h + i] = i < n ? w[4 * h + i] : 0u;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[4 * h + i] = 2 * i + 1 < n ? w[4 * h + i] : (2 * i < n ? w[4 * h + i] & 0xFFFFu : 0u);
+          }
+        }
+      }
     }
   }
   // the largest |element| as fp32 bits; at least 0x7F800000 where one is not finite

@@ -61,14 +61,63 @@ __device__ __forceinline__ void store_once(V* p, const V& v) {
   }
 }
 
+// `bytes` (1 to 16) bytes from any address, and zeros or neighbouring bytes after them. Only 16-byte granules that
+// hold one of these bytes are read.
+__device__ __forceinline__ uint4 load16_any(const void* p, int bytes) {
+  const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+  const uint4* g = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - m);
+  const uint4 lo = __ldg(g);
+  if (m == 0) return lo;
+  uint4 hi = make_uint4(0, 0, 0, 0);
+  if (m + bytes > 16) hi = __ldg(g + 1);
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = (m & 8u) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = (m & 4u) ? w[i + 1] : w[i];
+  const uint32_t b = (m & 3u) * 8u;
+  return make_uint4(__funnelshift_r(w[0], w[1], b), __funnelshift_r(w[1], w[2], b), __funnelshift_r(w[2], w[3], b),
+                    __funnelshift_r(w[3], w[4], b));
+}
+
+// The i-th of the 16-byte granules of memory that a row of H elements at `row` touches: the elements [first, first + n)
+// it holds. Rows on no 16-byte boundary are taken by the granules of what is written, so that all stores but a row's
+// first and last are whole.
+template <typename T>
+struct Granule {
+  static constexpr int kWhole = 16 / sizeof(T);
+  int first, n;
+  __device__ __forceinline__ Granule(const T* row, int H, int i) {
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) / static_cast<int>(sizeof(T));
+    const int e = i * kWhole - off;
+    first = e < 0 ? 0 : e;
+    n = min(e + kWhole, H) - first;
+  }
+  // granules that a row touches, at most
+  __host__ __device__ static int most(int H) { return (H + 2 * kWhole - 2) / kWhole; }
+  __device__ __forceinline__ Vec<T, kWhole> load(const T* row) const {
+    const uint4 w = load16_any(row + first, n * static_cast<int>(sizeof(T)));
+    Vec<T, kWhole> v;
+    memcpy(&v, &w, 16);
+    return v;
+  }
+  __device__ __forceinline__ void store(T* row, const Vec<T, kWhole>& v) const {
+    if (n == kWhole) {
+      *reinterpret_cast<Vec<T, kWhole>*>(row + first) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWhole; ++i)
+        if (i < n) row[first + i] = v.v[i];
+    }
+  }
+};
+
 inline int dtype_size(int dtype) { return dtype == MM_MOE_DTYPE_F32 ? 4 : 2; }
 inline bool dtype_known(int dtype) { return dtype >= MM_MOE_DTYPE_F32 && dtype <= MM_MOE_DTYPE_F16; }
 
-// The widest access (32, 16, 8, 4 or 2 bytes) that every given address and row
-// pitch is a multiple of; the bits of all of them are or-ed into `bits`.
-inline int access_bytes(uint64_t bits) {
-  return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
-}
+// The widest access (32 or 16 bytes, else 0) that every given address and row pitch is a multiple of; the bits of
+// all of them are or-ed into `bits`.
+inline int access_bytes(uint64_t bits) { return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0; }
 
 // f(T{}) with the element type a dtype names
 template <typename F>
