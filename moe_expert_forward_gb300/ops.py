@@ -17,7 +17,6 @@ allocated on are the caller's to keep alive.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import NamedTuple, Optional
 
 import torch
@@ -44,36 +43,32 @@ class Routing:
 
     def __init__(self, T: int, K: int, E: int, block_m: int, rows: int, device, scratch_ints: int):
         self.T, self.K, self.E, self.block_m, self.rows = T, K, E, block_m, rows
-        self._buf = torch.empty(4 + 2 * E + 1 + T * K + rows + scratch_ints, dtype=torch.int32, device=device)
-        self._status = self._buf.data_ptr()          # addresses, for the calls
-        self._cnt = self._status + 16
-        self._blk = self._cnt + 4 * E
-        self._slot = self._blk + 4 * (E + 1)
-        self._src = self._slot + 4 * T * K
-
-    def _view(self, address: int, n: int):
-        at = (address - self._status) // 4
-        return self._buf[at:at + n]
+        self._buf = torch.empty(5 + 2 * E + T * K + rows + scratch_ints, dtype=torch.int32, device=device)
+        self._status = p = self._buf.data_ptr()      # addresses, for the calls
+        self._cnt = p + 16
+        self._blk = p + 16 + 4 * E
+        self._slot = p = p + 20 + 8 * E
+        self._src = p + 4 * T * K
 
     @property
     def status(self):
-        return self._view(self._status, 4)
+        return self._buf.as_strided((4,), (1,), 0)
 
     @property
     def cnt(self):
-        return self._view(self._cnt, self.E)
+        return self._buf.as_strided((self.E,), (1,), 4)
 
     @property
     def blk_off(self):
-        return self._view(self._blk, self.E + 1)
+        return self._buf.as_strided((self.E + 1,), (1,), 4 + self.E)
 
     @property
     def slot(self):
-        return self._view(self._slot, self.T * self.K).view(self.T, self.K)
+        return self._buf.as_strided((self.T, self.K), (self.K, 1), 5 + 2 * self.E)
 
     @property
     def src(self):
-        return self._view(self._src, self.rows)
+        return self._buf.as_strided((self.rows,), (1,), 5 + 2 * self.E + self.T * self.K)
 
 
 class MxWeights(NamedTuple):
@@ -177,6 +172,13 @@ def pool_rows(T: int, K: int, E: int, block_m: int) -> int:
     return -(-(pairs + min(pairs, E) * (block_m - 1)) // block_m) * block_m
 
 
+SORT_ONE_LAUNCH = 3 << 16     # pairs up to which mm_moe_sort needs no scratch (mm_moe_sort_scratch_size)
+
+
+def _sort_scratch(T: int, K: int, E: int) -> int:
+    return 0 if T * K <= SORT_ONE_LAUNCH else 4 * 256 * E
+
+
 def sort_tokens(topk_idx, E: int, block_m: int = 16, stream=None) -> Routing:
     """The routing of topk_idx (int32 [T, K], -1 masked): pairs in ascending order
     inside each expert, every expert's rows padded to whole blocks of block_m (16 to
@@ -185,13 +187,12 @@ def sort_tokens(topk_idx, E: int, block_m: int = 16, stream=None) -> Routing:
         _bad("sort_tokens", f"topk_idx must be [T, K], got {tuple(topk_idx.shape)}")
     T, K = topk_idx.shape
     ip = _whole(topk_idx, "sort_tokens", "topk_idx", (T, K), torch.int32)
-    n = ctypes.c_size_t(0)
-    _check(lib().mm_moe_sort_scratch_size(T, K, E, ctypes.byref(n)), "mm_moe_sort_scratch_size")
-    if block_m < 1:
-        _bad("sort_tokens", f"block_m must be 16 to 256, got {block_m}")
+    if block_m < 1 or E < 1:
+        _bad("sort_tokens", f"block_m must be 16 to 256 and E at least 1, got {block_m} and {E}")
+    scratch = _sort_scratch(T, K, E)
     rows = pool_rows(T, K, E, block_m)
-    r = Routing(T, K, E, block_m, rows, topk_idx.device, n.value // 4)
-    _check(lib().mm_moe_sort(ip, T, K, E, block_m, r._cnt, r._blk, r._slot, r._src, rows, r._src + 4 * rows, n.value,
+    r = Routing(T, K, E, block_m, rows, topk_idx.device, scratch // 4)
+    _check(lib().mm_moe_sort(ip, T, K, E, block_m, r._cnt, r._blk, r._slot, r._src, rows, r._src + 4 * rows, scratch,
                              r._status, _stream(stream)), "mm_moe_sort")
     return r
 

@@ -114,6 +114,9 @@ def test_binding_sizes_agree_with_the_library(M):
     from moe_expert_forward_gb300 import ops
     for rows, C in ((1, 32), (129, 96), (1000, 4096)):
         assert M.mm_moe_mx_scale_size(rows, C) == ops._scale_bytes(rows, C)
+    for T in (0, 1, 1000, 24576, 24577, 100000):
+        for K, E in ((1, 1), (2, 60), (8, 1024)):
+            assert M.mm_moe_sort_scratch_size(T, K, E) == ops._sort_scratch(T, K, E), (T, K, E)
     for T in (0, 1, 2, 3, 4, 5, 100):
         for K in (0, 1, 3, 4, 8):
             for C in (32, 4096, 36384, 65536, 145632, 200000 // 32 * 32):
