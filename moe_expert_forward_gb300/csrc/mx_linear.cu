@@ -395,10 +395,13 @@ cudaError_t launch_mx_product(const MxProductArgs& p, cudaStream_t s) {
   if (p.rows == 0) return cudaSuccess;
   const int64_t blocks = (p.rows + kMxRows - 1) / kMxRows;
   const int sms = dev_info().sms;
-  // pairs where every pair of SMs has a whole task of full blocks
+  const int KS = mx_chunks(p.C) / 2;
+  // pairs where every pair of SMs has a whole task of full blocks and a task has 16 stages or more: a shorter one is
+  // mostly hand-over (us with the quantiser, pairs / one CTA a tile, 8192 x C x 4096: C 7168 109 / 119, 4096 72 / 74,
+  // 512 24 / 19; 2048 x 7168 x 4096 34.8 / 36.4)
   const int64_t full_pairs = p.blk_off ? 0 : p.rows / (2 * kMxRows);
-  if (full_pairs * ((p.N + 255) / 256) >= sms / 2) return launch_mx_product_pair(p, s);
-  const Tile t = choose_tile(blocks, p.rows < kMxRows ? static_cast<int>(p.rows) : kMxRows, p.N, mx_chunks(p.C) / 2, sms);
+  if (KS >= 16 && full_pairs * ((p.N + 255) / 256) >= sms / 2) return launch_mx_product_pair(p, s);
+  const Tile t = choose_tile(blocks, p.rows < kMxRows ? static_cast<int>(p.rows) : kMxRows, p.N, KS, sms);
   return with_dtype(p.dtype, [&](auto tag) {
     using T = decltype(tag);
     return t.parts > 1 ? launch_tile<T, true>(p, t, s) : launch_tile<T, false>(p, t, s);

@@ -166,6 +166,25 @@ def test_linear_many_tiles(ops, T, N):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,N,C", [(2500, 2600, 4096), (5000, 1030, 3872), (2561, 2560, 7200), (20000, 333, 4128)])
+def test_linear_pairs(ops, T, N, C, dt):
+    """Long contractions over many rows: CTA pairs, with odd blocks, partial tiles and rows of any alignment. The
+    reference takes the quantiser's own values (tested above) and is summed in 64 bits."""
+    codes, sf, w = weights(1, N, C, N)
+    x = torch.randn(T, C, generator=torch.Generator().manual_seed(T)).to(DT[dt]).cuda()
+    y = ops.mx_linear(x, ops.mx_weights(codes.cuda(), sf.cuda()))
+    q = ops.mx_dequantize(*ops.mx_quantize(x), C, torch.float32).double()
+    w = torch.from_numpy(w[0]).cuda()
+    want, size = q @ w.t(), q.abs() @ w.abs().t()
+    tol = (-(-C // 64) * 2.0 ** -22) * size + 1.01 * HALF_ULP[dt] * want.abs()
+    assert y.dtype == DT[dt] and ((y.double() - want).abs() <= tol).all()
+    if dt == "f32":
+        buf = torch.full((T, N + 5), 7.0, device="cuda")
+        ops.mx_linear(x, ops.mx_weights(codes.cuda(), sf.cuda()), out=buf[:, 3:N + 3])
+        assert torch.equal(buf[:, 3:N + 3], y) and (buf[:, :3] == 7).all() and (buf[:, N + 3:] == 7).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("T,N,C", [(1, 130, 4128), (2, 129, 8224), (3, 17, 3968), (4, 300, 4096), (1, 1, 12320), (5, 64, 4128)])
 def test_linear_few_rows(ops, T, N, C, dt):
     """One launch for up to four rows, over several steps of the contraction, and one row more."""
