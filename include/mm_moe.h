@@ -456,8 +456,8 @@ int mm_moe_sort(const int32_t* topk_idx, int T, int K, int E, int block_m, int32
 /* Tokens into the pool of a routing (mm_moe_sort's or mm_moe_dispatch's slot, src and blk_off of
  * the same T, K, E, block_m): rows[slot[t*K + k]] = x[t]; every other row of the
  * num_rows is zero (padding, and rows past the last block).  x [T, H],
- * row_stride elements between rows; rows [num_rows, H] contiguous.  H >= 1 of
- * any size; rows may start on any element (16-byte boundaries are the fastest).
+ * row_stride elements between rows; rows [num_rows, H] contiguous.  H of any
+ * size from 1 to 2^30; rows may start on any element (16-byte boundaries are the fastest).
  * num_rows at least T*K + min(T*K, E) * (block_m - 1); src holds
  * num_rows entries. */
 int mm_moe_permute(const void* x, int dtype, int64_t row_stride, int T, int H, int K, int E, int block_m,

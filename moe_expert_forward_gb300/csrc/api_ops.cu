@@ -8,12 +8,16 @@ using namespace mm;
 namespace {
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+// int32 and fp32 arrays; null counts
+template <typename... P>
+bool words(const P*... p) { return (... && aligned(p, 4)); }
 
 int done(cudaError_t e) { return e == cudaSuccess ? MM_MOE_OK : MM_MOE_ERR_CUDA; }
 
 bool device_ok() { return dev_info().cc_major == 10 && dev_info().cc_minor == 3; }
 
 constexpr int64_t kMaxPairs = int64_t(1) << 30;
+constexpr int kMaxCols = 1 << 30;                           // column indices are int32, with room for a granule
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 256;      // row indices are int32
 
 int check_route(const void* logits, int dtype, int64_t stride, int T, int E, int K, int score) {
@@ -26,7 +30,7 @@ int check_route(const void* logits, int dtype, int64_t stride, int T, int E, int
 
 // the pool of T*K pairs over E experts in blocks of block_m rows fits num_rows
 int check_rows(int dtype, int T, int H, int K, int64_t num_rows) {
-  if (!dtype_known(dtype) || T < 0 || H < 1 || K < 1 || K > kMaxK || num_rows < 0 || num_rows > kMaxRows)
+  if (!dtype_known(dtype) || T < 0 || H < 1 || H > kMaxCols || K < 1 || K > kMaxK || num_rows < 0 || num_rows > kMaxRows)
     return MM_MOE_ERR_INVALID_ARG;
   if (static_cast<int64_t>(T) * K > kMaxPairs) return MM_MOE_ERR_INVALID_ARG;
   return MM_MOE_OK;
@@ -44,7 +48,7 @@ int check_product(int64_t rows, int C, const void* w, const void* w_sfp, int E, 
   if (rows < 0 || rows > kMaxRows || C < 32 || C % 32 || N < 1 || E < 1 || E > kMaxE || !dtype_known(dtype))
     return MM_MOE_ERR_INVALID_ARG;
   if ((!routed && E != 1) || (routed && rows % 128)) return MM_MOE_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(E) * N > kMaxRows || C > (1 << 30) || out_stride < N) return MM_MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(E) * N > kMaxRows || C > kMaxCols || out_stride < N) return MM_MOE_ERR_INVALID_ARG;
   if (((rows + 127) / 128) * ((static_cast<int64_t>(N) + 63) / 64) > (int64_t(1) << 30)) return MM_MOE_ERR_INVALID_ARG;
   if (!w || !w_sfp || !aligned(w, 16) || !aligned(w_sfp, 16)) return MM_MOE_ERR_INVALID_ARG;
   if (rows > 0 && (!out || !aligned(out, dtype_size(dtype)))) return MM_MOE_ERR_INVALID_ARG;
@@ -71,9 +75,9 @@ extern "C" {
 int mm_moe_route(const void* logits, int dtype, int64_t row_stride, int T, int E, int K, const float* bias, int score,
                  int renorm, float scale, int32_t* topk_idx, float* topk_w, void* stream) {
   if (int r = check_route(logits, dtype, row_stride, T, E, K, score)) return r;
-  if (bias && (score != MM_MOE_SCORE_SIGMOID || !aligned(bias, 4))) return MM_MOE_ERR_INVALID_ARG;
+  if (bias && (score != MM_MOE_SCORE_SIGMOID || !words(bias))) return MM_MOE_ERR_INVALID_ARG;
   if (T == 0) return MM_MOE_OK;
-  if (!topk_idx || !topk_w || !aligned(topk_idx, 4) || !aligned(topk_w, 4)) return MM_MOE_ERR_INVALID_ARG;
+  if (!topk_idx || !topk_w || !words(topk_idx, topk_w)) return MM_MOE_ERR_INVALID_ARG;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   const RouteArgs a{logits, dtype, row_stride, T, E, K, bias, score, renorm != 0, scale, topk_idx, topk_w};
   return done(launch_route(a, static_cast<cudaStream_t>(stream)));
@@ -85,7 +89,7 @@ int mm_moe_route_backward(const void* logits, int dtype, int64_t row_stride, con
   if (int r = check_route(logits, dtype, row_stride, T, E, K, score)) return r;
   if (d_row_stride < E) return MM_MOE_ERR_INVALID_ARG;
   if (T == 0) return MM_MOE_OK;
-  if (!topk_idx || !d_topk_w || !d_logits || !aligned(topk_idx, 4) || !aligned(d_topk_w, 4) ||
+  if (!topk_idx || !d_topk_w || !d_logits || !words(topk_idx, d_topk_w) ||
       !aligned(d_logits, dtype_size(dtype)))
     return MM_MOE_ERR_INVALID_ARG;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
@@ -108,7 +112,8 @@ int mm_moe_sort(const int32_t* topk_idx, int T, int K, int E, int block_m, int32
   if (int r = mm_moe_sort_scratch_size(T, K, E, &need)) return r;
   if (int r = check_pool(T, K, E, block_m, src_capacity)) return r;
   if (!cnt || !blk_off || !status || (T > 0 && (!topk_idx || !slot || !src))) return MM_MOE_ERR_INVALID_ARG;
-  if (need && (!scratch || !aligned(scratch, 4))) return MM_MOE_ERR_INVALID_ARG;
+  if (!words(topk_idx, cnt, blk_off, slot, src, status)) return MM_MOE_ERR_INVALID_ARG;
+  if (need && (!scratch || !words(scratch))) return MM_MOE_ERR_INVALID_ARG;
   if (scratch_bytes < need) return MM_MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   return done(launch_sort(topk_idx, T, K, E, block_m, cnt, blk_off, slot, src, status, static_cast<int32_t*>(scratch),
@@ -124,7 +129,7 @@ int mm_moe_permute(const void* x, int dtype, int64_t row_stride, int T, int H, i
   if (num_rows == 0) return MM_MOE_OK;
   const int es = dtype_size(dtype);
   if (!rows || !src || !blk_off || (T > 0 && (!x || !slot))) return MM_MOE_ERR_INVALID_ARG;
-  if (!aligned(x, es) || !aligned(rows, es)) return MM_MOE_ERR_INVALID_ARG;
+  if (!aligned(x, es) || !aligned(rows, es) || !words(slot, src, blk_off)) return MM_MOE_ERR_INVALID_ARG;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   const RowsArgs a{dtype, T, H, K, E, block_m, num_rows, slot, src, blk_off};
   return done(launch_permute(a, x, row_stride, rows, static_cast<cudaStream_t>(stream)));
@@ -136,7 +141,7 @@ int mm_moe_unpermute(const void* rows, int dtype, int64_t num_rows, int T, int H
   if (out_stride < H) return MM_MOE_ERR_INVALID_ARG;
   if (T == 0) return MM_MOE_OK;
   const int es = dtype_size(dtype);
-  if (!rows || !slot || !out || !aligned(rows, es) || !aligned(out, es)) return MM_MOE_ERR_INVALID_ARG;
+  if (!rows || !slot || !out || !aligned(rows, es) || !aligned(out, es) || !words(slot, w)) return MM_MOE_ERR_INVALID_ARG;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   const RowsArgs a{dtype, T, H, K, 0, 0, num_rows, slot, nullptr, nullptr};
   return done(launch_unpermute(a, rows, w, out, out_stride, static_cast<cudaStream_t>(stream)));
@@ -152,23 +157,24 @@ int mm_moe_unpermute_backward(const void* d_out, int dtype, int64_t d_stride, co
   const int es = dtype_size(dtype);
   if (!d_rows || !src || !blk_off || (T > 0 && (!d_out || !slot)) || (T > 0 && d_w && !rows))
     return MM_MOE_ERR_INVALID_ARG;
-  if (!aligned(d_out, es) || !aligned(d_rows, es) || !aligned(rows, es)) return MM_MOE_ERR_INVALID_ARG;
+  if (!aligned(d_out, es) || !aligned(d_rows, es) || !aligned(rows, es) || !words(slot, src, blk_off, w, d_w))
+    return MM_MOE_ERR_INVALID_ARG;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   const RowsArgs a{dtype, T, H, K, E, block_m, num_rows, slot, src, blk_off};
   return done(launch_unpermute_backward(a, d_out, d_stride, rows, w, d_rows, d_w, static_cast<cudaStream_t>(stream)));
 }
 
 int mm_moe_mx_scale_size(int64_t rows, int C, size_t* bytes) {
-  if (!bytes || rows < 0 || rows > kMaxRows || C < 1 || C > (1 << 30)) return MM_MOE_ERR_INVALID_ARG;
+  if (!bytes || rows < 0 || rows > kMaxRows || C < 1 || C > kMaxCols) return MM_MOE_ERR_INVALID_ARG;
   *bytes = mx_sf_bytes(rows, C);
   return MM_MOE_OK;
 }
 
 int mm_moe_mx_quantize(const void* x, int dtype, int64_t row_stride, int64_t R, int C, const int32_t* slot, int K,
                        int64_t num_rows, void* codes, void* sf, int chunks, void* stream) {
-  if (!dtype_known(dtype) || R < 0 || R > kMaxRows || C < 1 || C > (1 << 30) || row_stride < C)
+  if (!dtype_known(dtype) || R < 0 || R > kMaxRows || C < 1 || C > kMaxCols || row_stride < C)
     return MM_MOE_ERR_INVALID_ARG;
-  if (slot && (K < 1 || K > kMaxK || num_rows < 0 || num_rows > kMaxRows || R * K > kMaxPairs))
+  if (slot && (!words(slot) || K < 1 || K > kMaxK || num_rows < 0 || num_rows > kMaxRows || R * K > kMaxPairs))
     return MM_MOE_ERR_INVALID_ARG;
   if (R == 0) return MM_MOE_OK;
   if (!x || !codes || !sf || !aligned(x, dtype_size(dtype)) || !aligned(codes, 16) || (chunks && !aligned(sf, 16)))
@@ -181,7 +187,7 @@ int mm_moe_mx_quantize(const void* x, int dtype, int64_t row_stride, int64_t R, 
 
 int mm_moe_mx_dequantize(const void* codes, const void* sf, int64_t R, int C, int dtype, void* out, int64_t out_stride,
                          void* stream) {
-  if (!dtype_known(dtype) || R < 0 || R > kMaxRows || C < 1 || C > (1 << 30) || out_stride < C)
+  if (!dtype_known(dtype) || R < 0 || R > kMaxRows || C < 1 || C > kMaxCols || out_stride < C)
     return MM_MOE_ERR_INVALID_ARG;
   if (R == 0) return MM_MOE_OK;
   if (!codes || !sf || !out || !aligned(codes, 16) || !aligned(out, dtype_size(dtype))) return MM_MOE_ERR_INVALID_ARG;
@@ -191,7 +197,7 @@ int mm_moe_mx_dequantize(const void* codes, const void* sf, int64_t R, int C, in
 }
 
 int mm_moe_mx_prepare(const void* sf, int E, int N, int C, void* sfp, void* stream) {
-  if (!sf || !sfp || !aligned(sfp, 16) || E < 1 || E > kMaxE || N < 1 || C < 1 || C > (1 << 30) ||
+  if (!sf || !sfp || !aligned(sfp, 16) || E < 1 || E > kMaxE || N < 1 || C < 1 || C > kMaxCols ||
       static_cast<int64_t>(E) * N > kMaxRows)
     return MM_MOE_ERR_INVALID_ARG;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
@@ -205,7 +211,7 @@ int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, co
   if (!cnt != !blk_off) return MM_MOE_ERR_INVALID_ARG;
   if (int r = check_product(rows, C, w, w_sfp, E, N, blk_off != nullptr, dtype, out, out_stride)) return r;
   if (rows == 0) return MM_MOE_OK;
-  if (!codes || !sf || !status || !aligned(codes, 16) || !aligned(sf, 16) || !aligned(status, 4))
+  if (!codes || !sf || !status || !aligned(codes, 16) || !aligned(sf, 16) || !words(status, cnt, blk_off))
     return MM_MOE_ERR_INVALID_ARG;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   const MxProductArgs a{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(sf), rows, C,
@@ -215,7 +221,7 @@ int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, co
 }
 
 int mm_moe_mx_linear_workspace(int T, int C, int N, int K, int64_t num_rows, size_t* bytes) {
-  if (!bytes || T < 0 || N < 1 || K < 0 || K > kMaxK || num_rows < 0 || num_rows > kMaxRows || C < 32 || C % 32 || C > (1 << 30))
+  if (!bytes || T < 0 || N < 1 || K < 0 || K > kMaxK || num_rows < 0 || num_rows > kMaxRows || C < 32 || C % 32 || C > kMaxCols)
     return MM_MOE_ERR_INVALID_ARG;
   if (K == 0 && num_rows != T) return MM_MOE_ERR_INVALID_ARG;
   *bytes = mx_few_rows(T, C, N, K) ? 0 : linear_layout(num_rows, C).total;
@@ -227,7 +233,8 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
                      int64_t num_rows, void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
                      unsigned timeout_ms, void* stream) {
   const bool routed = slot != nullptr;
-  if (T < 0 || row_stride < C || !cnt != !slot || !blk_off != !slot || (!routed && num_rows != T))
+  if (T < 0 || row_stride < C || !cnt != !slot || !blk_off != !slot || (!routed && num_rows != T) ||
+      !words(slot, cnt, blk_off))
     return MM_MOE_ERR_INVALID_ARG;
   if (int r = check_product(num_rows, C, w, w_sfp, E, N, routed, dtype, out, out_stride)) return r;
   if (routed) {

@@ -56,7 +56,7 @@ __device__ __forceinline__ uint2 twice_values(uint32_t w) {
 // NT rows of x at most per CTA (one where routed).
 template <typename T, int NT, bool kVec>
 __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) few_kernel(const FewArgs a, int rows, int sets) {
-  extern __shared__ uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem[];
   const int n32 = a.C / 32;
   // per row of x: the first and second 16 int8 of every block, then every block's scale
   uint4* s_lo = reinterpret_cast<uint4*>(smem);

@@ -110,6 +110,42 @@ def test_linear(M):
             M.mm_moe_mx_linear_workspace(*bad)
 
 
+def test_words_on_no_boundary_and_rows_of_any_length(M):
+    odd = A + 2                                     # an int32 or fp32 array there would fault on the device
+    bad = M.MM_MOE_ERR_INVALID_ARG
+    long = 1 << 30                                  # the longest row
+
+    def sort(idx=A, cnt=A, blk=A, slot=A, src=A, status=A):
+        return M.mm_moe_sort(idx, 4, 2, 4, 16, cnt, blk, slot, src, 8 + 4 * 15, None, 0, status, None)
+    for name in ("idx", "cnt", "blk", "slot", "src", "status"):
+        assert sort(**{name: odd}) == bad, name
+
+    def permute(H=8, slot=A, src=A, blk=A):
+        return M.mm_moe_permute(A, 1, H, 4, H, 2, 4, 16, slot, src, blk, A, 8 + 4 * 15, None)
+
+    def unpermute(H=8, slot=A, w=A):
+        return M.mm_moe_unpermute(A, 1, 68, 4, H, 2, slot, w, A, H, None)
+
+    def back(H=8, slot=A, src=A, blk=A, w=A, d_w=A):
+        return M.mm_moe_unpermute_backward(A, 1, H, A, 4, H, 2, 4, 16, slot, src, blk, w, A, 8 + 4 * 15, d_w, None)
+    for f, names in ((permute, ("slot", "src", "blk")), (unpermute, ("slot", "w")),
+                     (back, ("slot", "src", "blk", "w", "d_w"))):
+        for name in names:
+            assert f(**{name: odd}) == bad, (f.__name__, name)
+        assert f(H=long + 1) == bad, f.__name__
+    assert M.mm_moe_mx_quantize(A, 1, 64, 4, 64, odd, 1, 128, A, A, 1, None) == bad
+
+    def product(cnt=A, blk=A, status=A):
+        return M.mm_moe_mx_product(A, A, 128, 64, A, A, 4, 8, cnt, blk, 1, A, 8, status, 0, 0, None)
+
+    def linear(slot=A, cnt=A, blk=A):
+        return M.mm_moe_mx_linear(A, 1, 64, 8, 64, A, A, 4, 8, slot, 2, cnt, blk, 1024, A, 8, A, 1 << 20, 0, None)
+    for name in ("cnt", "blk", "status"):
+        assert product(**{name: odd}) == bad, name
+    for name in ("slot", "cnt", "blk"):
+        assert linear(**{name: odd}) == bad, name
+
+
 def test_binding_sizes_agree_with_the_library(M):
     from moe_expert_forward_gb300 import ops
     for rows, C in ((1, 32), (129, 96), (1000, 4096)):
