@@ -4,9 +4,10 @@
 // products of small integers per 16-byte load.
 //
 // Twice an e2m1 value is an integer of 4 bits and a sign (0, 1, 2, 3, 4, 6, 8, 12), so a
-// block of 32 is eight 4-way integer dots, exact, times 2^(ea + eb - 2), exact; the
-// blocks are summed in fp32, each lane's in ascending order, then over the warp in a
-// fixed tree.
+// block of 32 is eight 4-way integer dots, exact, times 2^(ea + eb - 2), exact where
+// the result is in fp32's range (a weight scale below one is multiplied first: the dot,
+// up to 4608, times x's scale alone may pass the largest fp32); the blocks are summed
+// in fp32, each lane's in ascending order, then over the warp in a fixed tree.
 //
 // What bounds it is latency, then the weights' bytes. A warp takes two weight
 // rows and a lane one block of 32 (16 bytes) of each per step; the first steps'
@@ -157,7 +158,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) few_kernel(const Fe
                 dot = __dp4a(static_cast<int>(d[r][i].x), static_cast<int>(xs[2 * i]), dot);
                 dot = __dp4a(static_cast<int>(d[r][i].y), static_cast<int>(xs[2 * i + 1]), dot);
               }
-              acc[r][t] += static_cast<float>(dot) * sx * sc[r];
+              // Neither order of the two scales loses a result that fits: with sc < 1 first, |dot| * sc is below 4608
+              // and, an integer times a power of two of 2^-127 at least, exact; with sx first where sc >= 1, a product
+              // that overflows does so with sc too.
+              const bool below = sc[r] < 1.0f;
+              acc[r][t] += static_cast<float>(dot) * (below ? sc[r] : sx) * (below ? sx : sc[r]);
             }
           }
         }
