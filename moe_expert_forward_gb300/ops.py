@@ -94,6 +94,17 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(stream, shape, dtype, device):
+    """An uninitialised tensor for a call on `stream`, of that stream's memory: what the current stream frees and takes
+    again would otherwise meet kernels that `stream` still runs."""
+    ptr = 0 if stream is None else _stream(stream)
+    if stream is None or ptr == _raw_stream(_device()):
+        return torch.empty(shape, dtype=dtype, device=device)
+    # stream 0 has no external form
+    with torch.cuda.stream(torch.cuda.ExternalStream(ptr) if ptr else torch.cuda.default_stream()):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _here(t, what: str, name: str):
     """A tensor on the current CUDA device."""
     if not isinstance(t, torch.Tensor) or t.get_device() != _device():
@@ -393,7 +404,7 @@ def mx_linear(x, weights: MxWeights, routing: Optional[Routing] = None, out=None
     ws, ws_bytes = None, 0
     if workspace is not None or not _few(T, C, weights.N, K):
         if workspace is None:
-            workspace = torch.empty(_linear_bytes(rows, C), dtype=torch.uint8, device=x.device)
+            workspace = _new(stream, _linear_bytes(rows, C), torch.uint8, x.device)
         else:
             _here(workspace, "mx_linear", "workspace")
             if not workspace.is_contiguous():

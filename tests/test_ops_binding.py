@@ -1,0 +1,77 @@
+"""What the tensor forms hand to the library: memory of which stream, of which device.  A stand-in takes the place of
+the library and of the device, so these run without a GPU."""
+import contextlib
+
+import pytest
+import torch
+
+import moe_expert_forward_gb300 as M
+from moe_expert_forward_gb300 import ops
+
+CURRENT, SIDE = 0, 7
+
+
+class Stand:
+    """Streams are numbers, the CPU is the current device; every tensor made is noted with the stream current then."""
+
+    def __init__(self):
+        self.current, self.made, self.shared, self.calls = CURRENT, [], [], []
+
+    @contextlib.contextmanager
+    def on(self, stream):
+        before, self.current = self.current, stream
+        yield
+        self.current = before
+
+    def maker(self, make):
+        def made(*args, **kw):
+            t = make(*args, **kw)
+            self.made.append((t.data_ptr(), self.current))
+            return t
+        return made
+
+    def __getattr__(self, name):           # the library: every entry point notes its arguments
+        def call(*args):
+            self.calls.append((name, args))
+            return M.MM_MOE_OK
+        return call
+
+    def args(self, name):
+        return [a for n, a in self.calls if n == name][-1]
+
+    def stream_of(self, address):
+        return [s for p, s in self.made if p == address][-1]
+
+
+@pytest.fixture
+def stand(monkeypatch):
+    s = Stand()
+    monkeypatch.setattr(ops, "lib", lambda: s)
+    monkeypatch.setattr(ops, "_device", lambda: -1)               # what a CPU tensor says of its device
+    monkeypatch.setattr(ops, "_raw_stream", lambda device: s.current)
+    monkeypatch.setattr(torch.cuda, "stream", s.on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: s.current)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: 0)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda p, device=None: p)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, on: s.shared.append((t.data_ptr(), on)))
+    for name in ("empty", "zeros"):
+        monkeypatch.setattr(torch, name, s.maker(getattr(torch, name)))
+    return s
+
+
+def weights(E, N, C):
+    return ops.MxWeights(torch.ones(E, N, C // 2, dtype=torch.uint8),
+                         torch.ones(E * ops._scale_bytes(N, C), dtype=torch.uint8), E, N, C)
+
+
+def test_the_workspace_of_a_linear_is_the_launch_streams(stand):
+    """The caller never sees it: on the current stream's pool it would be handed out again while `stream` runs."""
+    x, w = torch.ones(64, 64), weights(1, 32, 64)
+    for stream, owner in ((None, CURRENT), (SIDE, SIDE), (CURRENT, CURRENT)):
+        ops.mx_linear(x, w, stream=stream)
+        a = stand.args("mm_moe_mx_linear")
+        assert a[17] > 0 and stand.stream_of(a[16]) == owner and a[19] == owner
+    with stand.on(SIDE):                       # and the default stream's, where another is current
+        ops.mx_linear(x, w, stream=0)
+        assert stand.stream_of(stand.args("mm_moe_mx_linear")[16]) == 0
+    assert stand.current == CURRENT
