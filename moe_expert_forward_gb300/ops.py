@@ -94,15 +94,16 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _new(stream, shape, dtype, device):
-    """An uninitialised tensor for a call on `stream`, of that stream's memory: what the current stream frees and takes
-    again would otherwise meet kernels that `stream` still runs."""
+def _new(stream, shape, dtype, device, zero=False):
+    """A tensor (uninitialised, or zeroed in the order of `stream`) for a call on `stream`, of that stream's memory: what
+    the current stream frees and takes again would otherwise meet kernels that `stream` still runs."""
+    make = torch.zeros if zero else torch.empty
     ptr = 0 if stream is None else _stream(stream)
     if stream is None or ptr == _raw_stream(_device()):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
     # stream 0 has no external form
     with torch.cuda.stream(torch.cuda.ExternalStream(ptr) if ptr else torch.cuda.default_stream()):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
 
 
 def _here(t, what: str, name: str):
@@ -357,7 +358,7 @@ def mx_product(codes, sf, weights: MxWeights, routing: Optional[Routing] = None,
         _bad("mx_product", f"codes have {rows} rows, the routing's pool {routing.rows}")
     out, cnt, blk = _product_args("mx_product", weights, routing, rows, dtype, codes.device, out)
     if status is None:
-        status = torch.zeros(4, dtype=torch.int32, device=codes.device)
+        status = _new(stream, 4, torch.int32, codes.device, zero=True)
     st = _whole(status, "mx_product", "status", (4,), torch.int32)
     _check(lib().mm_moe_mx_product(cp, sp, rows, weights.C, weights.codes.data_ptr(), weights.sfp.data_ptr(), weights.E,
                                    weights.N, cnt, blk, _DTYPES[dtype], out.data_ptr(), _pitch(out), st, 0, 0,

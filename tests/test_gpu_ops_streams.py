@@ -66,3 +66,16 @@ def test_linears_on_two_streams_have_a_workspace_each(ops, linear):
         for s in streams:
             s.synchronize()
         assert all(torch.equal(o, y) for o, y in zip(outs, want))
+
+
+def test_a_product_on_a_busy_stream_keeps_its_status_word(ops, linear):
+    w, xs, want = linear
+    codes, sf = ops.mx_quantize(xs[0], chunks=True)
+    out = torch.empty(300, 512, device="cuda")
+    s, = side_streams(1)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+    ops.mx_product(codes, sf, w, out=out, dtype=torch.float32, stream=s)
+    kept = scribble([16])
+    s.synchronize()
+    assert torch.equal(out, want[0]) and all((k == 255).all() for k in kept)

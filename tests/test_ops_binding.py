@@ -75,3 +75,12 @@ def test_the_workspace_of_a_linear_is_the_launch_streams(stand):
         ops.mx_linear(x, w, stream=0)
         assert stand.stream_of(stand.args("mm_moe_mx_linear")[16]) == 0
     assert stand.current == CURRENT
+
+
+def test_the_status_word_of_a_product_is_the_launch_streams(stand):
+    """Its zeroing too: queued on another stream it would be in no order with the kernel."""
+    w = weights(1, 32, 64)
+    codes, sf = torch.ones(8, 32, dtype=torch.uint8), torch.ones(ops._scale_bytes(8, 64), dtype=torch.uint8)
+    for stream, owner in ((None, CURRENT), (SIDE, SIDE)):
+        ops.mx_product(codes, sf, w, stream=stream)
+        assert stand.stream_of(stand.args("mm_moe_mx_product")[13]) == owner
