@@ -12,8 +12,10 @@
 Argument marshalling and checks only; the arithmetic is in the CUDA library,
 whose C entry points (include/mm_moe.h) define each operator.  Every function
 enqueues on `stream` (default: the current stream) of the current device and
-returns at once.  Tensors used on a stream other than the one they were
-allocated on are the caller's to keep alive.
+returns at once.  What a call allocates is `stream`'s memory; its results are
+also marked as used on the stream that is current at the call.  Other uses of a
+tensor on a stream that it was not allocated on are the caller's to order and to
+keep alive.
 """
 from __future__ import annotations
 
@@ -41,9 +43,9 @@ class Routing:
     """
     __slots__ = ("T", "K", "E", "block_m", "rows", "_buf", "_status", "_cnt", "_blk", "_slot", "_src")
 
-    def __init__(self, T: int, K: int, E: int, block_m: int, rows: int, device, scratch_ints: int):
+    def __init__(self, T: int, K: int, E: int, block_m: int, rows: int, device, scratch_ints: int, stream=None):
         self.T, self.K, self.E, self.block_m, self.rows = T, K, E, block_m, rows
-        self._buf = torch.empty(5 + 2 * E + T * K + rows + scratch_ints, dtype=torch.int32, device=device)
+        self._buf = _result(stream, 5 + 2 * E + T * K + rows + scratch_ints, torch.int32, device)
         self._status = p = self._buf.data_ptr()      # addresses, for the calls
         self._cnt = p + 16
         self._blk = p + 16 + 4 * E
@@ -95,8 +97,8 @@ def _stream(stream) -> int:
 
 
 def _new(stream, shape, dtype, device, zero=False):
-    """A tensor (uninitialised, or zeroed in the order of `stream`) for a call on `stream`, of that stream's memory: what
-    the current stream frees and takes again would otherwise meet kernels that `stream` still runs."""
+    """A tensor (uninitialised, or zeroed in `stream`'s order) for a call on `stream`, of that stream's memory: what the
+    current stream frees and takes again would otherwise meet kernels that `stream` still runs."""
     make = torch.zeros if zero else torch.empty
     ptr = 0 if stream is None else _stream(stream)
     if stream is None or ptr == _raw_stream(_device()):
@@ -104,6 +106,15 @@ def _new(stream, shape, dtype, device, zero=False):
     # stream 0 has no external form
     with torch.cuda.stream(torch.cuda.ExternalStream(ptr) if ptr else torch.cuda.default_stream()):
         return make(shape, dtype=dtype, device=device)
+
+
+def _result(stream, shape, dtype, device):
+    """What a call on `stream` returns: memory that no work queued on the current stream still uses, and that is not
+    taken again before the work which the current stream has been given when it is freed."""
+    t = _new(stream, shape, dtype, device)
+    if stream is not None and _stream(stream) != _raw_stream(_device()):
+        t.record_stream(torch.cuda.current_stream())
+    return t
 
 
 def _here(t, what: str, name: str):
@@ -154,8 +165,8 @@ def route(logits, k: int, bias=None, score: str = "softmax", renorm: bool = True
     if score not in _SCORES:
         _bad("route", f"score must be one of {sorted(_SCORES)}, got {score!r}")
     bp = None if bias is None else _whole(bias, "route", "bias", (E,), torch.float32)
-    idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    idx = _result(stream, (T, k), torch.int32, logits.device)
+    w = _result(stream, (T, k), torch.float32, logits.device)
     _check(lib().mm_moe_route(logits.data_ptr(), code, _pitch(logits), T, E, k, bp, _SCORES[score], renorm, scale,
                               idx.data_ptr(), w.data_ptr(), _stream(stream)), "mm_moe_route")
     return idx, w
@@ -171,7 +182,7 @@ def route_backward(logits, topk_idx, d_topk_w, score: str = "softmax", renorm: b
     k = topk_idx.shape[-1]
     ip = _whole(topk_idx, "route_backward", "topk_idx", (T, k), torch.int32)
     dp = _whole(d_topk_w, "route_backward", "d_topk_w", (T, k), torch.float32)
-    d = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    d = _result(stream, (T, E), logits.dtype, logits.device)
     _check(lib().mm_moe_route_backward(logits.data_ptr(), code, _pitch(logits), ip, dp, T, E, k, _SCORES[score], renorm,
                                        scale, d.data_ptr(), E, _stream(stream)), "mm_moe_route_backward")
     return d
@@ -203,7 +214,7 @@ def sort_tokens(topk_idx, E: int, block_m: int = 16, stream=None) -> Routing:
         _bad("sort_tokens", f"block_m must be 16 to 256 and E at least 1, got {block_m} and {E}")
     scratch = _sort_scratch(T, K, E)
     rows = pool_rows(T, K, E, block_m)
-    r = Routing(T, K, E, block_m, rows, topk_idx.device, scratch // 4)
+    r = Routing(T, K, E, block_m, rows, topk_idx.device, scratch // 4, stream)
     _check(lib().mm_moe_sort(ip, T, K, E, block_m, r._cnt, r._blk, r._slot, r._src, rows, r._src + 4 * rows, scratch,
                              r._status, _stream(stream)), "mm_moe_sort")
     return r
@@ -216,7 +227,7 @@ def permute(x, routing: Routing, stream=None):
     T, H = x.shape
     if T != r.T:
         _bad("permute", f"x has {T} tokens, the routing {r.T}")
-    rows = torch.empty((r.rows, H), dtype=x.dtype, device=x.device)
+    rows = _result(stream, (r.rows, H), x.dtype, x.device)
     _check(lib().mm_moe_permute(x.data_ptr(), code, _pitch(x), T, H, r.K, r.E, r.block_m, r._slot,
                                 r._src, r._blk, rows.data_ptr(), r.rows, _stream(stream)),
            "mm_moe_permute")
@@ -232,7 +243,7 @@ def unpermute(rows, routing: Routing, topk_w=None, stream=None):
     if rows.shape[0] != r.rows or not rows.is_contiguous():
         _bad("unpermute", f"rows must be contiguous [{r.rows}, H], got {tuple(rows.shape)}")
     wp = None if topk_w is None else _whole(topk_w, "unpermute", "topk_w", (r.T, r.K), torch.float32)
-    out = torch.empty((r.T, H), dtype=rows.dtype, device=rows.device)
+    out = _result(stream, (r.T, H), rows.dtype, rows.device)
     _check(lib().mm_moe_unpermute(rows.data_ptr(), code, r.rows, r.T, H, r.K, r._slot, wp, out.data_ptr(), H,
                                   _stream(stream)), "mm_moe_unpermute")
     return out
@@ -255,8 +266,8 @@ def unpermute_backward(d_out, rows, routing: Routing, topk_w=None, stream=None):
     if topk_w is not None:
         wp = _whole(topk_w, "unpermute_backward", "topk_w", (T, r.K), torch.float32)
         rp = _whole(rows, "unpermute_backward", "rows", (r.rows, H), d_out.dtype)
-        d_w = torch.empty((T, r.K), dtype=torch.float32, device=d_out.device)
-    d_rows = torch.empty((r.rows, H), dtype=d_out.dtype, device=d_out.device)
+        d_w = _result(stream, (T, r.K), torch.float32, d_out.device)
+    d_rows = _result(stream, (r.rows, H), d_out.dtype, d_out.device)
     _check(lib().mm_moe_unpermute_backward(d_out.data_ptr(), code, _pitch(d_out), rp, T, H, r.K, r.E, r.block_m,
                                            r._slot, r._src, r._blk, wp,
                                            d_rows.data_ptr(), r.rows, None if d_w is None else d_w.data_ptr(),
@@ -285,8 +296,8 @@ def mx_quantize(x, routing: Optional[Routing] = None, chunks: bool = False, stre
             _bad("mx_quantize", f"x has {R} tokens, the routing {routing.T}")
         rows, slot, K = routing.rows, routing._slot, routing.K
     nb = -(-C // 32)
-    codes = torch.empty((rows, 16 * nb), dtype=torch.uint8, device=x.device)
-    sf = torch.empty(_scale_bytes(rows, C) if chunks else (rows, nb), dtype=torch.uint8, device=x.device)
+    codes = _result(stream, (rows, 16 * nb), torch.uint8, x.device)
+    sf = _result(stream, _scale_bytes(rows, C) if chunks else (rows, nb), torch.uint8, x.device)
     _check(lib().mm_moe_mx_quantize(x.data_ptr(), code, _pitch(x), R, C, slot, K, rows, codes.data_ptr(),
                                     sf.data_ptr(), chunks, _stream(stream)), "mm_moe_mx_quantize")
     return codes, sf
@@ -301,7 +312,7 @@ def mx_dequantize(codes, sf, C: int, dtype=torch.bfloat16, stream=None):
     sp = _whole(sf, "mx_dequantize", "sf", (R, nb), torch.uint8)
     if dtype not in _DTYPES:
         _bad("mx_dequantize", f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    out = torch.empty((R, C), dtype=dtype, device=codes.device)
+    out = _result(stream, (R, C), dtype, codes.device)
     _check(lib().mm_moe_mx_dequantize(cp, sp, R, C, _DTYPES[dtype], out.data_ptr(), C, _stream(stream)),
            "mm_moe_mx_dequantize")
     return out
@@ -317,12 +328,13 @@ def mx_weights(codes, sf, stream=None) -> MxWeights:
     E, N, C = codes.shape[0], codes.shape[1], codes.shape[2] * 2
     _whole(codes, "mx_weights", "codes", (E, N, C // 2), torch.uint8)
     sp = _whole(sf, "mx_weights", "sf", (E, N, C // 32), torch.uint8)
-    sfp = torch.empty(E * _scale_bytes(N, C), dtype=torch.uint8, device=codes.device)
+    sfp = _result(stream, E * _scale_bytes(N, C), torch.uint8, codes.device)
     _check(lib().mm_moe_mx_prepare(sp, E, N, C, sfp.data_ptr(), _stream(stream)), "mm_moe_mx_prepare")
     return MxWeights(codes, sfp, E, N, C)
 
 
-def _product_args(what: str, weights: MxWeights, routing: Optional[Routing], rows: int, dtype, device, out):
+def _product_args(what: str, weights: MxWeights, routing: Optional[Routing], rows: int, dtype, device, out,
+                  stream):
     """(out, cnt, blk_off) after the checks mx_product and mx_linear share."""
     if routing is None:
         if weights.E != 1:
@@ -334,7 +346,7 @@ def _product_args(what: str, weights: MxWeights, routing: Optional[Routing], row
                        f"{routing.block_m} and {routing.E}")
         cnt, blk = routing._cnt, routing._blk
     if out is None:
-        out = torch.empty((rows, weights.N), dtype=dtype, device=device)
+        out = _result(stream, (rows, weights.N), dtype, device)
     else:
         _rows(out, what, "out", weights.N, dtype)
         if out.shape[0] != rows:
@@ -356,7 +368,7 @@ def mx_product(codes, sf, weights: MxWeights, routing: Optional[Routing] = None,
         _bad("mx_product", f"dtype must be float32, bfloat16 or float16, got {dtype}")
     if routing is not None and routing.rows != rows:
         _bad("mx_product", f"codes have {rows} rows, the routing's pool {routing.rows}")
-    out, cnt, blk = _product_args("mx_product", weights, routing, rows, dtype, codes.device, out)
+    out, cnt, blk = _product_args("mx_product", weights, routing, rows, dtype, codes.device, out, stream)
     if status is None:
         status = _new(stream, 4, torch.int32, codes.device, zero=True)
     st = _whole(status, "mx_product", "status", (4,), torch.int32)
@@ -401,7 +413,7 @@ def mx_linear(x, weights: MxWeights, routing: Optional[Routing] = None, out=None
         if routing.T != T:
             _bad("mx_linear", f"x has {T} tokens, the routing {routing.T}")
         rows, slot, K = routing.rows, routing._slot, routing.K
-    out, cnt, blk = _product_args("mx_linear", weights, routing, rows, x.dtype, x.device, out)
+    out, cnt, blk = _product_args("mx_linear", weights, routing, rows, x.dtype, x.device, out, stream)
     ws, ws_bytes = None, 0
     if workspace is not None or not _few(T, C, weights.N, K):
         if workspace is None:

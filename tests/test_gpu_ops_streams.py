@@ -79,3 +79,39 @@ def test_a_product_on_a_busy_stream_keeps_its_status_word(ops, linear):
     kept = scribble([16])
     s.synchronize()
     assert torch.equal(out, want[0]) and all((k == 255).all() for k in kept)
+
+
+def test_results_on_an_idle_stream_are_not_what_the_current_one_still_writes(ops):
+    """The current stream is busy with a queued write to a block that it has already freed on the host's side."""
+    x = torch.randn(300, 1024, device="cuda")
+    idx = torch.arange(300, device="cuda", dtype=torch.int32).remainder(4).view(300, 1).contiguous()
+    r = ops.sort_tokens(idx, 4)
+    rows = ops.permute(x, r)
+    back = ops.unpermute(rows, r)
+    s, = side_streams(1)
+    torch.cuda.synchronize()
+    for call, want in ((lambda: ops.permute(x, r, stream=s), rows), (lambda: ops.unpermute(rows, r, stream=s), back)):
+        for _ in range(3):
+            torch.cuda._sleep(BUSY)
+            late = [torch.empty(want.numel() * 4, dtype=torch.uint8, device="cuda").fill_(255) for _ in range(4)]
+            del late
+            got = call()
+            s.synchronize()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+
+
+def test_results_outlive_their_last_use_on_the_current_stream(ops):
+    """Freed while the current stream still reads it, a result's memory does not go to the side stream's next call."""
+    x, y = torch.ones(300, 1024, device="cuda"), torch.zeros(300, 1024, device="cuda")
+    r = ops.sort_tokens(torch.zeros(300, 1, dtype=torch.int32, device="cuda"), 1)
+    s, = side_streams(1)
+    for _ in range(3):
+        rows = ops.permute(x, r, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda._sleep(BUSY)
+        copy = rows.clone()
+        del rows
+        other = [ops.permute(y, r, stream=s) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert (copy[r.slot[:, 0].long()] == 1).all() and not any(o.any() for o in other)

@@ -84,3 +84,30 @@ def test_the_status_word_of_a_product_is_the_launch_streams(stand):
     for stream, owner in ((None, CURRENT), (SIDE, SIDE)):
         ops.mx_product(codes, sf, w, stream=stream)
         assert stand.stream_of(stand.args("mm_moe_mx_product")[13]) == owner
+
+
+def results(stream):
+    """One call of every form that allocates a result, and what it returned."""
+    x, idx, w = torch.ones(6, 64), torch.ones(6, 2, dtype=torch.int32), weights(1, 32, 64)
+    routing = ops.sort_tokens(idx, 4, 128, stream=stream)
+    rows = ops.permute(x, routing, stream=stream)
+    topk_w = torch.ones(6, 2)
+    codes, sf = ops.mx_quantize(x, stream=stream)
+    chunked = ops.mx_quantize(x, chunks=True, stream=stream)
+    made = [routing._buf, rows, codes, sf, *chunked, ops.unpermute(rows, routing, topk_w, stream=stream),
+            ops.permute_backward(rows, routing, stream=stream),
+            *ops.unpermute_backward(x, rows, routing, topk_w, stream=stream), *ops.route(x, 2, stream=stream),
+            ops.route_backward(x, idx, topk_w, stream=stream), ops.mx_dequantize(codes, sf, 64, stream=stream),
+            ops.mx_weights(codes, sf, stream=stream).sfp, ops.mx_product(*chunked, w, stream=stream),
+            ops.mx_linear(x, w, stream=stream)]
+    return [t.data_ptr() for t in made], made        # made: kept, so that no address is used twice
+
+
+def test_results_are_the_launch_streams_and_marked_for_the_current_one(stand):
+    """The current stream's free memory may still be written by work queued there, which `stream` does not wait for."""
+    for stream, owner in ((None, CURRENT), (CURRENT, CURRENT), (SIDE, SIDE)):
+        stand.shared.clear()
+        pointers, kept = results(stream)
+        assert len(pointers) == 17 and [stand.stream_of(p) for p in pointers] == [owner] * 17
+        marked = [p for p, on in stand.shared if on == CURRENT]
+        assert set(pointers) <= set(marked) if owner == SIDE else not marked
