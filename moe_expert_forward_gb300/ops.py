@@ -123,6 +123,11 @@ def _here(t, what: str, name: str):
         _bad(what, f"{name} must be a tensor on the current CUDA device")
 
 
+def _routing_here(r: Routing, what: str):
+    """The calls pass a routing's addresses on, so it has to be the current device's."""
+    _here(r._buf, what, "routing")
+
+
 def _rows(t, what: str, name: str, cols: Optional[int] = None, dtype=None) -> int:
     """dtype code of a 2-D tensor with unit column stride and rows that do not overlap."""
     _here(t, what, name)
@@ -224,6 +229,7 @@ def permute(x, routing: Routing, stream=None):
     """Tokens x [T, H] at their pool rows: [routing.rows, H], zero on padding."""
     code = _rows(x, "permute", "x")
     r = routing
+    _routing_here(r, "permute")
     T, H = x.shape
     if T != r.T:
         _bad("permute", f"x has {T} tokens, the routing {r.T}")
@@ -239,6 +245,7 @@ def unpermute(rows, routing: Routing, topk_w=None, stream=None):
     rows times topk_w (fp32 [T, K]; None: ones), masked slots left out."""
     code = _rows(rows, "unpermute", "rows")
     r = routing
+    _routing_here(r, "unpermute")
     H = rows.shape[1]
     if rows.shape[0] != r.rows or not rows.is_contiguous():
         _bad("unpermute", f"rows must be contiguous [{r.rows}, H], got {tuple(rows.shape)}")
@@ -259,6 +266,7 @@ def unpermute_backward(d_out, rows, routing: Routing, topk_w=None, stream=None):
     fp32 [T, K]; without topk_w the second is None and rows is not read)."""
     code = _rows(d_out, "unpermute_backward", "d_out")
     r = routing
+    _routing_here(r, "unpermute_backward")
     T, H = d_out.shape
     if T != r.T:
         _bad("unpermute_backward", f"d_out has {T} tokens, the routing {r.T}")
@@ -292,6 +300,7 @@ def mx_quantize(x, routing: Optional[Routing] = None, chunks: bool = False, stre
         _bad("mx_quantize", "x has no columns")
     rows, slot, K = R, None, 1
     if routing is not None:
+        _routing_here(routing, "mx_quantize")
         if routing.T != R:
             _bad("mx_quantize", f"x has {R} tokens, the routing {routing.T}")
         rows, slot, K = routing.rows, routing._slot, routing.K
@@ -336,11 +345,14 @@ def mx_weights(codes, sf, stream=None) -> MxWeights:
 def _product_args(what: str, weights: MxWeights, routing: Optional[Routing], rows: int, dtype, device, out,
                   stream):
     """(out, cnt, blk_off) after the checks mx_product and mx_linear share."""
+    _here(weights.codes, what, "weights.codes")
+    _here(weights.sfp, what, "weights.sfp")
     if routing is None:
         if weights.E != 1:
             _bad(what, f"weights of {weights.E} experts need a routing")
         cnt = blk = None
     else:
+        _routing_here(routing, what)
         if routing.block_m != PRODUCT_BLOCK or routing.E != weights.E:
             _bad(what, f"the routing must have blocks of {PRODUCT_BLOCK} and {weights.E} experts, got "
                        f"{routing.block_m} and {routing.E}")

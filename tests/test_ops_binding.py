@@ -111,3 +111,37 @@ def test_results_are_the_launch_streams_and_marked_for_the_current_one(stand):
         assert len(pointers) == 17 and [stand.stream_of(p) for p in pointers] == [owner] * 17
         marked = [p for p, on in stand.shared if on == CURRENT]
         assert set(pointers) <= set(marked) if owner == SIDE else not marked
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor of another device than the current one."""
+
+    def get_device(self):
+        return 1
+
+
+def test_routings_and_weights_of_another_device_are_refused(stand):
+    """Their addresses go to the library as they are: another device's would be read, or fault, there."""
+    x, idx, topk_w = torch.ones(6, 64), torch.ones(6, 2, dtype=torch.int32), torch.ones(6, 2)
+    here, there = ops.sort_tokens(idx, 4, 128), ops.sort_tokens(idx, 4, 128)
+    there._buf = there._buf.as_subclass(Elsewhere)
+    w, rows = weights(4, 32, 64), ops.permute(x, here)
+    codes, sf = ops.mx_quantize(x, routing=here, chunks=True)
+    one = weights(1, 32, 64)
+    dense = ops.mx_quantize(x, chunks=True)
+    before = len(stand.calls)
+    for call in (lambda r: ops.permute(x, r), lambda r: ops.unpermute(rows, r, topk_w),
+                 lambda r: ops.permute_backward(rows, r), lambda r: ops.unpermute_backward(x, rows, r, topk_w),
+                 lambda r: ops.mx_quantize(x, routing=r), lambda r: ops.mx_product(codes, sf, w, routing=r),
+                 lambda r: ops.mx_linear(x, w, routing=r)):
+        with pytest.raises(M.MMError):
+            call(there)
+        assert len(stand.calls) == before
+        call(here)
+        before = len(stand.calls)
+    for field in ("codes", "sfp"):
+        far = one._replace(**{field: getattr(one, field).as_subclass(Elsewhere)})
+        for call in (lambda: ops.mx_linear(x, far), lambda: ops.mx_product(*dense, far)):
+            with pytest.raises(M.MMError):
+                call()
+    assert len(stand.calls) == before
