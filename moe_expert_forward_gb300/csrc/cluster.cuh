@@ -16,9 +16,10 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-// every thread of the cluster: what each wrote before is visible to all after
+// every thread of the cluster: what each wrote before is visible to all after. Not the .aligned form, which wants the
+// lanes of a warp together: callers come here from loops and waits that lanes leave one by one.
 __device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // shared::cluster address of the same location in CTA `rank`
 __device__ __forceinline__ uint32_t map_shared(const void* p, uint32_t rank) {
