@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
     for (int i = first; i < ntasks; i += stride, ++it) {
       const Task t = task_at(i, args, s_blk, s_cnt);
       const int buf = it % C::kAccBufs;
-      if (!mbar_wait(&tfull[buf], (it / C::kAccBufs) & 1, st, s_abort, kSiteTmemFull)) break;
+      if (!mbar_wait_warp(&tfull[buf], (it / C::kAccBufs) & 1, st, s_abort, kSiteTmemFull)) break;
       tc_fence_after();
       const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * BN + c0;
       const int row = quad * 32 + lane;

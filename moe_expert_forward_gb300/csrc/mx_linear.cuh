@@ -51,6 +51,13 @@ __device__ __forceinline__ int last_not_above(const int* a, int n, int v) {
   return lo;
 }
 
+// mbar_wait by a whole warp, of one answer for all of its lanes: each lane's own may differ where an abort or the limit
+// meets the barrier's completion, and what follows (loads from tensor memory, shuffles) takes all lanes or none.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const Status& st, volatile int* abort,
+                                               int where) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, st, abort, where));
+}
+
 // Two accumulators as one 32-bit word of 16-bit elements.
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {

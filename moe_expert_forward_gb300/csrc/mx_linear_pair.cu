@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int it = 0;
     for (int i = first; i < ntasks; i += stride, ++it) {
       const Task t = task_at(i, rank, args);
-      if (!mbar_wait(tfull, it & 1, st, s_abort, kSiteTmemFull)) break;
+      if (!mbar_wait_warp(tfull, it & 1, st, s_abort, kSiteTmemFull)) break;
       tc_fence_after();
       const int n = t.n * kTileN + c0;
       const int row0 = (warp & 3) * 32;
