@@ -429,7 +429,7 @@ int mm_moe_ep_barrier_ranks(void* const* peer_flags, int N, uint32_t epoch, unsi
  *   p      softmax over the row's E logits, or sigmoid of each
  *   topk_w scale * p / z (fp32 [T, K]); z = 1, or with renorm the sum of the chosen
  *          p (sigmoid: plus 1e-20).  The bias moves the choice only.  A logit of
- *          +inf makes its row's softmax weights NaN.
+ *          +inf makes its row's softmax weights NaN (0 still where topk_idx is -1).
  * topk_idx int32 [T, K] and topk_w are what mm_moe_forward and mm_moe_dispatch
  * take.  1 <= K <= 16, K <= E <= 1024. */
 int mm_moe_route(const void* logits, int dtype, int64_t row_stride, int T, int E, int K, const float* bias, int score,

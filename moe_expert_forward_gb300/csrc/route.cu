@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   if (renorm) p = __fdiv_rn(p, group_sum<G>(p) + 1e-20f);
   if (lane < K && t0 < T_) {
     topk_idx[static_cast<int64_t>(t) * K + lane] = my_e;
-    topk_w[static_cast<int64_t>(t) * K + lane] = p * scale;
+    // 0 where there is no choice, also where an infinite logit made the sum, and so p, NaN
+    topk_w[static_cast<int64_t>(t) * K + lane] = my_e >= 0 ? p * scale : 0.f;
   }
 }
 
