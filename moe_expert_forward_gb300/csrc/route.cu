@@ -26,9 +26,12 @@
 //                  bounds it (65536 rows of 160 read 21 MB, 3 us) and the reductions
 //                  and the work at a row's end are shared by four
 //
-// The softmax takes exp as 2^(x log2 e) by the fast unit, a few units in the last
-// place of fp32 off for the arguments (<= 0) that matter; the sigmoid, whose sums
-// with the bias decide the choice, takes expf and the IEEE division.
+// The softmax's exponentials of differences x <= 0 are 2^t by the fast unit, t = x log2 e
+// rounded, times 1 + c for what the rounding left out: e^x = 2^t e^c, c = x - t ln 2, |c| < 2^-16
+// where the result is not 0, so that 1 + c is e^c to fp32.  That stays within 4 units in the
+// last place however far a logit lies below the largest (without c: 15 at a distance of 40, 30 at
+// 80) and is shorter than expf.  The sigmoid, whose sums with the bias decide the choice, takes
+// expf and the IEEE division.
 #include <type_traits>
 
 #include "rowtypes.cuh"
@@ -119,13 +122,14 @@ __device__ __forceinline__ void clean2(T* v) {
   }
 }
 
-// 2^y by the fast unit; results below fp32's normal range are 0
-__device__ __forceinline__ float exp2_fast(float y) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
-  return r;
+// e^x of x <= 0; results below fp32's normal range are 0, NaN stays
+__device__ __forceinline__ float exp_below(float x) {
+  float t, r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(-128.0f));   // -inf and what overflows t: 0 all the same
+  t = x * 1.44269504f;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return fmaf(r, fmaf(t, -0.693147181f, x), r);
 }
-constexpr float kLog2e = 1.44269504f;
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
 
@@ -214,11 +218,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   float p = 0.f;
   if (score == MM_MOE_SCORE_SOFTMAX) {
     const float m = first ? value(first) : 0.f;   // the first choice is the row's largest logit
-    if (my_e >= 0) p = exp2_fast((value(my_key) - m) * kLog2e);
+    if (my_e >= 0) p = exp_below(value(my_key) - m);
     if (all) {
       float z = 0.f;
 #pragma unroll
-      for (int n = 0; n < N; ++n) z += exp2_fast((to_float(v[n]) - m) * kLog2e);
+      for (int n = 0; n < N; ++n) z += exp_below(to_float(v[n]) - m);
       z = group_sum<G>(z);
       if (my_e >= 0) p = __fdiv_rn(p, z);
     }
@@ -271,12 +275,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     if (m == -INFINITY) m = 0.f;                    // a row without logits: every exp is 0
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      v[n] = exp2_fast((v[n] - m) * kLog2e);
+      v[n] = exp_below(v[n] - m);
       z += v[n];
     }
     z = group_sum<G>(z);
     const float rz = z == 0.f ? 0.f : __fdiv_rn(1.0f, z);
-    const float p = e >= 0 ? exp2_fast((x - m) * kLog2e) * rz : 0.f;
+    const float p = e >= 0 ? exp_below(x - m) * rz : 0.f;
     const float s = group_sum<G>(g * p);
     d = p * (g - s);
     r = -rz * s;
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     for (int n = 0; n < N; ++n) v[n] = 0.f;
     if (score == MM_MOE_SCORE_SOFTMAX) {
       const float m = group_max<G>(x);
-      const float q0 = e >= 0 ? exp2_fast((x - m) * kLog2e) : 0.f;
+      const float q0 = e >= 0 ? exp_below(x - m) : 0.f;
       const float z = group_sum<G>(q0);
       const float q = e >= 0 ? __fdiv_rn(q0, z) : 0.f;
       d = q * (g - group_sum<G>(g * q));

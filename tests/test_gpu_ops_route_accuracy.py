@@ -1,10 +1,14 @@
-"""The router's weights of rows whose largest logit is infinite."""
+"""The router's weights and gradients relative to each value, however far it lies below the largest, and rows
+whose largest logit is infinite."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_ops_route import DT
+from test_gpu_ops_route import DT, plain, plain_gradient
 
 pytestmark = pytest.mark.gpu
+
+HALF = 2.0 ** -24
 
 
 @pytest.fixture(scope="module")
@@ -13,6 +17,52 @@ def ops():
     build.build()
     from moe_expert_forward_gb300 import ops
     return ops
+
+
+def far_rows(T, E, dt, seed):
+    """The largest logit 0, the others 8 to 84 below it in steps of 1/2: exact in every type, and so are the differences."""
+    g = torch.Generator().manual_seed(seed)
+    x = -torch.randint(16, 169, (T, E), generator=g).float() / 2
+    x[:, 3] = 0
+    return x.to(DT[dt])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T", [5, 16384])
+def test_softmax_weights_far_below_the_largest(ops, dt, renorm, T):
+    """Half units in the last place of fp32: 4 for the exponential (2 whole ones), 12 for at most 12 additions in a sum
+    that the largest term, exactly one, dominates, 1 for the division; the sum's other terms add less than 1."""
+    x = far_rows(T, 64, dt, T)
+    idx, w = ops.route(x.cuda(), 8, renorm=renorm)
+    some = slice(0, 200)
+    r_idx, r_w, _ = plain(x[some].double().numpy(), 8, None, "softmax", renorm, 1.0)
+    assert np.array_equal(idx[some].cpu().numpy(), r_idx)
+    err = np.abs(w[some].double().cpu().numpy() - r_w) / r_w
+    assert err.max() <= 18 * HALF, err.max() / HALF
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T", [5, 16384])
+def test_softmax_gradient_far_below_the_largest(ops, renorm, T):
+    """Incoming gradients of one sign, so that no sum cancels but the chosen logits': the others' relative error is that
+    of a weight (17 half units) and of the sum over the chosen (17, 8 products and 3 additions), two products more."""
+    x = far_rows(T, 64, "f32", T + 1)
+    g = 1 + torch.rand(T, 8, generator=torch.Generator().manual_seed(2))
+    idx, _ = ops.route(x.cuda(), 8, renorm=renorm)
+    d = ops.route_backward(x.cuda(), idx, g.cuda(), renorm=renorm)
+    some = slice(0, 200)
+    x64 = x[some].double().numpy()
+    r_idx, _, p = plain(x64, 8, None, "softmax", renorm, 1.0)
+    ref = plain_gradient(x64, r_idx, g[some].double().numpy(), p, "softmax", renorm, 1.0)
+    got = d[some].double().cpu().numpy()
+    other = np.ones(ref.shape, bool)
+    other[np.arange(len(ref))[:, None], r_idx] = False
+    if renorm:
+        assert (got[other] == 0).all()
+    else:
+        err = np.abs(got - ref)[other] / np.abs(ref)[other]
+        assert err.max() <= 48 * HALF, err.max() / HALF
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
