@@ -323,17 +323,28 @@ struct Form {
   static unsigned grid(int T) { return static_cast<unsigned>((T + 32 * kRouteWarps / G - 1) / (32 * kRouteWarps / G)); }
 };
 
-// Four rows a warp from so many rows on; below, the rows do not fill the SMs' warps. Measured, us forward, four rows a
-// warp / a warp a row, bf16: 65521x160 top-4 12.2 / 19.4, 16384x256 top-8 7.6 / 8.7, 8192x160 3.3 / 3.8, 2048x160
-// 2.3 / 2.2; fp32: 65521x160 20.9 / 28.8, 16384x160 6.4 / 8.2, 8192x256 top-8 9.4 / 8.3.
+// Four rows a warp from so many rows on; below, the rows do not fill the SMs' warps. Measured, us forward with cold
+// caches, four rows a warp / a warp a row, softmax with renorm, bf16: 65536x160 top-4 12.8 / 21.1, 16384x256 top-8
+// 8.5 / 9.2, 8192x256 top-8 5.6 / 5.7, 4096x256 top-8 4.0 / 3.5; fp32: 65536x160 21.6 / 30.8, 16384x256 top-8 15.8 /
+// 16.1, 8192x256 top-8 10.3 / 9.3.
 template <typename T>
 constexpr int kManyRows = sizeof(T) == 2 ? 8192 : 16384;
 
+// With a bias every logit is a sigmoid's argument and a lane has four times as many of them one after another: more
+// rows, and fewer experts, have to make up for it. The same figures, fp32 (bf16 the same within 5 %): 65536x64 top-6
+// 18.1 / 27.1, 16384x64 6.9 / 8.6, 8192x64 5.1 / 4.9; 65536x128 top-4 29.0 / 32.1, 32768x128 17.2 / 17.3, 16384x128
+// 11.3 / 10.0; 65536x160 39.1 / 39.6, 16384x160 13.9 / 12.0; 65536x256 top-8 79.7 / 70.3, 8192x256 16.1 / 12.4.
+template <typename T>
+bool many_rows(int rows, int E, bool bias) {
+  if (bias) return rows >= 16384 && E <= 160 && rows >= 256 * E;
+  return rows >= kManyRows<T>;
+}
+
 // f with the form that takes E logits a row; `bits` are the row pitches' and addresses' in bytes, or-ed.
 template <typename T, typename F>
-cudaError_t with_form(int rows, int E, int K, uint64_t bits, F f) {
-  if (rows >= kManyRows<T> && K <= 8 && E <= 256 && E % 2 == 0 && bits % (2 * sizeof(T)) == 0) {
-    const int n = (E + 15) / 16;
+cudaError_t with_form(int rows, int E, int K, bool bias, uint64_t bits, F f) {
+  if (many_rows<T>(rows, E, bias) && K <= 8 && E <= 256 && E % 2 == 0 && bits % (2 * sizeof(T)) == 0) {
+  const int n = (E + 15) / 16;
     if (n <= 2) return f(Form<2, 8, 2>{});
     if (n <= 4) return f(Form<4, 8, 2>{});
     if (n <= 6) return f(Form<6, 8, 2>{});
@@ -360,7 +371,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
   return with_dtype(a.dtype, [&](auto tag) {
     using T = decltype(tag);
     const uint64_t bits = reinterpret_cast<uintptr_t>(a.logits) | static_cast<uint64_t>(a.stride) * sizeof(T);
-    return with_form<T>(a.T, a.E, a.K, bits, [&](auto form) {
+    return with_form<T>(a.T, a.E, a.K, a.bias != nullptr, bits, [&](auto form) {
       using W = decltype(form);
       auto kernel = a.bias ? route_kernel<T, W::v, W::g, W::p, true> : route_kernel<T, W::v, W::g, W::p, false>;
       kernel<<<W::grid(a.T), 32 * kRouteWarps, 0, s>>>(static_cast<const T*>(a.logits), a.stride, a.T, a.E, a.K,
@@ -376,7 +387,7 @@ cudaError_t launch_route_backward(const RouteArgs& a, const int32_t* topk_idx, c
     using T = decltype(tag);
     const uint64_t bits = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(d_logits) |
                           static_cast<uint64_t>(a.stride | d_stride) * sizeof(T);
-    return with_form<T>(a.T, a.E, a.K, bits, [&](auto form) {
+    return with_form<T>(a.T, a.E, a.K, a.bias != nullptr, bits, [&](auto form) {
       using W = decltype(form);
       route_backward_kernel<T, W::v, W::g, W::p><<<W::grid(a.T), 32 * kRouteWarps, 0, s>>>(
           static_cast<const T*>(a.logits), a.stride, topk_idx, d_w, a.T, a.E, a.K, a.score, a.renorm, a.scale,

@@ -1,5 +1,5 @@
 """The router's weights and gradients relative to each value, however far it lies below the largest, and rows
-whose largest logit is infinite."""
+whose largest logit is infinite; and every form that the number of rows and experts chooses with a bias."""
 import numpy as np
 import pytest
 import torch
@@ -74,3 +74,19 @@ def test_no_choice_has_weight_zero_beside_an_infinite_logit(ops, dt, renorm, T):
     idx, w = ops.route(x.cuda(), 4, renorm=renorm)
     assert (idx.cpu() == torch.tensor([5, -1, -1, -1])).all()
     assert torch.isnan(w[:, 0]).all() and (w[:, 1:] == 0).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,K", [(16383, 64, 6), (16384, 64, 6), (32767, 128, 4), (32768, 128, 4), (16384, 160, 8),
+                                   (40960, 160, 8), (65536, 162, 2), (65536, 256, 8)])
+def test_bias_on_both_sides_of_the_row_rule(ops, T, E, K, dt):
+    """The rows' choices and weights are those of the same rows in a small batch, which takes a warp a row; a sum of at
+    most 8 scores in another order moves a weight by a few half units of 1."""
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    x = torch.randn(T, E, generator=g, device="cuda").to(DT[dt])
+    bias = torch.randn(E, generator=g, device="cuda")
+    idx, w = ops.route(x, K, bias=bias, score="sigmoid")
+    for at in (0, T // 2, T - 100):
+        i, v = ops.route(x[at:at + 100], K, bias=bias, score="sigmoid")
+        assert torch.equal(idx[at:at + 100], i)
+        assert (w[at:at + 100] - v).abs().max() <= 16 * HALF
