@@ -43,7 +43,11 @@ def serve(x, router, w1, w2, k):
     gate, up = gate_up.float().chunk(2, dim=1)
     inner = (torch.nn.functional.silu(gate) * up).to(x.dtype)
     down = ops.mx_product(*ops.mx_quantize(inner, chunks=True), second, routing=routing)
-    return ops.unpermute(down, routing, weight), (idx, weight, c1, s1, c2, s2)
+    y = ops.unpermute(down, routing, weight)
+    code, where = ops.sync_status()                                         # one check for all products so far
+    if code:
+        raise M.MMError(code, f"a 4-bit product (site {where})")
+    return y, (idx, weight, c1, s1, c2, s2)
 
 
 def fused(x, idx, weight, c1, s1, c2, s2):
@@ -121,6 +125,7 @@ def main(argv=None) -> dict:
     router = torch.randn(a.experts, a.hidden, generator=g, device="cuda") * a.hidden ** -0.5
     w1 = randn(a.experts, 2 * a.inner, a.hidden, scale=a.hidden ** -0.5)
     w2 = randn(a.experts, a.hidden, a.inner, scale=a.inner ** -0.5)
+    ops.sync_status()                                                       # what other work of this process left there
     y, kept = serve(x, router, w1, w2, a.topk)
     d_out = randn(a.tokens, a.hidden)
     mine = train_step(x, router, w1, w2, a.topk, d_out)

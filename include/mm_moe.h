@@ -517,7 +517,8 @@ int mm_moe_mx_prepare(const void* sf, int E, int N, int C, void* sfp, void* stre
  *              cnt[e] rows are written; other rows of out are left as they are.
  *   out        [rows, N], out_stride elements between rows
  *   status     device int32[4], zeroed by the caller: a wait past timeout_ms (0: 2000)
- *              leaves MM_MOE_ERR_TIMEOUT there and out undefined
+ *              leaves MM_MOE_ERR_TIMEOUT there (and in mm_moe_ops_status's record) and out
+ *              undefined
  *   debug_flags  0; bit 0 leaves one stage of each CTA unloaded, so that its wait runs out */
 int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, const void* w, const void* w_sfp, int E,
                       int N, const int32_t* cnt, const int32_t* blk_off, int dtype, void* out, int64_t out_stride,
@@ -529,7 +530,8 @@ int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, co
  *   slot   null: dense (E = 1, num_rows = T).  Else int32 [T, K] with cnt and blk_off of
  *          mm_moe_dispatch with block_m = 128, rows sorted by expert on the way.
  *   workspace  mm_moe_mx_linear_workspace bytes (K = 0: dense), 256-byte aligned; its
- *          status word is read by mm_moe_sync_status.  Up to 4 tokens of a dense linear, or
+ *          status word is read by mm_moe_sync_status (and a wait that ran out is in
+ *          mm_moe_ops_status's record too, whatever becomes of the workspace).  Up to 4 tokens of a dense linear, or
  *          16 pairs of a routed one, run in one launch where rows * N * C is small, and need
  *          none (0 bytes, null allowed; a workspace of 16 bytes or more gets its status
  *          word cleared). */
@@ -538,6 +540,13 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
                      int E, int N, const int32_t* slot, int K, const int32_t* cnt, const int32_t* blk_off,
                      int64_t num_rows, void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
                      unsigned timeout_ms, void* stream);
+
+/* Waits for `stream` and returns MM_MOE_ERR_TIMEOUT if a device wait of mm_moe_mx_product or
+ * mm_moe_mx_linear has run out on the current device, on any stream, since the last
+ * time this returned it; else MM_MOE_OK.  `where` (may be null) gets the site of the first
+ * such wait.  The record is the library's: it outlives the calls' status words and
+ * workspaces.  Not to be called while `stream` is being captured. */
+int mm_moe_ops_status(void* stream, int* where);
 
 /* Human-readable name of a return code. */
 const char* mm_moe_status_string(int code);

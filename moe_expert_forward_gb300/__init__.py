@@ -41,7 +41,7 @@ EXPORTS = ["mm_moe_default_options", "mm_moe_workspace_size", "mm_moe_weight_sf_
            "mm_moe_ep_barrier", "mm_moe_ep_barrier_ranks",
            "mm_moe_route", "mm_moe_route_backward", "mm_moe_sort_scratch_size", "mm_moe_sort", "mm_moe_permute", "mm_moe_unpermute", "mm_moe_unpermute_backward",
            "mm_moe_mx_scale_size", "mm_moe_mx_quantize", "mm_moe_mx_dequantize", "mm_moe_mx_prepare",
-           "mm_moe_mx_product", "mm_moe_mx_linear_workspace", "mm_moe_mx_linear"]
+           "mm_moe_mx_product", "mm_moe_mx_linear_workspace", "mm_moe_mx_linear", "mm_moe_ops_status"]
 
 
 class mm_moe_options(ctypes.Structure):
@@ -118,6 +118,7 @@ def lib() -> ctypes.CDLL:
             "mm_moe_mx_linear_workspace": (_I, [_I, _I, _I, _I, _I64, ctypes.POINTER(_SZ)]),
             "mm_moe_mx_linear": (_I, [_P, _I, _I64, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _I64, _P, _I64, _P, _SZ,
                                       ctypes.c_uint, _P]),
+            "mm_moe_ops_status": (_I, [_P, ctypes.POINTER(_I)]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -456,3 +457,9 @@ def mm_moe_mx_linear(x, dtype, row_stride, T, C, w, w_sfp, E, N, slot, K, cnt, b
                      workspace, ws_bytes, timeout_ms, stream) -> int:
     return lib().mm_moe_mx_linear(x, dtype, row_stride, T, C, w, w_sfp, E, N, slot, K, cnt, blk_off, num_rows, out,
                                   out_stride, workspace, ws_bytes, timeout_ms, stream)
+
+
+def mm_moe_ops_status(stream):
+    where = _I(0)
+    r = lib().mm_moe_ops_status(stream, ctypes.byref(where))
+    return r, where.value

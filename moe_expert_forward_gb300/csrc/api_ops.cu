@@ -262,4 +262,20 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
   return done(launch_mx_product(p, s));
 }
 
+int mm_moe_ops_status(void* stream, int* where) {
+  if (where) *where = 0;
+  int32_t* record = nullptr;
+  if (mx_report(&record) != cudaSuccess) return MM_MOE_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t h[4] = {0, 0, 0, 0};
+  if (cudaMemcpyAsync(h, record, sizeof(h), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MM_MOE_ERR_CUDA;
+  if (h[0] == 0) return MM_MOE_OK;
+  if (cudaMemsetAsync(record, 0, sizeof(h), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+    return MM_MOE_ERR_CUDA;
+  if (where) *where = h[1];
+  return h[0];
+}
+
 }  // extern "C"

@@ -13,6 +13,8 @@
 // Warps: 4 or 8 epilogue warps (one or two per TMEM lane quadrant), one that
 // issues scale copies and MMAs, and one TMA producer per stage.
 // Every wait is bounded; on a timeout each role winds down what it issued.
+#include <mutex>
+
 #include "cluster.cuh"
 #include "mx_linear.cuh"
 
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
         }
         step += nks;
       }
-      if (armed) mbar_wait_drain(&full[p], armed_parity, st, kSiteDrainCopies);
+      if (armed) mbar_drain(&full[p], armed_parity, st, s_abort, kSiteDrainCopies);
     }
   } else if (warp == C::kEpiWarps) {
     // ------------------------------------------------------------------ scale copies and MMAs
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
         phase ^= 1;
       }
       tc_commit(drain);
-      mbar_wait_drain(drain, 0, st, kSiteDrainMma);
+      mbar_drain(drain, 0, st, s_abort, kSiteDrainMma);
     }
     __syncwarp();
   } else {
@@ -318,7 +320,14 @@ __global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  if (threadIdx.x == 0) note_given_up(args, s_abort);
 }
+
+static __device__ int32_t g_report[4];
+
+constexpr int kMaxDevices = 64;
+int32_t* g_report_addr[kMaxDevices] = {nullptr};
+std::mutex g_report_mu;
 
 template <int BN, typename T, bool kSplit>
 cudaError_t launch_impl(const MxProductArgs& p, int parts, cudaStream_t s) {
@@ -391,8 +400,26 @@ cudaError_t launch_tile(const MxProductArgs& p, const Tile& t, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_mx_product(const MxProductArgs& p, cudaStream_t s) {
-  if (p.rows == 0) return cudaSuccess;
+cudaError_t mx_report(int32_t** record) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_report_mu);
+  if (!g_report_addr[dev]) {
+    void* p = nullptr;
+    e = cudaGetSymbolAddress(&p, g_report);
+    if (e != cudaSuccess) return e;
+    g_report_addr[dev] = static_cast<int32_t*>(p);
+  }
+  *record = g_report_addr[dev];
+  return cudaSuccess;
+}
+
+cudaError_t launch_mx_product(const MxProductArgs& args, cudaStream_t s) {
+  if (args.rows == 0) return cudaSuccess;
+  MxProductArgs p = args;
+  if (cudaError_t e = mx_report(&p.report)) return e;
   const int64_t blocks = (p.rows + kMxRows - 1) / kMxRows;
   const int sms = dev_info().sms;
   const int KS = mx_chunks(p.C) / 2;

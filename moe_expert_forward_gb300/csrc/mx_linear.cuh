@@ -28,6 +28,7 @@ struct MxArgs {
   int wait_prior;            // launched programmatically: activations come from the kernel before
   int unreachable;           // leave the last stage of the CTA's last task out
   int* status;
+  int* report;
   uint64_t timeout_ns;
 };
 
@@ -56,6 +57,18 @@ __device__ __forceinline__ int last_not_above(const int* a, int n, int v) {
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const Status& st, volatile int* abort,
                                                int where) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, st, abort, where));
+}
+
+// mbar_wait_drain, and on its limit the CTA's flag raised.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, const Status& st, volatile int* abort,
+                                           int where) {
+  if (!mbar_wait_drain(bar, parity, st, where)) *abort = 1;
+}
+
+// One thread of a CTA at its end: a wait that ran out goes into the library's record too, which is there to be read
+// when the call's own status word no longer is. The first one stays.
+__device__ __forceinline__ void note_given_up(const MxArgs& a, volatile int* abort) {
+  if (*abort && atomicCAS(a.report, 0, MM_MOE_ERR_TIMEOUT) == 0) a.report[1] = *(volatile int*)(a.status + 1);
 }
 
 // Two accumulators as one 32-bit word of 16-bit elements.
@@ -220,7 +233,7 @@ inline MxArgs mx_args(const MxProductArgs& p, int elem, int tile_n) {
   a.lines = (reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(a.out_pitch)) % 32 == 0;
   a.wait_prior = p.after_quantize;
   a.unreachable = p.unreachable;
-  a.status = p.status; a.timeout_ns = p.timeout_ns;
+  a.status = p.status; a.report = p.report; a.timeout_ns = p.timeout_ns;
   return a;
 }
 // codes of `rows` rows as [rows, C/2] bytes in boxes of one stage x box_rows

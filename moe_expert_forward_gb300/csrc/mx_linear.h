@@ -56,7 +56,10 @@ struct MxProductArgs {
   uint64_t timeout_ns;
   bool after_quantize;       // launched programmatically behind the quantiser
   bool unreachable;          // the last stage of each CTA's last task is never loaded (a test of the bounded waits)
+  int32_t* report = nullptr; // mx_report's record, filled in by launch_mx_product
 };
+// Device address of the current device's record of waits that ran out in any product: four words, zero until one did.
+cudaError_t mx_report(int32_t** record);
 cudaError_t launch_mx_product(const MxProductArgs& a, cudaStream_t s);
 // on CTA pairs: two 128-row blocks a task
 cudaError_t launch_mx_product_pair(const MxProductArgs& a, cudaStream_t s);

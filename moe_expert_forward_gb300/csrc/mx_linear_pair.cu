@@ -199,12 +199,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (rank == 0) {
         s_armed[p] = loaded;
-        if (loaded) mbar_wait_drain(&full[p], (loaded - 1) & 1, st, kSiteDrainCopies);
+        if (loaded) mbar_drain(&full[p], (loaded - 1) & 1, st, s_abort, kSiteDrainCopies);
       } else {
         st_cluster_int(map_shared(&s_peer[p], 0), loaded);
       }
       // the leader's last commit to this CTA's barrier has arrived before the CTA leaves
-      if (loaded && !*s_abort) mbar_wait_drain(&empty[p], (loaded - 1) & 1, st, kSiteDrainEmpty);
+      if (loaded && !*s_abort) mbar_drain(&empty[p], (loaded - 1) & 1, st, s_abort, kSiteDrainEmpty);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMAs (leader)
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase ^= 1;
       }
       tc_commit_pair(map_shared(drain, 0));
-      mbar_wait_drain(drain, 0, st, kSiteDrainMma);
+      mbar_drain(drain, 0, st, s_abort, kSiteDrainMma);
     }
     __syncwarp();
   } else if (warp == kScaleWarp) {
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase ^= 1;
       }
       tc_commit_pair(map_shared(drain + 1, 0));
-      mbar_wait_drain(drain + 1, 0, st, kSiteDrainMma);
+      mbar_drain(drain + 1, 0, st, s_abort, kSiteDrainMma);
     }
     __syncwarp();
   } else {
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int p = threadIdx.x;
     if (s_peer[p] > s_armed[p]) {
       mbar_arrive_expect_tx(&full[p], kCtaBytes);
-      mbar_wait_drain(&full[p], (s_peer[p] - 1) & 1, st, kSiteDrainCopies);
+      mbar_drain(&full[p], (s_peer[p] - 1) & 1, st, s_abort, kSiteDrainCopies);
     }
   }
   __syncthreads();
@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
   }
+  if (threadIdx.x == 0) note_given_up(args, s_abort);
 }
 
 }  // namespace

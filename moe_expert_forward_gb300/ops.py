@@ -8,6 +8,7 @@
   mx_weights, mx_product, mx_linear
                                 products of 4-bit operands: dense, or each expert's
                                 rows with its matrix
+  sync_status                   whether a device wait of a product has run out
 
 Argument marshalling and checks only; the arithmetic is in the CUDA library,
 whose C entry points (include/mm_moe.h) define each operator.  Every function
@@ -23,7 +24,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (MM_MOE_ERR_INVALID_ARG, MM_MOE_SCORE_SIGMOID, MM_MOE_SCORE_SOFTMAX, MMError, _check, lib)
+from . import (MM_MOE_ERR_INVALID_ARG, MM_MOE_SCORE_SIGMOID, MM_MOE_SCORE_SOFTMAX, MMError, _check, lib,
+               mm_moe_ops_status)
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _SCORES = {"softmax": MM_MOE_SCORE_SOFTMAX, "sigmoid": MM_MOE_SCORE_SIGMOID}
@@ -371,8 +373,9 @@ def mx_product(codes, sf, weights: MxWeights, routing: Optional[Routing] = None,
     """Product of 4-bit rows (mx_quantize with chunks) and weights: [rows, N].
 
     Dense with one matrix; with a routing (block_m = 128) every expert's rows take
-    its matrix and rows of padding are left as they are.  status: int32 [4] zeroed by
-    the caller, read for MM_MOE_ERR_TIMEOUT; allocated here when None."""
+    its matrix and rows of padding are left as they are.  A device wait that runs out
+    leaves the result undefined and is reported by sync_status, and in status (int32
+    [4] zeroed by the caller) where that is given."""
     rows = codes.shape[0]
     cp = _whole(codes, "mx_product", "codes", (rows, weights.C // 2), torch.uint8)
     sp = _whole(sf, "mx_product", "sf", (_scale_bytes(rows, weights.C),), torch.uint8)
@@ -415,9 +418,10 @@ def mx_linear(x, weights: MxWeights, routing: Optional[Routing] = None, out=None
 
     A few tokens (up to FEW_TOKENS, or FEW_PAIRS routed pairs) run in one launch without
     a workspace.  Dense: [T, N].  With a routing (block_m = 128): [routing.rows, N], every token's
-    row through its experts' matrices, rows of padding left as they are.  With a
-    workspace of the caller's (mx_linear_workspace), sync_status(workspace) of the
-    package reports a device wait that timed out."""
+    row through its experts' matrices, rows of padding left as they are.  A device
+    wait that runs out leaves the result undefined and is reported by sync_status, and by
+    the package's sync_status(workspace) where the workspace is the caller's
+    (mx_linear_workspace)."""
     code = _rows(x, "mx_linear", "x", weights.C)
     T, C = x.shape
     rows, slot, K = T, None, 0
@@ -439,3 +443,9 @@ def mx_linear(x, weights: MxWeights, routing: Optional[Routing] = None, out=None
                                   weights.sfp.data_ptr(), weights.E, weights.N, slot, K, cnt, blk, rows,
                                   out.data_ptr(), _pitch(out), ws, ws_bytes, 0, _stream(stream)), "mm_moe_mx_linear")
     return out
+
+
+def sync_status(stream=None):
+    """Waits for `stream`; (code, where) of the first device wait of a product that ran out on this device since the
+    last report, on any stream: MM_MOE_ERR_TIMEOUT and its site, or (0, 0)."""
+    return mm_moe_ops_status(_stream(stream))

@@ -145,3 +145,12 @@ def test_routings_and_weights_of_another_device_are_refused(stand):
             with pytest.raises(M.MMError):
                 call()
     assert len(stand.calls) == before
+
+
+def test_sync_status_asks_the_library(monkeypatch):
+    monkeypatch.setattr(ops, "mm_moe_ops_status", lambda stream: (M.MM_MOE_ERR_TIMEOUT, stream))
+    assert ops.sync_status(SIDE) == (M.MM_MOE_ERR_TIMEOUT, SIDE)
+    if not torch.cuda.is_available():
+        from moe_expert_forward_gb300 import build
+        build.build()
+        assert M.mm_moe_ops_status(None) == (M.MM_MOE_ERR_CUDA, 0)
