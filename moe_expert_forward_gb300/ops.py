@@ -17,6 +17,11 @@ returns at once.  What a call allocates is `stream`'s memory; its results are
 also marked as used on the stream that is current at the call.  Other uses of a
 tensor on a stream that it was not allocated on are the caller's to order and to
 keep alive.
+
+Nothing here is recorded by autograd: the *_backward calls give the gradients, for
+example from a torch.autograd.Function.  So while grad mode is on, the calls whose
+result a gradient would flow through refuse tensors that require one; detach them,
+or call under torch.no_grad().
 """
 from __future__ import annotations
 
@@ -125,6 +130,15 @@ def _here(t, what: str, name: str):
         _bad(what, f"{name} must be a tensor on the current CUDA device")
 
 
+def _no_grad(what: str, *tensors):
+    """A result without a gradient is no answer to a tensor that requires one."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                _bad(what, "a tensor requires grad, and autograd does not see this call: detach it, or call under "
+                           "torch.no_grad() (gradients: the *_backward calls)")
+
+
 def _routing_here(r: Routing, what: str):
     """The calls pass a routing's addresses on, so it has to be the current device's."""
     _here(r._buf, what, "routing")
@@ -168,6 +182,7 @@ def route(logits, k: int, bias=None, score: str = "softmax", renorm: bool = True
     -1, weight 0).  Weights: scale times the softmax over all experts, or the
     sigmoid, of the chosen logits, divided by their sum where renorm."""
     code = _rows(logits, "route", "logits")
+    _no_grad("route", logits, bias)
     T, E = logits.shape
     if score not in _SCORES:
         _bad("route", f"score must be one of {sorted(_SCORES)}, got {score!r}")
@@ -230,6 +245,7 @@ def sort_tokens(topk_idx, E: int, block_m: int = 16, stream=None) -> Routing:
 def permute(x, routing: Routing, stream=None):
     """Tokens x [T, H] at their pool rows: [routing.rows, H], zero on padding."""
     code = _rows(x, "permute", "x")
+    _no_grad("permute", x)
     r = routing
     _routing_here(r, "permute")
     T, H = x.shape
@@ -246,6 +262,7 @@ def unpermute(rows, routing: Routing, topk_w=None, stream=None):
     """Pool rows [routing.rows, H] back to tokens [T, H]: the sum of each token's
     rows times topk_w (fp32 [T, K]; None: ones), masked slots left out."""
     code = _rows(rows, "unpermute", "rows")
+    _no_grad("unpermute", rows, topk_w)
     r = routing
     _routing_here(r, "unpermute")
     H = rows.shape[1]
@@ -423,6 +440,7 @@ def mx_linear(x, weights: MxWeights, routing: Optional[Routing] = None, out=None
     the package's sync_status(workspace) where the workspace is the caller's
     (mx_linear_workspace)."""
     code = _rows(x, "mx_linear", "x", weights.C)
+    _no_grad("mx_linear", x)
     T, C = x.shape
     rows, slot, K = T, None, 0
     if routing is not None:

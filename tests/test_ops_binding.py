@@ -154,3 +154,26 @@ def test_sync_status_asks_the_library(monkeypatch):
         from moe_expert_forward_gb300 import build
         build.build()
         assert M.mm_moe_ops_status(None) == (M.MM_MOE_ERR_CUDA, 0)
+
+
+def test_tensors_that_require_grad_are_refused_where_a_gradient_would_be_lost(stand):
+    x, idx, topk_w = torch.ones(6, 64), torch.ones(6, 2, dtype=torch.int32), torch.ones(6, 2)
+    r, w = ops.sort_tokens(idx, 4, 128), weights(1, 32, 64)
+    rows = ops.permute(x, r)
+    need = [t.clone().requires_grad_() for t in (x, rows, topk_w)]
+    need_x, need_rows, need_w = need
+    calls = [lambda: ops.route(need_x, 2), lambda: ops.route(x, 2, bias=need_x[0], score="sigmoid"),
+             lambda: ops.permute(need_x, r), lambda: ops.unpermute(need_rows, r, topk_w),
+             lambda: ops.unpermute(rows, r, need_w), lambda: ops.mx_linear(need_x, w)]
+    for call in calls:
+        before = len(stand.calls)
+        with pytest.raises(M.MMError, match="requires grad"):
+            call()
+        assert len(stand.calls) == before
+        with torch.no_grad():
+            call()
+        assert len(stand.calls) == before + 1
+    # no gradient passes through these: rounding to 4 bits, and gradients themselves
+    ops.mx_quantize(need_x)
+    ops.route_backward(need_x, idx, topk_w)
+    ops.unpermute_backward(x, need_rows, r, need_w)
