@@ -10,8 +10,9 @@
 // What bounds it is latency, a chain of a few barriers, then each SM's scattered
 // stores; the two dispatch kernels spread over all SMs and take over where a warp's
 // run gets long. Measured (us, this kernel / the two): 1024 pairs over 256 experts
-// 6.3 / 12.3, 49152 over 384 9.9 / 20.5, 65536 over 256 10.5 / 17.6, 262144 over 256
-// 25.6 / 22.6.
+// 6.3 / 12.3, 49152 over 384 9.9 / 20.5, over 256 65536 10.5 / 16.5, 131072 15.5 / 18.5,
+// 196608 21.0 / 20.6, 229376 23.7 / 20.6, 262144 25.5 / 20.7; 196608 over 64 18.8 / 18.5,
+// over 384 21.8 / 28.0, over 1024 26.0 / 45.2.
 #include "cluster.cuh"
 #include "internal.h"
 
