@@ -22,9 +22,12 @@
 // the largest word below the last choice, one add-and-max per logit: of differences
 // k - last mod 2^32, those of words below `last` are the larger ones.  Two forms:
 //   G = 32, P = 1  a warp a row: few rows, where the latency of one row counts
-//   G = 8, P = 2   four rows a warp: many rows, where the issue of instructions
-//                  bounds it (65536 rows of 160 read 21 MB, 3 us) and the reductions
-//                  and the work at a row's end are shared by four
+//   G = 8, P = 2   four rows a warp: many rows; the reductions and the work at a
+//                  row's end are shared by four
+// What bounds many rows (65536 of 160 read 21 MB, 3 us): the choice, the integer pipe and the
+// issue slots while an SM is busy (67 % of them used; most warps that do not issue wait for
+// that pipe or for their turn), with a bias the chains of dependent instructions (96 registers
+// a thread leave 28 % of the warps); the gradient, the latency of its loads.
 //
 // The softmax's exponentials of differences x <= 0 are 2^t by the fast unit, t = x log2 e
 // rounded, times 1 + c for what the rounding left out: e^x = 2^t e^c, c = x - t ln 2, |c| < 2^-16
