@@ -14,9 +14,10 @@ Argument marshalling and checks only; the arithmetic is in the CUDA library,
 whose C entry points (include/mm_moe.h) define each operator.  Every function
 enqueues on `stream` (default: the current stream) of the current device and
 returns at once.  What a call allocates is `stream`'s memory; its results are
-also marked as used on the stream that is current at the call.  Other uses of a
-tensor on a stream that it was not allocated on are the caller's to order and to
-keep alive.
+also marked as used on the stream that is current at the call (7 us a tensor on the
+host; `with torch.cuda.stream(s):` around calls makes s the current stream and needs
+none of it).  Other uses of a tensor on a stream that it was not allocated on are
+the caller's to order and to keep alive.
 
 Nothing here is recorded by autograd: the *_backward calls give the gradients, for
 example from a torch.autograd.Function.  So while grad mode is on, the calls whose
@@ -103,25 +104,44 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _new(stream, shape, dtype, device, zero=False):
+_streams = {}            # torch's objects of streams by device and number; making one takes 2 us
+
+
+def _torch_stream(device: int, ptr: int, make):
+    key = (device, ptr)
+    if key not in _streams:
+        _streams[key] = make()
+    return _streams[key]
+
+
+def _new(stream, shape, dtype, device, zero=False, shared=False):
     """A tensor (uninitialised, or zeroed in `stream`'s order) for a call on `stream`, of that stream's memory: what the
-    current stream frees and takes again would otherwise meet kernels that `stream` still runs."""
+    current stream frees and takes again would otherwise meet kernels that `stream` still runs.  shared: marked as used
+    on the current stream too.  (torch.cuda.stream as a context would do; it takes about 15 us, a whole call 10.)"""
     make = torch.zeros if zero else torch.empty
-    ptr = 0 if stream is None else _stream(stream)
-    if stream is None or ptr == _raw_stream(_device()):
+    if stream is None:
         return make(shape, dtype=dtype, device=device)
+    ptr, dev = _stream(stream), _device()
+    current = _raw_stream(dev)
+    if ptr == current:
+        return make(shape, dtype=dtype, device=device)
+    here = _torch_stream(dev, current, torch.cuda.current_stream)
     # stream 0 has no external form
-    with torch.cuda.stream(torch.cuda.ExternalStream(ptr) if ptr else torch.cuda.default_stream()):
-        return make(shape, dtype=dtype, device=device)
+    there = _torch_stream(dev, ptr, lambda: torch.cuda.ExternalStream(ptr) if ptr else torch.cuda.default_stream())
+    torch.cuda.set_stream(there)
+    try:
+        t = make(shape, dtype=dtype, device=device)
+    finally:
+        torch.cuda.set_stream(here)
+    if shared:
+        t.record_stream(here)
+    return t
 
 
 def _result(stream, shape, dtype, device):
     """What a call on `stream` returns: memory that no work queued on the current stream still uses, and that is not
     taken again before the work which the current stream has been given when it is freed."""
-    t = _new(stream, shape, dtype, device)
-    if stream is not None and _stream(stream) != _raw_stream(_device()):
-        t.record_stream(torch.cuda.current_stream())
-    return t
+    return _new(stream, shape, dtype, device, shared=True)
 
 
 def _here(t, what: str, name: str):

@@ -50,6 +50,8 @@ def stand(monkeypatch):
     monkeypatch.setattr(ops, "_device", lambda: -1)               # what a CPU tensor says of its device
     monkeypatch.setattr(ops, "_raw_stream", lambda device: s.current)
     monkeypatch.setattr(torch.cuda, "stream", s.on)
+    monkeypatch.setattr(torch.cuda, "set_stream", lambda stream: setattr(s, "current", stream))
+    monkeypatch.setattr(ops, "_streams", {})
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: s.current)
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: 0)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda p, device=None: p)
