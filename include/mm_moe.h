@@ -543,7 +543,8 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
 
 /* Waits for `stream` and returns MM_MOE_ERR_TIMEOUT if a device wait of mm_moe_mx_product or
  * mm_moe_mx_linear has run out on the current device, on any stream, since the last
- * time this returned it; else MM_MOE_OK.  `where` (may be null) gets the site of the first
+ * time this returned it; else MM_MOE_OK (calls on other streams that are still running
+ * are not waited for).  `where` (may be null) gets the site of the first
  * such wait.  The record is the library's: it outlives the calls' status words and
  * workspaces.  Not to be called while `stream` is being captured. */
 int mm_moe_ops_status(void* stream, int* where);

@@ -154,7 +154,7 @@ def _no_grad(what: str, *tensors):
     """A result without a gradient is no answer to a tensor that requires one."""
     if torch.is_grad_enabled():
         for t in tensors:
-            if t is not None and t.requires_grad:
+            if getattr(t, "requires_grad", False):     # what is no tensor is refused by the checks after this
                 _bad(what, "a tensor requires grad, and autograd does not see this call: detach it, or call under "
                            "torch.no_grad() (gradients: the *_backward calls)")
 

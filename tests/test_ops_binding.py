@@ -175,6 +175,9 @@ def test_tensors_that_require_grad_are_refused_where_a_gradient_would_be_lost(st
         with torch.no_grad():
             call()
         assert len(stand.calls) == before + 1
+    for call in (lambda: ops.unpermute(rows, r, [1.0]), lambda: ops.route(x, 2, bias=[1.0], score="sigmoid")):
+        with pytest.raises(M.MMError, match="must be a tensor"):
+            call()
     # no gradient passes through these: rounding to 4 bits, and gradients themselves
     ops.mx_quantize(need_x)
     ops.route_backward(need_x, idx, topk_w)
