@@ -530,9 +530,10 @@ int mm_moe_mx_product(const void* codes, const void* sf, int64_t rows, int C, co
  *   slot   null: dense (E = 1, num_rows = T).  Else int32 [T, K] with cnt and blk_off of
  *          mm_moe_dispatch with block_m = 128, rows sorted by expert on the way.
  *   workspace  mm_moe_mx_linear_workspace bytes (K = 0: dense), 256-byte aligned; its
- *          status word is read by mm_moe_sync_status (and a wait that ran out is in
- *          mm_moe_ops_status's record too, whatever becomes of the workspace).  Up to 4 tokens of a dense linear, or
- *          16 pairs of a routed one, run in one launch where rows * N * C is small, and need
+ *          status word is read by mm_moe_sync_status (a wait that ran out is in
+ *          mm_moe_ops_status's record too, whatever becomes of the workspace).  Up to
+ *          4 tokens of a dense linear, or 16 pairs of a routed one, run in one
+ *          launch where rows * N * C is small, and need
  *          none (0 bytes, null allowed; a workspace of 16 bytes or more gets its status
  *          word cleared). */
 int mm_moe_mx_linear_workspace(int T, int C, int N, int K, int64_t num_rows, size_t* bytes);

@@ -281,9 +281,12 @@ def permute(x, routing: Routing, stream=None):
 def unpermute(rows, routing: Routing, topk_w=None, stream=None):
     """Pool rows [routing.rows, H] back to tokens [T, H]: the sum of each token's
     rows times topk_w (fp32 [T, K]; None: ones), masked slots left out."""
-    code = _rows(rows, "unpermute", "rows")
     _no_grad("unpermute", rows, topk_w)
-    r = routing
+    return _unpermute(rows, routing, topk_w, stream)
+
+
+def _unpermute(rows, r: Routing, topk_w, stream):
+    code = _rows(rows, "unpermute", "rows")
     _routing_here(r, "unpermute")
     H = rows.shape[1]
     if rows.shape[0] != r.rows or not rows.is_contiguous():
@@ -297,7 +300,7 @@ def unpermute(rows, routing: Routing, topk_w=None, stream=None):
 
 def permute_backward(d_rows, routing: Routing, stream=None):
     """Gradient of permute: the sum of the gradients of each token's rows, [T, H]."""
-    return unpermute(d_rows, routing, None, stream)
+    return _unpermute(d_rows, routing, None, stream)
 
 
 def unpermute_backward(d_out, rows, routing: Routing, topk_w=None, stream=None):

@@ -182,3 +182,4 @@ def test_tensors_that_require_grad_are_refused_where_a_gradient_would_be_lost(st
     ops.mx_quantize(need_x)
     ops.route_backward(need_x, idx, topk_w)
     ops.unpermute_backward(x, need_rows, r, need_w)
+    ops.permute_backward(need_rows, r)
