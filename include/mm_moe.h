@@ -411,7 +411,7 @@ int mm_moe_ep_barrier_ranks(void* const* peer_flags, int N, uint32_t epoch, unsi
 
 /* ------------------------------------------------------------------------
  * Operators around the expert layer: the router's top-k, tokens sorted by
- * expert and back, 4-bit quantisation and product.  Each enqueues its kernels
+ * expert and back, 4-bit quantisation and product; then rows in 8 bits.  Each enqueues its kernels
  * on `stream`; none allocates or synchronises.  Element types of rows: */
 #define MM_MOE_DTYPE_F32 0
 #define MM_MOE_DTYPE_BF16 1
@@ -542,8 +542,97 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
                      int64_t num_rows, void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
                      unsigned timeout_ms, void* stream);
 
-/* Waits for `stream` and returns MM_MOE_ERR_TIMEOUT if a device wait of mm_moe_mx_product or
- * mm_moe_mx_linear has run out on the current device, on any stream, since the last
+/* ------------------------------------------------------------------------
+ * Rows held in 8 bits: the layer's activations (x and x_sf), made by a quantiser or by
+ * the norm in front of the layer, and what a training step keeps of them.  The two
+ * forms ("variant") are the layer's:
+ *   MM_MOE_VARIANT_MX  codes e4m3 [rows, 32 ceil(C/32)], scales UE8M0 [rows, ceil(C/32)]:
+ *                      per 32 elements 2^e, e the smallest integer with
+ *                      448 * 2^e >= max(amax, 1e-10), the byte e + 127
+ *   MM_MOE_VARIANT_F8  codes e4m3 [rows, 128 ceil(C/128)], scales fp32 [rows,
+ *                      ceil(C/128)]: per 128 elements max(amax, 1e-10) / 448
+ * A row's last block is filled up with zeros; codes round to nearest, ties to the even
+ * code, and are 16-byte aligned.  A block with a NaN or an infinity gets zero codes and
+ * a scale of NaN (MX: byte 255), and everything computed from it is NaN; codes 0x7F and
+ * 0xFF do not occur. */
+int mm_moe_rows_quantize(const void* x, int dtype, int64_t row_stride, int64_t R, int C, int variant, void* codes,
+                         void* sf, void* stream);
+
+/* The values codes and scales stand for, rounded once: out [R, C] of `dtype` (bf16 and
+ * fp32 hold those of MX exactly), out_stride elements between rows. */
+int mm_moe_rows_dequantize(const void* codes, const void* sf, int64_t R, int C, int variant, int dtype, void* out,
+                           int64_t out_stride, void* stream);
+
+/* Root-mean-square norm with the residual's addition.
+ *   h    = x + residual, rounded to `dtype` (h = x without a residual)
+ *   rstd = 1 / sqrt(mean(h^2) + eps), fp32 [T], from the rounded h
+ *   y    = h * rstd * weight
+ *   x, residual  [T, H] of `dtype`, their strides in elements between rows
+ *   residual, h  both or neither (null); h [T, H] contiguous
+ *   weight       [H] of weight_dtype: `dtype` or fp32
+ *   y            [T, H] contiguous of `dtype`, or null
+ *   codes, sf    y in 8 bits of `variant` (from the fp32 y), or both null
+ *   rstd         what the gradients take
+ * eps >= 0; H of any size (up to 32768 elements a row is read once). */
+int mm_moe_rms_norm(const void* x, int dtype, int64_t x_stride, const void* residual, int64_t residual_stride,
+                    const void* weight, int weight_dtype, int64_t T, int H, float eps, void* h, void* y, int variant,
+                    void* codes, void* sf, float* rstd, void* stream);
+
+/* Gradients of mm_moe_rms_norm: with g = d_y * weight and n = h * rstd,
+ *   d_x = d_h + rstd * (g - n * mean(g * n))  of `dtype`, [T, H] contiguous: x's and the
+ *         residual's both; d_h (the gradient that reaches h otherwise) may be null
+ *   d_weight = sum over rows of d_y * n, fp32 [H], in a fixed order
+ * h is the forward call's (x without a residual).  scratch: mm_moe_rms_norm_scratch_size
+ * bytes, 16-byte aligned. */
+int mm_moe_rms_norm_scratch_size(int64_t T, int H, size_t* bytes);
+int mm_moe_rms_norm_backward(const void* d_y, int dtype, int64_t d_y_stride, const void* h, int64_t h_stride,
+                             const void* weight, int weight_dtype, const float* rstd, const void* d_h,
+                             int64_t d_h_stride, int64_t T, int H, void* d_x, float* d_weight, void* scratch,
+                             size_t scratch_bytes, void* stream);
+
+/* The activation between the experts' products: a = gate * sigmoid(gate) * up * w.
+ *   h      [rows, 2I] of `dtype`, [gate | up], h_stride elements between rows
+ *   slot, src, blk_off  null: every row counts, and w is null (ones).  Else the routing of
+ *          mm_moe_sort or mm_moe_dispatch (of T, K, E, block_m) whose pool the rows are:
+ *          w fp32 [T, K] (null: ones) is applied to each pair's row, and in rows that hold
+ *          no pair h is not read and every output is zero
+ *   a      [rows, I] contiguous of `dtype`, or null
+ *   codes, sf      a in 8 bits (MX, from the fp32 a), or null
+ *   kept, kept_sf  gate and up in 8 bits (MX) for the gradient, or null: codes
+ *          [rows, 2, 32 ceil(I/32)], scales [rows, 2, ceil(I/32)] */
+int mm_moe_swiglu(const void* h, int dtype, int64_t h_stride, int64_t rows, int I, int T, int K, int E, int block_m,
+                  const int32_t* slot, const int32_t* src, const int32_t* blk_off, const float* w, void* a,
+                  void* codes, void* sf, void* kept, void* kept_sf, void* stream);
+
+/* Gradients of mm_moe_swiglu at the kept values, s = sigmoid(gate):
+ *   d_h [rows, 2I] contiguous of `dtype`: d_a w up s (1 + gate (1 - s)) and d_a w gate s; zero
+ *          in rows that hold no pair (d_a is not read there)
+ *   d_w fp32 [T, K] or null (not computed): the sum over the pair's row of d_a gate s up, 0 where masked
+ *   d_a [rows, I] of `dtype`, d_stride elements between rows; the rest as in the forward call */
+int mm_moe_swiglu_backward(const void* d_a, int dtype, int64_t d_stride, const void* kept, const void* kept_sf,
+                           int64_t rows, int I, int T, int K, int E, int block_m, const int32_t* slot,
+                           const int32_t* src, const int32_t* blk_off, const float* w, void* d_h, float* d_w,
+                           void* stream);
+
+/* Weight gradients from rows kept in 8 bits (MX): out[e][n][c] = the sum over expert e's
+ * rows r of d_y[r][n] * x[r][c], fp32 sums rounded once.
+ *   d_y    bf16 [rows, N], d_stride elements between rows (16-byte aligned rows are the fastest)
+ *   codes, sf  x [rows, C], or with by_token [T, C]: the tokens' own rows
+ *   cnt, src, blk_off  null: one dense sum over all rows (T, K, E, block_m are not read).  Else the
+ *          routing whose pool the rows are: cnt[e] rows of expert e from row blk_off[e] * block_m on.
+ *          Other rows are not part of any sum, whatever they hold.
+ *   out    [E, N, C] (dense: [N, C]) contiguous of `dtype` (fp32 or bf16), fully overwritten;
+ *          zero for an expert without rows
+ * A device wait past timeout_ms (0: 2000) leaves out undefined and is reported by
+ * mm_moe_ops_status.  debug_flags: 0; bit 0 leaves one stage of each CTA unloaded, so that its
+ * wait runs out. */
+int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* codes, const void* sf, int C,
+                       int T, int K, int E, int block_m, const int32_t* cnt, const int32_t* src,
+                       const int32_t* blk_off, int by_token, int dtype, void* out, unsigned timeout_ms,
+                       int debug_flags, void* stream);
+
+/* Waits for `stream` and returns MM_MOE_ERR_TIMEOUT if a device wait of mm_moe_mx_product,
+ * mm_moe_mx_linear or mm_moe_weight_grad has run out on the current device, on any stream, since the last
  * time this returned it; else MM_MOE_OK (calls on other streams that are still running
  * are not waited for).  `where` (may be null) gets the site of the first
  * such wait.  The record is the library's: it outlives the calls' status words and

@@ -41,7 +41,9 @@ EXPORTS = ["mm_moe_default_options", "mm_moe_workspace_size", "mm_moe_weight_sf_
            "mm_moe_ep_barrier", "mm_moe_ep_barrier_ranks",
            "mm_moe_route", "mm_moe_route_backward", "mm_moe_sort_scratch_size", "mm_moe_sort", "mm_moe_permute", "mm_moe_unpermute", "mm_moe_unpermute_backward",
            "mm_moe_mx_scale_size", "mm_moe_mx_quantize", "mm_moe_mx_dequantize", "mm_moe_mx_prepare",
-           "mm_moe_mx_product", "mm_moe_mx_linear_workspace", "mm_moe_mx_linear", "mm_moe_ops_status"]
+           "mm_moe_mx_product", "mm_moe_mx_linear_workspace", "mm_moe_mx_linear", "mm_moe_ops_status",
+           "mm_moe_rows_quantize", "mm_moe_rows_dequantize", "mm_moe_rms_norm", "mm_moe_rms_norm_scratch_size",
+           "mm_moe_rms_norm_backward", "mm_moe_swiglu", "mm_moe_swiglu_backward", "mm_moe_weight_grad"]
 
 
 class mm_moe_options(ctypes.Structure):
@@ -119,6 +121,19 @@ def lib() -> ctypes.CDLL:
             "mm_moe_mx_linear": (_I, [_P, _I, _I64, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _I64, _P, _I64, _P, _SZ,
                                       ctypes.c_uint, _P]),
             "mm_moe_ops_status": (_I, [_P, ctypes.POINTER(_I)]),
+            # rows in 8 bits
+            "mm_moe_rows_quantize": (_I, [_P, _I, _I64, _I64, _I, _I, _P, _P, _P]),
+            "mm_moe_rows_dequantize": (_I, [_P, _P, _I64, _I, _I, _I, _P, _I64, _P]),
+            "mm_moe_rms_norm": (_I, [_P, _I, _I64, _P, _I64, _P, _I, _I64, _I, ctypes.c_float, _P, _P, _I, _P, _P, _P,
+                                     _P]),
+            "mm_moe_rms_norm_scratch_size": (_I, [_I64, _I, ctypes.POINTER(_SZ)]),
+            "mm_moe_rms_norm_backward": (_I, [_P, _I, _I64, _P, _I64, _P, _I, _P, _P, _I64, _I64, _I, _P, _P, _P, _SZ,
+                                              _P]),
+            "mm_moe_swiglu": (_I, [_P, _I, _I64, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+            "mm_moe_swiglu_backward": (_I, [_P, _I, _I64, _P, _P, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
+                                            _P]),
+            "mm_moe_weight_grad": (_I, [_P, _I64, _I64, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P,
+                                        ctypes.c_uint, _I, _P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -463,3 +478,48 @@ def mm_moe_ops_status(stream):
     where = _I(0)
     r = lib().mm_moe_ops_status(stream, ctypes.byref(where))
     return r, where.value
+
+
+# rows in 8 bits
+def mm_moe_rows_quantize(x, dtype, row_stride, R, C, variant, codes, sf, stream) -> int:
+    return lib().mm_moe_rows_quantize(x, dtype, row_stride, R, C, variant, codes, sf, stream)
+
+
+def mm_moe_rows_dequantize(codes, sf, R, C, variant, dtype, out, out_stride, stream) -> int:
+    return lib().mm_moe_rows_dequantize(codes, sf, R, C, variant, dtype, out, out_stride, stream)
+
+
+def mm_moe_rms_norm(x, dtype, x_stride, residual, residual_stride, weight, weight_dtype, T, H, eps, h, y, variant,
+                    codes, sf, rstd, stream) -> int:
+    return lib().mm_moe_rms_norm(x, dtype, x_stride, residual, residual_stride, weight, weight_dtype, T, H, eps, h, y,
+                                 variant, codes, sf, rstd, stream)
+
+
+def mm_moe_rms_norm_scratch_size(T, H) -> int:
+    n = _SZ(0)
+    _check(lib().mm_moe_rms_norm_scratch_size(T, H, ctypes.byref(n)), "mm_moe_rms_norm_scratch_size")
+    return n.value
+
+
+def mm_moe_rms_norm_backward(d_y, dtype, d_y_stride, h, h_stride, weight, weight_dtype, rstd, d_h, d_h_stride, T, H,
+                             d_x, d_weight, scratch, scratch_bytes, stream) -> int:
+    return lib().mm_moe_rms_norm_backward(d_y, dtype, d_y_stride, h, h_stride, weight, weight_dtype, rstd, d_h,
+                                          d_h_stride, T, H, d_x, d_weight, scratch, scratch_bytes, stream)
+
+
+def mm_moe_swiglu(h, dtype, h_stride, rows, I, T, K, E, block_m, slot, src, blk_off, w, a, codes, sf, kept, kept_sf,
+                  stream) -> int:
+    return lib().mm_moe_swiglu(h, dtype, h_stride, rows, I, T, K, E, block_m, slot, src, blk_off, w, a, codes, sf, kept,
+                               kept_sf, stream)
+
+
+def mm_moe_swiglu_backward(d_a, dtype, d_stride, kept, kept_sf, rows, I, T, K, E, block_m, slot, src, blk_off, w, d_h,
+                           d_w, stream) -> int:
+    return lib().mm_moe_swiglu_backward(d_a, dtype, d_stride, kept, kept_sf, rows, I, T, K, E, block_m, slot, src,
+                                        blk_off, w, d_h, d_w, stream)
+
+
+def mm_moe_weight_grad(d_y, d_stride, rows, N, codes, sf, C, T, K, E, block_m, cnt, src, blk_off, by_token, dtype, out,
+                       timeout_ms, debug_flags, stream) -> int:
+    return lib().mm_moe_weight_grad(d_y, d_stride, rows, N, codes, sf, C, T, K, E, block_m, cnt, src, blk_off, by_token,
+                                    dtype, out, timeout_ms, debug_flags, stream)

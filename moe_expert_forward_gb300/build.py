@@ -17,8 +17,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmm_moe.so")
 SOURCES = ["api.cu", "kernels_misc.cu", "gemm_mx.cu", "gemm_mx_sw.cu", "gemm_mx_pair.cu", "gemm_f8.cu", "dispatch_noalloc.cu", "ep.cu",
            "route.cu", "sort.cu", "rows.cu", "mx_quant.cu", "mx_linear.cu", "mx_linear_pair.cu", "mx_few.cu",
-           "api_ops.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "sched.cuh", "quant.cuh", "combine.cuh", "stream.cuh", "rowtypes.cuh", "mx_linear.h", "mx_linear.cuh", "mx_quant.cuh", "cluster.cuh"]
+           "api_ops.cu", "quant8.cu", "norm.cu", "swiglu.cu", "weight_grad.cu", "api_rows8.cu"]
+HEADERS = ["internal.h", "ptx.cuh", "sched.cuh", "quant.cuh", "combine.cuh", "stream.cuh", "rowtypes.cuh", "mx_linear.h", "mx_linear.cuh", "mx_quant.cuh", "cluster.cuh", "rows8.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -216,6 +216,89 @@ cudaError_t launch_unpermute(const RowsArgs& a, const void* rows, const float* w
 cudaError_t launch_unpermute_backward(const RowsArgs& a, const void* d_out, int64_t d_stride, const void* rows,
                                       const float* w, void* d_rows, float* d_w, cudaStream_t s);
 
+// Rows in 8 bits (quant8.cu): variant MM_MOE_VARIANT_MX or _F8.
+cudaError_t launch_quantize8(const void* x, int dtype, int64_t stride, int64_t R, int C, int variant, void* codes,
+                             void* sf, cudaStream_t s);
+cudaError_t launch_dequantize8(const void* codes, const void* sf, int64_t R, int C, int variant, int dtype, void* out,
+                               int64_t stride, cudaStream_t s);
+
+// The norm (norm.cu).
+constexpr int kNormBackSms = 152;          // its gradient's CTAs do not depend on the device: neither does the scratch
+struct NormLaunch {
+  const void* x;
+  int dtype;
+  int64_t x_stride;
+  const void* residual;      // or null, then h is null too
+  int64_t residual_stride;
+  const void* weight;
+  int weight_dtype;          // dtype or fp32
+  int64_t T;
+  int H;
+  float eps;
+  void* h;
+  void* y;                   // or null
+  int variant;
+  void* codes;               // or null
+  void* sf;
+  float* rstd;
+};
+cudaError_t launch_rms_norm(const NormLaunch& n, cudaStream_t s);
+struct NormBackLaunch {
+  const void* d_y;
+  int dtype;
+  int64_t d_y_stride;
+  const void* h;
+  int64_t h_stride;
+  const void* weight;
+  int weight_dtype;
+  const float* rstd;
+  const void* d_h;           // or null
+  int64_t d_h_stride;
+  int64_t T;
+  int H;
+  void* d_x;
+  float* d_weight;
+  void* scratch;             // norm_scratch_bytes
+};
+size_t norm_scratch_bytes(int64_t T, int H);
+cudaError_t launch_rms_norm_backward(const NormBackLaunch& n, cudaStream_t s);
+
+// The activation between the experts' products (swiglu.cu).
+struct SwigluRows {
+  int64_t rows;
+  int I;
+  const int32_t* slot;       // the routing of launch_sort; all null without one
+  const int32_t* src;
+  const int32_t* blk_off;
+  int E, block_m;
+  int64_t pairs;
+};
+cudaError_t launch_swiglu(const SwigluRows& r, int dtype, const void* h, int64_t stride, const float* w, void* a,
+                          void* codes, void* sf, void* kept, void* kept_sf, cudaStream_t s);
+cudaError_t launch_swiglu_backward(const SwigluRows& r, int dtype, const void* d_a, int64_t stride, const void* kept,
+                                   const void* kept_sf, const float* w, void* d_h, float* d_w, cudaStream_t s);
+
+// Weight gradients from rows in 8 bits (weight_grad.cu).
+struct WeightGradLaunch {
+  const void* d_y;           // bf16
+  int64_t d_stride;
+  int64_t rows;
+  int N;
+  const uint8_t* codes;
+  const uint8_t* sf;
+  int C;
+  const int32_t* cnt;        // null: dense
+  const int32_t* blk_off;
+  const int32_t* src;        // x's rows are tokens
+  int K, E, block_m;
+  int dtype;                 // of out: fp32 or bf16
+  void* out;
+  uint64_t timeout_ns;
+  bool unreachable;
+};
+int64_t weight_grad_tasks(int E, int N, int C);
+cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s);
+
 // TMA descriptor creation through the driver entry point.
 CUresult encode_tmap(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
                      const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swz);

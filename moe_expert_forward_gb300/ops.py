@@ -8,6 +8,12 @@
   mx_weights, mx_product, mx_linear
                                 products of 4-bit operands: dense, or each expert's
                                 rows with its matrix
+  quantize8, dequantize8        rows into 8 bits, the layer's x and x_sf, and back
+  rms_norm, rms_norm_backward   the norm in front of the layer with the residual's
+                                addition, in rows and in 8 bits, and the gradients
+  swiglu, swiglu_backward       the activation between the experts' products, and its
+                                gradients from gate and up kept in 8 bits
+  weight_grad                   weight gradients from rows kept in 8 bits
   sync_status                   whether a device wait of a product has run out
 
 Argument marshalling and checks only; the arithmetic is in the CUDA library,
@@ -30,8 +36,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (MM_MOE_ERR_INVALID_ARG, MM_MOE_SCORE_SIGMOID, MM_MOE_SCORE_SOFTMAX, MMError, _check, lib,
-               mm_moe_ops_status)
+from . import (MM_MOE_ERR_INVALID_ARG, MM_MOE_SCORE_SIGMOID, MM_MOE_SCORE_SOFTMAX, MM_MOE_VARIANT_F8,
+               MM_MOE_VARIANT_MX, MMError, _check, lib, mm_moe_ops_status)
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _SCORES = {"softmax": MM_MOE_SCORE_SOFTMAX, "sigmoid": MM_MOE_SCORE_SIGMOID}
@@ -486,7 +492,257 @@ def mx_linear(x, weights: MxWeights, routing: Optional[Routing] = None, out=None
     return out
 
 
+# ------------------------------------------------------------------ rows in 8 bits
+_FORMATS = {"mx": MM_MOE_VARIANT_MX, "f8": MM_MOE_VARIANT_F8}
+
+
+def _format(what: str, quant) -> int:
+    if quant not in _FORMATS:
+        _bad(what, f"the 8-bit form must be one of {sorted(_FORMATS)}, got {quant!r}")
+    return _FORMATS[quant]
+
+
+def _held_shapes(rows: int, C: int, variant: int):
+    """Shapes of the codes and the scales of rows of C elements, and the scales' type."""
+    if variant == MM_MOE_VARIANT_MX:
+        nb = -(-C // 32)
+        return (rows, 32 * nb), (rows, nb), torch.uint8
+    nb = -(-C // 128)
+    return (rows, 128 * nb), (rows, nb), torch.float32
+
+
+def _held(stream, rows: int, C: int, variant: int, device):
+    codes, sf, dtype = _held_shapes(rows, C, variant)
+    return _result(stream, codes, torch.uint8, device), _result(stream, sf, dtype, device)
+
+
+def quantize8(x, quant: str = "mx", stream=None):
+    """Rows x [R, C] into 8 bits: (codes u8, scales).
+
+    quant="mx": codes [R, 32 ceil(C/32)], scales u8 [R, ceil(C/32)] (UE8M0); "f8": codes
+    [R, 128 ceil(C/128)], scales fp32 [R, ceil(C/128)].  Where C is a multiple of 128 they
+    are the x and x_sf of the layer's variant of that name."""
+    code = _rows(x, "quantize8", "x")
+    v = _format("quantize8", quant)
+    R, C = x.shape
+    if C < 1:
+        _bad("quantize8", "x has no columns")
+    codes, sf = _held(stream, R, C, v, x.device)
+    _check(lib().mm_moe_rows_quantize(x.data_ptr(), code, _pitch(x), R, C, v, codes.data_ptr(), sf.data_ptr(),
+                                      _stream(stream)), "mm_moe_rows_quantize")
+    return codes, sf
+
+
+def _held_args(what: str, codes, sf, C: int, name: str = "codes"):
+    """(rows, variant, address of the codes, address of the scales) of rows in 8 bits; the scales' type names the form."""
+    _here(codes, what, name)
+    _here(sf, what, "sf")
+    if C < 1 or codes.dim() != 2:
+        _bad(what, f"{name} must be [rows, bytes] of rows of C >= 1 elements, got {tuple(codes.shape)} and C = {C}")
+    v = MM_MOE_VARIANT_F8 if sf.dtype == torch.float32 else MM_MOE_VARIANT_MX
+    R = codes.shape[0]
+    c_shape, s_shape, s_type = _held_shapes(R, C, v)
+    return R, v, _whole(codes, what, name, c_shape, torch.uint8), _whole(sf, what, "sf", s_shape, s_type)
+
+
+def dequantize8(codes, sf, C: int, dtype=torch.bfloat16, stream=None):
+    """The values of quantize8's codes and scales (whose type tells the form): [R, C]."""
+    R, v, cp, sp = _held_args("dequantize8", codes, sf, C)
+    if dtype not in _DTYPES:
+        _bad("dequantize8", f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    out = _result(stream, (R, C), dtype, codes.device)
+    _check(lib().mm_moe_rows_dequantize(cp, sp, R, C, v, _DTYPES[dtype], out.data_ptr(), C, _stream(stream)),
+           "mm_moe_rows_dequantize")
+    return out
+
+
+class Norm(NamedTuple):
+    """What rms_norm returns; None where it was not asked for."""
+    y: Optional[torch.Tensor]       # [T, H]
+    codes: Optional[torch.Tensor]   # y in 8 bits, as quantize8's
+    sf: Optional[torch.Tensor]
+    h: torch.Tensor                 # x + residual (x itself without a residual)
+    rstd: torch.Tensor              # fp32 [T]
+
+
+def _norm_weight(weight, what: str, H: int, dtype):
+    if not isinstance(weight, torch.Tensor) or weight.dtype != torch.float32:
+        return _whole(weight, what, "weight", (H,), dtype), _DTYPES[dtype]
+    return _whole(weight, what, "weight", (H,), torch.float32), _DTYPES[torch.float32]
+
+
+def rms_norm(x, weight, residual=None, eps: float = 1e-6, rows: bool = True, quant: Optional[str] = None,
+             stream=None) -> Norm:
+    """h = x + residual, and y = h * rstd * weight with rstd = 1 / sqrt(mean(h^2) + eps).
+
+    x, residual [T, H] of one type, weight [H] of that type or fp32.  y as rows of x's type
+    (rows) and in 8 bits (quant="mx" or "f8", from the fp32 y): the layer's input."""
+    code = _rows(x, "rms_norm", "x")
+    _no_grad("rms_norm", x, weight, residual)
+    T, H = x.shape
+    if H < 1:
+        _bad("rms_norm", "x has no columns")
+    wp, w_code = _norm_weight(weight, "rms_norm", H, x.dtype)
+    h, rp, r_pitch, hp = x, None, H, None
+    if residual is not None:
+        _rows(residual, "rms_norm", "residual", H, x.dtype)
+        if residual.shape[0] != T:
+            _bad("rms_norm", f"x has {T} rows, residual {residual.shape[0]}")
+        h = _result(stream, (T, H), x.dtype, x.device)
+        rp, r_pitch, hp = residual.data_ptr(), _pitch(residual), h.data_ptr()
+    v, codes, sf, cp, sp = 0, None, None, None, None
+    if quant is not None:
+        v = _format("rms_norm", quant)
+        codes, sf = _held(stream, T, H, v, x.device)
+        cp, sp = codes.data_ptr(), sf.data_ptr()
+    y = _result(stream, (T, H), x.dtype, x.device) if rows else None
+    rstd = _result(stream, (T,), torch.float32, x.device)
+    _check(lib().mm_moe_rms_norm(x.data_ptr(), code, _pitch(x), rp, r_pitch, wp, w_code, T, H, eps, hp,
+                                 None if y is None else y.data_ptr(), v, cp, sp, rstd.data_ptr(), _stream(stream)),
+           "mm_moe_rms_norm")
+    return Norm(y, codes, sf, h, rstd)
+
+
+NORM_CTAS = 2 * 152      # of the gradient, at most: mm_moe_rms_norm_scratch_size's rule
+
+
+def _norm_scratch(T: int, H: int) -> int:
+    groups, threads = -(-H // 16), 32
+    while threads < 256 and 2 * threads < groups:
+        threads *= 2
+    per_cta = 256 // threads
+    return 4 * min(-(-T // per_cta), NORM_CTAS) * per_cta * 16 * groups
+
+
+def rms_norm_backward(d_y, h, weight, rstd, d_h=None, stream=None):
+    """Gradients of rms_norm: (d_x [T, H], of x and of the residual alike; d_weight fp32 [H]).
+
+    h and rstd as rms_norm returned them; d_h: the gradient that reaches h besides the
+    norm's (the residual stream's), added to d_x."""
+    code = _rows(d_y, "rms_norm_backward", "d_y")
+    T, H = d_y.shape
+    if H < 1:
+        _bad("rms_norm_backward", "d_y has no columns")
+    for t, name in ((h, "h"), (d_h, "d_h")):
+        if t is not None:
+            _rows(t, "rms_norm_backward", name, H, d_y.dtype)
+            if t.shape[0] != T:
+                _bad("rms_norm_backward", f"d_y has {T} rows, {name} {t.shape[0]}")
+    if h is None:
+        _bad("rms_norm_backward", "h must be what rms_norm returned")
+    wp, w_code = _norm_weight(weight, "rms_norm_backward", H, d_y.dtype)
+    sp = _whole(rstd, "rms_norm_backward", "rstd", (T,), torch.float32)
+    d_x = _result(stream, (T, H), d_y.dtype, d_y.device)
+    d_weight = _result(stream, (H,), torch.float32, d_y.device)
+    scratch_bytes = _norm_scratch(T, H)
+    scratch = _new(stream, scratch_bytes, torch.uint8, d_y.device)
+    _check(lib().mm_moe_rms_norm_backward(d_y.data_ptr(), code, _pitch(d_y), h.data_ptr(), _pitch(h), wp, w_code, sp,
+                                          None if d_h is None else d_h.data_ptr(), H if d_h is None else _pitch(d_h), T,
+                                          H, d_x.data_ptr(), d_weight.data_ptr(), scratch.data_ptr(), scratch_bytes,
+                                          _stream(stream)), "mm_moe_rms_norm_backward")
+    return d_x, d_weight
+
+
+class Gated(NamedTuple):
+    """What swiglu returns; None where it was not asked for."""
+    a: Optional[torch.Tensor]         # [rows, I]
+    codes: Optional[torch.Tensor]     # a in 8 bits ("mx"), as quantize8's
+    sf: Optional[torch.Tensor]
+    kept: Optional[torch.Tensor]      # gate and up in 8 bits: u8 [rows, 2, 32 ceil(I/32)]
+    kept_sf: Optional[torch.Tensor]   # u8 [rows, 2, ceil(I/32)]
+
+
+def _pool(what: str, routing: Optional[Routing], topk_w, rows: int):
+    """(T, K, E, block_m, slot, src, blk_off, w) of a call on a routing's pool of rows, or on rows alone."""
+    if routing is None:
+        if topk_w is not None:
+            _bad(what, "topk_w needs a routing")
+        return 0, 0, 0, 0, None, None, None, None
+    r = routing
+    _routing_here(r, what)
+    if r.rows != rows:
+        _bad(what, f"the call has {rows} rows, the routing's pool {r.rows}")
+    wp = None if topk_w is None else _whole(topk_w, what, "topk_w", (r.T, r.K), torch.float32)
+    return r.T, r.K, r.E, r.block_m, r._slot, r._src, r._blk, wp
+
+
+def swiglu(h, routing: Optional[Routing] = None, topk_w=None, rows: bool = True, quant: bool = False,
+           keep: bool = False, stream=None) -> Gated:
+    """a = gate * sigmoid(gate) * up of rows h [rows, 2 I] = [gate | up], times topk_w (fp32 [T, K]) of each row's pair
+    where it is given; with a routing, rows of padding are not read and zero in every output.
+
+    a as rows of h's type (rows) and in 8 bits (quant), and gate and up in 8 bits for
+    swiglu_backward (keep); all "mx"."""
+    code = _rows(h, "swiglu", "h")
+    _no_grad("swiglu", h, topk_w)
+    R, I2 = h.shape
+    I = I2 // 2
+    if I < 1 or I2 % 2:
+        _bad("swiglu", f"h must be [rows, 2 I], got {tuple(h.shape)}")
+    if not (rows or quant or keep):
+        _bad("swiglu", "none of rows, quant and keep is asked for")
+    pool = _pool("swiglu", routing, topk_w, R)
+    nb = -(-I // 32)
+    a = _result(stream, (R, I), h.dtype, h.device) if rows else None
+    codes, sf = _held(stream, R, I, MM_MOE_VARIANT_MX, h.device) if quant else (None, None)
+    kept = _result(stream, (R, 2, 32 * nb), torch.uint8, h.device) if keep else None
+    kept_sf = _result(stream, (R, 2, nb), torch.uint8, h.device) if keep else None
+    out = [None if t is None else t.data_ptr() for t in (a, codes, sf, kept, kept_sf)]
+    _check(lib().mm_moe_swiglu(h.data_ptr(), code, _pitch(h), R, I, *pool, *out, _stream(stream)), "mm_moe_swiglu")
+    return Gated(a, codes, sf, kept, kept_sf)
+
+
+def swiglu_backward(d_a, kept, kept_sf, routing: Optional[Routing] = None, topk_w=None, stream=None):
+    """Gradients of swiglu at the kept values: (d_h [rows, 2 I] of d_a's type, zero on padding, and d_topk_w fp32
+    [T, K], 0 where masked; None without topk_w)."""
+    code = _rows(d_a, "swiglu_backward", "d_a")
+    R, I = d_a.shape
+    if I < 1:
+        _bad("swiglu_backward", "d_a has no columns")
+    nb = -(-I // 32)
+    kp = _whole(kept, "swiglu_backward", "kept", (R, 2, 32 * nb), torch.uint8)
+    sp = _whole(kept_sf, "swiglu_backward", "kept_sf", (R, 2, nb), torch.uint8)
+    pool = _pool("swiglu_backward", routing, topk_w, R)
+    d_h = _result(stream, (R, 2 * I), d_a.dtype, d_a.device)
+    d_w = None if topk_w is None else _result(stream, (routing.T, routing.K), torch.float32, d_a.device)
+    _check(lib().mm_moe_swiglu_backward(d_a.data_ptr(), code, _pitch(d_a), kp, sp, R, I, *pool, d_h.data_ptr(),
+                                        None if d_w is None else d_w.data_ptr(), _stream(stream)),
+           "mm_moe_swiglu_backward")
+    return d_h, d_w
+
+
+def weight_grad(d_y, codes, sf, C: int, routing: Optional[Routing] = None, by_token: bool = False,
+                dtype=torch.bfloat16, stream=None):
+    """Gradient of the weights of y = x w^T from x kept in 8 bits ("mx"): d_y^T x.
+
+    d_y bf16 [rows, N].  Dense: x [rows, C], the result [N, C].  With a routing: the rows
+    are its pool's, every expert's own sum [E, N, C], zero for an expert without rows;
+    padding takes no part, whatever it holds.  by_token: x [T, C] are the tokens' rows.
+    dtype: bfloat16 or float32.  A device wait that runs out leaves the result undefined
+    and is reported by sync_status."""
+    _rows(d_y, "weight_grad", "d_y", dtype=torch.bfloat16)
+    R, N = d_y.shape
+    if N < 1:
+        _bad("weight_grad", "d_y has no columns")
+    x_rows, v, cp, sp = _held_args("weight_grad", codes, sf, C)
+    if v != MM_MOE_VARIANT_MX:
+        _bad("weight_grad", "x must be held as \"mx\"")
+    if dtype not in (torch.bfloat16, torch.float32):
+        _bad("weight_grad", f"dtype must be bfloat16 or float32, got {dtype}")
+    T, K, E, block_m, slot, src, blk, _ = _pool("weight_grad", routing, None, R)
+    if by_token and routing is None:
+        _bad("weight_grad", "by_token needs a routing")
+    need = T if by_token else R
+    if x_rows != need:
+        _bad("weight_grad", f"x has {x_rows} rows, not {need}")
+    out = _result(stream, (N, C) if routing is None else (E, N, C), dtype, d_y.device)
+    _check(lib().mm_moe_weight_grad(d_y.data_ptr(), _pitch(d_y), R, N, cp, sp, C, T, K, E, block_m,
+                                    None if routing is None else routing._cnt, src, blk, by_token, _DTYPES[dtype],
+                                    out.data_ptr(), 0, 0, _stream(stream)), "mm_moe_weight_grad")
+    return out
+
+
 def sync_status(stream=None):
-    """Waits for `stream`; (code, where) of the first device wait of a product that ran out on this device since the
+    """Waits for `stream`; (code, where) of the first device wait of a product (weight_grad among them) that ran out on this device since the
     last report, on any stream: MM_MOE_ERR_TIMEOUT and its site, or (0, 0)."""
     return mm_moe_ops_status(_stream(stream))

@@ -1,0 +1,208 @@
+"""weight_grad against the formula in 64 bits."""
+import time
+
+import numpy as np
+import pytest
+import torch
+
+from rows8_util import U, d64, randn, routing, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from moe_expert_forward_gb300 import build
+    build.build()
+    from moe_expert_forward_gb300 import ops
+    ops.sync_status()              # what other tests let run out
+    return ops
+
+
+def whole(seed, *shape):
+    """Whole numbers from -4 to 4: sums of products are exact in fp32, in any order."""
+    return torch.randint(-4, 5, shape, generator=torch.Generator().manual_seed(seed)).float()
+
+
+def check(ops, d_y, x, r=None, by_token=False, exact=True):
+    """d_y [rows, N] bf16 and x (fp32, held in 8 bits here) on the host."""
+    C = x.shape[1]
+    codes, sf = ops.quantize8(x.cuda())
+    got = ops.weight_grad(d_y.cuda(), codes, sf, C, r, by_token, torch.float32)
+    xv, dv = values(codes, sf, C), d64(d_y)
+    if r is None:
+        spans = [(dv, xv)]
+    else:
+        cnt, blk, src = r.cnt.cpu().numpy(), r.blk_off.cpu().numpy(), r.src.cpu().numpy()
+        spans = []
+        for e in range(r.E):
+            rows = np.arange(cnt[e]) + blk[e] * r.block_m
+            spans.append((dv[rows], xv[src[rows] // r.K] if by_token else xv[rows]))
+    want = np.stack([d.T @ v for d, v in spans])
+    # fp32 sums of exact products, each addition off by at most one step (2 U) of the magnitudes added up
+    tol = np.stack([np.abs(d).T @ np.abs(v) * (len(d) + 4) * 2 * U for d, v in spans])
+    got64 = d64(got).reshape(want.shape)
+    if exact:
+        assert np.array_equal(got64, want)
+    assert (np.abs(got64 - want) <= tol).all()
+    half = ops.weight_grad(d_y.cuda(), codes, sf, C, r, by_token)
+    assert half.dtype == torch.bfloat16 and torch.equal(half, got.bfloat16())      # the same sums, rounded once
+    assert ops.sync_status() == (0, 0)
+    return got
+
+
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 63, 64, 65, 128, 300, 1000])
+@pytest.mark.parametrize("N,C", [(128, 256), (8, 32), (136, 288)])
+def test_dense_rows(ops, rows, N, C):
+    check(ops, whole(rows, rows, N).bfloat16(), whole(rows + 1, rows, C))
+
+
+@pytest.mark.parametrize("N,C", [(1, 1), (1, 256), (7, 33), (64, 31), (127, 255), (129, 257), (130, 1000), (200, 48), (333, 1001),
+                                 (16, 4096), (4096, 16), (264, 520), (384, 768)])
+def test_dense_widths(ops, N, C):
+    check(ops, whole(N, 150, N).bfloat16(), whole(C, 150, C))
+
+
+def test_dense_random_values(ops):
+    """Scales of every size, sums of 20000 rows."""
+    x = randn(1, 20000, 96) * torch.exp2(torch.arange(96).remainder(17) - 8.0)
+    check(ops, randn(2, 20000, 72, dt="bf16"), x, exact=False)
+
+
+def test_scales_at_the_ends_of_their_range(ops):
+    """Codes and scale bytes as a caller may hold them: 2^-127 to 2^127, subnormal codes, both zeros."""
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes = codes[(codes & 127) != 127]                    # every code but NaN
+    codes = torch.cat([codes, codes[:2]])[None].repeat(4, 1).contiguous()
+    one = torch.ones(4, 1, dtype=torch.bfloat16, device="cuda")
+    for byte in (0, 1, 60, 119, 127, 134, 135, 136, 200, 245):
+        sf = torch.full((4, 8), byte, dtype=torch.uint8)
+        for row in range(4):
+            d_y = torch.zeros_like(one)
+            d_y[row] = 1
+            got = d64(ops.weight_grad(d_y, codes.cuda(), sf.cuda(), 256, dtype=torch.float32))[0]
+            want = values(codes[:1], sf[:1], 256)[0]
+            # bf16 has every value but those between its subnormals, which are 2^-133 apart
+            assert (np.abs(got - want) <= (2.0 ** -134 if byte < 4 else 0)).all(), byte
+    sf = torch.full((4, 8), 255, dtype=torch.uint8, device="cuda")
+    assert torch.isnan(ops.weight_grad(one, codes.cuda(), sf, 256, dtype=torch.float32)).all()
+
+
+@pytest.mark.parametrize("by_token", [False, True])
+@pytest.mark.parametrize("T,E,K,block,masked", [(1, 3, 1, 16, 0.0), (40, 6, 2, 16, 0.1), (200, 5, 5, 128, 0.5), (300, 40, 3, 32, 0.0),
+                                                (33, 4, 2, 256, 1.0), (0, 4, 2, 16, 0.0), (700, 3, 2, 48, 0.0)])
+@pytest.mark.parametrize("N,C", [(136, 288), (33, 70)])
+def test_routed(ops, T, E, K, block, masked, by_token, N, C):
+    """Padding holds NaN in d_y, and in x where x has pool rows."""
+    idx = routing(T, E, K, masked, T)
+    r = ops.sort_tokens(idx.cuda(), E, block)
+    at = r.slot.cpu().flatten()
+    at = at[at >= 0].long()
+    d_y = torch.full((r.rows, N), float("nan"))
+    d_y[at] = whole(1, len(at), N)
+    x = whole(2, T if by_token else r.rows, C)
+    if not by_token:
+        pad = torch.ones(r.rows, dtype=torch.bool)
+        pad[at] = False
+        x[pad] = float("nan")
+    got = check(ops, d_y.bfloat16(), x, r, by_token)
+    empty = (r.cnt == 0).cpu()
+    assert not got.cpu()[empty].any()
+
+
+def test_one_expert_takes_everything(ops):
+    r = ops.sort_tokens(torch.full((500, 1), 3, dtype=torch.int32, device="cuda"), 6)
+    d_y = whole(1, r.rows, 200)
+    check(ops, d_y.bfloat16(), whole(2, 500, 100), r, True)
+
+
+def test_strided_and_unaligned_d_y(ops):
+    wide = whole(1, 100, 500).bfloat16().cuda()
+    x = whole(2, 100, 300).cuda()
+    codes, sf = ops.quantize8(x)
+    for lo, hi in ((0, 256), (1, 257), (3, 100), (8, 500), (4, 12)):
+        a, b = ops.weight_grad(wide[:, lo:hi], codes, sf, 300), ops.weight_grad(wide[:, lo:hi].contiguous(), codes, sf, 300)
+        assert torch.equal(a, b)
+        assert torch.equal(a.float(), (wide[:, lo:hi].float().t() @ ops.dequantize8(codes, sf, 300, torch.float32)).bfloat16().float())
+
+
+def test_many_tiles_and_repeats(ops):
+    """More tiles than SMs, several a CTA, bit-equal from run to run."""
+    d_y, x = randn(1, 700, 2048, dt="bf16").cuda(), randn(2, 700, 3000).cuda()
+    codes, sf = ops.quantize8(x)
+    first = ops.weight_grad(d_y, codes, sf, 3000, dtype=torch.float32)
+    want = d_y.double().t() @ ops.dequantize8(codes, sf, 3000, torch.float32).double()
+    size = d_y.double().abs().t() @ ops.dequantize8(codes, sf, 3000, torch.float32).double().abs()
+    assert ((first.double() - want).abs() <= 704 * 2 * U * size).all()
+    for _ in range(5):
+        assert torch.equal(ops.weight_grad(d_y, codes, sf, 3000, dtype=torch.float32), first)
+
+
+def test_nan_reaches_its_own_sums_only(ops):
+    d_y, x = whole(1, 90, 40).bfloat16().cuda(), whole(2, 90, 100).cuda()
+    codes, sf = ops.quantize8(x)
+    clean = ops.weight_grad(d_y, codes, sf, 100, dtype=torch.float32)
+    d_y[50, 7] = float("nan")
+    x[60, 70] = float("inf")                               # its block: columns 64 to 95
+    codes, sf = ops.quantize8(x)
+    got = ops.weight_grad(d_y, codes, sf, 100, dtype=torch.float32)
+    bad = torch.zeros(40, 100, dtype=torch.bool, device="cuda")
+    bad[7], bad[:, 64:96] = True, True
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], clean[~bad])
+
+
+def test_empty(ops):
+    codes, sf = ops.quantize8(torch.empty(0, 40, device="cuda"))
+    for dtype in (torch.bfloat16, torch.float32):
+        w = ops.weight_grad(torch.empty(0, 24, device="cuda", dtype=torch.bfloat16), codes, sf, 40, dtype=dtype)
+        assert w.shape == (24, 40) and not w.any()
+
+
+def test_output_past_four_gigabytes(ops):
+    """200 experts of 4096 x 4096 in bf16: 6.7 GB."""
+    E, N, C = 200, 4096, 4096
+    idx = torch.arange(1000, device="cuda", dtype=torch.int32).remainder(E - 1).view(-1, 1).contiguous()
+    r = ops.sort_tokens(idx, E)
+    d_y, x = torch.randn(r.rows, N, device="cuda", dtype=torch.bfloat16), torch.randn(1000, C, device="cuda")
+    codes, sf = ops.quantize8(x)
+    got = ops.weight_grad(d_y, codes, sf, C, r, True)
+    xv = ops.dequantize8(codes, sf, C, torch.float32)
+    for e in (0, 57, 128, 129, 198):
+        t = torch.nonzero(idx[:, 0] == e)[:, 0]
+        rows = d_y[r.slot[t, 0].long()].double()
+        want, size = rows.t() @ xv[t].double(), rows.abs().t() @ xv[t].double().abs()
+        assert ((got[e].double() - want).abs() <= 2.0 ** -8 * 1.01 * want.abs() + 20 * U * size).all()
+    assert not got[199].any()
+
+
+@pytest.mark.parametrize("rows,N,C,routed", [(300, 300, 600, False), (3000, 2000, 6000, False), (8192, 128, 256, False),
+                                             (600, 300, 600, True)])
+def test_a_stage_that_never_comes(ops, monkeypatch, rows, N, C, routed):
+    """The call gives up after its limit, says so once, and leaves the GPU in order."""
+    import moe_expert_forward_gb300 as M
+    r = None
+    if routed:
+        r = ops.sort_tokens(torch.arange(rows, device="cuda", dtype=torch.int32).remainder(3).view(-1, 1).contiguous(), 3)
+        rows = r.rows
+    d_y = torch.ones(rows, N, device="cuda", dtype=torch.bfloat16)
+    codes, sf = ops.quantize8(torch.ones(rows, C, device="cuda"))
+    want = ops.weight_grad(d_y, codes, sf, C, r)
+    assert ops.sync_status() == (0, 0)
+
+    class Short:
+        def __getattr__(self, name):
+            return getattr(real, name)
+
+        def mm_moe_weight_grad(self, *a):
+            return real.mm_moe_weight_grad(*a[:17], 50, 1, a[19])
+    real = M.lib()
+    monkeypatch.setattr(ops, "lib", lambda: Short())
+    torch.cuda.synchronize()
+    began = time.monotonic()
+    ops.weight_grad(d_y, codes, sf, C, r)
+    code, where = ops.sync_status()
+    assert time.monotonic() - began < 5
+    assert code == M.MM_MOE_ERR_TIMEOUT and 181 <= where <= 187
+    assert ops.sync_status() == (0, 0)
+    monkeypatch.setattr(ops, "lib", lambda: real)
+    assert torch.equal(ops.weight_grad(d_y, codes, sf, C, r), want) and ops.sync_status() == (0, 0)
