@@ -616,20 +616,25 @@ int mm_moe_swiglu_backward(const void* d_a, int dtype, int64_t d_stride, const v
 
 /* Weight gradients from rows kept in 8 bits (MX): out[e][n][c] = the sum over expert e's
  * rows r of d_y[r][n] * x[r][c], fp32 sums rounded once.
- *   d_y    bf16 [rows, N], d_stride elements between rows (16-byte aligned rows are the fastest)
+ *   d_y    bf16 [rows, N], d_stride elements between rows
  *   codes, sf  x [rows, C], or with by_token [T, C]: the tokens' own rows
  *   cnt, src, blk_off  null: one dense sum over all rows (T, K, E, block_m are not read).  Else the
  *          routing whose pool the rows are: cnt[e] rows of expert e from row blk_off[e] * block_m on.
  *          Other rows are not part of any sum, whatever they hold.
  *   out    [E, N, C] (dense: [N, C]) contiguous of `dtype` (fp32 or bf16), fully overwritten;
  *          zero for an expert without rows
+ *   scratch  mm_moe_weight_grad_scratch_size bytes (x_rows: rows, or T with by_token), 16-byte
+ *          aligned: copies of d_y and of sf where their rows do not start on 16-byte and 4-byte
+ *          boundaries; else none (0 bytes, null allowed)
  * A device wait past timeout_ms (0: 2000) leaves out undefined and is reported by
  * mm_moe_ops_status.  debug_flags: 0; bit 0 leaves one stage of each CTA unloaded, so that its
  * wait runs out. */
+int mm_moe_weight_grad_scratch_size(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf,
+                                    int64_t x_rows, int C, size_t* bytes);
 int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* codes, const void* sf, int C,
                        int T, int K, int E, int block_m, const int32_t* cnt, const int32_t* src,
-                       const int32_t* blk_off, int by_token, int dtype, void* out, unsigned timeout_ms,
-                       int debug_flags, void* stream);
+                       const int32_t* blk_off, int by_token, int dtype, void* out, void* scratch,
+                       size_t scratch_bytes, unsigned timeout_ms, int debug_flags, void* stream);
 
 /* Waits for `stream` and returns MM_MOE_ERR_TIMEOUT if a device wait of mm_moe_mx_product,
  * mm_moe_mx_linear or mm_moe_weight_grad has run out on the current device, on any stream, since the last

@@ -43,7 +43,8 @@ EXPORTS = ["mm_moe_default_options", "mm_moe_workspace_size", "mm_moe_weight_sf_
            "mm_moe_mx_scale_size", "mm_moe_mx_quantize", "mm_moe_mx_dequantize", "mm_moe_mx_prepare",
            "mm_moe_mx_product", "mm_moe_mx_linear_workspace", "mm_moe_mx_linear", "mm_moe_ops_status",
            "mm_moe_rows_quantize", "mm_moe_rows_dequantize", "mm_moe_rms_norm", "mm_moe_rms_norm_scratch_size",
-           "mm_moe_rms_norm_backward", "mm_moe_swiglu", "mm_moe_swiglu_backward", "mm_moe_weight_grad"]
+           "mm_moe_rms_norm_backward", "mm_moe_swiglu", "mm_moe_swiglu_backward", "mm_moe_weight_grad_scratch_size",
+           "mm_moe_weight_grad"]
 
 
 class mm_moe_options(ctypes.Structure):
@@ -132,7 +133,8 @@ def lib() -> ctypes.CDLL:
             "mm_moe_swiglu": (_I, [_P, _I, _I64, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
             "mm_moe_swiglu_backward": (_I, [_P, _I, _I64, _P, _P, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
                                             _P]),
-            "mm_moe_weight_grad": (_I, [_P, _I64, _I64, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P,
+            "mm_moe_weight_grad_scratch_size": (_I, [_P, _I64, _I64, _I, _P, _I64, _I, ctypes.POINTER(_SZ)]),
+            "mm_moe_weight_grad": (_I, [_P, _I64, _I64, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _SZ,
                                         ctypes.c_uint, _I, _P]),
         }
         for name, (res, args) in sig.items():
@@ -519,7 +521,14 @@ def mm_moe_swiglu_backward(d_a, dtype, d_stride, kept, kept_sf, rows, I, T, K, E
                                         blk_off, w, d_h, d_w, stream)
 
 
+def mm_moe_weight_grad_scratch_size(d_y, d_stride, rows, N, sf, x_rows, C) -> int:
+    n = _SZ(0)
+    _check(lib().mm_moe_weight_grad_scratch_size(d_y, d_stride, rows, N, sf, x_rows, C, ctypes.byref(n)),
+           "mm_moe_weight_grad_scratch_size")
+    return n.value
+
+
 def mm_moe_weight_grad(d_y, d_stride, rows, N, codes, sf, C, T, K, E, block_m, cnt, src, blk_off, by_token, dtype, out,
-                       timeout_ms, debug_flags, stream) -> int:
+                       scratch, scratch_bytes, timeout_ms, debug_flags, stream) -> int:
     return lib().mm_moe_weight_grad(d_y, d_stride, rows, N, codes, sf, C, T, K, E, block_m, cnt, src, blk_off, by_token,
-                                    dtype, out, timeout_ms, debug_flags, stream)
+                                    dtype, out, scratch, scratch_bytes, timeout_ms, debug_flags, stream)

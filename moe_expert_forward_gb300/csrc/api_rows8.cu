@@ -138,10 +138,19 @@ int mm_moe_swiglu_backward(const void* d_a, int dtype, int64_t d_stride, const v
                                      static_cast<cudaStream_t>(stream)));
 }
 
+int mm_moe_weight_grad_scratch_size(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int64_t x_rows,
+                                    int C, size_t* bytes) {
+  if (!bytes || rows < 0 || rows > kMaxRows || N < 1 || N > kMaxCols || d_stride < N || x_rows < 0 || x_rows > kMaxRows ||
+      C < 1 || C > kMaxCols)
+    return MM_MOE_ERR_INVALID_ARG;
+  *bytes = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, x_rows, C);
+  return MM_MOE_OK;
+}
+
 int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* codes, const void* sf, int C,
                        int T, int K, int E, int block_m, const int32_t* cnt, const int32_t* src,
-                       const int32_t* blk_off, int by_token, int dtype, void* out, unsigned timeout_ms,
-                       int debug_flags, void* stream) {
+                       const int32_t* blk_off, int by_token, int dtype, void* out, void* scratch, size_t scratch_bytes,
+                       unsigned timeout_ms, int debug_flags, void* stream) {
   if (rows < 0 || rows > kMaxRows || N < 1 || N > kMaxCols || C < 1 || C > kMaxCols || d_stride < N ||
       (dtype != MM_MOE_DTYPE_F32 && dtype != MM_MOE_DTYPE_BF16) || !cnt != !src || (by_token && !cnt))
     return MM_MOE_ERR_INVALID_ARG;
@@ -150,14 +159,18 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
   if (static_cast<int64_t>(E) * N > kMaxRows || weight_grad_tasks(E, N, C) > (int64_t(1) << 30))
     return MM_MOE_ERR_INVALID_ARG;
   if (!out || !aligned(out, dtype_size(dtype))) return MM_MOE_ERR_INVALID_ARG;
-  if (rows > 0 && (!d_y || !codes || !aligned(d_y, 2) || !held_ok(codes, sf, MM_MOE_VARIANT_MX)))
+  if (rows > 0 && !(cnt && T == 0) && (!d_y || !codes || !aligned(d_y, 2) || !held_ok(codes, sf, MM_MOE_VARIANT_MX)))
     return MM_MOE_ERR_INVALID_ARG;
+  const size_t need = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, by_token ? T : rows, C);
+  if (need && (!scratch || !aligned(scratch, 16))) return MM_MOE_ERR_INVALID_ARG;
+  if (scratch_bytes < need) return MM_MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (rows == 0)
+  if (rows == 0 || (cnt && T == 0))            // sums of nothing
     return done(cudaMemsetAsync(out, 0, static_cast<size_t>(E) * N * C * dtype_size(dtype), s));
   const WeightGradLaunch p{d_y, d_stride, rows, N, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(sf),
-                           C, cnt, blk_off, by_token ? src : nullptr, K, E, block_m, dtype, out,
+                           C, cnt, blk_off, by_token ? src : nullptr, K, E, block_m,
+                           cnt ? static_cast<int64_t>(T) * K : 0, dtype, out, scratch,
                            static_cast<uint64_t>(timeout_ms ? timeout_ms : 2000) * 1000000ull, (debug_flags & 1) != 0};
   return done(launch_weight_grad(p, s));
 }

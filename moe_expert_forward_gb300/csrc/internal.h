@@ -291,11 +291,15 @@ struct WeightGradLaunch {
   const int32_t* blk_off;
   const int32_t* src;        // x's rows are tokens
   int K, E, block_m;
+  int64_t pairs;             // T * K
   int dtype;                 // of out: fp32 or bf16
   void* out;
+  void* scratch;             // weight_grad_scratch_bytes
   uint64_t timeout_ns;
   bool unreachable;
 };
+size_t weight_grad_scratch_bytes(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int64_t x_rows,
+                                 int C);
 int64_t weight_grad_tasks(int E, int N, int C);
 cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s);
 

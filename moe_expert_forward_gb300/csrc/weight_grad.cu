@@ -9,12 +9,30 @@
 // which run along the contraction: converter warps decode codes into bf16 on their way
 // into shared memory instead, where TMA brings d_y next to them.
 //
-// A task is 128 columns of d_y (M) times 256 of x (N) of one expert; the contraction
-// runs in stages of 64 rows, four MMAs a stage.  Persistent CTAs take tasks in a fixed
-// stride; the accumulator is double buffered, so that a task's stores overlap the next
-// one's products.
+// A task is 256 columns of d_y (M) times 256 of x (N) of one expert, by a CTA pair
+// (cta_group::2); the contraction runs in stages of 64 rows, four MMAs a stage.  Why
+// pairs: each CTA holds 128 columns of either operand, so a code is decoded once for 256
+// columns of d_y, and a stage moves 64 KB through each SM's shared memory in the 512 cycles of
+// its MMAs where a 128 x 256 tile of one CTA would move 96.  Persistent pairs take tasks
+// in a fixed stride; the accumulator is double buffered, so that a task's stores overlap
+// the next one's products.  With few tasks a cluster of 2 or 4 pairs takes one, each
+// pair a range of its stages, and the parts meet in shared memory.
 //
-// Warps: 8 epilogue, 1 MMA, 1 TMA producer, 8 converters.  Every wait is bounded.
+// fp32 results are sums of sums over 1024 rows (kSegment stages), added by the epilogue:
+// the MMA's accumulation drops bits below its accumulator's last, and 8192 rows in one
+// accumulator were 3.7e-6 off (rounding to nearest: 3.6e-7).
+//
+// Codes come by TMA too (gathered four rows an instruction where x's rows are tokens), their scales by 4-byte
+// asynchronous copies, into a ring of their own: converters that load for themselves keep the SM's loads in flight at
+// their limit, and wait for it (1000 cycles a stage and more).  Rows of d_y, or of scales, that start on no 16-byte,
+// or 4-byte, boundary are copied first.
+//
+// The loops of all roles have to fit the instruction cache together: none is unrolled over its ring (unrolled, a third
+// of the fetches missed and a stage took 1500 cycles).
+//
+// Warps per CTA: 4 epilogue, 1 MMA (the leader's issues for both), 1 TMA producer of
+// d_y, 1 of codes and scales, 1 that waits for a stage's operands, fences them towards
+// the tensor cores and tells the leader, 8 converters.  Every wait is bounded.
 #include "cluster.cuh"
 #include "mx_linear.cuh"
 #include "rows8.cuh"
@@ -22,44 +40,56 @@
 namespace mm {
 namespace {
 
-constexpr int kStages = 4;
+constexpr int kStages = 5;                       // of operands
+constexpr int kRaw = 6;                          // of codes
 constexpr int kRowsPerStage = 64;
-constexpr int kTileN = 128;                      // columns of d_y: M
-constexpr int kTileC = 256;                      // columns of x: N
-constexpr int kEpiWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kConvert0 = 10, kConvertWarps = 8;
+constexpr int kTile = 256;                       // columns of d_y (M) and of x (N) of a pair; 128 of each in a CTA
+constexpr int kEpiWarps = 4, kConvertWarps = 8;
+constexpr int kMmaWarp = kEpiWarps, kTmaWarp = kMmaWarp + 1, kCodesWarp = kTmaWarp + 1, kHandWarp = kCodesWarp + 1,
+              kConvert0 = kHandWarp + 1;
 constexpr int kThreads = 32 * (kConvert0 + kConvertWarps);
 constexpr int kAtom = 1024;                      // 8 rows of 64 columns
 constexpr int kChunkBytes = kRowsPerStage * 128; // 64 columns of a stage
-constexpr int kABytes = kTileN / 64 * kChunkBytes, kBBytes = kTileC / 64 * kChunkBytes;
+constexpr int kHalfBytes = 2 * kChunkBytes;      // 128 columns: one CTA's share of an operand
+constexpr int kRawBytes = kRowsPerStage * 128;   // 128 columns of codes
+constexpr int kRawSf = kRowsPerStage * 4;        // and their scales
+constexpr int kGroups = 2;                       // of converter warps, which take turns at the stages
+constexpr int kRowStep = 8 * kConvertWarps / (2 * kGroups);      // between the rows of a converter lane
+constexpr int kLaneRows = kRowsPerStage / kRowStep;
+constexpr int kSegment = 16;                     // stages of one fp32 accumulator
+constexpr int kMostParts = 4;
 
 struct Smem {
   static constexpr int a = 0;
-  static constexpr int b = a + kStages * kABytes;
-  static constexpr int bars = b + kStages * kBBytes;
-  static constexpr int nbars = 3 * kStages + 5;  // full of A and of B, empty, tfull, tempty, drain
+  static constexpr int b = a + kStages * kHalfBytes;
+  static constexpr int raw = b + kStages * kHalfBytes;
+  static constexpr int raw_sf = raw + kRaw * kRawBytes;
+  static constexpr int bars = raw_sf + kRaw * kRawSf;
+  static constexpr int nbars = 4 * kStages + 2 * kRaw + 5;       // full_a, full_b, full, empty, raw_full, raw_empty, ...
   static constexpr int meta = bars + nbars * 8 + 16;             // blk_off[E + 1], cnt[E]
+  static constexpr int kPartPitch = kTile + 4;   // floats of a row of partial sums
   static int total(int E) { return meta + (2 * E + 1) * 4 + 1024; }
 };
 static_assert(Smem::meta + (2 * kMaxE + 1) * 4 + 1024 <= 232448, "shared memory");
+static_assert(128 * Smem::kPartPitch * 4 <= Smem::raw, "partial sums fit the stages");
 
 enum : int {
-  kSiteEmpty = 181, kSiteFullA = 182, kSiteFullB = 183, kSiteTmemEmpty = 184, kSiteTmemFull = 185,
-  kSiteDrainCopies = 186, kSiteDrainMma = 187
+  kSiteEmpty = 181, kSiteFullA = 182, kSiteFull = 183, kSiteTmemEmpty = 184, kSiteTmemFull = 185, kSiteDrainCopies = 186,
+  kSiteDrainMma = 187, kSiteDrainEmpty = 188, kSiteFullB = 189, kSiteRawFull = 190,
+  kSiteRawEmpty = 191
 };
 
 struct Args {
-  const __nv_bfloat16* d_y;
-  int64_t dy_stride;
   int N, C, E, block_m;
   int NT, CT;                // tiles of N and of C
   int rows;                  // of d_y
-  const uint8_t* codes;
-  const uint8_t* sf;
-  int pitch, blocks;         // bytes of a row of codes, scales of a row
+  const uint32_t* sf;
+  int sf_words;              // words from one row of scales to the next
   const int* cnt;            // null: dense
   const int* blk_off;
   const int* src;            // x's rows are tokens: pool row -> pair; null: x's rows are d_y's
   int K;
+  uint32_t per_k;            // floor((2^32 - 1) / K)
   char* out;
   int64_t out_pitch;         // bytes of a row of out
   int unreachable;           // leave x of the CTA's last stage out
@@ -70,22 +100,37 @@ struct Args {
 // kind::f16: fp32 accumulator (1 in [5:4]), A and B bf16 (1 in [9:7] and [12:10]), both MN-major (bits 15 and 16),
 // N >> 3 in [22:17], M >> 4 in [28:24].
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
-                            (static_cast<uint32_t>(kTileC >> 3) << 17) | (static_cast<uint32_t>(kTileN >> 4) << 24);
+                            (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
 
-__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_f16_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// Arrive at the same barrier of both CTAs of the pair (bits of their ranks in `ctas`) once this thread's MMAs have completed.
+__device__ __forceinline__ void tc_commit_both(uint64_t* bar, uint16_t ctas) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
+               "h"(ctas)
+               : "memory");
 }
 // this thread's shared-memory stores before later reads by the tensor cores
 __device__ __forceinline__ void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Arrive on the leader's barrier, releasing within this CTA: all that is handed over lies in this CTA's shared memory,
+// fenced towards the tensor cores that read it, and no thread of the other CTA looks at it. (Releasing to the cluster waits
+// for whatever the SM has in flight, about 2000 cycles a stage.)
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 struct Task {
   int e, n0, c0;
-  int64_t row0;              // first row of the expert
+  int row0;                  // first row of the expert
   int rows;                  // its rows
 };
 __device__ __forceinline__ Task task_at(int i, const Args& a, const int* s_blk, const int* s_cnt) {
@@ -94,55 +139,122 @@ __device__ __forceinline__ Task task_at(int i, const Args& a, const int* s_blk, 
   i /= a.NT;
   const int ct = i % a.CT;
   t.e = i / a.CT;
-  t.n0 = nt * kTileN;
-  t.c0 = ct * kTileC;
-  t.row0 = a.cnt ? static_cast<int64_t>(s_blk[t.e]) * a.block_m : 0;
-  t.rows = a.cnt ? max(0, static_cast<int>(min(static_cast<int64_t>(s_cnt[t.e]), a.rows - t.row0))) : a.rows;
+  t.n0 = nt * kTile;
+  t.c0 = ct * kTile;
+  t.row0 = a.cnt ? s_blk[t.e] * a.block_m : 0;
+  t.rows = a.cnt ? max(0, min(s_cnt[t.e], a.rows - t.row0)) : a.rows;
   return t;
 }
 
-// Two e4m3 codes, in bytes 1 and 3 of w, as bf16 times 2^-120: sign to bit 15, exponent and fraction to bits 10 to 4, where
-// they stand for the same value with bf16's larger bias (subnormals too).
-__device__ __forceinline__ uint32_t widen(uint32_t w) { return ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u); }
+// The stages a pair runs through: task by task, of each the part'th of `parts` ranges.
+struct Cursor {
+  Task t;
+  int task, stride, ntasks, part, parts;
+  int ks, end;               // this stage, and the end of the range
+  __device__ __forceinline__ Cursor(int first, int stride, int ntasks, int part, int parts)
+      : task(first - stride), stride(stride), ntasks(ntasks), part(part), parts(parts), ks(0), end(0) {}
+  // the next task with stages; false past the last
+  __device__ __forceinline__ bool next_task(const Args& a, const int* s_blk, const int* s_cnt) {
+    do {
+      task += stride;
+      if (task >= ntasks) return false;
+      t = task_at(task, a, s_blk, s_cnt);
+      const int nks = (t.rows + kRowsPerStage - 1) / kRowsPerStage;
+      ks = static_cast<int>(static_cast<int64_t>(nks) * part / parts);
+      end = static_cast<int>(static_cast<int64_t>(nks) * (part + 1) / parts);
+    } while (ks >= end);
+    return true;
+  }
+  __device__ __forceinline__ bool next(const Args& a, const int* s_blk, const int* s_cnt) {
+    return ++ks < end || next_task(a, s_blk, s_cnt);
+  }
+};
+
+// A slot of a ring of N, in turn.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++s == N) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Four bytes into shared memory, and (arrive_after_copies) this thread's arrival on a barrier once all such copies of it
+// are there.
+__device__ __forceinline__ void copy_word_async(uint32_t dst, const uint32_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Four rows of a tensor map whose box is one row high.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int c, const int (&row)[4],
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(smem_u32(bar)),
+      "l"(policy)
+      : "memory");
+}
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 16 codes times 2^(byte - 127) as 16 bf16, exact where bf16 has the value. Byte 255: NaN.
+// 16 codes times 2^(byte - 127) as 16 bf16, exact where bf16 has the value; byte kNoRow: zeros.
+// A code's sign, exponent and fraction at bf16's bits 15 and 10 to 4 stand for the same value times 2^-120, bf16's larger
+// bias (subnormals too): the high byte is the sign and three bits of the exponent, the low one the other four bits.
+// kLarge: bytes of 135 (2^8) and up too, whose factor is past bf16's range and comes in two, and 255, NaN.
+constexpr uint32_t kNoRow = 0u - 120u;
+__device__ __forceinline__ bool is_large(uint32_t byte) { return byte - 135u < 121u; }
+template <bool kLarge>
 __device__ __forceinline__ void to_bf16(const uint4& c, uint32_t byte, uint32_t (&w)[8]) {
   const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-  // 2^(byte - 127) 2^120 has the exponent field byte + 120; past 254 in two factors
-  const uint32_t f1 = min(byte + 120u, 254u) << 7, p1 = byte == 255u ? 0x7FC07FC0u : f1 | (f1 << 16);
+  // 2^(byte - 127) 2^120 has the exponent field byte + 120, twice in a word
+  uint32_t p1 = (byte + 120u) * 0x00800080u, p2 = 0x3F803F80u;
+  if (kLarge && is_large(byte)) {
+    p1 = byte == 255u ? 0x7FC07FC0u : 254u * 0x00800080u;
+    p2 = (byte - 134u + 127u) * 0x00800080u;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    w[2 * i] = mul_bf16x2(widen(__byte_perm(in[i], 0, 0x1404)), p1);
-    w[2 * i + 1] = mul_bf16x2(widen(__byte_perm(in[i], 0, 0x3424)), p1);
-  }
-  if (byte > 134u) {
-    const uint32_t f2 = (min(byte, 254u) - 134u + 127u) << 7, p2 = f2 | (f2 << 16);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = mul_bf16x2(w[i], p2);
+    const uint32_t high = (((in[i] >> 4) & 0x07070707u) | (in[i] & 0xF8F8F8F8u)) & 0x87878787u;
+    const uint32_t low = (in[i] << 4) & 0xF0F0F0F0u;
+    w[2 * i] = mul_bf16x2(__byte_perm(low, high, 0x5140), p1);
+    w[2 * i + 1] = mul_bf16x2(__byte_perm(low, high, 0x7362), p1);
+    if (kLarge) {
+      w[2 * i] = mul_bf16x2(w[2 * i], p2);
+      w[2 * i + 1] = mul_bf16x2(w[2 * i + 1], p2);
+    }
   }
 }
 
-// One stage of x as a converter lane holds it: 16 columns of each of its four rows.
-struct Fetched {
-  uint4 c[4];
-  uint32_t byte[4];
+struct Maps {
+  CUtensorMap d_y, codes;
 };
 
-// kTma: d_y comes by TMA (16-byte aligned rows); else the converters load it.
-template <typename T, bool kTma, bool kLines>
+// kSplit: a cluster takes one task, each pair a range of its stages; the partial accumulators meet in shared memory.
+// kLines: see store_accumulator.
+template <typename T, bool kSplit, bool kLines>
 __global__ void __launch_bounds__(kThreads, 1)
-    weight_grad_kernel(const __grid_constant__ CUtensorMap map, const Args args) {
+    weight_grad_kernel(const __grid_constant__ Maps maps, const Args args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + Smem::bars);
-  uint64_t* full_b = full_a + kStages;
-  uint64_t* empty = full_b + kStages;
-  uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + 2;
+  uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + Smem::bars);   // this CTA's d_y has landed
+  uint64_t* full_b = full_a + kStages;           // this CTA's x has been decoded
+  uint64_t* full = full_b + kStages;             // leader: both CTAs' operands are there
+  uint64_t* empty = full + kStages;              // the stage's MMAs have completed
+  uint64_t* raw_full = empty + kStages;          // codes and scales of a stage are there
+  uint64_t* raw_empty = raw_full + kRaw;         // and have been read
+  uint64_t* tfull = raw_empty + kRaw;
+  uint64_t* tempty = tfull + 2;                  // leader: both CTAs have read the accumulator
   uint64_t* drain = tempty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full_a + Smem::nbars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
@@ -151,190 +263,248 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t rank = crank & 1, leader = crank & ~1u;       // of the pair
   const Status st{args.report, args.timeout_ns};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full_a[i], 1);
-      mbar_init(&full_b[i], kConvertWarps);
+      mbar_init(&full_b[i], kConvertWarps / kGroups);
+      mbar_init(&full[i], 2);
       mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&raw_full[i], 1 + 32);
+      mbar_init(&raw_empty[i], kConvertWarps / kGroups);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], kEpiWarps);
+      mbar_init(&tempty[i], 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(s_tmem, 512);
-    tmem_relinquish();
-  }
+  if (warp == kMmaWarp) tmem_alloc_pair(s_tmem, 512);
   if (args.cnt) {
     for (int i = threadIdx.x; i <= args.E; i += kThreads) s_blk[i] = args.blk_off[i];
     for (int i = threadIdx.x; i < args.E; i += kThreads) s_cnt[i] = args.cnt[i];
   }
   tc_fence_before();
   __syncthreads();
+  cluster_barrier();                             // every CTA's barriers exist before anything targets them
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const int ntasks = args.E * args.NT * args.CT;
-  const int first = blockIdx.x, stride = gridDim.x;
+  const int parts = kSplit ? static_cast<int>(cluster_nctarank() >> 1) : 1;
+  const int part = kSplit ? static_cast<int>(crank >> 1) : 0;
+  const int first = static_cast<int>(blockIdx.x >> 1) / parts, stride = static_cast<int>(gridDim.x >> 1) / parts;
+  // accumulators of a task's n stages
+  auto segments = [](int n) { return sizeof(T) == 4 && !kSplit ? (n + kSegment - 1) / kSegment : 1; };
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------------ d_y by TMA
-    if (kTma && lane == 0) {
+    if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
-      int step = 0;                              // stages so far
-      int armed[kStages];                        // phases armed of each stage
-#pragma unroll
-      for (int s = 0; s < kStages; ++s) armed[s] = 0;
-      bool live = true;
-      for (int i = first; i < ntasks && live; i += stride) {
-        const Task t = task_at(i, args, s_blk, s_cnt);
-        const int nks = (t.rows + kRowsPerStage - 1) / kRowsPerStage;
-        for (int ks = 0; ks < nks && live; ++ks, ++step) {
-          const int s = step % kStages;
-          live = !*s_abort && mbar_wait(&empty[s], ((step / kStages) & 1) ^ 1, st, s_abort, kSiteEmpty);
-          if (!live) break;
-          mbar_arrive_expect_tx(&full_a[s], kABytes);
-#pragma unroll
-          for (int q = 0; q < kStages; ++q) armed[q] += q == s;
-          uint8_t* d = smem + Smem::a + s * kABytes;
-          const int row = static_cast<int>(t.row0) + ks * kRowsPerStage;
-          tma_load_2d(d, &map, &full_a[s], t.n0, row, pol);
-          tma_load_2d(d + kChunkBytes, &map, &full_a[s], t.n0 + 64, row, pol);
-        }
+      Cursor at(first, stride, ntasks, part, parts);
+      Ring<kStages> ring;
+      int steps = 0;                             // stages loaded
+      while (at.next(args, s_blk, s_cnt)) {
+        const int s = ring.s;
+        if (*s_abort || !mbar_wait(&empty[s], ring.phase ^ 1, st, s_abort, kSiteEmpty)) break;
+        mbar_arrive_expect_tx(&full_a[s], kHalfBytes);
+        uint8_t* d = smem + Smem::a + s * kHalfBytes;
+        const int row = at.t.row0 + at.ks * kRowsPerStage, n = at.t.n0 + static_cast<int>(rank) * 128;
+        tma_load_2d(d, &maps.d_y, &full_a[s], n, row, pol);
+        tma_load_2d(d + kChunkBytes, &maps.d_y, &full_a[s], n + 64, row, pol);
+        ring.step();
+        ++steps;
       }
-#pragma unroll
-      for (int s = 0; s < kStages; ++s)
-        if (armed[s]) mbar_drain(&full_a[s], (armed[s] - 1) & 1, st, s_abort, kSiteDrainCopies);
+#pragma unroll 1
+      for (int s = 0; s < kStages && s < steps; ++s) {
+        const uint32_t last = ((steps - 1 - s) / kStages) & 1;   // its last phase
+        mbar_drain(&full_a[s], last, st, s_abort, kSiteDrainCopies);
+        // the leader's last commit to this CTA's barrier has arrived before the CTA leaves
+        if (!*s_abort) mbar_drain(&empty[s], last, st, s_abort, kSiteDrainEmpty);
+      }
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ MMAs
-    if (lane == 0) {
+    // ------------------------------------------------------------------ MMAs (leader)
+    if (rank == 0 && lane == 0) {
       // 64-column chunks kChunkBytes apart, 8-row groups one atom apart
       const uint64_t da0 = make_smem_desc(smem_u32(smem + Smem::a), kChunkBytes, kAtom, 2);
       const uint64_t db0 = make_smem_desc(smem_u32(smem + Smem::b), kChunkBytes, kAtom, 2);
-      int step = 0, it = 0;
-      bool live = true;
-      for (int i = first; i < ntasks && live; i += stride) {
-        const Task t = task_at(i, args, s_blk, s_cnt);
-        if (t.rows == 0) continue;
+      const uint16_t both = static_cast<uint16_t>(3u << leader);
+      Cursor at(first, stride, ntasks, part, parts);
+      uint32_t acc = tmem;
+      int it = 0, left = 0, in_acc = 0;          // accumulators so far; stages left of this one, and in it so far
+      bool live = at.next_task(args, s_blk, s_cnt);
+      auto start = [&]() {                       // an accumulator
         const int buf = it & 1;
-        live = !*s_abort && mbar_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, st, s_abort, kSiteTmemEmpty);
+        acc = tmem + buf * kTile;
+        left = at.end - at.ks;
+        if (sizeof(T) == 4 && !kSplit) left = min(left, kSegment);
+        in_acc = 0;
+        live = !*s_abort && mbar_wait_cluster(&tempty[buf], ((it >> 1) & 1) ^ 1, st, s_abort, kSiteTmemEmpty);
         tc_fence_after();
-        const uint32_t acc = tmem + buf * kTileC;
-        for (int row = 0; row < t.rows && live; row += kRowsPerStage, ++step) {
-          const int s = step % kStages;
-          const uint32_t phase = (step / kStages) & 1;
-          if (kTma) live = mbar_wait(&full_a[s], phase, st, s_abort, kSiteFullA);
-          live = live && mbar_wait(&full_b[s], phase, st, s_abort, kSiteFullB);
-          if (!live) break;
-          tc_fence_after();
-          const uint64_t da = da0 + ((s * kABytes) >> 4), db = db0 + ((s * kBBytes) >> 4);
-          const int n = min(4, (t.rows - row + 15) / 16);
-          for (int k = 0; k < n; ++k)            // 16 rows: two atoms
-            tc_mma_f16(acc, da + k * (2 * kAtom >> 4), db + k * (2 * kAtom >> 4), kIdesc, (row | k) != 0);
-          tc_commit(&empty[s]);
+      };
+      if (live) start();
+      Ring<kStages> ring;
+      while (live) {
+        const int s = ring.s;
+        if (!mbar_wait_cluster(&full[s], ring.phase, st, s_abort, kSiteFull)) break;
+        tc_fence_after();
+        const uint64_t da = da0 + ((s * kHalfBytes) >> 4), db = db0 + ((s * kHalfBytes) >> 4);
+        const int rows = at.t.rows - at.ks * kRowsPerStage;
+        tc_mma_f16_pair(acc, da, db, kIdesc, in_acc);
+#pragma unroll
+        for (int k = 1; k < 4; ++k)              // 16 rows: two atoms
+          if (rows > 16 * k) tc_mma_f16_pair(acc, da + k * (2 * kAtom >> 4), db + k * (2 * kAtom >> 4), kIdesc, 1);
+        tc_commit_both(&empty[s], both);
+        ring.step();
+        in_acc = 1;
+        ++at.ks;
+        if (--left == 0) {
+          tc_commit_both(&tfull[it & 1], both);
+          ++it;
+          live = at.ks < at.end || at.next_task(args, s_blk, s_cnt);
+          if (live) start();
         }
-        if (!live) break;
-        tc_commit(&tfull[buf]);
-        ++it;
       }
-      tc_commit(drain);
+      tc_commit_pair(map_shared(drain, leader));
       mbar_drain(drain, 0, st, s_abort, kSiteDrainMma);
     }
     __syncwarp();
-  } else if (warp >= kConvert0) {
-    // ------------------------------------------------------------------ x into bf16
-    // a warp takes 64 columns of every second group of 8 rows; 4 lanes a row, so that 8 lanes' 16-byte stores (two rows
-    // of one chunk) fall into 8 different bank groups
-    const int cw = warp - kConvert0, chunk = cw & 3, r8 = lane >> 2, q = lane & 3;
-    int task = first - stride, ks = 0, nks = 0;
-    Task t{};
-    auto next = [&]() -> bool {                  // the stage after this one
-      if (++ks < nks) return true;
-      do {
-        task += stride;
-        if (task >= ntasks) return false;
-        t = task_at(task, args, s_blk, s_cnt);
-      } while (t.rows == 0);
-      ks = 0;
-      nks = (t.rows + kRowsPerStage - 1) / kRowsPerStage;
+  } else if (warp == kCodesWarp) {
+    // ------------------------------------------------------------------ codes by TMA, scales by loads
+    const uint64_t pol = policy_evict_normal();
+    Cursor at(first, stride, ntasks, part, parts);
+    Ring<kRaw> ring;
+    // the next stage: its column, and this lane's rows of it, r and r + 32 (their pairs, where x's rows are tokens). Past
+    // the expert's last row that is the last one.
+    int col = 0, row[2] = {0, 0};
+    auto plan = [&]() -> bool {
+      if (!at.next(args, s_blk, s_cnt)) return false;
+      col = at.t.c0 + static_cast<int>(rank) * 128;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        row[i] = at.t.row0 + min(at.ks * kRowsPerStage + lane + 32 * i, at.t.rows - 1);
+        if (args.src) row[i] = __ldg(args.src + row[i]);
+      }
       return true;
     };
-    auto fetch = [&](Fetched& f) {
-      const int col = t.c0 + chunk * 64 + q * 16;
+    int steps = 0;                               // stages loaded
+    for (bool live = plan(); live; live = plan(), ring.step(), ++steps) {
+      const int s = ring.s;
+      if (*s_abort || !mbar_wait_warp(&raw_empty[s], ring.phase ^ 1, st, s_abort, kSiteRawEmpty)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&raw_full[s], kRawBytes);
+      __syncwarp();
+      uint8_t* d = smem + Smem::raw + s * kRawBytes;
+      if (args.src) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = ks * kRowsPerStage + ((cw >> 2) + 2 * i) * 8 + r8;
-        int64_t row = -1;
-        if (r < t.rows && col < args.pitch) {
-          row = t.row0 + r;
-          if (args.src) {
-            const int pair = __ldg(args.src + row);
-            row = pair < 0 ? -1 : pair / args.K;
-          }
+        for (int i = 0; i < 2; ++i) {            // pair / K by the reciprocal's first 32 bits: at most one too small
+          const uint32_t t = __umulhi(static_cast<uint32_t>(row[i]), args.per_k);
+          row[i] = static_cast<int>(t + (row[i] - t * args.K >= static_cast<uint32_t>(args.K)));
         }
-        f.c[i] = make_uint4(0, 0, 0, 0);
-        f.byte[i] = 127;
-        if (row >= 0) {
-          f.c[i] = __ldg(reinterpret_cast<const uint4*>(args.codes + row * args.pitch + col));
-          f.byte[i] = __ldg(args.sf + row * args.blocks + (col >> 5));
-        }
-      }
-    };
-    int step = 0;
-    bool live = next();
-    Fetched f;
-    if (live) fetch(f);
-    while (live) {
-      const Fetched g = f;
-      const int rows = t.rows - ks * kRowsPerStage;      // left from this stage on
-      const int n0 = t.n0;
-      const int64_t row0 = t.row0 + ks * kRowsPerStage;
-      live = next();
-      if (live) fetch(f);
-      else if (args.unreachable) break;
-      const int s = step % kStages;
-      const uint32_t phase = (step / kStages) & 1;
-      if (!mbar_wait_warp(&empty[s], phase ^ 1, st, s_abort, kSiteEmpty)) break;
-      uint8_t* b = smem + Smem::b + s * kBBytes + chunk * kChunkBytes;
-      uint8_t* am = smem + Smem::a + s * kABytes;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[8];
-        to_bf16(g.c[i], g.byte[i], w);
-        uint8_t* p = b + ((cw >> 2) + 2 * i) * kAtom + r8 * 128;
-        *reinterpret_cast<uint4*>(p + (((2 * q) ^ r8) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(p + (((2 * q + 1) ^ r8) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-      }
-      if constexpr (!kTma) {                     // d_y by hand: 16 lanes a row
+        int four[4];                             // rows 4 l to 4 l + 3 in lane l
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = i * 16 + cw * 2 + (lane >> 4), p = lane & 15;
-          const int n = args.N - (n0 + p * 8);
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (r < rows && n > 0) {
-            v = load16_any(args.d_y + (row0 + r) * args.dy_stride + n0 + p * 8, (n < 8 ? n : 8) * 2);
-            if (n < 8) {
-              uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) w[j] = 2 * j + 1 < n ? w[j] : (2 * j < n ? w[j] & 0xFFFFu : 0u);
-              v = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          *reinterpret_cast<uint4*>(am + (p >> 3) * kChunkBytes + (r >> 3) * kAtom + (r & 7) * 128 +
-                                    (((p & 7) ^ (r & 7)) << 4)) = v;
+          const int lo = __shfl_sync(0xffffffffu, row[0], (4 * lane + i) & 31);
+          const int hi = __shfl_sync(0xffffffffu, row[1], (4 * lane + i) & 31);
+          four[i] = lane < 8 ? lo : hi;
         }
-      } else if (rows < kRowsPerStage && (rows & 15)) {
+        if (lane < 16) tma_gather4(d + lane * 512, &maps.codes, &raw_full[s], col, four, pol);
+      } else if (lane == 0) {
+        tma_load_2d(d, &maps.codes, &raw_full[s], col, at.t.row0 + at.ks * kRowsPerStage, pol);
+      }
+      const uint32_t sf = smem_u32(smem + Smem::raw_sf + s * kRawSf) + lane * 4;
+      const int word = min(col >> 7, args.sf_words - 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        copy_word_async(sf + 128 * i, args.sf + static_cast<int64_t>(row[i]) * args.sf_words + word);
+      arrive_after_copies(&raw_full[s]);
+    }
+    if (lane == 0)
+#pragma unroll 1
+      for (int s = 0; s < kRaw && s < steps; ++s)
+        mbar_drain(&raw_full[s], ((steps - 1 - s) / kRaw) & 1, st, s_abort, kSiteDrainCopies);
+    __syncwarp();
+  } else if (warp >= kConvert0) {
+    // ------------------------------------------------------------------ x into bf16
+    // Two groups of warps take turns at the stages. A warp takes 64 columns (the other 64 in odd rows) of every second
+    // group of 8 rows, 4 lanes a row: 8 lanes' 16-byte accesses, two rows, fall into 8 different bank groups, of the codes
+    // and of the operand.
+    const int cw = warp - kConvert0, group = cw % kGroups, r8 = lane >> 2, q = lane & 3;
+    const int chunk = ((cw / kGroups) & 1) ^ (r8 & 1), my_row = cw / (2 * kGroups) * 8 + r8;
+    const uint8_t* const raw0 = smem + Smem::raw + my_row * 128 + chunk * 64 + q * 16;
+    const uint8_t* const sf0 = smem + Smem::raw_sf + my_row * 4 + chunk * 2 + (q >> 1);
+    uint8_t* const b0 = smem + Smem::b + chunk * kChunkBytes + my_row * 128;
+    const int lo = ((2 * q) ^ r8) << 4, hi = ((2 * q + 1) ^ r8) << 4;
+    Cursor at(first, stride, ntasks, part, parts);
+    Ring<kRaw> raw;
+    Ring<kStages> ring;
+    int turn = group;
+    bool live = at.next(args, s_blk, s_cnt);
+    while (live) {
+      const int rows = at.t.rows - at.ks * kRowsPerStage;      // of the expert from this stage on
+      live = at.next(args, s_blk, s_cnt);
+      if (turn == 0) {
+        if (!live && args.unreachable) break;
+        if (!mbar_wait_warp(&raw_full[raw.s], raw.phase, st, s_abort, kSiteRawFull)) break;
+        uint4 c[kLaneRows];
+        uint32_t byte[kLaneRows];
+#pragma unroll
+        for (int i = 0; i < kLaneRows; ++i) {
+          c[i] = *reinterpret_cast<const uint4*>(raw0 + raw.s * kRawBytes + i * kRowStep * 128);
+          byte[i] = sf0[raw.s * kRawSf + i * kRowStep * 4];
+        }
+        bool large = false;
+#pragma unroll
+        for (int i = 0; i < kLaneRows; ++i) {
+          if (my_row + kRowStep * i >= rows) byte[i] = kNoRow;
+          large = large || is_large(byte[i]);
+        }
+        if (!mbar_wait_warp(&empty[ring.s], ring.phase ^ 1, st, s_abort, kSiteEmpty)) break;
+        auto decode = [&](auto tag) {
+#pragma unroll
+          for (int i = 0; i < kLaneRows; ++i) {
+            uint32_t w[8];
+            to_bf16<decltype(tag)::value>(c[i], byte[i], w);
+            uint8_t* p = b0 + ring.s * kHalfBytes + i * kRowStep * 128;
+            *reinterpret_cast<uint4*>(p + lo) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(p + hi) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        };
+        if (__any_sync(0xffffffffu, large)) decode(std::true_type{});
+        else decode(std::false_type{});
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full_b[ring.s]);
+          mbar_arrive(&raw_empty[raw.s]);
+        }
+      }
+      turn = turn == 0 ? kGroups - 1 : turn - 1;
+      raw.step();
+      ring.step();
+    }
+  } else if (warp == kHandWarp) {
+    // ------------------------------------------------------------------ both operands to the leader
+    Cursor at(first, stride, ntasks, part, parts);
+    Ring<kStages> ring;
+    const uint32_t full0 = map_shared(full, leader);
+    for (; at.next(args, s_blk, s_cnt); ring.step()) {
+      const int s = ring.s;
+      if (!mbar_wait_warp(&full_a[s], ring.phase, st, s_abort, kSiteFullA) ||
+          !mbar_wait_warp(&full_b[s], ring.phase, st, s_abort, kSiteFullB))
+        break;
+      const int rows = at.t.rows - at.ks * kRowsPerStage;      // left from this stage on
+      if (rows < kRowsPerStage && (rows & 15)) {
         // the sum ends inside an MMA: whatever d_y's rows behind it hold becomes zero
-        if (!mbar_wait_warp(&full_a[s], phase, st, s_abort, kSiteFullA)) break;
-        const int end = (rows + 15) & ~15;
-        for (int i = (rows * 16) + cw * 32 + lane; i < end * 16; i += 32 * kConvertWarps) {
+        uint8_t* am = smem + Smem::a + s * kHalfBytes;
+        const int stop = (rows + 15) & ~15;
+        for (int i = rows * 16 + lane; i < stop * 16; i += 32) {
           const int r = i >> 4, p = i & 15;
           *reinterpret_cast<uint4*>(am + (p >> 3) * kChunkBytes + (r >> 3) * kAtom + (r & 7) * 128 + ((p & 7) << 4)) =
               make_uint4(0, 0, 0, 0);
@@ -342,92 +512,234 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full_b[s]);
-      ++step;
+      if (lane == 0) arrive_leader(full0 + s * 8);
     }
   } else {
     // ------------------------------------------------------------------ epilogue
     constexpr int kCols = 64;                    // columns of a warp at a time
-    const int quad = warp & 3, half = (warp >> 2) * (kTileC / 2);
+    constexpr int kShare = kTile / (kEpiWarps / 4);              // columns of a warp
+    const int quad = warp & 3, half = (warp >> 2) * kShare;
     int it = 0;
     for (int i = first; i < ntasks; i += stride) {
       const Task t = task_at(i, args, s_blk, s_cnt);
-      const int64_t row = static_cast<int64_t>(t.e) * args.N + t.n0 + quad * 32;
-      const int rows = args.N - t.n0 - quad * 32;
-      if (t.rows == 0) {                         // an expert without rows
-        for (int r = 0; r < 32 && r < rows; ++r) {
-          T* p = reinterpret_cast<T*>(args.out + (row + r) * args.out_pitch);
-          for (int c = t.c0 + half + lane; c < min(args.C, t.c0 + half + kTileC / 2); c += 32) p[c] = from_float<T>(0.f);
+      const int n0 = t.n0 + static_cast<int>(rank) * 128 + quad * 32;
+      const int64_t row = static_cast<int64_t>(t.e) * args.N + n0;
+      const int rows = args.N - n0;
+      const int nks = (t.rows + kRowsPerStage - 1) / kRowsPerStage;
+      if constexpr (kSplit) {                    // every MMA of the part has completed: the stages' memory is free
+        const bool any = static_cast<int64_t>(nks) * part / parts < static_cast<int64_t>(nks) * (part + 1) / parts;
+        if (any && !mbar_wait_warp(tfull, 0, st, s_abort, kSiteTmemFull)) break;
+        tc_fence_after();
+        float* d = reinterpret_cast<float*>(smem) + (quad * 32 + lane) * Smem::kPartPitch + half;
+#pragma unroll 1
+        for (int c = 0; c < kShare; c += 32) {
+          uint32_t v[32];
+          if (any) {
+            tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + half + c, v);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<uint4*>(d + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
         continue;
       }
-      const int buf = it & 1;
-      if (!mbar_wait_warp(&tfull[buf], (it >> 1) & 1, st, s_abort, kSiteTmemFull)) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < kTileC / 2; c += kCols) {
-        const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTileC + half + c;
-        const int col = t.c0 + half + c;
-        store_accumulator<T, kCols, kLines>(src, args.out + row * args.out_pitch + col * static_cast<int64_t>(sizeof(T)),
-                                            args.out_pitch, rows, args.C - col, lane, [&] {
-                                              if (c + kCols < kTileC / 2) return;
-                                              tc_fence_before();
-                                              __syncwarp();
-                                              if (lane == 0) mbar_arrive(&tempty[buf]);
-                                            });
+      if (nks == 0) {                            // an expert without rows
+        for (int r = 0; r < 32 && r < rows; ++r) {
+          T* p = reinterpret_cast<T*>(args.out + (row + r) * args.out_pitch);
+          for (int c = t.c0 + half + lane; c < min(args.C, t.c0 + half + kShare); c += 32) p[c] = from_float<T>(0.f);
+        }
+        continue;
       }
-      ++it;
+      bool ok = true;
+      for (int seg = 0; seg < segments(nks) && ok; ++seg, ++it) {
+        const int buf = it & 1;
+        ok = mbar_wait_warp(&tfull[buf], (it >> 1) & 1, st, s_abort, kSiteTmemFull);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < kShare; c += kCols) {
+          const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTile + half + c;
+          const int col = t.c0 + half + c;
+          char* dst = args.out + row * args.out_pitch + col * static_cast<int64_t>(sizeof(T));
+          auto release = [&] {
+            if (c + kCols < kShare) return;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_shared(&tempty[buf], leader));
+          };
+          if (sizeof(T) == 4 && seg > 0)
+            store_accumulator<T, kCols, kLines, sizeof(T) == 4>(src, dst, args.out_pitch, rows, args.C - col, lane, release);
+          else
+            store_accumulator<T, kCols, kLines>(src, dst, args.out_pitch, rows, args.C - col, lane, release);
+        }
+      }
+      if (!ok) break;
     }
   }
+  if constexpr (kSplit) {
+    // every CTA adds up its share of its rows' columns, the parts in order
+    __syncthreads();
+    cluster_barrier();
+    if (first < ntasks) {
+      const Task t = task_at(first, args, s_blk, s_cnt);
+      const int n0 = t.n0 + static_cast<int>(rank) * 128;
+      const int quads = kTile / 4 / parts;       // groups of four columns
+      const int rows = min(128, args.N - n0);
+      for (int i = threadIdx.x; i < rows * quads; i += kThreads) {
+        const int r = i / quads;
+        const int c = part * (kTile / parts) + (i - r * quads) * 4;
+        const float* src = reinterpret_cast<const float*>(smem) + r * Smem::kPartPitch + c;
+        float4 sum = peer_float4(src, rank);
+        for (int s = 1; s < parts; ++s) {
+          const float4 v = peer_float4(src, 2 * s + rank);
+          sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+        }
+        Vec<T, 4> o;
+        o.v[0] = from_float<T>(sum.x); o.v[1] = from_float<T>(sum.y);
+        o.v[2] = from_float<T>(sum.z); o.v[3] = from_float<T>(sum.w);
+        T* dst = reinterpret_cast<T*>(args.out + (static_cast<int64_t>(t.e) * args.N + n0 + r) * args.out_pitch) + t.c0 + c;
+        if (kLines && t.c0 + c + 4 <= args.C) {
+          *reinterpret_cast<Vec<T, 4>*>(dst) = o;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (t.c0 + c + j < args.C) dst[j] = o.v[j];
+        }
+      }
+    }
+  }
+  // nothing targets a CTA that has left: the other's arrivals, and its reads of the partial sums
   __syncthreads();
+  cluster_barrier();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
+// Rows of d_y on no 16-byte boundary into rows of whole 16-byte pieces, and rows of scales on no 4-byte boundary into rows
+// of whole words: `pieces` a row and a thread each, of T.
+constexpr int kCopyThreads = 256;
 template <typename T>
-cudaError_t launch(const WeightGradLaunch& p, const Args& a, cudaStream_t s) {
-  const bool tma = reinterpret_cast<uintptr_t>(p.d_y) % 16 == 0 && p.d_stride % 8 == 0;
-  const bool lines = (reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(a.out_pitch)) % 32 == 0;
-  CUtensorMap map{};
-  if (tma && encode_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.d_y, static_cast<uint64_t>(p.N),
-                            static_cast<uint64_t>(p.rows), static_cast<uint64_t>(p.d_stride) * 2, 64, kRowsPerStage,
-                            CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
-  auto kernel = tma ? (lines ? weight_grad_kernel<T, true, true> : weight_grad_kernel<T, true, false>)
-                    : (lines ? weight_grad_kernel<T, false, true> : weight_grad_kernel<T, false, false>);
-  if (cudaError_t e = configure_kernel(reinterpret_cast<const void*>(kernel), 0, Smem::total(kMaxE))) return e;
-  const int64_t tasks = static_cast<int64_t>(a.E) * a.NT * a.CT;
-  const int sms = dev_info().sms;
-  kernel<<<static_cast<unsigned>(tasks < sms ? tasks : sms), kThreads, Smem::total(p.cnt ? a.E : 0), s>>>(map, a);
+__global__ void __launch_bounds__(kCopyThreads)
+    align_rows_kernel(const char* __restrict__ x, int64_t pitch, int64_t rows, int bytes, int pieces, T* __restrict__ out) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
+  const int64_t r = i / pieces;
+  const int c = static_cast<int>(i - r * pieces) * static_cast<int>(sizeof(T));
+  if (r >= rows) return;
+  const uint4 v = load16_any(x + r * pitch + c, min(static_cast<int>(sizeof(T)), bytes - c));
+  memcpy(out + i, &v, sizeof(T));                // past the row: columns that no tile stores
+}
+template <typename T>
+cudaError_t align_rows(const void* x, int64_t pitch, int64_t rows, int bytes, void* out, cudaStream_t s) {
+  const int pieces = (bytes + static_cast<int>(sizeof(T)) - 1) / static_cast<int>(sizeof(T));
+  const int64_t all = rows * pieces;
+  align_rows_kernel<T><<<static_cast<unsigned>((all + kCopyThreads - 1) / kCopyThreads), kCopyThreads, 0, s>>>(
+      static_cast<const char*>(x), pitch, rows, bytes, pieces, static_cast<T*>(out));
   return cudaGetLastError();
+}
+
+template <typename T, bool kSplit>
+cudaError_t launch(const WeightGradLaunch& p, const Args& a, const Maps& maps, int parts, cudaStream_t s) {
+  const bool lines = (reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(a.out_pitch)) % 32 == 0;
+  auto kernel = lines ? weight_grad_kernel<T, kSplit, true> : weight_grad_kernel<T, kSplit, false>;
+  const void* fn = reinterpret_cast<const void*>(kernel);
+  if (cudaError_t e = configure_kernel(fn, 0, Smem::total(kMaxE))) return e;
+  int64_t pairs = static_cast<int64_t>(a.E) * a.NT * a.CT * parts;
+  if (!kSplit) {
+    int most = 0;
+    if (cudaError_t e = max_pair_clusters(fn, kThreads, Smem::total(kMaxE), &most)) return e;
+    if (most < 1) return cudaErrorInvalidConfiguration;
+    if (pairs > most) pairs = most;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem::total(p.cnt ? a.E : 0);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * parts; attr[0].val.clusterDim.y = 1; attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, a);
+}
+
+// The copies a call needs, in its scratch: of d_y, then of the scales.
+struct Copies {
+  size_t d_y, sf;            // bytes, 0: none
+};
+Copies copies_of(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int64_t x_rows, int C) {
+  const int blocks = blocks8(C, MM_MOE_VARIANT_MX);
+  Copies c{0, 0};
+  if (reinterpret_cast<uintptr_t>(d_y) % 16 || d_stride % 8) c.d_y = static_cast<size_t>(rows) * ((N + 7) / 8) * 16;
+  if (reinterpret_cast<uintptr_t>(sf) % 4 || blocks % 4) c.sf = static_cast<size_t>(x_rows) * ((blocks + 3) / 4) * 4;
+  return c;
 }
 
 }  // namespace
 
 int64_t weight_grad_tasks(int E, int N, int C) {
-  return static_cast<int64_t>(E) * ((N + kTileN - 1) / kTileN) * ((C + kTileC - 1) / kTileC);
+  return static_cast<int64_t>(E) * ((N + kTile - 1) / kTile) * ((C + kTile - 1) / kTile);
+}
+
+size_t weight_grad_scratch_bytes(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int64_t x_rows,
+                                 int C) {
+  const Copies c = copies_of(d_y, d_stride, rows, N, sf, x_rows, C);
+  return c.d_y + c.sf;
 }
 
 cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
   Args a{};
   if (cudaError_t e = mx_report(&a.report)) return e;
-  a.d_y = static_cast<const __nv_bfloat16*>(p.d_y);
-  a.dy_stride = p.d_stride;
   a.N = p.N; a.C = p.C; a.E = p.E; a.block_m = p.block_m;
-  a.NT = (p.N + kTileN - 1) / kTileN;
-  a.CT = (p.C + kTileC - 1) / kTileC;
+  a.NT = (p.N + kTile - 1) / kTile;
+  a.CT = (p.C + kTile - 1) / kTile;
   a.rows = static_cast<int>(p.rows);
-  a.codes = p.codes; a.sf = p.sf;
-  a.blocks = blocks8(p.C, MM_MOE_VARIANT_MX);
-  a.pitch = a.blocks * kMxBlock;
   a.cnt = p.cnt; a.blk_off = p.blk_off; a.src = p.src; a.K = p.K;
+  a.per_k = p.K > 0 ? 0xFFFFFFFFu / static_cast<uint32_t>(p.K) : 0;
   a.out = static_cast<char*>(p.out);
   a.out_pitch = static_cast<int64_t>(p.C) * dtype_size(p.dtype);
   a.unreachable = p.unreachable;
   a.timeout_ns = p.timeout_ns;
-  return p.dtype == MM_MOE_DTYPE_F32 ? launch<float>(p, a, s) : launch<__nv_bfloat16>(p, a, s);
+  const int64_t x_rows = p.src ? p.pairs / p.K : p.rows;
+  const int blocks = blocks8(p.C, MM_MOE_VARIANT_MX);
+  const Copies copies = copies_of(p.d_y, p.d_stride, p.rows, p.N, p.sf, x_rows, p.C);
+  const void *d_y = p.d_y, *sf = p.sf;
+  uint64_t pitch = static_cast<uint64_t>(p.d_stride) * 2;
+  if (copies.d_y) {
+    if (cudaError_t e = align_rows<uint4>(p.d_y, p.d_stride * 2, p.rows, p.N * 2, p.scratch, s)) return e;
+    d_y = p.scratch;
+    pitch = static_cast<uint64_t>((p.N + 7) / 8) * 16;
+  }
+  if (copies.sf) {
+    char* to = static_cast<char*>(p.scratch) + copies.d_y;
+    if (cudaError_t e = align_rows<uint32_t>(p.sf, blocks, x_rows, blocks, to, s)) return e;
+    sf = to;
+  }
+  a.sf = static_cast<const uint32_t*>(sf);
+  a.sf_words = (blocks + 3) / 4;
+  Maps maps;
+  if (encode_tmap_2d(&maps.d_y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_y, static_cast<uint64_t>(p.N),
+                     static_cast<uint64_t>(p.rows), pitch, 64, kRowsPerStage, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  // a row of codes, four of them gathered by an instruction, or the rows of a stage
+  const uint64_t bytes = static_cast<uint64_t>(blocks) * kMxBlock;
+  if (encode_tmap_2d(&maps.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, bytes, static_cast<uint64_t>(x_rows), bytes, 128,
+                     p.src ? 1 : kRowsPerStage, CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  // parts of at least four stages, as many as leave no SM without work
+  const int64_t tasks = weight_grad_tasks(p.E, p.N, p.C);
+  const int64_t stages = ((p.cnt ? static_cast<int64_t>(p.pairs) / p.E : p.rows) + kRowsPerStage - 1) / kRowsPerStage;
+  int parts = 1;
+  while (parts < kMostParts && tasks * parts * 4 <= dev_info().sms && stages >= 8 * parts) parts *= 2;
+  if (p.dtype == MM_MOE_DTYPE_F32)
+    return parts > 1 ? launch<float, true>(p, a, maps, parts, s) : launch<float, false>(p, a, maps, 1, s);
+  return parts > 1 ? launch<__nv_bfloat16, true>(p, a, maps, parts, s) : launch<__nv_bfloat16, false>(p, a, maps, 1, s);
 }
 
 }  // namespace mm

@@ -81,15 +81,25 @@ def test_swiglu(M):
 def test_weight_grad(M):
     n = 8 + 4 * 15
 
-    def g(dy=A, ds=64, rows=n, N=64, codes=A, sf=A, C=64, T=4, K=2, E=4, bm=16, cnt=A, src=A, blk=A, tok=0, dtype=1, out=A):
-        return M.mm_moe_weight_grad(dy, ds, rows, N, codes, sf, C, T, K, E, bm, cnt, src, blk, tok, dtype, out, 0, 0, None)
+    def g(dy=A, ds=64, rows=n, N=64, codes=A, sf=A, C=64, T=4, K=2, E=4, bm=16, cnt=A, src=A, blk=A, tok=0, dtype=1, out=A,
+          scr=None, n_scr=0):
+        return M.mm_moe_weight_grad(dy, ds, rows, N, codes, sf, C, T, K, E, bm, cnt, src, blk, tok, dtype, out, scr, n_scr, 0, 0,
+                                    None)
     dense = dict(cnt=None, src=None, blk=None)
     refused(M, g, [dict(dy=None), dict(dy=A + 1), dict(ds=63), dict(rows=-1), dict(N=0), dict(N=LONG + 1, ds=LONG + 1),
                    dict(codes=None), dict(codes=A + 8), dict(sf=None), dict(C=0), dict(C=LONG + 1), dict(T=-1), dict(K=0),
                    dict(K=5), dict(E=0), dict(E=1025), dict(bm=8), dict(bm=20), dict(cnt=None), dict(src=None),
                    dict(blk=None), dict(cnt=A + 2), dict(rows=n - 1), dict(dtype=2), dict(dtype=-1), dict(out=None),
                    dict(out=A + 1), dict(dtype=0, out=A + 2), dict(dense, tok=1), dict(N=1 << 29, ds=1 << 29),
-                   dict(dense, N=1 << 20, ds=1 << 20, C=1 << 30)])
+                   dict(dense, N=1 << 20, ds=1 << 20, C=1 << 30), dict(ds=65), dict(dy=A + 2), dict(ds=65, scr=A + 8, n_scr=1 << 20)])
+    need = M.mm_moe_weight_grad_scratch_size(A, 65, n, 64, A, n, 64)
+    assert need == (16 * 8 + 4) * n and M.mm_moe_weight_grad_scratch_size(A, 64, n, 64, A, n, 128) == 0
+    assert g(ds=65, scr=A, n_scr=need - 1) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL
+    assert g(tok=1, scr=A, n_scr=15) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL         # scales of four tokens, a word each
+    for bad in ((A, 63, n, 64, A, n, 64), (A, 64, -1, 64, A, n, 64), (A, 64, n, 0, A, n, 64), (A, 64, n, 64, A, -1, 64),
+                (A, 64, n, 64, A, n, 0)):
+        with pytest.raises(M.MMError):
+            M.mm_moe_weight_grad_scratch_size(*bad)
 
 
 def test_binding_sizes_agree_with_the_library(M):
@@ -97,6 +107,11 @@ def test_binding_sizes_agree_with_the_library(M):
     for T in (0, 1, 7, 303, 304, 305, 1217, 2432, 2433, 100000):
         for H in (1, 16, 17, 512, 513, 1001, 1024, 1025, 4096, 7168, 8192, 8193, 16384, 16400, 100000):
             assert M.mm_moe_rms_norm_scratch_size(T, H) == ops._norm_scratch(T, H), (T, H)
+    for at in (A, A + 2, A + 8, A + 16):
+        for pitch, N in ((64, 64), (64, 63), (65, 64), (72, 65), (1, 1), (8, 1)):
+            for sf, C in ((A, 128), (A, 129), (A, 96), (A + 1, 256), (A + 4, 1024)):
+                args = (at, pitch, 77, N, sf, 33, C)
+                assert M.mm_moe_weight_grad_scratch_size(*args) == ops._grad_scratch(*args), args
 
 
 # ------------------------------------------------------------------ tensor forms, with a stand-in for the library
