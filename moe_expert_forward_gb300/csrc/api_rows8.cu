@@ -138,12 +138,11 @@ int mm_moe_swiglu_backward(const void* d_a, int dtype, int64_t d_stride, const v
                                      static_cast<cudaStream_t>(stream)));
 }
 
-int mm_moe_weight_grad_scratch_size(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int64_t x_rows,
-                                    int C, size_t* bytes) {
-  if (!bytes || rows < 0 || rows > kMaxRows || N < 1 || N > kMaxCols || d_stride < N || x_rows < 0 || x_rows > kMaxRows ||
-      C < 1 || C > kMaxCols)
+int mm_moe_weight_grad_scratch_size(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C,
+                                    int by_token, size_t* bytes) {
+  if (!bytes || rows < 0 || rows > kMaxRows || N < 1 || N > kMaxCols || d_stride < N || C < 1 || C > kMaxCols)
     return MM_MOE_ERR_INVALID_ARG;
-  *bytes = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, x_rows, C);
+  *bytes = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0);
   return MM_MOE_OK;
 }
 
@@ -161,7 +160,7 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
   if (!out || !aligned(out, dtype_size(dtype))) return MM_MOE_ERR_INVALID_ARG;
   if (rows > 0 && !(cnt && T == 0) && (!d_y || !codes || !aligned(d_y, 2) || !held_ok(codes, sf, MM_MOE_VARIANT_MX)))
     return MM_MOE_ERR_INVALID_ARG;
-  const size_t need = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, by_token ? T : rows, C);
+  const size_t need = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0);
   if (need && (!scratch || !aligned(scratch, 16))) return MM_MOE_ERR_INVALID_ARG;
   if (scratch_bytes < need) return MM_MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;

@@ -298,8 +298,8 @@ struct WeightGradLaunch {
   uint64_t timeout_ns;
   bool unreachable;
 };
-size_t weight_grad_scratch_bytes(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int64_t x_rows,
-                                 int C);
+size_t weight_grad_scratch_bytes(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C,
+                                 bool by_token);
 int64_t weight_grad_tasks(int E, int N, int C);
 cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s);
 

@@ -22,10 +22,11 @@
 // the MMA's accumulation drops bits below its accumulator's last, and 8192 rows in one
 // accumulator were 3.7e-6 off (rounding to nearest: 3.6e-7).
 //
-// Codes come by TMA too (gathered four rows an instruction where x's rows are tokens), their scales by 4-byte
-// asynchronous copies, into a ring of their own: converters that load for themselves keep the SM's loads in flight at
-// their limit, and wait for it (1000 cycles a stage and more).  Rows of d_y, or of scales, that start on no 16-byte,
-// or 4-byte, boundary are copied first.
+// Codes come by TMA too, their scales by 4-byte asynchronous copies, into a ring of their own: converters that load
+// for themselves keep the SM's loads in flight at their limit, and wait for it (1000 cycles a stage and more).  Where
+// x's rows are tokens, a kernel before this one copies them to their pool rows (TMA's own gather, four rows an
+// instruction, took 1900 cycles a stage; 64 experts of 384 rows 1426 us instead of 785 and 30).  Rows of d_y, or of
+// scales, that start on no 16-byte, or 4-byte, boundary are copied first too.
 //
 // The loops of all roles have to fit the instruction cache together: none is unrolled over its ring (unrolled, a third
 // of the fetches missed and a stage took 1500 cycles).
@@ -40,11 +41,11 @@
 namespace mm {
 namespace {
 
-constexpr int kStages = 5;                       // of operands
+constexpr int kStages = 4;                       // of operands
 constexpr int kRaw = 6;                          // of codes
 constexpr int kRowsPerStage = 64;
 constexpr int kTile = 256;                       // columns of d_y (M) and of x (N) of a pair; 128 of each in a CTA
-constexpr int kEpiWarps = 4, kConvertWarps = 8;
+constexpr int kEpiWarps = 4, kConvertWarps = 12;
 constexpr int kMmaWarp = kEpiWarps, kTmaWarp = kMmaWarp + 1, kCodesWarp = kTmaWarp + 1, kHandWarp = kCodesWarp + 1,
               kConvert0 = kHandWarp + 1;
 constexpr int kThreads = 32 * (kConvert0 + kConvertWarps);
@@ -53,25 +54,27 @@ constexpr int kChunkBytes = kRowsPerStage * 128; // 64 columns of a stage
 constexpr int kHalfBytes = 2 * kChunkBytes;      // 128 columns: one CTA's share of an operand
 constexpr int kRawBytes = kRowsPerStage * 128;   // 128 columns of codes
 constexpr int kRawSf = kRowsPerStage * 4;        // and their scales
-constexpr int kGroups = 2;                       // of converter warps, which take turns at the stages
+constexpr int kGroups = 3;                       // of converter warps, which take turns at the stages
 constexpr int kRowStep = 8 * kConvertWarps / (2 * kGroups);      // between the rows of a converter lane
 constexpr int kLaneRows = kRowsPerStage / kRowStep;
 constexpr int kSegment = 16;                     // stages of one fp32 accumulator
 constexpr int kMostParts = 4;
+constexpr int kBoxBytes = 32 * 128;              // 32 rows of 128 bytes of results
 
 struct Smem {
   static constexpr int a = 0;
   static constexpr int b = a + kStages * kHalfBytes;
   static constexpr int raw = b + kStages * kHalfBytes;
   static constexpr int raw_sf = raw + kRaw * kRawBytes;
-  static constexpr int bars = raw_sf + kRaw * kRawSf;
+  static constexpr int out = (raw_sf + kRaw * kRawSf + 1023) / 1024 * 1024;      // two boxes of results of each epilogue warp
+  static constexpr int bars = out + kEpiWarps * 2 * kBoxBytes;
   static constexpr int nbars = 4 * kStages + 2 * kRaw + 5;       // full_a, full_b, full, empty, raw_full, raw_empty, ...
   static constexpr int meta = bars + nbars * 8 + 16;             // blk_off[E + 1], cnt[E]
   static constexpr int kPartPitch = kTile + 4;   // floats of a row of partial sums
   static int total(int E) { return meta + (2 * E + 1) * 4 + 1024; }
 };
 static_assert(Smem::meta + (2 * kMaxE + 1) * 4 + 1024 <= 232448, "shared memory");
-static_assert(128 * Smem::kPartPitch * 4 <= Smem::raw, "partial sums fit the stages");
+static_assert(128 * Smem::kPartPitch * 4 <= Smem::out, "partial sums fit the stages and codes");
 
 enum : int {
   kSiteEmpty = 181, kSiteFullA = 182, kSiteFull = 183, kSiteTmemEmpty = 184, kSiteTmemFull = 185, kSiteDrainCopies = 186,
@@ -87,9 +90,6 @@ struct Args {
   int sf_words;              // words from one row of scales to the next
   const int* cnt;            // null: dense
   const int* blk_off;
-  const int* src;            // x's rows are tokens: pool row -> pair; null: x's rows are d_y's
-  int K;
-  uint32_t per_k;            // floor((2^32 - 1) / K)
   char* out;
   int64_t out_pitch;         // bytes of a row of out
   int unreachable;           // leave x of the CTA's last stage out
@@ -121,9 +121,9 @@ __device__ __forceinline__ void tc_commit_both(uint64_t* bar, uint16_t ctas) {
 // this thread's shared-memory stores before later reads by the tensor cores
 __device__ __forceinline__ void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Arrive on the leader's barrier, releasing within this CTA: all that is handed over lies in this CTA's shared memory,
-// fenced towards the tensor cores that read it, and no thread of the other CTA looks at it. (Releasing to the cluster waits
-// for whatever the SM has in flight, about 2000 cycles a stage.)
+// Arrive on the leader's barrier, releasing within this CTA: all that is handed over lies in this CTA's shared memory or
+// tensor memory, fenced towards the tensor cores that use it, and no thread of the other CTA looks at it. (Releasing to
+// the cluster waits for whatever the SM has in flight, about 2000 cycles a stage.)
 __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -170,6 +170,33 @@ struct Cursor {
   }
 };
 
+// 32 rows of 128 bytes from shared memory to out, or (kAdd, fp32) added to what is there.
+template <bool kAdd>
+__device__ __forceinline__ void tma_store_box(const CUtensorMap* m, const void* src, int c, int n, int e) {
+  if constexpr (kAdd)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(smem_u32(src)), "r"(c), "r"(n), "r"(e)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(smem_u32(src)), "r"(c), "r"(n), "r"(e)
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// all but this thread's last kLeft boxes have been read from shared memory; tma_stored: written
+template <int kLeft>
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory"); }
+__device__ __forceinline__ void tma_stored() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// One lane of a whole warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // A slot of a ring of N, in turn.
 template <int N>
 struct Ring {
@@ -190,17 +217,6 @@ __device__ __forceinline__ void copy_word_async(uint32_t dst, const uint32_t* sr
 }
 __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// Four rows of a tensor map whose box is one row high.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int c, const int (&row)[4],
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(c), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(smem_u32(bar)),
-      "l"(policy)
-      : "memory");
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -237,12 +253,12 @@ __device__ __forceinline__ void to_bf16(const uint4& c, uint32_t byte, uint32_t 
 }
 
 struct Maps {
-  CUtensorMap d_y, codes;
+  CUtensorMap d_y, codes, out;
 };
 
 // kSplit: a cluster takes one task, each pair a range of its stages; the partial accumulators meet in shared memory.
-// kLines: see store_accumulator.
-template <typename T, bool kSplit, bool kLines>
+// kTma: out's rows are 16-byte aligned, and results leave by TMA.
+template <typename T, bool kSplit, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ Maps maps, const Args args) {
   extern __shared__ uint8_t smem_raw[];
@@ -332,49 +348,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMAs (leader)
-    if (rank == 0 && lane == 0) {
+    // the whole warp goes through the loop, and one lane issues: what the instructions take stays in uniform registers
+    if (rank == 0) {
+      const bool issues = elect_one();
       // 64-column chunks kChunkBytes apart, 8-row groups one atom apart
       const uint64_t da0 = make_smem_desc(smem_u32(smem + Smem::a), kChunkBytes, kAtom, 2);
       const uint64_t db0 = make_smem_desc(smem_u32(smem + Smem::b), kChunkBytes, kAtom, 2);
       const uint16_t both = static_cast<uint16_t>(3u << leader);
       Cursor at(first, stride, ntasks, part, parts);
+      Ring<kStages> ring;
       uint32_t acc = tmem;
-      int it = 0, left = 0, in_acc = 0;          // accumulators so far; stages left of this one, and in it so far
+      int it = 0, left = 0, in_acc = 0, rows = 0;     // accumulators so far; of this one: stages left, stages in it; rows left
       bool live = at.next_task(args, s_blk, s_cnt);
+      auto wait = [&](uint64_t* bar, uint32_t phase, int where) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar, phase, st, s_abort, where));
+        tc_fence_after();
+        return ok;
+      };
       auto start = [&]() {                       // an accumulator
         const int buf = it & 1;
         acc = tmem + buf * kTile;
         left = at.end - at.ks;
         if (sizeof(T) == 4 && !kSplit) left = min(left, kSegment);
         in_acc = 0;
-        live = !*s_abort && mbar_wait_cluster(&tempty[buf], ((it >> 1) & 1) ^ 1, st, s_abort, kSiteTmemEmpty);
-        tc_fence_after();
+        rows = at.t.rows - at.ks * kRowsPerStage;
+        live = !__any_sync(0xffffffffu, *s_abort) && wait(&tempty[buf], ((it >> 1) & 1) ^ 1, kSiteTmemEmpty);
       };
       if (live) start();
-      Ring<kStages> ring;
       while (live) {
         const int s = ring.s;
-        if (!mbar_wait_cluster(&full[s], ring.phase, st, s_abort, kSiteFull)) break;
-        tc_fence_after();
+        if (!wait(&full[s], ring.phase, kSiteFull)) break;
         const uint64_t da = da0 + ((s * kHalfBytes) >> 4), db = db0 + ((s * kHalfBytes) >> 4);
-        const int rows = at.t.rows - at.ks * kRowsPerStage;
-        tc_mma_f16_pair(acc, da, db, kIdesc, in_acc);
+        if (issues) {
+          tc_mma_f16_pair(acc, da, db, kIdesc, in_acc);
 #pragma unroll
-        for (int k = 1; k < 4; ++k)              // 16 rows: two atoms
-          if (rows > 16 * k) tc_mma_f16_pair(acc, da + k * (2 * kAtom >> 4), db + k * (2 * kAtom >> 4), kIdesc, 1);
-        tc_commit_both(&empty[s], both);
+          for (int k = 1; k < 4; ++k)            // 16 rows: two atoms
+            if (rows > 16 * k) tc_mma_f16_pair(acc, da + k * (2 * kAtom >> 4), db + k * (2 * kAtom >> 4), kIdesc, 1);
+          tc_commit_both(&empty[s], both);
+        }
+        __syncwarp();
         ring.step();
         in_acc = 1;
+        rows -= kRowsPerStage;
         ++at.ks;
         if (--left == 0) {
-          tc_commit_both(&tfull[it & 1], both);
+          if (issues) tc_commit_both(&tfull[it & 1], both);
+          __syncwarp();
           ++it;
           live = at.ks < at.end || at.next_task(args, s_blk, s_cnt);
           if (live) start();
         }
       }
-      tc_commit_pair(map_shared(drain, leader));
-      mbar_drain(drain, 0, st, s_abort, kSiteDrainMma);
+      if (issues) {
+        tc_commit_pair(map_shared(drain, leader));
+        mbar_drain(drain, 0, st, s_abort, kSiteDrainMma);
+      }
     }
     __syncwarp();
   } else if (warp == kCodesWarp) {
@@ -382,48 +410,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t pol = policy_evict_normal();
     Cursor at(first, stride, ntasks, part, parts);
     Ring<kRaw> ring;
-    // the next stage: its column, and this lane's rows of it, r and r + 32 (their pairs, where x's rows are tokens). Past
-    // the expert's last row that is the last one.
-    int col = 0, row[2] = {0, 0};
-    auto plan = [&]() -> bool {
-      if (!at.next(args, s_blk, s_cnt)) return false;
-      col = at.t.c0 + static_cast<int>(rank) * 128;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        row[i] = at.t.row0 + min(at.ks * kRowsPerStage + lane + 32 * i, at.t.rows - 1);
-        if (args.src) row[i] = __ldg(args.src + row[i]);
-      }
-      return true;
-    };
     int steps = 0;                               // stages loaded
-    for (bool live = plan(); live; live = plan(), ring.step(), ++steps) {
+    for (; at.next(args, s_blk, s_cnt); ring.step(), ++steps) {
       const int s = ring.s;
-      if (*s_abort || !mbar_wait_warp(&raw_empty[s], ring.phase ^ 1, st, s_abort, kSiteRawEmpty)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&raw_full[s], kRawBytes);
-      __syncwarp();
-      uint8_t* d = smem + Smem::raw + s * kRawBytes;
-      if (args.src) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {            // pair / K by the reciprocal's first 32 bits: at most one too small
-          const uint32_t t = __umulhi(static_cast<uint32_t>(row[i]), args.per_k);
-          row[i] = static_cast<int>(t + (row[i] - t * args.K >= static_cast<uint32_t>(args.K)));
-        }
-        int four[4];                             // rows 4 l to 4 l + 3 in lane l
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int lo = __shfl_sync(0xffffffffu, row[0], (4 * lane + i) & 31);
-          const int hi = __shfl_sync(0xffffffffu, row[1], (4 * lane + i) & 31);
-          four[i] = lane < 8 ? lo : hi;
-        }
-        if (lane < 16) tma_gather4(d + lane * 512, &maps.codes, &raw_full[s], col, four, pol);
-      } else if (lane == 0) {
-        tma_load_2d(d, &maps.codes, &raw_full[s], col, at.t.row0 + at.ks * kRowsPerStage, pol);
+      if (!mbar_wait_warp(&raw_empty[s], ring.phase ^ 1, st, s_abort, kSiteRawEmpty)) break;
+      const int col = at.t.c0 + static_cast<int>(rank) * 128, row0 = at.t.row0 + at.ks * kRowsPerStage;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&raw_full[s], kRawBytes);
+        tma_load_2d(smem + Smem::raw + s * kRawBytes, &maps.codes, &raw_full[s], col, row0, pol);
       }
       const uint32_t sf = smem_u32(smem + Smem::raw_sf + s * kRawSf) + lane * 4;
       const int word = min(col >> 7, args.sf_words - 1);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        copy_word_async(sf + 128 * i, args.sf + static_cast<int64_t>(row[i]) * args.sf_words + word);
+        copy_word_async(sf + 128 * i, args.sf + static_cast<int64_t>(min(row0 + lane + 32 * i, args.rows - 1)) * args.sf_words + word);
       arrive_after_copies(&raw_full[s]);
     }
     if (lane == 0)
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kConvert0) {
     // ------------------------------------------------------------------ x into bf16
-    // Two groups of warps take turns at the stages. A warp takes 64 columns (the other 64 in odd rows) of every second
+    // Three groups of warps take turns at the stages. A warp takes 64 columns (the other 64 in odd rows) of every second
     // group of 8 rows, 4 lanes a row: 8 lanes' 16-byte accesses, two rows, fall into 8 different bank groups, of the codes
     // and of the operand.
     const int cw = warp - kConvert0, group = cw % kGroups, r8 = lane >> 2, q = lane & 3;
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kCols = 64;                    // columns of a warp at a time
     constexpr int kShare = kTile / (kEpiWarps / 4);              // columns of a warp
     const int quad = warp & 3, half = (warp >> 2) * kShare;
-    int it = 0;
+    int it = 0, box_turn = 0;
     for (int i = first; i < ntasks; i += stride) {
       const Task t = task_at(i, args, s_blk, s_cnt);
       const int n0 = t.n0 + static_cast<int>(rank) * 128 + quad * 32;
@@ -560,25 +560,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait_warp(&tfull[buf], (it >> 1) & 1, st, s_abort, kSiteTmemFull);
         if (!ok) break;
         tc_fence_after();
+        auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader(map_shared(&tempty[buf], leader));
+        };
+        const uint32_t src0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTile + half;
+        if constexpr (kTma) {
+          constexpr int kBox = 128 / sizeof(T);  // columns of a box
+          if (seg > 0 && lane == 0) tma_stored();          // what the boxes are added to
 #pragma unroll 1
-        for (int c = 0; c < kShare; c += kCols) {
-          const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTile + half + c;
-          const int col = t.c0 + half + c;
-          char* dst = args.out + row * args.out_pitch + col * static_cast<int64_t>(sizeof(T));
-          auto release = [&] {
-            if (c + kCols < kShare) return;
-            tc_fence_before();
+          for (int c = 0; c < kShare; c += kBox) {
+            uint32_t w[32];
+            if constexpr (sizeof(T) == 4) {
+              tmem_ld_32x32b_x32(src0 + c, w);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(src0 + c + 32 * h, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[16 * h + j] = pack2<T>(v[2 * j], v[2 * j + 1]);
+              }
+            }
+            if (c + kBox == kShare) release();
+            const int col = t.c0 + half + c;
+            if (rows <= 0 || col >= args.C) continue;
+            uint8_t* box = smem + Smem::out + (warp * 2 + (box_turn & 1)) * kBoxBytes;
+            ++box_turn;
+            if (lane == 0) tma_store_read<1>();  // the box before the last one's is free
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_shared(&tempty[buf], leader));
-          };
-          if (sizeof(T) == 4 && seg > 0)
-            store_accumulator<T, kCols, kLines, sizeof(T) == 4>(src, dst, args.out_pitch, rows, args.C - col, lane, release);
-          else
-            store_accumulator<T, kCols, kLines>(src, dst, args.out_pitch, rows, args.C - col, lane, release);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              if (sizeof(T) == 4 && seg > 0) tma_store_box<true>(&maps.out, box, col, n0, t.e);
+              else tma_store_box<false>(&maps.out, box, col, n0, t.e);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kShare; c += kCols) {
+            const int col = t.c0 + half + c;
+            char* dst = args.out + row * args.out_pitch + col * static_cast<int64_t>(sizeof(T));
+            auto last = [&] {
+              if (c + kCols == kShare) release();
+            };
+            if (sizeof(T) == 4 && seg > 0)
+              store_accumulator<T, kCols, false, sizeof(T) == 4>(src0 + c, dst, args.out_pitch, rows, args.C - col, lane, last);
+            else
+              store_accumulator<T, kCols, false>(src0 + c, dst, args.out_pitch, rows, args.C - col, lane, last);
+          }
         }
       }
       if (!ok) break;
     }
+    if (kTma && lane == 0) tma_stored();
+    __syncwarp();
   }
   if constexpr (kSplit) {
     // every CTA adds up its share of its rows' columns, the parts in order
@@ -602,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         o.v[0] = from_float<T>(sum.x); o.v[1] = from_float<T>(sum.y);
         o.v[2] = from_float<T>(sum.z); o.v[3] = from_float<T>(sum.w);
         T* dst = reinterpret_cast<T*>(args.out + (static_cast<int64_t>(t.e) * args.N + n0 + r) * args.out_pitch) + t.c0 + c;
-        if (kLines && t.c0 + c + 4 <= args.C) {
+        if (kTma && t.c0 + c + 4 <= args.C) {
           *reinterpret_cast<Vec<T, 4>*>(dst) = o;
         } else {
 #pragma unroll
@@ -621,9 +664,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Rows of x in token order into the pool rows that hold a pair of theirs, a warp a row: `pieces` of 16 bytes of codes, and
+// the scales as whole words.
+constexpr int kCopyThreads = 256;
+__global__ void __launch_bounds__(kCopyThreads)
+    gather_rows_kernel(const uint4* __restrict__ codes, int pieces, const uint8_t* __restrict__ sf, int blocks,
+                       const int32_t* __restrict__ src, const int32_t* __restrict__ blk_off, int E, int block_m, int K,
+                       int64_t rows, uint4* __restrict__ out, uint32_t* __restrict__ out_sf) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (kCopyThreads / 32) + (threadIdx.x >> 5);
+  if (r >= rows || r >= static_cast<int64_t>(__ldg(blk_off + E)) * block_m) return;
+  const int pair = __ldg(src + r);
+  if (pair < 0) return;                          // padding: no sum reads it
+  const int64_t t = pair / K;
+  const int words = (blocks + 3) / 4;
+  for (int i = lane; i < words; i += 32)
+    out_sf[r * words + i] = load16_any(sf + t * blocks + 4 * i, min(4, blocks - 4 * i)).x;
+#pragma unroll 4
+  for (int i = lane; i < pieces; i += 32) out[r * pieces + i] = __ldg(codes + t * pieces + i);
+}
+
 // Rows of d_y on no 16-byte boundary into rows of whole 16-byte pieces, and rows of scales on no 4-byte boundary into rows
 // of whole words: `pieces` a row and a thread each, of T.
-constexpr int kCopyThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kCopyThreads)
     align_rows_kernel(const char* __restrict__ x, int64_t pitch, int64_t rows, int bytes, int pieces, T* __restrict__ out) {
@@ -644,9 +706,17 @@ cudaError_t align_rows(const void* x, int64_t pitch, int64_t rows, int bytes, vo
 }
 
 template <typename T, bool kSplit>
-cudaError_t launch(const WeightGradLaunch& p, const Args& a, const Maps& maps, int parts, cudaStream_t s) {
-  const bool lines = (reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(a.out_pitch)) % 32 == 0;
-  auto kernel = lines ? weight_grad_kernel<T, kSplit, true> : weight_grad_kernel<T, kSplit, false>;
+cudaError_t launch(const WeightGradLaunch& p, const Args& a, Maps& maps, int parts, cudaStream_t s) {
+  const bool tma = (reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(a.out_pitch)) % 16 == 0;
+  if (tma && !kSplit) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(p.C), static_cast<uint64_t>(p.N), static_cast<uint64_t>(a.E)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(a.out_pitch), static_cast<uint64_t>(a.out_pitch) * p.N};
+    const uint32_t box[3] = {128 / sizeof(T), 32, 1};
+    if (encode_tmap(&maps.out, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.out,
+                    dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  auto kernel = tma ? weight_grad_kernel<T, kSplit, true> : weight_grad_kernel<T, kSplit, false>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   if (cudaError_t e = configure_kernel(fn, 0, Smem::total(kMaxE))) return e;
   int64_t pairs = static_cast<int64_t>(a.E) * a.NT * a.CT * parts;
@@ -669,15 +739,16 @@ cudaError_t launch(const WeightGradLaunch& p, const Args& a, const Maps& maps, i
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
 
-// The copies a call needs, in its scratch: of d_y, then of the scales.
+// The copies a call needs, in its scratch: of d_y, of the codes, of the scales. Bytes, 0: none.
 struct Copies {
-  size_t d_y, sf;            // bytes, 0: none
+  size_t d_y, codes, sf;
 };
-Copies copies_of(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int64_t x_rows, int C) {
+Copies copies_of(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C, bool by_token) {
   const int blocks = blocks8(C, MM_MOE_VARIANT_MX);
-  Copies c{0, 0};
+  Copies c{0, 0, 0};
   if (reinterpret_cast<uintptr_t>(d_y) % 16 || d_stride % 8) c.d_y = static_cast<size_t>(rows) * ((N + 7) / 8) * 16;
-  if (reinterpret_cast<uintptr_t>(sf) % 4 || blocks % 4) c.sf = static_cast<size_t>(x_rows) * ((blocks + 3) / 4) * 4;
+  if (by_token) c.codes = static_cast<size_t>(rows) * blocks * kMxBlock;
+  if (by_token || reinterpret_cast<uintptr_t>(sf) % 4 || blocks % 4) c.sf = static_cast<size_t>(rows) * ((blocks + 3) / 4) * 4;
   return c;
 }
 
@@ -687,10 +758,10 @@ int64_t weight_grad_tasks(int E, int N, int C) {
   return static_cast<int64_t>(E) * ((N + kTile - 1) / kTile) * ((C + kTile - 1) / kTile);
 }
 
-size_t weight_grad_scratch_bytes(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int64_t x_rows,
-                                 int C) {
-  const Copies c = copies_of(d_y, d_stride, rows, N, sf, x_rows, C);
-  return c.d_y + c.sf;
+size_t weight_grad_scratch_bytes(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C,
+                                 bool by_token) {
+  const Copies c = copies_of(d_y, d_stride, rows, N, sf, C, by_token);
+  return c.d_y + c.codes + c.sf;
 }
 
 cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
@@ -700,37 +771,44 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
   a.NT = (p.N + kTile - 1) / kTile;
   a.CT = (p.C + kTile - 1) / kTile;
   a.rows = static_cast<int>(p.rows);
-  a.cnt = p.cnt; a.blk_off = p.blk_off; a.src = p.src; a.K = p.K;
-  a.per_k = p.K > 0 ? 0xFFFFFFFFu / static_cast<uint32_t>(p.K) : 0;
+  a.cnt = p.cnt; a.blk_off = p.blk_off;
   a.out = static_cast<char*>(p.out);
   a.out_pitch = static_cast<int64_t>(p.C) * dtype_size(p.dtype);
   a.unreachable = p.unreachable;
   a.timeout_ns = p.timeout_ns;
-  const int64_t x_rows = p.src ? p.pairs / p.K : p.rows;
   const int blocks = blocks8(p.C, MM_MOE_VARIANT_MX);
-  const Copies copies = copies_of(p.d_y, p.d_stride, p.rows, p.N, p.sf, x_rows, p.C);
-  const void *d_y = p.d_y, *sf = p.sf;
+  const bool by_token = p.src != nullptr;
+  const Copies copies = copies_of(p.d_y, p.d_stride, p.rows, p.N, p.sf, p.C, by_token);
+  const void *d_y = p.d_y, *codes = p.codes, *sf = p.sf;
   uint64_t pitch = static_cast<uint64_t>(p.d_stride) * 2;
+  char* to = static_cast<char*>(p.scratch);
   if (copies.d_y) {
-    if (cudaError_t e = align_rows<uint4>(p.d_y, p.d_stride * 2, p.rows, p.N * 2, p.scratch, s)) return e;
-    d_y = p.scratch;
+    if (cudaError_t e = align_rows<uint4>(p.d_y, p.d_stride * 2, p.rows, p.N * 2, to, s)) return e;
+    d_y = to;
     pitch = static_cast<uint64_t>((p.N + 7) / 8) * 16;
+    to += copies.d_y;
   }
-  if (copies.sf) {
-    char* to = static_cast<char*>(p.scratch) + copies.d_y;
-    if (cudaError_t e = align_rows<uint32_t>(p.sf, blocks, x_rows, blocks, to, s)) return e;
+  if (copies.codes) {
+    const int per = kCopyThreads / 32;
+    gather_rows_kernel<<<static_cast<unsigned>((p.rows + per - 1) / per), kCopyThreads, 0, s>>>(
+        reinterpret_cast<const uint4*>(p.codes), blocks * kMxBlock / 16, p.sf, blocks, p.src, p.blk_off, p.E, p.block_m, p.K,
+        p.rows, reinterpret_cast<uint4*>(to), reinterpret_cast<uint32_t*>(to + copies.codes));
+    if (cudaError_t e = cudaGetLastError()) return e;
+    codes = to;
+    sf = to + copies.codes;
+  } else if (copies.sf) {
+    if (cudaError_t e = align_rows<uint32_t>(p.sf, blocks, p.rows, blocks, to, s)) return e;
     sf = to;
   }
   a.sf = static_cast<const uint32_t*>(sf);
   a.sf_words = (blocks + 3) / 4;
-  Maps maps;
+  Maps maps{};
   if (encode_tmap_2d(&maps.d_y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_y, static_cast<uint64_t>(p.N),
                      static_cast<uint64_t>(p.rows), pitch, 64, kRowsPerStage, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  // a row of codes, four of them gathered by an instruction, or the rows of a stage
   const uint64_t bytes = static_cast<uint64_t>(blocks) * kMxBlock;
-  if (encode_tmap_2d(&maps.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, bytes, static_cast<uint64_t>(x_rows), bytes, 128,
-                     p.src ? 1 : kRowsPerStage, CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
+  if (encode_tmap_2d(&maps.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, bytes, static_cast<uint64_t>(p.rows), bytes, 128,
+                     kRowsPerStage, CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   // parts of at least four stages, as many as leave no SM without work
   const int64_t tasks = weight_grad_tasks(p.E, p.N, p.C);

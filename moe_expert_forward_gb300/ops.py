@@ -711,12 +711,13 @@ def swiglu_backward(d_a, kept, kept_sf, routing: Optional[Routing] = None, topk_
     return d_h, d_w
 
 
-def _grad_scratch(d_y: int, pitch: int, rows: int, N: int, sf: int, x_rows: int, C: int) -> int:
-    """mm_moe_weight_grad_scratch_size's rule: copies of rows that are not 16-byte, or of scales that are not 4-byte,
-    aligned."""
+def _grad_scratch(d_y: int, pitch: int, rows: int, N: int, sf: int, C: int, by_token: bool) -> int:
+    """mm_moe_weight_grad_scratch_size's rule: the tokens' rows at their pool rows; copies of rows that are not 16-byte, or
+    of scales that are not 4-byte, aligned."""
     blocks = -(-C // 32)
-    return (0 if d_y % 16 == 0 and pitch % 8 == 0 else rows * -(-N // 8) * 16) + \
-        (0 if sf % 4 == 0 and blocks % 4 == 0 else x_rows * -(-blocks // 4) * 4)
+    copied = by_token or sf % 4 != 0 or blocks % 4 != 0
+    return rows * ((0 if d_y % 16 == 0 and pitch % 8 == 0 else -(-N // 8) * 16) + (32 * blocks if by_token else 0) +
+                   (-(-blocks // 4) * 4 if copied else 0))
 
 
 def weight_grad(d_y, codes, sf, C: int, routing: Optional[Routing] = None, by_token: bool = False,
@@ -744,7 +745,7 @@ def weight_grad(d_y, codes, sf, C: int, routing: Optional[Routing] = None, by_to
     if x_rows != need:
         _bad("weight_grad", f"x has {x_rows} rows, not {need}")
     out = _result(stream, (N, C) if routing is None else (E, N, C), dtype, d_y.device)
-    scratch_bytes = _grad_scratch(d_y.data_ptr(), _pitch(d_y), R, N, sp, x_rows, C)
+    scratch_bytes = _grad_scratch(d_y.data_ptr(), _pitch(d_y), R, N, sp, C, by_token)
     scratch = _new(stream, scratch_bytes, torch.uint8, d_y.device).data_ptr() if scratch_bytes else None
     _check(lib().mm_moe_weight_grad(d_y.data_ptr(), _pitch(d_y), R, N, cp, sp, C, T, K, E, block_m,
                                     None if routing is None else routing._cnt, src, blk, by_token, _DTYPES[dtype],

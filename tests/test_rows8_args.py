@@ -92,12 +92,11 @@ def test_weight_grad(M):
                    dict(blk=None), dict(cnt=A + 2), dict(rows=n - 1), dict(dtype=2), dict(dtype=-1), dict(out=None),
                    dict(out=A + 1), dict(dtype=0, out=A + 2), dict(dense, tok=1), dict(N=1 << 29, ds=1 << 29),
                    dict(dense, N=1 << 20, ds=1 << 20, C=1 << 30), dict(ds=65), dict(dy=A + 2), dict(ds=65, scr=A + 8, n_scr=1 << 20)])
-    need = M.mm_moe_weight_grad_scratch_size(A, 65, n, 64, A, n, 64)
-    assert need == (16 * 8 + 4) * n and M.mm_moe_weight_grad_scratch_size(A, 64, n, 64, A, n, 128) == 0
+    need = M.mm_moe_weight_grad_scratch_size(A, 65, n, 64, A, 64, 0)
+    assert need == (16 * 8 + 4) * n and M.mm_moe_weight_grad_scratch_size(A, 64, n, 64, A, 128, 0) == 0
     assert g(ds=65, scr=A, n_scr=need - 1) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL
-    assert g(tok=1, scr=A, n_scr=15) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL         # scales of four tokens, a word each
-    for bad in ((A, 63, n, 64, A, n, 64), (A, 64, -1, 64, A, n, 64), (A, 64, n, 0, A, n, 64), (A, 64, n, 64, A, -1, 64),
-                (A, 64, n, 64, A, n, 0)):
+    assert g(tok=1, scr=A, n_scr=(64 + 4) * n - 1) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL
+    for bad in ((A, 63, n, 64, A, 64, 0), (A, 64, -1, 64, A, 64, 0), (A, 64, n, 0, A, 64, 0), (A, 64, n, 64, A, 0, 0)):
         with pytest.raises(M.MMError):
             M.mm_moe_weight_grad_scratch_size(*bad)
 
@@ -110,8 +109,9 @@ def test_binding_sizes_agree_with_the_library(M):
     for at in (A, A + 2, A + 8, A + 16):
         for pitch, N in ((64, 64), (64, 63), (65, 64), (72, 65), (1, 1), (8, 1)):
             for sf, C in ((A, 128), (A, 129), (A, 96), (A + 1, 256), (A + 4, 1024)):
-                args = (at, pitch, 77, N, sf, 33, C)
-                assert M.mm_moe_weight_grad_scratch_size(*args) == ops._grad_scratch(*args), args
+                for by_token in (False, True):
+                    args = (at, pitch, 77, N, sf, C, by_token)
+                    assert M.mm_moe_weight_grad_scratch_size(*args) == ops._grad_scratch(*args), args
 
 
 # ------------------------------------------------------------------ tensor forms, with a stand-in for the library
