@@ -625,12 +625,13 @@ int mm_moe_swiglu_backward(const void* d_a, int dtype, int64_t d_stride, const v
  *          zero for an expert without rows
  *   scratch  mm_moe_weight_grad_scratch_size bytes, 16-byte aligned: with by_token x's rows
  *          at their pool rows, and copies of d_y and of sf where their rows do not start on 16-byte
- *          and 4-byte boundaries; else none (0 bytes, null allowed)
+ *          and 4-byte boundaries, and partial sums where few columns share many rows (K = E = 0:
+ *          dense); often none (0 bytes, null allowed)
  * A device wait past timeout_ms (0: 2000) leaves out undefined and is reported by
  * mm_moe_ops_status.  debug_flags: 0; bit 0 leaves one stage of each CTA unloaded, so that its
  * wait runs out. */
 int mm_moe_weight_grad_scratch_size(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C,
-                                    int by_token, size_t* bytes);
+                                    int T, int K, int E, int by_token, size_t* bytes);
 int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* codes, const void* sf, int C,
                        int T, int K, int E, int block_m, const int32_t* cnt, const int32_t* src,
                        const int32_t* blk_off, int by_token, int dtype, void* out, void* scratch,

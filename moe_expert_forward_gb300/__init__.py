@@ -133,7 +133,7 @@ def lib() -> ctypes.CDLL:
             "mm_moe_swiglu": (_I, [_P, _I, _I64, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
             "mm_moe_swiglu_backward": (_I, [_P, _I, _I64, _P, _P, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
                                             _P]),
-            "mm_moe_weight_grad_scratch_size": (_I, [_P, _I64, _I64, _I, _P, _I, _I, ctypes.POINTER(_SZ)]),
+            "mm_moe_weight_grad_scratch_size": (_I, [_P, _I64, _I64, _I, _P, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
             "mm_moe_weight_grad": (_I, [_P, _I64, _I64, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _SZ,
                                         ctypes.c_uint, _I, _P]),
         }
@@ -521,9 +521,9 @@ def mm_moe_swiglu_backward(d_a, dtype, d_stride, kept, kept_sf, rows, I, T, K, E
                                         blk_off, w, d_h, d_w, stream)
 
 
-def mm_moe_weight_grad_scratch_size(d_y, d_stride, rows, N, sf, C, by_token) -> int:
+def mm_moe_weight_grad_scratch_size(d_y, d_stride, rows, N, sf, C, T, K, E, by_token) -> int:
     n = _SZ(0)
-    _check(lib().mm_moe_weight_grad_scratch_size(d_y, d_stride, rows, N, sf, C, by_token, ctypes.byref(n)),
+    _check(lib().mm_moe_weight_grad_scratch_size(d_y, d_stride, rows, N, sf, C, T, K, E, by_token, ctypes.byref(n)),
            "mm_moe_weight_grad_scratch_size")
     return n.value
 

@@ -21,6 +21,8 @@ bool variant_known(int v) { return v == MM_MOE_VARIANT_MX || v == MM_MOE_VARIANT
 bool rows_known(int dtype, int64_t rows, int cols) {
   return dtype_known(dtype) && rows >= 0 && rows <= kMaxRows && cols >= 1 && cols <= kMaxCols;
 }
+// rows of one sum of a weight gradient: all (E = 0: dense), or an expert's on average
+int64_t terms_of(int64_t rows, int T, int K, int E) { return E ? static_cast<int64_t>(T) * K / E : rows; }
 // codes and scales of rows, both or neither
 bool held_ok(const void* codes, const void* sf, int variant) {
   if (!codes || !sf) return !codes && !sf;
@@ -139,10 +141,11 @@ int mm_moe_swiglu_backward(const void* d_a, int dtype, int64_t d_stride, const v
 }
 
 int mm_moe_weight_grad_scratch_size(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C,
-                                    int by_token, size_t* bytes) {
-  if (!bytes || rows < 0 || rows > kMaxRows || N < 1 || N > kMaxCols || d_stride < N || C < 1 || C > kMaxCols)
+                                    int T, int K, int E, int by_token, size_t* bytes) {
+  if (!bytes || rows < 0 || rows > kMaxRows || N < 1 || N > kMaxCols || d_stride < N || C < 1 || C > kMaxCols || T < 0 ||
+      K < 0 || K > kMaxK || E < 0 || E > kMaxE || !K != !E || (by_token && !E))
     return MM_MOE_ERR_INVALID_ARG;
-  *bytes = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0);
+  *bytes = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0, E ? E : 1, terms_of(rows, T, K, E));
   return MM_MOE_OK;
 }
 
@@ -160,7 +163,8 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
   if (!out || !aligned(out, dtype_size(dtype))) return MM_MOE_ERR_INVALID_ARG;
   if (rows > 0 && !(cnt && T == 0) && (!d_y || !codes || !aligned(d_y, 2) || !held_ok(codes, sf, MM_MOE_VARIANT_MX)))
     return MM_MOE_ERR_INVALID_ARG;
-  const size_t need = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0);
+  const int64_t terms = terms_of(rows, T, K, cnt ? E : 0);
+  const size_t need = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0, E, terms);
   if (need && (!scratch || !aligned(scratch, 16))) return MM_MOE_ERR_INVALID_ARG;
   if (scratch_bytes < need) return MM_MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
@@ -169,7 +173,7 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
     return done(cudaMemsetAsync(out, 0, static_cast<size_t>(E) * N * C * dtype_size(dtype), s));
   const WeightGradLaunch p{d_y, d_stride, rows, N, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(sf),
                            C, cnt, blk_off, by_token ? src : nullptr, K, E, block_m,
-                           cnt ? static_cast<int64_t>(T) * K : 0, dtype, out, scratch,
+                           terms, dtype, out, scratch,
                            static_cast<uint64_t>(timeout_ms ? timeout_ms : 2000) * 1000000ull, (debug_flags & 1) != 0};
   return done(launch_weight_grad(p, s));
 }

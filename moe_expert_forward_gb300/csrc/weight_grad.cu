@@ -15,8 +15,9 @@
 // columns of d_y, and a stage moves 64 KB through each SM's shared memory in the 512 cycles of
 // its MMAs where a 128 x 256 tile of one CTA would move 96.  Persistent pairs take tasks
 // in a fixed stride; the accumulator is double buffered, so that a task's stores overlap
-// the next one's products.  With few tasks a cluster of 2 or 4 pairs takes one, each
-// pair a range of its stages, and the parts meet in shared memory.
+// the next one's products.  Few tasks are split along the contraction into parts of their own, whose fp32 sums go to
+// scratch and are added up in order by a second kernel. (Clusters of 8 CTAs that add up in shared memory do not all fit
+// at once: 8192x256x4096 50 us.)
 //
 // fp32 results are sums of sums over 1024 rows (kSegment stages), added by the epilogue:
 // the MMA's accumulation drops bits below its accumulator's last, and 8192 rows in one
@@ -33,7 +34,7 @@
 //
 // Warps per CTA: 4 epilogue, 1 MMA (the leader's issues for both), 1 TMA producer of
 // d_y, 1 of codes and scales, 1 that waits for a stage's operands, fences them towards
-// the tensor cores and tells the leader, 8 converters.  Every wait is bounded.
+// the tensor cores and tells the leader, 12 converters.  Every wait is bounded.
 #include "cluster.cuh"
 #include "mx_linear.cuh"
 #include "rows8.cuh"
@@ -58,7 +59,8 @@ constexpr int kGroups = 3;                       // of converter warps, which ta
 constexpr int kRowStep = 8 * kConvertWarps / (2 * kGroups);      // between the rows of a converter lane
 constexpr int kLaneRows = kRowsPerStage / kRowStep;
 constexpr int kSegment = 16;                     // stages of one fp32 accumulator
-constexpr int kMostParts = 4;
+constexpr int kMostParts = 16;
+constexpr int kSplitPairs = 76;                  // CTA pairs that parts are made for; the scratch does not depend on the device
 constexpr int kBoxBytes = 32 * 128;              // 32 rows of 128 bytes of results
 
 struct Smem {
@@ -70,11 +72,9 @@ struct Smem {
   static constexpr int bars = out + kEpiWarps * 2 * kBoxBytes;
   static constexpr int nbars = 4 * kStages + 2 * kRaw + 5;       // full_a, full_b, full, empty, raw_full, raw_empty, ...
   static constexpr int meta = bars + nbars * 8 + 16;             // blk_off[E + 1], cnt[E]
-  static constexpr int kPartPitch = kTile + 4;   // floats of a row of partial sums
   static int total(int E) { return meta + (2 * E + 1) * 4 + 1024; }
 };
 static_assert(Smem::meta + (2 * kMaxE + 1) * 4 + 1024 <= 232448, "shared memory");
-static_assert(128 * Smem::kPartPitch * 4 <= Smem::out, "partial sums fit the stages and codes");
 
 enum : int {
   kSiteEmpty = 181, kSiteFullA = 182, kSiteFull = 183, kSiteTmemEmpty = 184, kSiteTmemFull = 185, kSiteDrainCopies = 186,
@@ -85,13 +85,14 @@ enum : int {
 struct Args {
   int N, C, E, block_m;
   int NT, CT;                // tiles of N and of C
+  int tasks, parts;          // E NT CT, and the parts of each
   int rows;                  // of d_y
   const uint32_t* sf;
   int sf_words;              // words from one row of scales to the next
   const int* cnt;            // null: dense
   const int* blk_off;
   char* out;
-  int64_t out_pitch;         // bytes of a row of out
+  int64_t out_pitch;         // bytes of a row of out; [parts][E][N] rows
   int unreachable;           // leave x of the CTA's last stage out
   int* report;
   uint64_t timeout_ns;
@@ -128,45 +129,47 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// A part of a task: the sum over stages [ks, end) of an expert's rows.
 struct Task {
-  int e, n0, c0;
+  int slab, n0, c0;          // [part][expert] of out
   int row0;                  // first row of the expert
   int rows;                  // its rows
+  int ks, end;
 };
 __device__ __forceinline__ Task task_at(int i, const Args& a, const int* s_blk, const int* s_cnt) {
   Task t;
+  const int part = a.parts > 1 ? i / a.tasks : 0;
+  i -= part * a.tasks;
   const int nt = i % a.NT;
   i /= a.NT;
-  const int ct = i % a.CT;
-  t.e = i / a.CT;
+  const int ct = i % a.CT, e = i / a.CT;
+  t.slab = part * a.E + e;
   t.n0 = nt * kTile;
   t.c0 = ct * kTile;
-  t.row0 = a.cnt ? s_blk[t.e] * a.block_m : 0;
-  t.rows = a.cnt ? max(0, min(s_cnt[t.e], a.rows - t.row0)) : a.rows;
+  t.row0 = a.cnt ? s_blk[e] * a.block_m : 0;
+  t.rows = a.cnt ? max(0, min(s_cnt[e], a.rows - t.row0)) : a.rows;
+  const int nks = (t.rows + kRowsPerStage - 1) / kRowsPerStage;
+  t.ks = a.parts > 1 ? static_cast<int>(static_cast<int64_t>(nks) * part / a.parts) : 0;
+  t.end = a.parts > 1 ? static_cast<int>(static_cast<int64_t>(nks) * (part + 1) / a.parts) : nks;
   return t;
 }
 
-// The stages a pair runs through: task by task, of each the part'th of `parts` ranges.
+// The stages a pair runs through, task by task.
 struct Cursor {
-  Task t;
-  int task, stride, ntasks, part, parts;
-  int ks, end;               // this stage, and the end of the range
-  __device__ __forceinline__ Cursor(int first, int stride, int ntasks, int part, int parts)
-      : task(first - stride), stride(stride), ntasks(ntasks), part(part), parts(parts), ks(0), end(0) {}
+  Task t;                    // t.ks: this stage
+  int task, stride, ntasks;
+  __device__ __forceinline__ Cursor(int first, int stride, int ntasks) : t{}, task(first - stride), stride(stride), ntasks(ntasks) {}
   // the next task with stages; false past the last
   __device__ __forceinline__ bool next_task(const Args& a, const int* s_blk, const int* s_cnt) {
     do {
       task += stride;
       if (task >= ntasks) return false;
       t = task_at(task, a, s_blk, s_cnt);
-      const int nks = (t.rows + kRowsPerStage - 1) / kRowsPerStage;
-      ks = static_cast<int>(static_cast<int64_t>(nks) * part / parts);
-      end = static_cast<int>(static_cast<int64_t>(nks) * (part + 1) / parts);
-    } while (ks >= end);
+    } while (t.ks >= t.end);
     return true;
   }
   __device__ __forceinline__ bool next(const Args& a, const int* s_blk, const int* s_cnt) {
-    return ++ks < end || next_task(a, s_blk, s_cnt);
+    return ++t.ks < t.end || next_task(a, s_blk, s_cnt);
   }
 };
 
@@ -256,9 +259,8 @@ struct Maps {
   CUtensorMap d_y, codes, out;
 };
 
-// kSplit: a cluster takes one task, each pair a range of its stages; the partial accumulators meet in shared memory.
 // kTma: out's rows are 16-byte aligned, and results leave by TMA.
-template <typename T, bool kSplit, bool kTma>
+template <typename T, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ Maps maps, const Args args) {
   extern __shared__ uint8_t smem_raw[];
@@ -279,8 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t crank = cluster_ctarank();
-  const uint32_t rank = crank & 1, leader = crank & ~1u;       // of the pair
+  const uint32_t rank = cluster_ctarank();
   const Status st{args.report, args.timeout_ns};
 
   if (threadIdx.x == 0) {
@@ -312,18 +313,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_barrier();                             // every CTA's barriers exist before anything targets them
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const int ntasks = args.E * args.NT * args.CT;
-  const int parts = kSplit ? static_cast<int>(cluster_nctarank() >> 1) : 1;
-  const int part = kSplit ? static_cast<int>(crank >> 1) : 0;
-  const int first = static_cast<int>(blockIdx.x >> 1) / parts, stride = static_cast<int>(gridDim.x >> 1) / parts;
+  const int ntasks = args.tasks * args.parts;
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   // accumulators of a task's n stages
-  auto segments = [](int n) { return sizeof(T) == 4 && !kSplit ? (n + kSegment - 1) / kSegment : 1; };
+  auto segments = [](int n) { return sizeof(T) == 4 ? (n + kSegment - 1) / kSegment : 1; };
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------------ d_y by TMA
     if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
-      Cursor at(first, stride, ntasks, part, parts);
+      Cursor at(first, stride, ntasks);
       Ring<kStages> ring;
       int steps = 0;                             // stages loaded
       while (at.next(args, s_blk, s_cnt)) {
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (*s_abort || !mbar_wait(&empty[s], ring.phase ^ 1, st, s_abort, kSiteEmpty)) break;
         mbar_arrive_expect_tx(&full_a[s], kHalfBytes);
         uint8_t* d = smem + Smem::a + s * kHalfBytes;
-        const int row = at.t.row0 + at.ks * kRowsPerStage, n = at.t.n0 + static_cast<int>(rank) * 128;
+        const int row = at.t.row0 + at.t.ks * kRowsPerStage, n = at.t.n0 + static_cast<int>(rank) * 128;
         tma_load_2d(d, &maps.d_y, &full_a[s], n, row, pol);
         tma_load_2d(d + kChunkBytes, &maps.d_y, &full_a[s], n + 64, row, pol);
         ring.step();
@@ -354,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 64-column chunks kChunkBytes apart, 8-row groups one atom apart
       const uint64_t da0 = make_smem_desc(smem_u32(smem + Smem::a), kChunkBytes, kAtom, 2);
       const uint64_t db0 = make_smem_desc(smem_u32(smem + Smem::b), kChunkBytes, kAtom, 2);
-      const uint16_t both = static_cast<uint16_t>(3u << leader);
-      Cursor at(first, stride, ntasks, part, parts);
+      const uint16_t both = 3;
+      Cursor at(first, stride, ntasks);
       Ring<kStages> ring;
       uint32_t acc = tmem;
       int it = 0, left = 0, in_acc = 0, rows = 0;     // accumulators so far; of this one: stages left, stages in it; rows left
@@ -368,10 +367,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto start = [&]() {                       // an accumulator
         const int buf = it & 1;
         acc = tmem + buf * kTile;
-        left = at.end - at.ks;
-        if (sizeof(T) == 4 && !kSplit) left = min(left, kSegment);
+        left = at.t.end - at.t.ks;
+        if (sizeof(T) == 4) left = min(left, kSegment);
         in_acc = 0;
-        rows = at.t.rows - at.ks * kRowsPerStage;
+        rows = at.t.rows - at.t.ks * kRowsPerStage;
         live = !__any_sync(0xffffffffu, *s_abort) && wait(&tempty[buf], ((it >> 1) & 1) ^ 1, kSiteTmemEmpty);
       };
       if (live) start();
@@ -390,17 +389,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring.step();
         in_acc = 1;
         rows -= kRowsPerStage;
-        ++at.ks;
+        ++at.t.ks;
         if (--left == 0) {
           if (issues) tc_commit_both(&tfull[it & 1], both);
           __syncwarp();
           ++it;
-          live = at.ks < at.end || at.next_task(args, s_blk, s_cnt);
+          live = at.t.ks < at.t.end || at.next_task(args, s_blk, s_cnt);
           if (live) start();
         }
       }
       if (issues) {
-        tc_commit_pair(map_shared(drain, leader));
+        tc_commit_pair(map_shared(drain, 0));
         mbar_drain(drain, 0, st, s_abort, kSiteDrainMma);
       }
     }
@@ -408,13 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kCodesWarp) {
     // ------------------------------------------------------------------ codes by TMA, scales by loads
     const uint64_t pol = policy_evict_normal();
-    Cursor at(first, stride, ntasks, part, parts);
+    Cursor at(first, stride, ntasks);
     Ring<kRaw> ring;
     int steps = 0;                               // stages loaded
     for (; at.next(args, s_blk, s_cnt); ring.step(), ++steps) {
       const int s = ring.s;
       if (!mbar_wait_warp(&raw_empty[s], ring.phase ^ 1, st, s_abort, kSiteRawEmpty)) break;
-      const int col = at.t.c0 + static_cast<int>(rank) * 128, row0 = at.t.row0 + at.ks * kRowsPerStage;
+      const int col = at.t.c0 + static_cast<int>(rank) * 128, row0 = at.t.row0 + at.t.ks * kRowsPerStage;
       if (lane == 0) {
         mbar_arrive_expect_tx(&raw_full[s], kRawBytes);
         tma_load_2d(smem + Smem::raw + s * kRawBytes, &maps.codes, &raw_full[s], col, row0, pol);
@@ -442,13 +441,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint8_t* const sf0 = smem + Smem::raw_sf + my_row * 4 + chunk * 2 + (q >> 1);
     uint8_t* const b0 = smem + Smem::b + chunk * kChunkBytes + my_row * 128;
     const int lo = ((2 * q) ^ r8) << 4, hi = ((2 * q + 1) ^ r8) << 4;
-    Cursor at(first, stride, ntasks, part, parts);
+    Cursor at(first, stride, ntasks);
     Ring<kRaw> raw;
     Ring<kStages> ring;
     int turn = group;
     bool live = at.next(args, s_blk, s_cnt);
     while (live) {
-      const int rows = at.t.rows - at.ks * kRowsPerStage;      // of the expert from this stage on
+      const int rows = at.t.rows - at.t.ks * kRowsPerStage;      // of the expert from this stage on
       live = at.next(args, s_blk, s_cnt);
       if (turn == 0) {
         if (!live && args.unreachable) break;
@@ -491,15 +490,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kHandWarp) {
     // ------------------------------------------------------------------ both operands to the leader
-    Cursor at(first, stride, ntasks, part, parts);
+    Cursor at(first, stride, ntasks);
     Ring<kStages> ring;
-    const uint32_t full0 = map_shared(full, leader);
+    const uint32_t full0 = map_shared(full, 0);
     for (; at.next(args, s_blk, s_cnt); ring.step()) {
       const int s = ring.s;
       if (!mbar_wait_warp(&full_a[s], ring.phase, st, s_abort, kSiteFullA) ||
           !mbar_wait_warp(&full_b[s], ring.phase, st, s_abort, kSiteFullB))
         break;
-      const int rows = at.t.rows - at.ks * kRowsPerStage;      // left from this stage on
+      const int rows = at.t.rows - at.t.ks * kRowsPerStage;      // left from this stage on
       if (rows < kRowsPerStage && (rows & 15)) {
         // the sum ends inside an MMA: whatever d_y's rows behind it hold becomes zero
         uint8_t* am = smem + Smem::a + s * kHalfBytes;
@@ -523,31 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = first; i < ntasks; i += stride) {
       const Task t = task_at(i, args, s_blk, s_cnt);
       const int n0 = t.n0 + static_cast<int>(rank) * 128 + quad * 32;
-      const int64_t row = static_cast<int64_t>(t.e) * args.N + n0;
+      const int64_t row = static_cast<int64_t>(t.slab) * args.N + n0;
       const int rows = args.N - n0;
-      const int nks = (t.rows + kRowsPerStage - 1) / kRowsPerStage;
-      if constexpr (kSplit) {                    // every MMA of the part has completed: the stages' memory is free
-        const bool any = static_cast<int64_t>(nks) * part / parts < static_cast<int64_t>(nks) * (part + 1) / parts;
-        if (any && !mbar_wait_warp(tfull, 0, st, s_abort, kSiteTmemFull)) break;
-        tc_fence_after();
-        float* d = reinterpret_cast<float*>(smem) + (quad * 32 + lane) * Smem::kPartPitch + half;
-#pragma unroll 1
-        for (int c = 0; c < kShare; c += 32) {
-          uint32_t v[32];
-          if (any) {
-            tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + half + c, v);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0;
-          }
-#pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<uint4*>(d + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-        }
-        continue;
-      }
-      if (nks == 0) {                            // an expert without rows
+      const int nks = t.end - t.ks;
+      if (nks == 0) {                            // an expert without rows, or without any for this part
         for (int r = 0; r < 32 && r < rows; ++r) {
           T* p = reinterpret_cast<T*>(args.out + (row + r) * args.out_pitch);
           for (int c = t.c0 + half + lane; c < min(args.C, t.c0 + half + kShare); c += 32) p[c] = from_float<T>(0.f);
@@ -563,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto release = [&] {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_leader(map_shared(&tempty[buf], leader));
+          if (lane == 0) arrive_leader(map_shared(&tempty[buf], 0));
         };
         const uint32_t src0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTile + half;
         if constexpr (kTma) {
@@ -599,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
-              if (sizeof(T) == 4 && seg > 0) tma_store_box<true>(&maps.out, box, col, n0, t.e);
-              else tma_store_box<false>(&maps.out, box, col, n0, t.e);
+              if (sizeof(T) == 4 && seg > 0) tma_store_box<true>(&maps.out, box, col, n0, t.slab);
+              else tma_store_box<false>(&maps.out, box, col, n0, t.slab);
             }
           }
         } else {
@@ -623,39 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kTma && lane == 0) tma_stored();
     __syncwarp();
   }
-  if constexpr (kSplit) {
-    // every CTA adds up its share of its rows' columns, the parts in order
-    __syncthreads();
-    cluster_barrier();
-    if (first < ntasks) {
-      const Task t = task_at(first, args, s_blk, s_cnt);
-      const int n0 = t.n0 + static_cast<int>(rank) * 128;
-      const int quads = kTile / 4 / parts;       // groups of four columns
-      const int rows = min(128, args.N - n0);
-      for (int i = threadIdx.x; i < rows * quads; i += kThreads) {
-        const int r = i / quads;
-        const int c = part * (kTile / parts) + (i - r * quads) * 4;
-        const float* src = reinterpret_cast<const float*>(smem) + r * Smem::kPartPitch + c;
-        float4 sum = peer_float4(src, rank);
-        for (int s = 1; s < parts; ++s) {
-          const float4 v = peer_float4(src, 2 * s + rank);
-          sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
-        }
-        Vec<T, 4> o;
-        o.v[0] = from_float<T>(sum.x); o.v[1] = from_float<T>(sum.y);
-        o.v[2] = from_float<T>(sum.z); o.v[3] = from_float<T>(sum.w);
-        T* dst = reinterpret_cast<T*>(args.out + (static_cast<int64_t>(t.e) * args.N + n0 + r) * args.out_pitch) + t.c0 + c;
-        if (kTma && t.c0 + c + 4 <= args.C) {
-          *reinterpret_cast<Vec<T, 4>*>(dst) = o;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (t.c0 + c + j < args.C) dst[j] = o.v[j];
-        }
-      }
-    }
-  }
-  // nothing targets a CTA that has left: the other's arrivals, and its reads of the partial sums
+  // nothing targets a CTA that has left
   __syncthreads();
   cluster_barrier();
   if (warp == kMmaWarp) {
@@ -705,50 +651,96 @@ cudaError_t align_rows(const void* x, int64_t pitch, int64_t rows, int bytes, vo
   return cudaGetLastError();
 }
 
-template <typename T, bool kSplit>
-cudaError_t launch(const WeightGradLaunch& p, const Args& a, Maps& maps, int parts, cudaStream_t s) {
-  const bool tma = (reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(a.out_pitch)) % 16 == 0;
-  if (tma && !kSplit) {
-    const uint64_t dims[3] = {static_cast<uint64_t>(p.C), static_cast<uint64_t>(p.N), static_cast<uint64_t>(a.E)};
-    const uint64_t strides[2] = {static_cast<uint64_t>(a.out_pitch), static_cast<uint64_t>(a.out_pitch) * p.N};
+// out [rows, C] = the sum over parts, in order, of sums [parts][rows][pitch]; a thread 4 columns.
+template <typename T>
+__global__ void __launch_bounds__(kCopyThreads)
+    add_parts_kernel(const float* __restrict__ sums, int parts, int64_t rows, int C, int pitch, T* __restrict__ out) {
+  pdl_wait();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
+  const int quads = pitch / 4;
+  const int64_t r = i / quads;
+  const int c = static_cast<int>(i - r * quads) * 4;
+  if (r >= rows) return;
+  const float4* p = reinterpret_cast<const float4*>(sums) + i;
+  float4 v = __ldg(p);
+  for (int k = 1; k < parts; ++k) {
+    const float4 w = __ldg(p + k * rows * quads);
+    v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+  }
+  const float f[4] = {v.x, v.y, v.z, v.w};
+  T* o = out + r * C + c;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (c + j < C) o[j] = from_float<T>(f[j]);
+}
+template <typename T>
+cudaError_t add_parts(const float* sums, int parts, int64_t rows, int C, int pitch, void* out, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows * (pitch / 4) + kCopyThreads - 1) / kCopyThreads));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, add_parts_kernel<T>, sums, parts, rows, C, pitch, static_cast<T*>(out));
+}
+
+// a.out and a.out_pitch: where the sums go, of T.
+template <typename T>
+cudaError_t launch(const Args& a, Maps& maps, cudaStream_t s) {
+  const bool tma = (reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(a.out_pitch)) % 16 == 0;
+  if (tma) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(a.C), static_cast<uint64_t>(a.N),
+                              static_cast<uint64_t>(a.E) * static_cast<uint64_t>(a.parts)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(a.out_pitch), static_cast<uint64_t>(a.out_pitch) * a.N};
     const uint32_t box[3] = {128 / sizeof(T), 32, 1};
-    if (encode_tmap(&maps.out, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.out,
+    if (encode_tmap(&maps.out, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.out,
                     dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  auto kernel = tma ? weight_grad_kernel<T, kSplit, true> : weight_grad_kernel<T, kSplit, false>;
+  auto kernel = tma ? weight_grad_kernel<T, true> : weight_grad_kernel<T, false>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   if (cudaError_t e = configure_kernel(fn, 0, Smem::total(kMaxE))) return e;
-  int64_t pairs = static_cast<int64_t>(a.E) * a.NT * a.CT * parts;
-  if (!kSplit) {
-    int most = 0;
-    if (cudaError_t e = max_pair_clusters(fn, kThreads, Smem::total(kMaxE), &most)) return e;
-    if (most < 1) return cudaErrorInvalidConfiguration;
-    if (pairs > most) pairs = most;
-  }
+  int most = 0;
+  if (cudaError_t e = max_pair_clusters(fn, kThreads, Smem::total(kMaxE), &most)) return e;
+  if (most < 1) return cudaErrorInvalidConfiguration;
+  const int pairs = a.tasks * a.parts;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (pairs < most ? pairs : most)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Smem::total(p.cnt ? a.E : 0);
+  cfg.dynamicSmemBytes = Smem::total(a.cnt ? a.E : 0);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * parts; attr[0].val.clusterDim.y = 1; attr[0].val.clusterDim.z = 1;
+  attr[0].val.clusterDim.x = 2; attr[0].val.clusterDim.y = 1; attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
 
-// The copies a call needs, in its scratch: of d_y, of the codes, of the scales. Bytes, 0: none.
+// Parts of a task's contraction of `terms` rows: as many as pairs of SMs have room for, of 8 stages at least.
+int parts_of(int64_t tasks, int64_t terms) {
+  const int64_t stages = (terms + kRowsPerStage - 1) / kRowsPerStage;
+  const int64_t n = kSplitPairs / tasks < stages / 8 ? kSplitPairs / tasks : stages / 8;
+  return static_cast<int>(n < 1 ? 1 : n > kMostParts ? kMostParts : n);
+}
+int sums_pitch(int C) { return (C + 3) / 4 * 4; }
+
+// What a call keeps in its scratch: copies of d_y, of the codes and of the scales, and parts' sums. Bytes, 0: none.
 struct Copies {
-  size_t d_y, codes, sf;
+  size_t d_y, codes, sf, sums;
 };
-Copies copies_of(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C, bool by_token) {
+Copies copies_of(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C, bool by_token, int E,
+                 int64_t terms) {
   const int blocks = blocks8(C, MM_MOE_VARIANT_MX);
-  Copies c{0, 0, 0};
+  Copies c{0, 0, 0, 0};
   if (reinterpret_cast<uintptr_t>(d_y) % 16 || d_stride % 8) c.d_y = static_cast<size_t>(rows) * ((N + 7) / 8) * 16;
   if (by_token) c.codes = static_cast<size_t>(rows) * blocks * kMxBlock;
-  if (by_token || reinterpret_cast<uintptr_t>(sf) % 4 || blocks % 4) c.sf = static_cast<size_t>(rows) * ((blocks + 3) / 4) * 4;
+  if (by_token || reinterpret_cast<uintptr_t>(sf) % 4 || blocks % 4) c.sf = (static_cast<size_t>(rows) * ((blocks + 3) / 4) * 4 + 15) / 16 * 16;
+  const int parts = parts_of(weight_grad_tasks(E, N, C), terms);
+  if (parts > 1) c.sums = static_cast<size_t>(parts) * E * N * sums_pitch(C) * sizeof(float);
   return c;
 }
 
@@ -759,9 +751,9 @@ int64_t weight_grad_tasks(int E, int N, int C) {
 }
 
 size_t weight_grad_scratch_bytes(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C,
-                                 bool by_token) {
-  const Copies c = copies_of(d_y, d_stride, rows, N, sf, C, by_token);
-  return c.d_y + c.codes + c.sf;
+                                 bool by_token, int E, int64_t terms) {
+  const Copies c = copies_of(d_y, d_stride, rows, N, sf, C, by_token, E, terms);
+  return c.d_y + c.codes + c.sf + c.sums;
 }
 
 cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
@@ -772,13 +764,15 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
   a.CT = (p.C + kTile - 1) / kTile;
   a.rows = static_cast<int>(p.rows);
   a.cnt = p.cnt; a.blk_off = p.blk_off;
+  a.tasks = static_cast<int>(weight_grad_tasks(p.E, p.N, p.C));
+  a.parts = parts_of(a.tasks, p.terms);
   a.out = static_cast<char*>(p.out);
   a.out_pitch = static_cast<int64_t>(p.C) * dtype_size(p.dtype);
   a.unreachable = p.unreachable;
   a.timeout_ns = p.timeout_ns;
   const int blocks = blocks8(p.C, MM_MOE_VARIANT_MX);
   const bool by_token = p.src != nullptr;
-  const Copies copies = copies_of(p.d_y, p.d_stride, p.rows, p.N, p.sf, p.C, by_token);
+  const Copies copies = copies_of(p.d_y, p.d_stride, p.rows, p.N, p.sf, p.C, by_token, p.E, p.terms);
   const void *d_y = p.d_y, *codes = p.codes, *sf = p.sf;
   uint64_t pitch = static_cast<uint64_t>(p.d_stride) * 2;
   char* to = static_cast<char*>(p.scratch);
@@ -810,14 +804,15 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
   if (encode_tmap_2d(&maps.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, bytes, static_cast<uint64_t>(p.rows), bytes, 128,
                      kRowsPerStage, CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  // parts of at least four stages, as many as leave no SM without work
-  const int64_t tasks = weight_grad_tasks(p.E, p.N, p.C);
-  const int64_t stages = ((p.cnt ? static_cast<int64_t>(p.pairs) / p.E : p.rows) + kRowsPerStage - 1) / kRowsPerStage;
-  int parts = 1;
-  while (parts < kMostParts && tasks * parts * 4 <= dev_info().sms && stages >= 8 * parts) parts *= 2;
-  if (p.dtype == MM_MOE_DTYPE_F32)
-    return parts > 1 ? launch<float, true>(p, a, maps, parts, s) : launch<float, false>(p, a, maps, 1, s);
-  return parts > 1 ? launch<__nv_bfloat16, true>(p, a, maps, parts, s) : launch<__nv_bfloat16, false>(p, a, maps, 1, s);
+  if (a.parts == 1) return p.dtype == MM_MOE_DTYPE_F32 ? launch<float>(a, maps, s) : launch<__nv_bfloat16>(a, maps, s);
+  const int pitch_c = sums_pitch(p.C);
+  float* sums = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + copies.d_y + copies.codes + copies.sf);
+  a.out = reinterpret_cast<char*>(sums);
+  a.out_pitch = static_cast<int64_t>(pitch_c) * sizeof(float);
+  if (cudaError_t e = launch<float>(a, maps, s)) return e;
+  const int64_t rows = static_cast<int64_t>(p.E) * p.N;
+  return p.dtype == MM_MOE_DTYPE_F32 ? add_parts<float>(sums, a.parts, rows, p.C, pitch_c, p.out, s)
+                                     : add_parts<__nv_bfloat16>(sums, a.parts, rows, p.C, pitch_c, p.out, s);
 }
 
 }  // namespace mm

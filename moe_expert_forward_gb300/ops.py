@@ -711,13 +711,22 @@ def swiglu_backward(d_a, kept, kept_sf, routing: Optional[Routing] = None, topk_
     return d_h, d_w
 
 
-def _grad_scratch(d_y: int, pitch: int, rows: int, N: int, sf: int, C: int, by_token: bool) -> int:
-    """mm_moe_weight_grad_scratch_size's rule: the tokens' rows at their pool rows; copies of rows that are not 16-byte, or
-    of scales that are not 4-byte, aligned."""
+GRAD_TILE, GRAD_STAGE, GRAD_PAIRS, GRAD_PARTS = 256, 64, 76, 16     # mm_moe_weight_grad_scratch_size's rule
+
+
+def _grad_scratch(d_y: int, pitch: int, rows: int, N: int, sf: int, C: int, T: int, K: int, E: int, by_token: bool) -> int:
+    """The tokens' rows at their pool rows; copies of rows that are not 16-byte, or of scales that are not 4-byte,
+    aligned; and partial sums (E = 0: dense)."""
     blocks = -(-C // 32)
-    copied = by_token or sf % 4 != 0 or blocks % 4 != 0
-    return rows * ((0 if d_y % 16 == 0 and pitch % 8 == 0 else -(-N // 8) * 16) + (32 * blocks if by_token else 0) +
-                   (-(-blocks // 4) * 4 if copied else 0))
+    n = 0 if d_y % 16 == 0 and pitch % 8 == 0 else rows * -(-N // 8) * 16
+    if by_token:
+        n += rows * 32 * blocks
+    if by_token or sf % 4 or blocks % 4:
+        n += -(-rows * -(-blocks // 4) * 4 // 16) * 16
+    tasks = max(E, 1) * -(-N // GRAD_TILE) * -(-C // GRAD_TILE)
+    stages = -(-(T * K // E if E else rows) // GRAD_STAGE)
+    parts = min(GRAD_PAIRS // tasks, stages // 8, GRAD_PARTS)
+    return n + (parts * max(E, 1) * N * -(-C // 4) * 16 if parts > 1 else 0)
 
 
 def weight_grad(d_y, codes, sf, C: int, routing: Optional[Routing] = None, by_token: bool = False,
@@ -745,7 +754,7 @@ def weight_grad(d_y, codes, sf, C: int, routing: Optional[Routing] = None, by_to
     if x_rows != need:
         _bad("weight_grad", f"x has {x_rows} rows, not {need}")
     out = _result(stream, (N, C) if routing is None else (E, N, C), dtype, d_y.device)
-    scratch_bytes = _grad_scratch(d_y.data_ptr(), _pitch(d_y), R, N, sp, C, by_token)
+    scratch_bytes = _grad_scratch(d_y.data_ptr(), _pitch(d_y), R, N, sp, C, T, K, E, by_token)
     scratch = _new(stream, scratch_bytes, torch.uint8, d_y.device).data_ptr() if scratch_bytes else None
     _check(lib().mm_moe_weight_grad(d_y.data_ptr(), _pitch(d_y), R, N, cp, sp, C, T, K, E, block_m,
                                     None if routing is None else routing._cnt, src, blk, by_token, _DTYPES[dtype],

@@ -92,11 +92,15 @@ def test_weight_grad(M):
                    dict(blk=None), dict(cnt=A + 2), dict(rows=n - 1), dict(dtype=2), dict(dtype=-1), dict(out=None),
                    dict(out=A + 1), dict(dtype=0, out=A + 2), dict(dense, tok=1), dict(N=1 << 29, ds=1 << 29),
                    dict(dense, N=1 << 20, ds=1 << 20, C=1 << 30), dict(ds=65), dict(dy=A + 2), dict(ds=65, scr=A + 8, n_scr=1 << 20)])
-    need = M.mm_moe_weight_grad_scratch_size(A, 65, n, 64, A, 64, 0)
-    assert need == (16 * 8 + 4) * n and M.mm_moe_weight_grad_scratch_size(A, 64, n, 64, A, 128, 0) == 0
+    need = M.mm_moe_weight_grad_scratch_size(A, 65, n, 64, A, 64, 4, 2, 4, 0)
+    assert need == 16 * 8 * n + 4 * n and M.mm_moe_weight_grad_scratch_size(A, 64, n, 64, A, 128, 4, 2, 4, 0) == 0
     assert g(ds=65, scr=A, n_scr=need - 1) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL
     assert g(tok=1, scr=A, n_scr=(64 + 4) * n - 1) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL
-    for bad in ((A, 63, n, 64, A, 64, 0), (A, 64, -1, 64, A, 64, 0), (A, 64, n, 0, A, 64, 0), (A, 64, n, 64, A, 0, 0)):
+    # the router's gradient: 16 tiles, four parts of each
+    assert M.mm_moe_weight_grad_scratch_size(A, 256, 8192, 256, A, 4096, 0, 0, 0, 0) == 4 * 256 * 4096 * 4
+    for bad in ((A, 63, n, 64, A, 64, 4, 2, 4, 0), (A, 64, -1, 64, A, 64, 4, 2, 4, 0), (A, 64, n, 0, A, 64, 4, 2, 4, 0),
+                (A, 64, n, 64, A, 0, 4, 2, 4, 0), (A, 64, n, 64, A, 64, -1, 2, 4, 0), (A, 64, n, 64, A, 64, 4, 17, 4, 0),
+                (A, 64, n, 64, A, 64, 4, 0, 4, 0), (A, 64, n, 64, A, 64, 0, 0, 0, 1)):
         with pytest.raises(M.MMError):
             M.mm_moe_weight_grad_scratch_size(*bad)
 
@@ -109,9 +113,10 @@ def test_binding_sizes_agree_with_the_library(M):
     for at in (A, A + 2, A + 8, A + 16):
         for pitch, N in ((64, 64), (64, 63), (65, 64), (72, 65), (1, 1), (8, 1)):
             for sf, C in ((A, 128), (A, 129), (A, 96), (A + 1, 256), (A + 4, 1024)):
-                for by_token in (False, True):
-                    args = (at, pitch, 77, N, sf, C, by_token)
-                    assert M.mm_moe_weight_grad_scratch_size(*args) == ops._grad_scratch(*args), args
+                for rows in (77, 5000, 100000):
+                    for T, K, E, by_token in ((0, 0, 0, False), (2000, 2, 3, False), (2000, 2, 3, True), (50000, 6, 9, True)):
+                        args = (at, pitch, rows, N, sf, C, T, K, E, by_token)
+                        assert M.mm_moe_weight_grad_scratch_size(*args) == ops._grad_scratch(*args), args
 
 
 # ------------------------------------------------------------------ tensor forms, with a stand-in for the library
