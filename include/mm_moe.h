@@ -573,7 +573,9 @@ int mm_moe_rows_dequantize(const void* codes, const void* sf, int64_t R, int C, 
  *   y            [T, H] contiguous of `dtype`, or null
  *   codes, sf    y in 8 bits of `variant` (from the fp32 y), or both null
  *   rstd         what the gradients take
- * eps >= 0; H of any size (up to 32768 elements a row is read once). */
+ * eps >= 0; H of any size (up to 16384 elements a row is read once).  A device wait of 2 s
+ * that runs out (many long rows come by copies that are waited for) leaves the results
+ * undefined and is reported by mm_moe_ops_status; the gradients' too. */
 int mm_moe_rms_norm(const void* x, int dtype, int64_t x_stride, const void* residual, int64_t residual_stride,
                     const void* weight, int weight_dtype, int64_t T, int H, float eps, void* h, void* y, int variant,
                     void* codes, void* sf, float* rstd, void* stream);
@@ -638,7 +640,7 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
                        size_t scratch_bytes, unsigned timeout_ms, int debug_flags, void* stream);
 
 /* Waits for `stream` and returns MM_MOE_ERR_TIMEOUT if a device wait of mm_moe_mx_product,
- * mm_moe_mx_linear or mm_moe_weight_grad has run out on the current device, on any stream, since the last
+ * mm_moe_mx_linear, mm_moe_weight_grad, mm_moe_rms_norm or its gradients has run out on the current device, on any stream, since the last
  * time this returned it; else MM_MOE_OK (calls on other streams that are still running
  * are not waited for).  `where` (may be null) gets the site of the first
  * such wait.  The record is the library's: it outlives the calls' status words and

@@ -223,7 +223,7 @@ cudaError_t launch_dequantize8(const void* codes, const void* sf, int64_t R, int
                                int64_t stride, cudaStream_t s);
 
 // The norm (norm.cu).
-constexpr int kNormBackSms = 152;          // its gradient's CTAs do not depend on the device: neither does the scratch
+constexpr int kNormSms = 152;              // its gradient's CTAs do not depend on the device: neither does the scratch
 struct NormLaunch {
   const void* x;
   int dtype;

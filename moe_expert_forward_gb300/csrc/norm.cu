@@ -7,10 +7,16 @@
 //
 // Memory bounds both (read x and the residual, write h, y and the codes; back: read
 // d_y, h and d_h, write d_x).  A row stays in the registers of its threads, 16
-// elements a lane and access, between the sum and its use, up to kHeld elements;
-// longer rows are read twice.  For d_weight a thread keeps the same columns of every
-// row that its CTA takes, so the sums over tokens stay in registers too; the CTAs'
-// parts are added up, in order, by a second kernel.
+// elements a lane and access, between the sum and its use.
+//   ring   many long rows: persistent CTAs take rows in a fixed stride, and bulk copies
+//          bring the next ones into a ring in shared memory meanwhile, so that loads are in
+//          flight through the sum and the stores. Weights stay in registers.
+//   rows   few rows, short ones, or rows on no 32-byte boundary: loaded by their threads.
+//          Rows longer than the threads hold are read twice.
+// For d_weight a thread keeps the same columns of every row that its CTA takes, so the
+// sums over tokens stay in registers too; the CTAs' parts are added up, in order, by a
+// second kernel.
+#include "mx_linear.cuh"
 #include "rows8.cuh"
 
 namespace mm {
@@ -18,6 +24,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostThreads = 512;
+constexpr int kRingBytes = 192 * 1024;           // of the rings of an SM's CTAs
+constexpr int kMostStages = 6;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+enum : int { kSiteForward = 201, kSiteBackward = 202 };
 
 struct NormArgs {
   const void* x;
@@ -172,10 +182,21 @@ struct NormBackArgs {
   int64_t T;
   int H;
   void* d_x;
-  float* parts;              // [CTAs x rows of a CTA][pitch]
+  float* parts;              // [CTAs][pitch]
   int pitch;
   int row_threads;
 };
+
+// d: d_h on entry, d_x on return; sum: d_weight's part of these columns.
+__device__ __forceinline__ void back16(const float (&y)[16], const float (&h)[16], const float (&w)[16], float r, float mean,
+                                       float (&d)[16], float (&sum)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float n = h[i] * r;
+    sum[i] = fmaf(y[i], n, sum[i]);
+    d[i] = fmaf(r, fmaf(y[i], w[i], -n * mean), d[i]);
+  }
+}
 
 // One CTA takes rows in a fixed stride; each group of row_threads threads sums d_weight's part of its own rows.
 template <typename T, bool kVec, int G>
@@ -186,8 +207,7 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_backward_kernel(const N
   const int P = a.row_threads, rows = blockDim.x / P;
   const int l = threadIdx.x % P;
   const int groups = ((a.H + 15) / 16 + 31) / 32 * 32;
-  const int64_t mine = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / P;
-  float* part = a.parts + mine * a.pitch;
+  float* part = a.parts + static_cast<int64_t>(blockIdx.x) * a.pitch;
   float acc[G > 0 ? G : 1][16];
   if constexpr (G > 0) {
 #pragma unroll
@@ -228,12 +248,7 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_backward_kernel(const N
       vh.floats(n);
       vd.floats(d);
       load_weight<T, kVec>(a.weight, a.w_f32, g * 16, a.H, w);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float ni = n[i] * r;
-        sum[i] = fmaf(y[i], ni, sum[i]);
-        d[i] += r * (y[i] * w[i] - ni * mean);
-      }
+      back16(y, n, w, r, mean, d, sum);
       uint32_t o[Group<T>::kWords];
       round16<T>(d, o);
       store_groups<T, kVec>(dx + g * 16, live ? min(16, a.H - g * 16) : 0, o, run);
@@ -281,6 +296,17 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_backward_kernel(const N
     }
   }
   if constexpr (G > 0) {
+    if (rows > 1) {                              // G is 1: the CTA's groups of threads in order
+      float* all = reinterpret_cast<float*>(s_dyn);
+      __syncthreads();                           // the rows on their way out have left shared memory
+#pragma unroll
+      for (int c = 0; c < 16; ++c) all[c * blockDim.x + threadIdx.x] = acc[0][c];
+      __syncthreads();
+      if (threadIdx.x >= P) return;
+      for (int k = 1; k < rows; ++k)
+#pragma unroll
+        for (int c = 0; c < 16; ++c) acc[0][c] += all[c * blockDim.x + k * P + threadIdx.x];
+    }
 #pragma unroll
     for (int i = 0; i < G; ++i) {
       const int c = (i * P + l) * 16;
@@ -292,55 +318,312 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_backward_kernel(const N
   }
 }
 
-// d_weight: the parts of each column in order. A CTA takes 32 columns, its warps every eighth part.
-__global__ void __launch_bounds__(kThreads)
+// Rows of whole 32-byte pieces that bulk copies bring into a ring in shared memory: `arrays` of them a stage.
+struct RowRing {
+  uint8_t* base;
+  uint64_t* full;
+  int* abort;
+  int stages, arrays;
+  uint32_t row_bytes;
+  int s;                     // of the row at hand
+  uint32_t phase;
+  int loads;                 // by the loading thread
+
+  __device__ __forceinline__ RowRing(uint8_t* smem, int stages, int arrays, uint32_t row_bytes)
+      : base(smem), stages(stages), arrays(arrays), row_bytes(row_bytes), s(0), phase(0), loads(0) {
+    full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(stages) * arrays * row_bytes);
+    abort = reinterpret_cast<int*>(full + stages);
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+      *abort = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
+  static int bytes(int stages, int arrays, uint32_t row_bytes) { return stages * (arrays * static_cast<int>(row_bytes) + 8) + 16; }
+  __device__ __forceinline__ const uint8_t* row(int stage, int array) const {
+    return base + (static_cast<size_t>(stage) * arrays + array) * row_bytes;
+  }
+  // One thread: the arrays' rows at p[] into the stage after the last one's, which nobody reads any more.
+  template <int N>
+  __device__ __forceinline__ void load(const void* const (&p)[N]) {
+    const int stage = loads++ % stages;
+    mbar_arrive_expect_tx(&full[stage], arrays * row_bytes);
+    int k = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (p[i]) bulk_load(const_cast<uint8_t*>(row(stage, k++)), p[i], row_bytes, &full[stage]);
+  }
+  // Every thread: the rows of stage s are there. `abort` gives the CTA one answer behind its next barrier.
+  __device__ __forceinline__ bool wait(const Status& st, int where) {
+    return mbar_wait(&full[s], phase, st, abort, where);
+  }
+  __device__ __forceinline__ void step() {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+  // The loading thread, after a wait that ran out: what it has in flight.
+  __device__ __forceinline__ void drain(const Status& st, int where) const {
+    for (int i = 0; i < stages && i < loads; ++i) mbar_wait_drain(&full[i], ((loads - 1 - i) / stages) & 1, st, where);
+  }
+};
+// 16 elements of a row in shared memory, zeros past H.
+template <typename T>
+__device__ __forceinline__ void take16(Group<T>& v, const uint8_t* row, int g, int H) {
+  if (g * 16 >= H) {
+    v.clear();
+    return;
+  }
+  const uint4* p = reinterpret_cast<const uint4*>(row) + g * (Group<T>::kWords / 4);
+#pragma unroll
+  for (int q = 0; q < Group<T>::kWords / 4; ++q) {
+    const uint4 w = p[q];
+    v.w[4 * q] = w.x; v.w[4 * q + 1] = w.y; v.w[4 * q + 2] = w.z; v.w[4 * q + 3] = w.w;
+  }
+}
+// The sum of v over the CTA, in each of its threads; s_part alternates between two arrays, so that one barrier does.
+__device__ __forceinline__ float cta_sum(float v, float* s_part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) v += s_part[i];
+  return v;
+}
+
+template <typename T, typename W, int G>
+__global__ void __launch_bounds__(kMostThreads)
+    rms_norm_ring_kernel(const NormArgs a, int stages, int* report) {
+  extern __shared__ __align__(128) unsigned char s_dyn[];
+  __shared__ float s_part[2][kMostThreads / 32];
+  const uint32_t row_bytes = a.H * static_cast<uint32_t>(sizeof(T));
+  RowRing ring(s_dyn, stages, a.residual ? 2 : 1, row_bytes);
+  const Status st{report, kTimeoutNs};
+  const int l = threadIdx.x;
+  auto load = [&](int64_t row) {
+    const void* const p[2] = {static_cast<const T*>(a.x) + row * a.x_stride,
+                              a.residual ? static_cast<const T*>(a.residual) + row * a.r_stride : nullptr};
+    ring.load(p);
+  };
+  int64_t next = blockIdx.x;                     // the row to load
+  if (l == 0)
+    for (int i = 0; i < stages && next < a.T; ++i, next += gridDim.x) load(next);
+  Group<W> w[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) w[i].template load<true>(static_cast<const W*>(a.weight), (i * static_cast<int>(blockDim.x) + l) * 16, a.H);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, ring.step(), turn ^= 1) {
+    const bool ok = ring.wait(st, kSiteForward);
+    Group<T> h[G];
+    float s = 0.f;
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int g = i * static_cast<int>(blockDim.x) + l;
+        take16(h[i], ring.row(ring.s, 0), g, a.H);
+        float f[16];
+        h[i].floats(f);
+        if (a.residual) {
+          Group<T> r;
+          take16(r, ring.row(ring.s, 1), g, a.H);
+          float q[16];
+          r.floats(q);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) f[c] += q[c];
+          round16<T>(f, h[i].w);
+          store_groups<T, true>(static_cast<T*>(a.h) + row * a.H + g * 16, g * 16 < a.H ? 16 : 0, h[i].w, nullptr);
+          h[i].floats(f);
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) s = fmaf(f[c], f[c], s);
+      }
+    }
+    s = cta_sum(s, s_part[turn]);                // and everyone has read the stage
+    if (*reinterpret_cast<volatile int*>(ring.abort)) break;
+    if (l == 0 && next < a.T) {
+      load(next);
+      next += gridDim.x;
+    }
+    const float r = 1.0f / sqrtf(s / static_cast<float>(a.H) + a.eps);
+    if (l == 0) a.rstd[row] = r;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int g = i * static_cast<int>(blockDim.x) + l;
+      float f[16], q[16];
+      h[i].floats(f);
+      w[i].floats(q);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) f[c] = f[c] * r * q[c];
+      if (a.y) {
+        uint32_t o[Group<T>::kWords];
+        round16<T>(f, o);
+        store_groups<T, true>(static_cast<T*>(a.y) + row * a.H + g * 16, g * 16 < a.H ? 16 : 0, o, nullptr);
+      }
+      if (a.out.codes && i * kThreads + (l & ~31) < a.out.groups) {
+        if (g * 16 >= a.H)                       // past the row: zeros, also where r is not finite
+#pragma unroll
+          for (int c = 0; c < 16; ++c) f[c] = 0.f;
+        store8(a.out, row, g, g < a.out.groups, f, amax_bits16(f));
+      }
+    }
+  }
+  if (*reinterpret_cast<volatile int*>(ring.abort) && l == 0) ring.drain(st, kSiteForward);
+}
+
+template <typename T, typename W, int G>
+__global__ void __launch_bounds__(kMostThreads)
+    rms_norm_backward_ring_kernel(const NormBackArgs a, int stages, int* report) {
+  extern __shared__ __align__(128) unsigned char s_dyn[];
+  __shared__ float s_part[2][kMostThreads / 32];
+  const uint32_t row_bytes = a.H * static_cast<uint32_t>(sizeof(T));
+  RowRing ring(s_dyn, stages, a.d_h ? 3 : 2, row_bytes);
+  const Status st{report, kTimeoutNs};
+  const int l = threadIdx.x;
+  auto load = [&](int64_t row) {
+    const void* const p[3] = {static_cast<const T*>(a.d_y) + row * a.dy_stride, static_cast<const T*>(a.h) + row * a.h_stride,
+                              a.d_h ? static_cast<const T*>(a.d_h) + row * a.dh_stride : nullptr};
+    ring.load(p);
+  };
+  int64_t next = blockIdx.x;
+  if (l == 0)
+    for (int i = 0; i < stages && next < a.T; ++i, next += gridDim.x) load(next);
+  Group<W> w[G];
+  float acc[G][16];
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    w[i].template load<true>(static_cast<const W*>(a.weight), (i * static_cast<int>(blockDim.x) + l) * 16, a.H);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) acc[i][c] = 0.f;
+  }
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, ring.step(), turn ^= 1) {
+    const bool ok = ring.wait(st, kSiteBackward);
+    const float r = __ldg(a.rstd + row);
+    float s = 0.f;
+    if (ok)
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int g = i * static_cast<int>(blockDim.x) + l;
+        Group<T> v;
+        float y[16], n[16], q[16];
+        take16(v, ring.row(ring.s, 0), g, a.H);
+        v.floats(y);
+        take16(v, ring.row(ring.s, 1), g, a.H);
+        v.floats(n);
+        w[i].floats(q);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) s = fmaf(y[c] * q[c], n[c] * r, s);
+      }
+    s = cta_sum(s, s_part[turn]);                // and everyone is done with the row before
+    if (*reinterpret_cast<volatile int*>(ring.abort)) break;
+    if (l == 0 && row != blockIdx.x && next < a.T) {
+      load(next);
+      next += gridDim.x;
+    }
+    const float mean = s / static_cast<float>(a.H);
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int g = i * static_cast<int>(blockDim.x) + l;
+      Group<T> v;
+      float y[16], n[16], d[16], q[16];
+      take16(v, ring.row(ring.s, 0), g, a.H);
+      v.floats(y);
+      take16(v, ring.row(ring.s, 1), g, a.H);
+      v.floats(n);
+      if (a.d_h) take16(v, ring.row(ring.s, 2), g, a.H);
+      else v.clear();
+      v.floats(d);
+      w[i].floats(q);
+      back16(y, n, q, r, mean, d, acc[i]);
+      round16<T>(d, v.w);
+      store_groups<T, true>(static_cast<T*>(a.d_x) + row * a.H + g * 16, g * 16 < a.H ? 16 : 0, v.w, nullptr);
+    }
+  }
+  float* part = a.parts + static_cast<int64_t>(blockIdx.x) * a.pitch;
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const int c = (i * static_cast<int>(blockDim.x) + l) * 16;
+    if (c < a.H)
+#pragma unroll
+      for (int q = 0; q < 16; q += 4)
+        *reinterpret_cast<float4*>(part + c + q) = make_float4(acc[i][q], acc[i][q + 1], acc[i][q + 2], acc[i][q + 3]);
+  }
+  if (*reinterpret_cast<volatile int*>(ring.abort) && l == 0) ring.drain(st, kSiteBackward);
+}
+
+// d_weight: the parts of each column in order. A CTA takes 32 columns, each of its 32 warps every 32nd part.
+__global__ void __launch_bounds__(1024)
     norm_weight_kernel(const float* __restrict__ parts, int pitch, int count, int H, float* __restrict__ d_weight) {
-  __shared__ float s[kThreads / 32][32];
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
+  pdl_wait();
   if (c < H) {
 #pragma unroll 8
-    for (int p = warp; p < count; p += kThreads / 32) v += parts[static_cast<int64_t>(p) * pitch + c];
+    for (int p = warp; p < count; p += 32) v += parts[static_cast<int64_t>(p) * pitch + c];
   }
   s[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && c < H) {
+  v = s[lane][warp];                             // column `warp` of the CTA's
 #pragma unroll
-    for (int i = 1; i < kThreads / 32; ++i) v += s[i][lane];
-    d_weight[c] = v;
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < H) d_weight[blockIdx.x * 32 + warp] = v;
 }
 
 // Threads of a row, its groups a thread (0: more than are held) and rows of a CTA.
 struct Shape {
   int P, G, rows;
 };
-Shape shape_for(int groups, int held) {
+Shape shape_for(int groups) {
   Shape s;
-  s.P = row_threads(groups, held > 1 ? 2 : 1, kThreads);
-  if (s.P * held < groups) s.P = row_threads(groups, held, kMostThreads);
-  s.G = 0;
-  for (int g = 1; g <= held && !s.G; g *= 2)
-    if (s.P * g >= groups) s.G = g;
+  const int warps = (groups + 31) / 32;
+  s.G = warps <= 16 ? 1 : warps <= 32 ? 2 : 0;
+  s.P = s.G == 0 ? kMostThreads : (warps + s.G - 1) / s.G * 32;
   s.rows = s.P < kThreads ? kThreads / s.P : 1;
   return s;
 }
 
-constexpr int kHeldForward = 4, kHeldBack = 2;   // groups a thread
-
-Shape back_shape(int H) { return shape_for((H + 15) / 16, kHeldBack); }
-int64_t back_ctas(int64_t T, const Shape& s) {
-  const int64_t all = (T + s.rows - 1) / s.rows, most = 2 * int64_t(kNormBackSms);
-  return all < most ? all : most;
+// A ring's CTAs: threads, groups of each, stages, CTAs.
+struct RingShape {
+  int threads, G, stages, ctas;
+};
+// stages 0: not by a ring. Its threads hold 16384 elements of a row; a row has 2 KB at least, and there are more rows
+// than CTAs that would take them.
+RingShape ring_for(int64_t T, int H, int elem, int arrays, bool vec) {
+  RingShape r{0, 0, 0, 0};
+  const int64_t stage = static_cast<int64_t>(arrays) * H * elem;
+  if (!vec || H * static_cast<int64_t>(elem) < 2048 || H > 32 * kMostThreads || T <= 2 * kNormSms) return r;
+  const int groups = (H + 15) / 16;
+  r.threads = groups <= 2 * kThreads ? kThreads : kMostThreads;
+  r.G = groups <= r.threads ? 1 : 2;
+  const int per_sm = kMostThreads / r.threads;
+  r.ctas = per_sm * kNormSms;
+  const int n = static_cast<int>(kRingBytes / per_sm / stage);
+  r.stages = n < 2 ? 0 : n < kMostStages ? n : kMostStages;
+  return r;
 }
+
+// Most CTAs, and parts of d_weight, of the gradients.
+int64_t back_ctas(int64_t T) { return T < 2 * int64_t(kNormSms) ? T : 2 * int64_t(kNormSms); }
 int back_pitch(int H) { return (H + 15) / 16 * 16; }
+
+// f(W{}, G) of a ring's kernel: weights' type, and groups a thread
+template <typename T, typename F>
+cudaError_t with_ring(bool w_f32, int G, F f) {
+  auto go = [&](auto w) {
+    return G == 1 ? f(w, std::integral_constant<int, 1>{}) : f(w, std::integral_constant<int, 2>{});
+  };
+  return w_f32 ? go(float{}) : go(T{});
+}
 
 }  // namespace
 
 size_t norm_scratch_bytes(int64_t T, int H) {
-  const Shape s = back_shape(H);
-  return static_cast<size_t>(back_ctas(T, s)) * s.rows * back_pitch(H) * sizeof(float);
+  return static_cast<size_t>(back_ctas(T)) * back_pitch(H) * sizeof(float);
 }
 
 cudaError_t launch_rms_norm(const NormLaunch& n, cudaStream_t s) {
@@ -349,11 +632,27 @@ cudaError_t launch_rms_norm(const NormLaunch& n, cudaStream_t s) {
              n.eps, n.h, n.y, {}, n.rstd, 0};
   if (n.codes)
     a.out = Out8{n.variant, static_cast<uint8_t*>(n.codes), n.sf, groups8(n.H, n.variant), blocks8(n.H, n.variant)};
-  const Shape sh = shape_for(n.codes ? a.out.groups : (n.H + 15) / 16, kHeldForward);
-  a.row_threads = sh.P;
   const int64_t pitch = static_cast<int64_t>(n.H) * elem;
   const bool vec = whole_groups(n.x, n.x_stride * elem, n.H) && whole_groups(n.residual, n.residual_stride * elem, n.H) &&
                    whole_groups(n.h, pitch, n.H) && whole_groups(n.y, pitch, n.H) && whole_groups(n.weight, 0, n.H);
+  const int arrays = n.residual ? 2 : 1;
+  const RingShape ring = ring_for(n.T, n.H, elem, arrays, vec);
+  if (ring.stages) {
+    int* report = nullptr;
+    if (cudaError_t e = mx_report(&report)) return e;
+    const int smem = RowRing::bytes(ring.stages, arrays, static_cast<uint32_t>(pitch));
+    return with_dtype(n.dtype, [&](auto tag) {
+      using T = decltype(tag);
+      return with_ring<T>(a.w_f32, ring.G, [&](auto w, auto g) {
+        auto kernel = rms_norm_ring_kernel<T, decltype(w), decltype(g)::value>;
+        if (cudaError_t e = configure_kernel(reinterpret_cast<const void*>(kernel), 0, kRingBytes + 1024)) return e;
+        kernel<<<ring.ctas, ring.threads, smem, s>>>(a, ring.stages, report);
+        return cudaGetLastError();
+      });
+    });
+  }
+  const Shape sh = shape_for(n.codes ? a.out.groups : (n.H + 15) / 16);
+  a.row_threads = sh.P;
   const unsigned grid = static_cast<unsigned>((n.T + sh.rows - 1) / sh.rows);
   const int threads = sh.P * sh.rows;
   return with_dtype(n.dtype, [&](auto tag) {
@@ -363,7 +662,6 @@ cudaError_t launch_rms_norm(const NormLaunch& n, cudaStream_t s) {
       constexpr bool V = decltype(v)::value;
       if (sh.G == 1) rms_norm_kernel<T, V, 1><<<grid, threads, smem, s>>>(a);
       else if (sh.G == 2) rms_norm_kernel<T, V, 2><<<grid, threads, smem, s>>>(a);
-      else if (sh.G == 4) rms_norm_kernel<T, V, 4><<<grid, threads, smem, s>>>(a);
       else rms_norm_kernel<T, V, 0><<<grid, threads, smem, s>>>(a);
       return cudaGetLastError();
     };
@@ -374,31 +672,60 @@ cudaError_t launch_rms_norm(const NormLaunch& n, cudaStream_t s) {
 cudaError_t launch_rms_norm_backward(const NormBackLaunch& n, cudaStream_t s) {
   if (n.T == 0) return cudaMemsetAsync(n.d_weight, 0, sizeof(float) * static_cast<size_t>(n.H), s);
   const int elem = dtype_size(n.dtype);
-  const Shape sh = back_shape(n.H);
+  const Shape sh = shape_for((n.H + 15) / 16);
   const int64_t pitch = static_cast<int64_t>(n.H) * elem;
   const NormBackArgs a{n.d_y, n.d_y_stride, n.h, n.h_stride, n.weight, n.weight_dtype == MM_MOE_DTYPE_F32, n.rstd, n.d_h,
                        n.d_h_stride, n.T, n.H, n.d_x, static_cast<float*>(n.scratch), back_pitch(n.H), sh.P};
   const bool vec = whole_groups(n.d_y, n.d_y_stride * elem, n.H) && whole_groups(n.h, n.h_stride * elem, n.H) &&
                    whole_groups(n.d_h, n.d_h_stride * elem, n.H) && whole_groups(n.d_x, pitch, n.H) &&
                    whole_groups(n.weight, 0, n.H);
-  const unsigned grid = static_cast<unsigned>(back_ctas(n.T, sh));
-  const int threads = sh.P * sh.rows;
-  const cudaError_t e = with_dtype(n.dtype, [&](auto tag) {
-    using T = decltype(tag);
-    const size_t smem = vec ? 0 : threads / 32 * 512 * sizeof(T);
-    auto go = [&](auto v) {
-      constexpr bool V = decltype(v)::value;
-      if (sh.G == 1) rms_norm_backward_kernel<T, V, 1><<<grid, threads, smem, s>>>(a);
-      else if (sh.G == 2) rms_norm_backward_kernel<T, V, 2><<<grid, threads, smem, s>>>(a);
-      else rms_norm_backward_kernel<T, V, 0><<<grid, threads, smem, s>>>(a);
-      return cudaGetLastError();
-    };
-    return vec ? go(std::true_type{}) : go(std::false_type{});
-  });
+  const int arrays = n.d_h ? 3 : 2;
+  const RingShape ring = ring_for(n.T, n.H, elem, arrays, vec);
+  int count = ring.ctas;
+  cudaError_t e;
+  if (ring.stages) {
+    int* report = nullptr;
+    e = mx_report(&report);
+    if (e != cudaSuccess) return e;
+    const int smem = RowRing::bytes(ring.stages, arrays, static_cast<uint32_t>(pitch));
+    e = with_dtype(n.dtype, [&](auto tag) {
+      using T = decltype(tag);
+      return with_ring<T>(a.w_f32, ring.G, [&](auto w, auto g) {
+        auto kernel = rms_norm_backward_ring_kernel<T, decltype(w), decltype(g)::value>;
+        if (cudaError_t c = configure_kernel(reinterpret_cast<const void*>(kernel), 0, kRingBytes + 1024)) return c;
+        kernel<<<ring.ctas, ring.threads, smem, s>>>(a, ring.stages, report);
+        return cudaGetLastError();
+      });
+    });
+  } else {
+    const int64_t all = (n.T + sh.rows - 1) / sh.rows;
+    count = static_cast<int>(all < back_ctas(n.T) ? all : back_ctas(n.T));
+    const int threads = sh.P * sh.rows;
+    e = with_dtype(n.dtype, [&](auto tag) {
+      using T = decltype(tag);
+      size_t smem = vec ? 0 : threads / 32 * 512 * sizeof(T);
+      if (sh.rows > 1 && smem < static_cast<size_t>(threads) * 64) smem = static_cast<size_t>(threads) * 64;
+      auto go = [&](auto v) {
+        constexpr bool V = decltype(v)::value;
+        if (sh.G == 1) rms_norm_backward_kernel<T, V, 1><<<count, threads, smem, s>>>(a);
+        else if (sh.G == 2) rms_norm_backward_kernel<T, V, 2><<<count, threads, smem, s>>>(a);
+        else rms_norm_backward_kernel<T, V, 0><<<count, threads, smem, s>>>(a);
+        return cudaGetLastError();
+      };
+      return vec ? go(std::true_type{}) : go(std::false_type{});
+    });
+  }
   if (e != cudaSuccess) return e;
-  norm_weight_kernel<<<static_cast<unsigned>((n.H + 31) / 32), kThreads, 0, s>>>(
-      a.parts, a.pitch, static_cast<int>(grid) * sh.rows, n.H, n.d_weight);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((n.H + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_weight_kernel, static_cast<const float*>(a.parts), a.pitch, count, n.H, n.d_weight);
 }
 
 }  // namespace mm

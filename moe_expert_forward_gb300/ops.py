@@ -607,11 +607,7 @@ NORM_CTAS = 2 * 152      # of the gradient, at most: mm_moe_rms_norm_scratch_siz
 
 
 def _norm_scratch(T: int, H: int) -> int:
-    groups, threads = -(-H // 16), 32
-    while threads < 256 and 2 * threads < groups:
-        threads *= 2
-    per_cta = 256 // threads
-    return 4 * min(-(-T // per_cta), NORM_CTAS) * per_cta * 16 * groups
+    return 4 * min(T, NORM_CTAS) * -(-H // 16) * 16
 
 
 def rms_norm_backward(d_y, h, weight, rstd, d_h=None, stream=None):

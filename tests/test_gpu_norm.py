@@ -14,6 +14,7 @@ def ops():
     from moe_expert_forward_gb300 import build
     build.build()
     from moe_expert_forward_gb300 import ops
+    ops.sync_status()              # what other tests let run out
     return ops
 
 
@@ -95,6 +96,19 @@ def test_tokens(ops, T, H):
     w = 1 + 0.3 * randn(3, H)
     n = forward(ops, x, res, w, "mx")
     backward(ops, randn(T + 2, T, H, dt="bf16"), n.h.cpu(), w, n.rstd.cpu(), randn(T + 3, T, H, dt="bf16"))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("H", [512, 1024, 2064, 4096, 4112, 7168, 8192, 8208, 16384])
+@pytest.mark.parametrize("T", [305, 700])
+def test_many_long_rows(ops, T, H, dt):
+    """Rows that come by copies into a ring, with and without a residual, weights of both types."""
+    for i in range(2):
+        x, res = randn(H + i, T, H, dt=dt), randn(H + 9, T, H, dt=dt) if i else None
+        w = (1 + 0.3 * randn(H + 1, H)).to(DT[dt if i else "f32"])
+        n = forward(ops, x, res, w, ("mx", "f8")[i])
+        backward(ops, randn(H + 2, T, H, dt=dt), n.h.cpu(), w, n.rstd.cpu(), randn(H + 3, T, H, dt=dt) if i else None)
+    assert ops.sync_status() == (0, 0)
 
 
 def test_no_rows_give_a_zero_weight_gradient(ops):
