@@ -85,21 +85,25 @@ struct Out8 {
   int groups, blocks;        // of a row
 };
 // Group g of a row of codes and (its block's first lane) the scale. `live`: the group is one of the row's.
-__device__ __forceinline__ void store8(const Out8& o, int64_t row, int g, bool live, const float (&f)[16], uint32_t am) {
+__device__ __forceinline__ void store_mx(const Out8& o, int64_t row, int g, bool live, const float (&f)[16], uint32_t am) {
   uint32_t scale;
-  if (o.variant == MM_MOE_VARIANT_MX) {
-    const uint4 c = encode_mx(f, am, scale);
-    if (live) {
-      reinterpret_cast<uint4*>(o.codes)[row * o.groups + g] = c;
-      if ((g & 1) == 0) static_cast<uint8_t*>(o.sf)[row * o.blocks + (g >> 1)] = static_cast<uint8_t>(scale);
-    }
-  } else {
-    const uint4 c = encode_f8(f, am, scale);
-    if (live) {
-      reinterpret_cast<uint4*>(o.codes)[row * o.groups + g] = c;
-      if ((g & 7) == 0) static_cast<float*>(o.sf)[row * o.blocks + (g >> 3)] = __uint_as_float(scale);
-    }
+  const uint4 c = encode_mx(f, am, scale);
+  if (live) {
+    reinterpret_cast<uint4*>(o.codes)[row * o.groups + g] = c;
+    if ((g & 1) == 0) static_cast<uint8_t*>(o.sf)[row * o.blocks + (g >> 1)] = static_cast<uint8_t>(scale);
   }
+}
+__device__ __forceinline__ void store_f8(const Out8& o, int64_t row, int g, bool live, const float (&f)[16], uint32_t am) {
+  uint32_t scale;
+  const uint4 c = encode_f8(f, am, scale);
+  if (live) {
+    reinterpret_cast<uint4*>(o.codes)[row * o.groups + g] = c;
+    if ((g & 7) == 0) static_cast<float*>(o.sf)[row * o.blocks + (g >> 3)] = __uint_as_float(scale);
+  }
+}
+__device__ __forceinline__ void store8(const Out8& o, int64_t row, int g, bool live, const float (&f)[16], uint32_t am) {
+  if (o.variant == MM_MOE_VARIANT_MX) store_mx(o, row, g, live, f, am);
+  else store_f8(o, row, g, live, f, am);
 }
 
 // Four e4m3 codes of a word as fp32, exact.
@@ -139,9 +143,28 @@ __device__ __forceinline__ void round16(const float (&f)[16], uint32_t (&w)[Grou
   memcpy(w, v, sizeof(v));
 }
 
+// 16 bytes of shared memory from any even offset of a 16-byte aligned array on; the granule that holds the last of them
+// exists.
+__device__ __forceinline__ uint4 shared16_any(const void* array, int offset) {
+  const int m = offset & 15;
+  const uint4* g = reinterpret_cast<const uint4*>(static_cast<const char*>(array) + (offset - m));
+  const uint4 lo = g[0];
+  if (m == 0) return lo;
+  const uint4 hi = g[1];
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = (m & 8) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = (m & 4) ? w[i + 1] : w[i];
+  const uint32_t b = (m & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], b), __funnelshift_r(w[1], w[2], b), __funnelshift_r(w[2], w[3], b),
+                    __funnelshift_r(w[3], w[4], b));
+}
+
 // Stores the 16-element groups of a warp, each of n (up to 16) elements from `at` on; all lanes take part.
 //   kVec    whole groups on 32-byte boundaries: 32 bytes an instruction
-//   else    anywhere: through shared memory (512 elements a warp), so that consecutive lanes store consecutive elements
+//   else    anywhere, through shared memory (512 elements a warp): groups that follow each other by the 16-byte granules of
+//           memory they cover, others so that consecutive lanes store consecutive elements
 template <typename T, bool kVec>
 __device__ __forceinline__ void store_groups(T* at, int n, const uint32_t (&w)[Group<T>::kWords], T* warp_smem) {
   if constexpr (kVec) {
@@ -150,19 +173,35 @@ __device__ __forceinline__ void store_groups(T* at, int n, const uint32_t (&w)[G
       for (int h = 0; h < Group<T>::kWords / 8; ++h) st_global_v8(reinterpret_cast<float*>(at) + 8 * h, w + 8 * h);
     }
   } else {
+    constexpr int kSize = sizeof(T), kWhole = 16 / kSize, kRun = 512;
     const int lane = threadIdx.x & 31;
+    const unsigned long long p = reinterpret_cast<unsigned long long>(at), p0 = __shfl_sync(0xffffffffu, p, 0);
     __syncwarp();
 #pragma unroll
     for (int q = 0; q < Group<T>::kWords / 4; ++q)
       reinterpret_cast<uint4*>(warp_smem)[lane * (Group<T>::kWords / 4) + q] =
           make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    const bool run = __all_sync(0xffffffffu, n == 16 && p == p0 + static_cast<unsigned long long>(lane) * 16 * kSize);
     __syncwarp();
+    if (run) {
+      T* to = reinterpret_cast<T*>(p0);
+      const int before = static_cast<int>(p0 & 15) / kSize;      // elements of the first granule that are not the run's
+#pragma unroll
+      for (int i = 0; i < kRun / kWhole / 32; ++i) {
+        const int first = (i * 32 + lane) * kWhole - before;     // the granule's first element
+        if (first >= 0) *reinterpret_cast<uint4*>(to + first) = shared16_any(warp_smem, first * kSize);
+      }
+      // what the run has of its first and of its last granule
+      if (before && lane < kWhole - before) to[lane] = warp_smem[lane];
+      if (lane < before) to[kRun - before + lane] = warp_smem[kRun - before + lane];
+      return;
+    }
     const int e = lane & 15;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int j = 2 * i + (lane >> 4);         // the lane whose group these 16 elements are
-      T* p = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), j));
-      if (e < __shfl_sync(0xffffffffu, n, j)) p[e] = warp_smem[j * 16 + e];
+      T* q = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, p, j));
+      if (e < __shfl_sync(0xffffffffu, n, j)) q[e] = warp_smem[j * 16 + e];
     }
   }
 }

@@ -8,12 +8,13 @@
 // that training need not keep the experts' outputs for the weights' gradient.
 //
 // Memory bounds both (forward: 4 bytes an element of a read and 2 written in 16 bits,
-// and 2 1/16 where kept; back: 2 and 2 1/16 read, 4 written).  A row has a group of
-// threads, 16 columns a lane and step, and everything about an element stays in its
-// lane but a block's amax and the row's dot.
+// and 2 1/16 where kept; back: 2 and 2 1/16 read, 4 written).  A CTA takes a few rows,
+// looks their pairs and weights up at once, and then has two independent groups of 16
+// columns a lane in flight; everything about an element stays in its lane but a block's
+// amax and the row's dot.
 //
 // 16-bit rows take the fast exponential and reciprocal (within 2^-20, under a
-// hundredth of the rounding of the result); fp32 rows expf and the IEEE division.
+// hundredth of the rounding of the result; without denormals, a third of the instructions); fp32 rows expf and the IEEE division.
 #include "rows8.cuh"
 
 namespace mm {
@@ -25,71 +26,123 @@ constexpr int kMx = MM_MOE_VARIANT_MX;
 template <typename T>
 __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (sizeof(T) == 4) return __fdiv_rn(1.0f, 1.0f + expf(-g));
-  else return rcp_approx(1.0f + __expf(-g));
+  else {
+    float e;                                     // exp(-g) as a power of two; what is below 2^-126 is 0
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    return rcp_approx(1.0f + e);
+  }
 }
 
-// The pair of a pool row, or -1 where the row is padding. Without a routing a row is its own.
-__device__ __forceinline__ int64_t pair_of(const SwigluRows& r, int64_t row) {
-  if (row >= r.rows) return -1;
-  if (!r.src) return row;
-  if (row >= static_cast<int64_t>(__ldg(r.blk_off + r.E)) * r.block_m) return -1;
-  return __ldg(r.src + row);
+constexpr int kMostRows = 64;        // of a CTA
+constexpr int kFlight = 1;           // groups of 16 columns a lane has in flight
+
+// The CTA's rows: their pairs (-1: padding, or past the end) and weights. Without a routing a row is its own pair.
+struct Rows {
+  int64_t pair[kMostRows];
+  float w[kMostRows];
+};
+__device__ __forceinline__ void look_up(Rows& s, const SwigluRows& r, const float* __restrict__ w, int64_t row0, int rows) {
+  for (int i = threadIdx.x; i < rows; i += kThreads) {
+    const int64_t row = row0 + i;
+    int64_t pair = -1;
+    if (row < r.rows) pair = !r.src ? row : row < static_cast<int64_t>(__ldg(r.blk_off + r.E)) * r.block_m ? __ldg(r.src + row) : -1;
+    s.pair[i] = pair;
+    s.w[i] = pair >= 0 ? (w ? __ldg(w + pair) : 1.f) : 0.f;
+  }
+  __syncthreads();
 }
 
+// `rows` rows of a CTA, as groups of 16 columns in a row; a row's groups are those its codes fill, an even number, so that
+// blocks lie inside a warp.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads)
-    swiglu_kernel(const SwigluRows r, const T* __restrict__ h, int64_t stride, const float* __restrict__ w,
-                  T* __restrict__ a, const Out8 q, const Out8 kept, int P) {
+__global__ void __launch_bounds__(kThreads, 4)
+    swiglu_kernel(const SwigluRows r, int rows, const T* __restrict__ h, int64_t stride, const float* __restrict__ w,
+                  T* __restrict__ a, const Out8 q, const Out8 kept) {
+  __shared__ Rows s_rows;
   __shared__ alignas(16) T s_run[kVec ? 1 : kThreads / 32 * 512];
   T* run = kVec ? s_run : s_run + (threadIdx.x >> 5) * 512;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / P) + threadIdx.x / P;
-  const int l = threadIdx.x % P, I = r.I;
-  const int64_t pair = pair_of(r, row);
-  const float weight = pair >= 0 ? (w ? __ldg(w + pair) : 1.f) : 0.f;
-  const T* hr = h + (pair >= 0 ? row : 0) * stride;
-  const int groups = blocks8(I, kMx) * 2;
-  const bool in = row < r.rows;
-  for (int g = l; g - (l & 31) < groups; g += P) {
-    Group<T> vg, vu;
-    if (pair >= 0 && g * 16 < I) {
-      vg.template load<kVec>(hr, g * 16, I);
-      vu.template load<kVec>(hr + I, g * 16, I);
-    } else {
-      vg.clear();
-      vu.clear();
-    }
-    float gate[16], up[16];
-    vg.floats(gate);
-    vu.floats(up);
-    if (kept.codes) {                            // gate and up as blocks of one row of both
-      store8(kept, row * 2, g, in && g < groups, gate, vg.amax_bits());
-      store8(kept, row * 2 + 1, g, in && g < groups, up, vu.amax_bits());
-    }
-    float f[16];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows;
+  look_up(s_rows, r, w, row0, rows);
+  const int I = r.I, groups = kept.groups, items = rows * groups;
+  for (int i0 = threadIdx.x; i0 - static_cast<int>(threadIdx.x & 31) < items; i0 += kFlight * kThreads) {
+    Group<T> vg[kFlight], vu[kFlight];
+    int at[kFlight], gg[kFlight];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = gate[i] * sigmoid<T>(gate[i]) * up[i] * weight;
-    if (pair < 0)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] = 0.f;
-    if (q.codes) {
-      float z[16];                               // past the row: zeros, also where the weight is not finite
-#pragma unroll
-      for (int i = 0; i < 16; ++i) z[i] = g * 16 + i < I ? f[i] : 0.f;
-      store8(q, row, g, in && g < groups, z, amax_bits16(z));
+    for (int u = 0; u < kFlight; ++u) {
+      const int i = i0 + u * kThreads;
+      at[u] = i / groups;
+      gg[u] = i - at[u] * groups;
+      if (i < items && s_rows.pair[at[u]] >= 0 && gg[u] * 16 < I) {
+        const T* hr = h + (row0 + at[u]) * stride;
+        vg[u].template load<kVec>(hr, gg[u] * 16, I);
+        vu[u].template load<kVec>(hr + I, gg[u] * 16, I);
+      } else {
+        vg[u].clear();
+        vu[u].clear();
+      }
     }
-    if (a) {
-      uint32_t o[Group<T>::kWords];
-      round16<T>(f, o);
-      store_groups<T, kVec>(a + row * I + g * 16, in ? min(16, I - g * 16) : 0, o, run);
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      if (i0 + u * kThreads - static_cast<int>(threadIdx.x & 31) >= items) break;       // the whole warp
+      const int64_t row = row0 + at[u];
+      const int g = gg[u];
+      const bool in = i0 + u * kThreads < items && row < r.rows;
+      const bool live = in && s_rows.pair[at[u]] >= 0;
+      if (!__any_sync(0xffffffffu, live)) {      // padding: zeros, and the scale of zeros
+        const uint8_t zero = static_cast<uint8_t>(ue8m0_exponent_e4m3(0.f) + 127);
+        if (in && kept.codes) {
+          reinterpret_cast<uint4*>(kept.codes)[row * 2 * groups + g] = make_uint4(0, 0, 0, 0);
+          reinterpret_cast<uint4*>(kept.codes)[(row * 2 + 1) * groups + g] = make_uint4(0, 0, 0, 0);
+          static_cast<uint8_t*>(kept.sf)[(row * 2 + (g & 1)) * kept.blocks + (g >> 1)] = zero;
+        }
+        if (in && q.codes) {
+          reinterpret_cast<uint4*>(q.codes)[row * groups + g] = make_uint4(0, 0, 0, 0);
+          if ((g & 1) == 0) static_cast<uint8_t*>(q.sf)[row * q.blocks + (g >> 1)] = zero;
+        }
+        if (a) {
+          uint32_t o[Group<T>::kWords];
+#pragma unroll
+          for (int c = 0; c < Group<T>::kWords; ++c) o[c] = 0;
+          store_groups<T, kVec>(a + row * I + g * 16, in ? min(16, I - g * 16) : 0, o, run);
+        }
+        continue;
+      }
+      float gate[16], up[16];
+      vg[u].floats(gate);
+      vu[u].floats(up);
+      if (kept.codes) {                          // gate and up as blocks of one row of both
+        store_mx(kept, row * 2, g, in, gate, vg[u].amax_bits());
+        store_mx(kept, row * 2 + 1, g, in, up, vu[u].amax_bits());
+      }
+      const float weight = live ? s_rows.w[at[u]] : 0.f;
+      float f[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) f[c] = 0.f;
+      if (live)
+#pragma unroll
+        for (int c = 0; c < 16; ++c) f[c] = gate[c] * sigmoid<T>(gate[c]) * up[c] * weight;
+      if (q.codes) {
+        float z[16];                             // past the row: zeros, also where the weight is not finite
+#pragma unroll
+        for (int c = 0; c < 16; ++c) z[c] = g * 16 + c < I ? f[c] : 0.f;
+        store_mx(q, row, g, in, z, amax_bits16(z));
+      }
+      if (a) {
+        uint32_t o[Group<T>::kWords];
+        round16<T>(f, o);
+        store_groups<T, kVec>(a + row * I + g * 16, in ? min(16, I - g * 16) : 0, o, run);
+      }
     }
   }
 }
 
+// P threads a row; a group of threads has two of the CTA's rows in flight. Their dots meet in shared memory.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads)
-    swiglu_backward_kernel(const SwigluRows r, const T* __restrict__ d_a, int64_t stride, const Out8 kept,
+__global__ void __launch_bounds__(kThreads, 4)
+    swiglu_backward_kernel(const SwigluRows r, int rows, const T* __restrict__ d_a, int64_t stride, const Out8 kept,
                            const float* __restrict__ w, T* __restrict__ d_h, float* __restrict__ d_w, int P) {
-  __shared__ float s_part[kThreads / 32];
+  __shared__ Rows s_rows;
+  __shared__ float s_dot[kMostRows][kThreads / 32];
   __shared__ alignas(16) T s_run[kVec ? 1 : kThreads / 32 * 512];
   T* run = kVec ? s_run : s_run + (threadIdx.x >> 5) * 512;
   // pairs that no row holds: masked slots
@@ -97,58 +150,93 @@ __global__ void __launch_bounds__(kThreads)
     for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < r.pairs;
          p += static_cast<int64_t>(gridDim.x) * kThreads)
       if (__ldg(r.slot + p) < 0) d_w[p] = 0.f;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / P) + threadIdx.x / P;
-  const int l = threadIdx.x % P, I = r.I;
-  const int64_t pair = pair_of(r, row);
-  const float weight = pair >= 0 ? (w ? __ldg(w + pair) : 1.f) : 0.f;
-  const bool in = row < r.rows;
-  const T* dr = d_a + (pair >= 0 ? row : 0) * stride;
-  const uint4* codes = reinterpret_cast<const uint4*>(kept.codes) + (pair >= 0 ? row : 0) * 2 * kept.groups;
-  const uint8_t* sf = static_cast<const uint8_t*>(kept.sf) + (pair >= 0 ? row : 0) * 2 * kept.blocks;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows;
+  look_up(s_rows, r, w, row0, rows);
+  const int l = threadIdx.x % P, sub = threadIdx.x / P, subs = kThreads / P, I = r.I;
   const int groups = (I + 15) / 16;
-  float dot = 0.f;
-  for (int g = l; g - (l & 31) < groups; g += P) {
-    float og[16], ou[16];
-    if (pair >= 0 && g < groups) {
-      Group<T> vd;
-      vd.template load<kVec>(dr, g * 16, I);
-      float gate[16], up[16], d[16];
-      const uint4 cg = __ldg(codes + g), cu = __ldg(codes + kept.groups + g);
-      decode16(cg, ue8m0_value(__ldg(sf + (g >> 1))), gate);
-      decode16(cu, ue8m0_value(__ldg(sf + kept.blocks + (g >> 1))), up);
-      vd.floats(d);
+  for (int i0 = sub; i0 < rows; i0 += kFlight * subs) {
+    float dot[kFlight];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float s = sigmoid<T>(gate[i]);
-        const float silu = gate[i] * s;
-        if (g * 16 + i < I) dot = fmaf(d[i] * silu, up[i], dot);
-        const float dw = d[i] * weight;
-        og[i] = dw * up[i] * (s * (1.0f + gate[i] * (1.0f - s)));
-        ou[i] = dw * silu;
+    for (int u = 0; u < kFlight; ++u) dot[u] = 0.f;
+    for (int g = l; g - (l & 31) < groups; g += P) {
+      Group<T> vd[kFlight];
+      uint4 cg[kFlight], cu[kFlight];
+      uint32_t sg[kFlight], su[kFlight];
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int i = i0 + u * subs;
+        const bool live = i < rows && s_rows.pair[i] >= 0 && g < groups;
+        vd[u].clear();
+        cg[u] = cu[u] = make_uint4(0, 0, 0, 0);
+        sg[u] = su[u] = 0;
+        if (live) {
+          const int64_t row = row0 + i;
+          const uint4* codes = reinterpret_cast<const uint4*>(kept.codes) + row * 2 * kept.groups + g;
+          const uint8_t* sf = static_cast<const uint8_t*>(kept.sf) + row * 2 * kept.blocks + (g >> 1);
+          vd[u].template load<kVec>(d_a + row * stride, g * 16, I);
+          cg[u] = __ldg(codes);
+          cu[u] = __ldg(codes + kept.groups);
+          sg[u] = __ldg(sf);
+          su[u] = __ldg(sf + kept.blocks);
+        }
       }
-    } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) og[i] = ou[i] = 0.f;
+      for (int u = 0; u < kFlight; ++u) {
+        const int i = i0 + u * subs;
+        if (i >= rows) break;                    // the whole group of threads
+        float og[16], ou[16];
+        if (s_rows.pair[i] >= 0 && g < groups) {
+          const float weight = s_rows.w[i];
+          float gate[16], up[16], d[16];
+          decode16(cg[u], ue8m0_value(sg[u]), gate);
+          decode16(cu[u], ue8m0_value(su[u]), up);
+          vd[u].floats(d);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float s = sigmoid<T>(gate[c]);
+            const float silu = gate[c] * s;
+            if (kVec || g * 16 + c < I) dot[u] = fmaf(d[c] * silu, up[c], dot[u]);
+            const float dw = d[c] * weight;
+            og[c] = dw * up[c] * (s * (1.0f + gate[c] * (1.0f - s)));
+            ou[c] = dw * silu;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) og[c] = ou[c] = 0.f;
+        }
+        uint32_t o[Group<T>::kWords];
+        T* at = d_h + (row0 + i) * 2 * I + g * 16;
+        const int n = row0 + i < r.rows ? min(16, I - g * 16) : 0;
+        round16<T>(og, o);
+        store_groups<T, kVec>(at, n, o, run);
+        round16<T>(ou, o);
+        store_groups<T, kVec>(at + I, n, o, run);
+      }
     }
-    uint32_t o[Group<T>::kWords];
-    T* at = d_h + row * 2 * I + g * 16;
-    const int n = in ? min(16, I - g * 16) : 0;
-    round16<T>(og, o);
-    store_groups<T, kVec>(at, n, o, run);
-    round16<T>(ou, o);
-    store_groups<T, kVec>(at + I, n, o, run);
+    if (d_w)
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+        if (i0 + u * subs < rows && (threadIdx.x & 31) == 0) s_dot[i0 + u * subs][l >> 5] = dot[u];
+      }
   }
   if (!d_w) return;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-  if (P > 32) {
-    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = dot;
-    __syncthreads();
-    dot = 0.f;
-    if (l == 0)
-      for (int i = 0; i < P / 32; ++i) dot += s_part[threadIdx.x / 32 + i];
-  }
-  if (l == 0 && pair >= 0) d_w[pair] = dot;
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows; i += kThreads)
+    if (s_rows.pair[i] >= 0) {
+      float v = 0.f;
+      for (int k = 0; k < P / 32; ++k) v += s_dot[i][k];
+      d_w[s_rows.pair[i]] = v;
+    }
+}
+
+// Rows of a CTA: about four groups of 16 columns a thread, fewer where that leaves SMs without a CTA.
+int cta_rows(int64_t rows, int groups) {
+  int64_t n = 4 * kThreads / groups;
+  const int64_t spread = rows / (4 * dev_info().sms);
+  n = n < spread ? n : spread;
+  return static_cast<int>(n < 1 ? 1 : n > kMostRows ? kMostRows : n);
 }
 
 Out8 kept_rows(void* codes, void* sf, int I) {
@@ -161,15 +249,15 @@ cudaError_t launch_swiglu(const SwigluRows& r, int dtype, const void* h, int64_t
                           void* codes, void* sf, void* kept, void* kept_sf, cudaStream_t s) {
   const int elem = dtype_size(dtype);
   const bool vec = whole_groups(h, stride * elem, r.I) && whole_groups(a, static_cast<int64_t>(r.I) * elem, r.I);
-  const int P = row_threads(groups8(r.I, kMx), 1, kThreads);
-  const unsigned grid = static_cast<unsigned>((r.rows + kThreads / P - 1) / (kThreads / P));
+  const int rows = cta_rows(r.rows, groups8(r.I, kMx));
+  const unsigned grid = static_cast<unsigned>((r.rows + rows - 1) / rows);
   const Out8 q = kept_rows(codes, sf, r.I), k = kept_rows(kept, kept_sf, r.I);
   return with_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     const T* p = static_cast<const T*>(h);
     T* o = static_cast<T*>(a);
-    if (vec) swiglu_kernel<T, true><<<grid, kThreads, 0, s>>>(r, p, stride, w, o, q, k, P);
-    else swiglu_kernel<T, false><<<grid, kThreads, 0, s>>>(r, p, stride, w, o, q, k, P);
+    if (vec) swiglu_kernel<T, true><<<grid, kThreads, 0, s>>>(r, rows, p, stride, w, o, q, k);
+    else swiglu_kernel<T, false><<<grid, kThreads, 0, s>>>(r, rows, p, stride, w, o, q, k);
     return cudaGetLastError();
   });
 }
@@ -179,14 +267,17 @@ cudaError_t launch_swiglu_backward(const SwigluRows& r, int dtype, const void* d
   const int elem = dtype_size(dtype);
   const bool vec = whole_groups(d_a, stride * elem, r.I) && whole_groups(d_h, static_cast<int64_t>(r.I) * elem, r.I);
   const int P = row_threads((r.I + 15) / 16, 1, kThreads);
-  const unsigned grid = static_cast<unsigned>((r.rows + kThreads / P - 1) / (kThreads / P));
+  int rows = cta_rows(r.rows, (r.I + 15) / 16);
+  const int subs = kThreads / P;
+  rows = rows < subs ? subs : rows / subs * subs;
+  const unsigned grid = static_cast<unsigned>((r.rows + rows - 1) / rows);
   const Out8 k = kept_rows(const_cast<void*>(kept), const_cast<void*>(kept_sf), r.I);
   return with_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     const T* p = static_cast<const T*>(d_a);
     T* o = static_cast<T*>(d_h);
-    if (vec) swiglu_backward_kernel<T, true><<<grid, kThreads, 0, s>>>(r, p, stride, k, w, o, d_w, P);
-    else swiglu_backward_kernel<T, false><<<grid, kThreads, 0, s>>>(r, p, stride, k, w, o, d_w, P);
+    if (vec) swiglu_backward_kernel<T, true><<<grid, kThreads, 0, s>>>(r, rows, p, stride, k, w, o, d_w, P);
+    else swiglu_backward_kernel<T, false><<<grid, kThreads, 0, s>>>(r, rows, p, stride, k, w, o, d_w, P);
     return cudaGetLastError();
   });
 }
