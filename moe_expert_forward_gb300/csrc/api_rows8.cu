@@ -172,7 +172,7 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
   if (rows == 0 || (cnt && T == 0))            // sums of nothing
     return done(cudaMemsetAsync(out, 0, static_cast<size_t>(E) * N * C * dtype_size(dtype), s));
   const WeightGradLaunch p{d_y, d_stride, rows, N, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(sf),
-                           C, cnt, blk_off, by_token ? src : nullptr, K, E, block_m,
+                           C, cnt, blk_off, src, by_token != 0, K, E, block_m,
                            terms, dtype, out, scratch,
                            static_cast<uint64_t>(timeout_ms ? timeout_ms : 2000) * 1000000ull, (debug_flags & 1) != 0};
   return done(launch_weight_grad(p, s));

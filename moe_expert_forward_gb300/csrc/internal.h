@@ -289,7 +289,8 @@ struct WeightGradLaunch {
   int C;
   const int32_t* cnt;        // null: dense
   const int32_t* blk_off;
-  const int32_t* src;        // x's rows are tokens
+  const int32_t* src;
+  bool by_token;             // x's rows are tokens
   int K, E, block_m;
   int64_t terms;             // rows of a sum, of an expert on average
   int dtype;                 // of out: fp32 or bf16

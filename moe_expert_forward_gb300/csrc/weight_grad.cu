@@ -26,8 +26,8 @@
 // Codes come by TMA too, their scales by 4-byte asynchronous copies, into a ring of their own: converters that load
 // for themselves keep the SM's loads in flight at their limit, and wait for it (1000 cycles a stage and more).  Where
 // x's rows are tokens, a kernel before this one copies them to their pool rows (TMA's own gather, four rows an
-// instruction, took 1900 cycles a stage; 64 experts of 384 rows 1426 us instead of 785 and 30).  Rows of d_y, or of
-// scales, that start on no 16-byte, or 4-byte, boundary are copied first too.
+// instruction, took 1900 cycles a stage).  Rows of d_y, or of scales, that start on no 16-byte, or 4-byte, boundary are
+// copied first too.  With many tiles of N that kernel decodes x instead, and the product takes both operands by TMA.
 //
 // The loops of all roles have to fit the instruction cache together: none is unrolled over its ring (unrolled, a third
 // of the fetches missed and a stage took 1500 cycles).
@@ -93,7 +93,7 @@ struct Args {
   const int* blk_off;
   char* out;
   int64_t out_pitch;         // bytes of a row of out; [parts][E][N] rows
-  int unreachable;           // leave x of the CTA's last stage out
+  int unreachable;           // the CTA's last stage is not handed over
   int* report;
   uint64_t timeout_ns;
 };
@@ -259,8 +259,8 @@ struct Maps {
   CUtensorMap d_y, codes, out;
 };
 
-// kTma: out's rows are 16-byte aligned, and results leave by TMA.
-template <typename T, bool kTma>
+// kTma: out's rows are 16-byte aligned, and results leave by TMA. kDecoded: x comes in bf16.
+template <typename T, bool kTma, bool kDecoded>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ Maps maps, const Args args) {
   extern __shared__ uint8_t smem_raw[];
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full_a[i], 1);
-      mbar_init(&full_b[i], kConvertWarps / kGroups);
+      mbar_init(&full_b[i], kConvertWarps / kGroups);        // (not used where x comes in bf16)
       mbar_init(&full[i], 2);
       mbar_init(&empty[i], 1);
     }
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto segments = [](int n) { return sizeof(T) == 4 ? (n + kSegment - 1) / kSegment : 1; };
 
   if (warp == kTmaWarp) {
-    // ------------------------------------------------------------------ d_y by TMA
+    // ------------------------------------------------------------------ d_y (and x in bf16) by TMA
     if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
       Cursor at(first, stride, ntasks);
@@ -328,11 +328,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (at.next(args, s_blk, s_cnt)) {
         const int s = ring.s;
         if (*s_abort || !mbar_wait(&empty[s], ring.phase ^ 1, st, s_abort, kSiteEmpty)) break;
-        mbar_arrive_expect_tx(&full_a[s], kHalfBytes);
-        uint8_t* d = smem + Smem::a + s * kHalfBytes;
-        const int row = at.t.row0 + at.t.ks * kRowsPerStage, n = at.t.n0 + static_cast<int>(rank) * 128;
-        tma_load_2d(d, &maps.d_y, &full_a[s], n, row, pol);
-        tma_load_2d(d + kChunkBytes, &maps.d_y, &full_a[s], n + 64, row, pol);
+        mbar_arrive_expect_tx(&full_a[s], kDecoded ? 2 * kHalfBytes : kHalfBytes);
+        const int row = at.t.row0 + at.t.ks * kRowsPerStage, half = static_cast<int>(rank) * 128;
+        auto load = [&](uint8_t* d, const CUtensorMap* m, int c) {
+          tma_load_2d(d, m, &full_a[s], c, row, pol);
+          tma_load_2d(d + kChunkBytes, m, &full_a[s], c + 64, row, pol);
+        };
+        load(smem + Smem::a + s * kHalfBytes, &maps.d_y, at.t.n0 + half);
+        if (kDecoded) load(smem + Smem::b + s * kHalfBytes, &maps.codes, at.t.c0 + half);
         ring.step();
         ++steps;
       }
@@ -404,6 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (kDecoded && (warp == kCodesWarp || warp >= kConvert0)) {
+    // x comes in bf16
   } else if (warp == kCodesWarp) {
     // ------------------------------------------------------------------ codes by TMA, scales by loads
     const uint64_t pol = policy_evict_normal();
@@ -450,7 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = at.t.rows - at.t.ks * kRowsPerStage;      // of the expert from this stage on
       live = at.next(args, s_blk, s_cnt);
       if (turn == 0) {
-        if (!live && args.unreachable) break;
         if (!mbar_wait_warp(&raw_full[raw.s], raw.phase, st, s_abort, kSiteRawFull)) break;
         uint4 c[kLaneRows];
         uint32_t byte[kLaneRows];
@@ -493,12 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor at(first, stride, ntasks);
     Ring<kStages> ring;
     const uint32_t full0 = map_shared(full, 0);
-    for (; at.next(args, s_blk, s_cnt); ring.step()) {
-      const int s = ring.s;
+    bool live = at.next(args, s_blk, s_cnt);
+    for (; live; ring.step()) {
+      const int s = ring.s, rows = at.t.rows - at.t.ks * kRowsPerStage;      // left from this stage on
+      live = at.next(args, s_blk, s_cnt);
+      if (!live && args.unreachable) break;
       if (!mbar_wait_warp(&full_a[s], ring.phase, st, s_abort, kSiteFullA) ||
-          !mbar_wait_warp(&full_b[s], ring.phase, st, s_abort, kSiteFullB))
+          (!kDecoded && !mbar_wait_warp(&full_b[s], ring.phase, st, s_abort, kSiteFullB)))
         break;
-      const int rows = at.t.rows - at.t.ks * kRowsPerStage;      // left from this stage on
       if (rows < kRowsPerStage && (rows & 15)) {
         // the sum ends inside an MMA: whatever d_y's rows behind it hold becomes zero
         uint8_t* am = smem + Smem::a + s * kHalfBytes;
@@ -630,6 +636,34 @@ __global__ void __launch_bounds__(kCopyThreads)
   for (int i = lane; i < pieces; i += 32) out[r * pieces + i] = __ldg(codes + t * pieces + i);
 }
 
+// The rows of x that the sums take in bf16, a warp a row: a pool row's token's (by_token), or its own; zeros where it holds
+// no pair (its 16 rows may be an MMA's). Without a routing every row is its own.
+__global__ void __launch_bounds__(kCopyThreads)
+    decode_rows_kernel(const uint4* __restrict__ codes, int pieces, const uint8_t* __restrict__ sf, int blocks,
+                       const int32_t* __restrict__ src, const int32_t* __restrict__ blk_off, int E, int block_m, int K,
+                       int by_token, int64_t rows, uint4* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (kCopyThreads / 32) + (threadIdx.x >> 5);
+  if (r >= rows || (src && r >= static_cast<int64_t>(__ldg(blk_off + E)) * block_m)) return;
+  const int pair = src ? __ldg(src + r) : 0;
+  const int64_t t = by_token ? pair / K : r;
+  uint4* o = out + r * pieces * 2;
+#pragma unroll 2
+  for (int i0 = 0; i0 < pieces; i0 += 32) {
+    const int i = i0 + lane;
+    uint4 c = make_uint4(0, 0, 0, 0);
+    uint32_t byte = kNoRow;
+    if (pair >= 0 && i < pieces) {
+      c = __ldg(codes + t * pieces + i);
+      byte = __ldg(sf + t * blocks + (i >> 1));
+    }
+    uint32_t w[8];
+    if (__any_sync(0xffffffffu, is_large(byte))) to_bf16<true>(c, byte, w);
+    else to_bf16<false>(c, byte, w);
+    if (i < pieces) st_global_v8(reinterpret_cast<float*>(o + 2 * i), w);
+  }
+}
+
 // Rows of d_y on no 16-byte boundary into rows of whole 16-byte pieces, and rows of scales on no 4-byte boundary into rows
 // of whole words: `pieces` a row and a thread each, of T.
 template <typename T>
@@ -688,7 +722,7 @@ cudaError_t add_parts(const float* sums, int parts, int64_t rows, int C, int pit
 }
 
 // a.out and a.out_pitch: where the sums go, of T.
-template <typename T>
+template <typename T, bool kDecoded>
 cudaError_t launch(const Args& a, Maps& maps, cudaStream_t s) {
   const bool tma = (reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(a.out_pitch)) % 16 == 0;
   if (tma) {
@@ -700,7 +734,7 @@ cudaError_t launch(const Args& a, Maps& maps, cudaStream_t s) {
                     dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  auto kernel = tma ? weight_grad_kernel<T, true> : weight_grad_kernel<T, false>;
+  auto kernel = tma ? weight_grad_kernel<T, true, kDecoded> : weight_grad_kernel<T, false, kDecoded>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   if (cudaError_t e = configure_kernel(fn, 0, Smem::total(kMaxE))) return e;
   int most = 0;
@@ -728,17 +762,25 @@ int parts_of(int64_t tasks, int64_t terms) {
 }
 int sums_pitch(int C) { return (C + 3) / 4 * 4; }
 
+// Whether x is decoded into bf16 rows before the product, and not by its converters: with many tiles of N each of which
+// would decode the same codes. 8192 rows, C = 4096, first / by converters, us: N 512 67 / 51, 1024 77 / 66, 2048 121 / 120,
+// 4096 215 / 239; 64 experts of 384 rows, 4096 x 4096, 768 / 872.
+constexpr int kDecodeTiles = 8;
+bool decodes_first(int N) { return N > (kDecodeTiles - 1) * kTile; }
+
 // What a call keeps in its scratch: copies of d_y, of the codes and of the scales, and parts' sums. Bytes, 0: none.
 struct Copies {
-  size_t d_y, codes, sf, sums;
+  size_t d_y, codes, sf, sums;                   // (codes: x in bf16 where it is decoded first)
 };
 Copies copies_of(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C, bool by_token, int E,
                  int64_t terms) {
   const int blocks = blocks8(C, MM_MOE_VARIANT_MX);
   Copies c{0, 0, 0, 0};
   if (reinterpret_cast<uintptr_t>(d_y) % 16 || d_stride % 8) c.d_y = static_cast<size_t>(rows) * ((N + 7) / 8) * 16;
-  if (by_token) c.codes = static_cast<size_t>(rows) * blocks * kMxBlock;
-  if (by_token || reinterpret_cast<uintptr_t>(sf) % 4 || blocks % 4) c.sf = (static_cast<size_t>(rows) * ((blocks + 3) / 4) * 4 + 15) / 16 * 16;
+  if (decodes_first(N)) c.codes = static_cast<size_t>(rows) * blocks * kMxBlock * 2;
+  else if (by_token) c.codes = static_cast<size_t>(rows) * blocks * kMxBlock;
+  if (decodes_first(N)) c.sf = 0;
+  else if (by_token || reinterpret_cast<uintptr_t>(sf) % 4 || blocks % 4) c.sf = (static_cast<size_t>(rows) * ((blocks + 3) / 4) * 4 + 15) / 16 * 16;
   const int parts = parts_of(weight_grad_tasks(E, N, C), terms);
   if (parts > 1) c.sums = static_cast<size_t>(parts) * E * N * sums_pitch(C) * sizeof(float);
   return c;
@@ -771,7 +813,7 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
   a.unreachable = p.unreachable;
   a.timeout_ns = p.timeout_ns;
   const int blocks = blocks8(p.C, MM_MOE_VARIANT_MX);
-  const bool by_token = p.src != nullptr;
+  const bool by_token = p.by_token, decoded = decodes_first(p.N);
   const Copies copies = copies_of(p.d_y, p.d_stride, p.rows, p.N, p.sf, p.C, by_token, p.E, p.terms);
   const void *d_y = p.d_y, *codes = p.codes, *sf = p.sf;
   uint64_t pitch = static_cast<uint64_t>(p.d_stride) * 2;
@@ -782,11 +824,17 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
     pitch = static_cast<uint64_t>((p.N + 7) / 8) * 16;
     to += copies.d_y;
   }
+  const unsigned per = kCopyThreads / 32, grid = static_cast<unsigned>((p.rows + per - 1) / per);
+  const uint4* x = reinterpret_cast<const uint4*>(p.codes);
+  const int pieces = blocks * kMxBlock / 16;
+  if (decoded)
+    decode_rows_kernel<<<grid, kCopyThreads, 0, s>>>(x, pieces, p.sf, blocks, p.src, p.blk_off, p.E, p.block_m, p.K, by_token,
+                                                     p.rows, reinterpret_cast<uint4*>(to));
+  else if (by_token)
+    gather_rows_kernel<<<grid, kCopyThreads, 0, s>>>(x, pieces, p.sf, blocks, p.src, p.blk_off, p.E, p.block_m, p.K, p.rows,
+                                                     reinterpret_cast<uint4*>(to),
+                                                     reinterpret_cast<uint32_t*>(to + copies.codes));
   if (copies.codes) {
-    const int per = kCopyThreads / 32;
-    gather_rows_kernel<<<static_cast<unsigned>((p.rows + per - 1) / per), kCopyThreads, 0, s>>>(
-        reinterpret_cast<const uint4*>(p.codes), blocks * kMxBlock / 16, p.sf, blocks, p.src, p.blk_off, p.E, p.block_m, p.K,
-        p.rows, reinterpret_cast<uint4*>(to), reinterpret_cast<uint32_t*>(to + copies.codes));
     if (cudaError_t e = cudaGetLastError()) return e;
     codes = to;
     sf = to + copies.codes;
@@ -800,16 +848,22 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
   if (encode_tmap_2d(&maps.d_y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d_y, static_cast<uint64_t>(p.N),
                      static_cast<uint64_t>(p.rows), pitch, 64, kRowsPerStage, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const uint64_t bytes = static_cast<uint64_t>(blocks) * kMxBlock;
-  if (encode_tmap_2d(&maps.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, bytes, static_cast<uint64_t>(p.rows), bytes, 128,
-                     kRowsPerStage, CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
+  const uint64_t cols = static_cast<uint64_t>(blocks) * kMxBlock;
+  if ((decoded ? encode_tmap_2d(&maps.codes, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, codes, cols, static_cast<uint64_t>(p.rows),
+                                cols * 2, 64, kRowsPerStage, CU_TENSOR_MAP_SWIZZLE_128B)
+               : encode_tmap_2d(&maps.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, cols, static_cast<uint64_t>(p.rows), cols,
+                                128, kRowsPerStage, CU_TENSOR_MAP_SWIZZLE_NONE)) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  if (a.parts == 1) return p.dtype == MM_MOE_DTYPE_F32 ? launch<float>(a, maps, s) : launch<__nv_bfloat16>(a, maps, s);
+  auto go = [&](auto tag) {
+    using T = decltype(tag);
+    return decoded ? launch<T, true>(a, maps, s) : launch<T, false>(a, maps, s);
+  };
+  if (a.parts == 1) return p.dtype == MM_MOE_DTYPE_F32 ? go(float{}) : go(__nv_bfloat16{});
   const int pitch_c = sums_pitch(p.C);
   float* sums = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + copies.d_y + copies.codes + copies.sf);
   a.out = reinterpret_cast<char*>(sums);
   a.out_pitch = static_cast<int64_t>(pitch_c) * sizeof(float);
-  if (cudaError_t e = launch<float>(a, maps, s)) return e;
+  if (cudaError_t e = go(float{})) return e;
   const int64_t rows = static_cast<int64_t>(p.E) * p.N;
   return p.dtype == MM_MOE_DTYPE_F32 ? add_parts<float>(sums, a.parts, rows, p.C, pitch_c, p.out, s)
                                      : add_parts<__nv_bfloat16>(sums, a.parts, rows, p.C, pitch_c, p.out, s);

@@ -63,6 +63,28 @@ def test_dense_widths(ops, N, C):
     check(ops, whole(N, 150, N).bfloat16(), whole(C, 150, C))
 
 
+@pytest.mark.parametrize("rows,N,C", [(1, 1800, 40), (70, 2048, 96), (200, 1793, 300), (17, 2304, 33)])
+def test_dense_decoded_first(ops, rows, N, C):
+    check(ops, whole(N, rows, N).bfloat16(), whole(C, rows, C))
+
+
+@pytest.mark.parametrize("by_token", [False, True])
+def test_routed_decoded_first(ops, by_token):
+    """Many columns of d_y, experts of 0 to 40 rows, NaN in the padding of both operands."""
+    T, E, N, C = 61, 7, 1900, 100
+    r = ops.sort_tokens(routing(T, E, 2, 0.2, 3).cuda(), E)
+    at = r.slot.cpu().flatten()
+    at = at[at >= 0].long()
+    d_y = torch.full((r.rows, N), float("nan"))
+    d_y[at] = whole(1, len(at), N)
+    x = whole(2, T if by_token else r.rows, C)
+    if not by_token:
+        pad = torch.ones(r.rows, dtype=torch.bool)
+        pad[at] = False
+        x[pad] = float("nan")
+    check(ops, d_y.bfloat16(), x, r, by_token)
+
+
 def test_dense_random_values(ops):
     """Scales of every size, sums of 20000 rows."""
     x = randn(1, 20000, 96) * torch.exp2(torch.arange(96).remainder(17) - 8.0)
@@ -74,18 +96,19 @@ def test_scales_at_the_ends_of_their_range(ops):
     codes = torch.arange(256, dtype=torch.uint8)
     codes = codes[(codes & 127) != 127]                    # every code but NaN
     codes = torch.cat([codes, codes[:2]])[None].repeat(4, 1).contiguous()
-    one = torch.ones(4, 1, dtype=torch.bfloat16, device="cuda")
     for byte in (0, 1, 60, 119, 127, 134, 135, 136, 200, 245):
         sf = torch.full((4, 8), byte, dtype=torch.uint8)
-        for row in range(4):
-            d_y = torch.zeros_like(one)
+        for row, N in ((0, 1), (3, 1), (2, 2000)):             # by the converters, and decoded first
+            d_y = torch.zeros(4, N, dtype=torch.bfloat16, device="cuda")
             d_y[row] = 1
             got = d64(ops.weight_grad(d_y, codes.cuda(), sf.cuda(), 256, dtype=torch.float32))[0]
             want = values(codes[:1], sf[:1], 256)[0]
             # bf16 has every value but those between its subnormals, which are 2^-133 apart
             assert (np.abs(got - want) <= (2.0 ** -134 if byte < 4 else 0)).all(), byte
     sf = torch.full((4, 8), 255, dtype=torch.uint8, device="cuda")
-    assert torch.isnan(ops.weight_grad(one, codes.cuda(), sf, 256, dtype=torch.float32)).all()
+    for N in (1, 2000):
+        ones = torch.ones(4, N, dtype=torch.bfloat16, device="cuda")
+        assert torch.isnan(ops.weight_grad(ones, codes.cuda(), sf, 256, dtype=torch.float32)).all()
 
 
 @pytest.mark.parametrize("by_token", [False, True])
@@ -175,7 +198,7 @@ def test_output_past_four_gigabytes(ops):
     assert not got[199].any()
 
 
-@pytest.mark.parametrize("rows,N,C,routed", [(300, 300, 600, False), (3000, 2000, 6000, False), (8192, 128, 256, False),
+@pytest.mark.parametrize("rows,N,C,routed", [(300, 300, 600, False), (3000, 2000, 6000, False), (3000, 1000, 6000, False), (8192, 128, 256, False),
                                              (600, 300, 600, True)])
 def test_a_stage_that_never_comes(ops, monkeypatch, rows, N, C, routed):
     """The call gives up after its limit, says so once, and leaves the GPU in order."""
