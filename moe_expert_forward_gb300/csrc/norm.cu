@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostThreads = 512;
-constexpr int kRingBytes = 192 * 1024;           // of the rings of an SM's CTAs
+constexpr int kRingBytes = 160 * 1024;           // of the rings of an SM's CTAs
 constexpr int kMostStages = 6;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 enum : int { kSiteForward = 201, kSiteBackward = 202 };

@@ -57,24 +57,24 @@ __device__ __forceinline__ uint4 encode_f8(const float (&f)[16], uint32_t am, ui
   for (int o = 1; o < 8; o *= 2) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
   const bool bad = am >= 0x7F800000u;
   const float s = __fdiv_rn(fmaxf(__uint_as_float(bad ? 0u : am), 1e-10f), 448.0f);
+  // f times the reciprocal a little less and a little more (2^-20; it and the products round by 2^-24) has the IEEE
+  // quotient between: where both round to the same codes those are its codes, and else, next to a border, the lane
+  // divides. (8192x7168 with a division of every element 173 us.)
+  const float inv = __frcp_rn(s), less = inv * (1.0f - 0x1p-20f), more = inv * (1.0f + 0x1p-20f);
   float v[16];
-  // q = f * rn(1 / s) is within 4 fp32 ulps of the IEEE quotient, so both round to the same code unless a border between
-  // two codes lies that near (a fraction of 1/2 of e4m3's last bit: bits 19 to 0 near 0x80000) or the code is subnormal,
-  // below 2^-6, with other borders: only then is the lane's group divided. (8192x7168 with a division of every element
-  // 173 us.)
-  const float inv = __frcp_rn(s);
-  bool near = false;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    v[i] = f[i] * inv;
-    const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-    near = near || (b & 0xFFFFFu) - 0x7FFFCu <= 8u || b - 1u < 0x3C7FFFFFu;
-  }
-  if (near)
+  for (int i = 0; i < 16; ++i) v[i] = f[i] * less;
+  uint4 c = pack_e4m3x16(v);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = f[i] * more;
+  const uint4 d = pack_e4m3x16(v);
+  if (c.x != d.x || c.y != d.y || c.z != d.z || c.w != d.w) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(f[i], s);
+    c = pack_e4m3x16(v);
+  }
   scale = bad ? 0x7FC00000u : __float_as_uint(s);
-  return bad ? make_uint4(0, 0, 0, 0) : pack_e4m3x16(v);
+  return bad ? make_uint4(0, 0, 0, 0) : c;
 }
 
 // Codes and scales of rows; cols: code bytes of a row.

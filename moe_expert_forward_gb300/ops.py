@@ -100,7 +100,7 @@ def _bad(what: str, why: str):
     raise MMError(MM_MOE_ERR_INVALID_ARG, f"{what}: {why}")
 
 
-_device = torch.cuda.current_device
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device   # the second is the first behind checks
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # absent in builds of torch without CUDA
 
 
@@ -128,11 +128,6 @@ def _new(stream, shape, dtype, device, zero=False, shared=False):
     """A tensor (uninitialised, or zeroed in `stream`'s order) for a call on `stream`, of that stream's memory: what the
     current stream frees and takes again would otherwise meet kernels that `stream` still runs.  shared: marked as used
     on the current stream too.  (torch.cuda.stream as a context would do; it takes about 15 us, a whole call 10.)"""
-    if stream is None and not zero and _empty_cuda is not None and type(device) is torch.device and device.type == "cuda":
-        if type(shape) is int:
-            return _empty_cuda((shape,), (1,), dtype)
-        if len(shape) == 2:
-            return _empty_cuda(shape, (shape[1], 1), dtype)
     make = torch.zeros if zero else torch.empty
     if stream is None:
         return make(shape, dtype=dtype, device=device)
@@ -157,6 +152,19 @@ def _result(stream, shape, dtype, device):
     """What a call on `stream` returns: memory that no work queued on the current stream still uses, and that is not
     taken again before the work which the current stream has been given when it is freed."""
     return _new(stream, shape, dtype, device, shared=True)
+
+
+def _result_rows(stream, rows: int, cols: int, dtype, like):
+    """_result of [rows, cols] on the device of `like`."""
+    if stream is None and _empty_cuda is not None and like.is_cuda:
+        return _empty_cuda((rows, cols), (cols, 1), dtype)
+    return _new(stream, (rows, cols), dtype, like.device, shared=True)
+
+
+def _result_1d(stream, n: int, dtype, like):
+    if stream is None and _empty_cuda is not None and like.is_cuda:
+        return _empty_cuda((n,), (1,), dtype)
+    return _new(stream, (n,), dtype, like.device, shared=True)
 
 
 def _here(t, what: str, name: str):
@@ -520,9 +528,12 @@ def _held_shapes(rows: int, C: int, variant: int):
     return (rows, 128 * nb), (rows, nb), torch.float32
 
 
-def _held(stream, rows: int, C: int, variant: int, device):
-    codes, sf, dtype = _held_shapes(rows, C, variant)
-    return _result(stream, codes, torch.uint8, device), _result(stream, sf, dtype, device)
+def _held(stream, rows: int, C: int, variant: int, like):
+    if variant == MM_MOE_VARIANT_MX:
+        nb = -(-C // 32)
+        return _result_rows(stream, rows, 32 * nb, torch.uint8, like), _result_rows(stream, rows, nb, torch.uint8, like)
+    nb = -(-C // 128)
+    return _result_rows(stream, rows, 128 * nb, torch.uint8, like), _result_rows(stream, rows, nb, torch.float32, like)
 
 
 def quantize8(x, quant: str = "mx", stream=None):
@@ -536,7 +547,7 @@ def quantize8(x, quant: str = "mx", stream=None):
     R, C = x.shape
     if C < 1:
         _bad("quantize8", "x has no columns")
-    codes, sf = _held(stream, R, C, v, x.device)
+    codes, sf = _held(stream, R, C, v, x)
     _check(lib().mm_moe_rows_quantize(x.data_ptr(), code, _pitch(x), R, C, v, codes.data_ptr(), sf.data_ptr(),
                                       _stream(stream)), "mm_moe_rows_quantize")
     return codes, sf
@@ -559,7 +570,7 @@ def dequantize8(codes, sf, C: int, dtype=torch.bfloat16, stream=None):
     R, v, cp, sp = _held_args("dequantize8", codes, sf, C)
     if dtype not in _DTYPES:
         _bad("dequantize8", f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    out = _result(stream, (R, C), dtype, codes.device)
+    out = _result_rows(stream, R, C, dtype, codes)
     _check(lib().mm_moe_rows_dequantize(cp, sp, R, C, v, _DTYPES[dtype], out.data_ptr(), C, _stream(stream)),
            "mm_moe_rows_dequantize")
     return out
@@ -597,15 +608,15 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, rows: bool = True, qua
         _rows(residual, "rms_norm", "residual", H, x.dtype)
         if residual.shape[0] != T:
             _bad("rms_norm", f"x has {T} rows, residual {residual.shape[0]}")
-        h = _result(stream, (T, H), x.dtype, x.device)
+        h = _result_rows(stream, T, H, x.dtype, x)
         rp, r_pitch, hp = residual.data_ptr(), _pitch(residual), h.data_ptr()
     v, codes, sf, cp, sp = 0, None, None, None, None
     if quant is not None:
         v = _format("rms_norm", quant)
-        codes, sf = _held(stream, T, H, v, x.device)
+        codes, sf = _held(stream, T, H, v, x)
         cp, sp = codes.data_ptr(), sf.data_ptr()
-    y = _result(stream, (T, H), x.dtype, x.device) if rows else None
-    rstd = _result(stream, T, torch.float32, x.device)
+    y = _result_rows(stream, T, H, x.dtype, x) if rows else None
+    rstd = _result_1d(stream, T, torch.float32, x)
     _check(lib().mm_moe_rms_norm(x.data_ptr(), code, _pitch(x), rp, r_pitch, wp, w_code, T, H, eps, hp,
                                  None if y is None else y.data_ptr(), v, cp, sp, rstd.data_ptr(), _stream(stream)),
            "mm_moe_rms_norm")
@@ -637,10 +648,10 @@ def rms_norm_backward(d_y, h, weight, rstd, d_h=None, stream=None):
         _bad("rms_norm_backward", "h must be what rms_norm returned")
     wp, w_code = _norm_weight(weight, "rms_norm_backward", H, d_y.dtype)
     sp = _whole(rstd, "rms_norm_backward", "rstd", (T,), torch.float32)
-    d_x = _result(stream, (T, H), d_y.dtype, d_y.device)
-    d_weight = _result(stream, H, torch.float32, d_y.device)
+    d_x = _result_rows(stream, T, H, d_y.dtype, d_y)
+    d_weight = _result_1d(stream, H, torch.float32, d_y)
     scratch_bytes = _norm_scratch(T, H)
-    scratch = _new(stream, scratch_bytes, torch.uint8, d_y.device)
+    scratch = _result_1d(stream, scratch_bytes, torch.uint8, d_y)
     _check(lib().mm_moe_rms_norm_backward(d_y.data_ptr(), code, _pitch(d_y), h.data_ptr(), _pitch(h), wp, w_code, sp,
                                           None if d_h is None else d_h.data_ptr(), H if d_h is None else _pitch(d_h), T,
                                           H, d_x.data_ptr(), d_weight.data_ptr(), scratch.data_ptr(), scratch_bytes,
@@ -688,10 +699,10 @@ def swiglu(h, routing: Optional[Routing] = None, topk_w=None, rows: bool = True,
         _bad("swiglu", "none of rows, quant and keep is asked for")
     pool = _pool("swiglu", routing, topk_w, R)
     nb = -(-I // 32)
-    a = _result(stream, (R, I), h.dtype, h.device) if rows else None
-    codes, sf = _held(stream, R, I, MM_MOE_VARIANT_MX, h.device) if quant else (None, None)
-    kept = _result(stream, (R, 64 * nb), torch.uint8, h.device).view(R, 2, 32 * nb) if keep else None
-    kept_sf = _result(stream, (R, 2 * nb), torch.uint8, h.device).view(R, 2, nb) if keep else None
+    a = _result_rows(stream, R, I, h.dtype, h) if rows else None
+    codes, sf = _held(stream, R, I, MM_MOE_VARIANT_MX, h) if quant else (None, None)
+    kept = _result_rows(stream, R, 64 * nb, torch.uint8, h).view(R, 2, 32 * nb) if keep else None
+    kept_sf = _result_rows(stream, R, 2 * nb, torch.uint8, h).view(R, 2, nb) if keep else None
     out = [None if t is None else t.data_ptr() for t in (a, codes, sf, kept, kept_sf)]
     _check(lib().mm_moe_swiglu(h.data_ptr(), code, _pitch(h), R, I, *pool, *out, _stream(stream)), "mm_moe_swiglu")
     return Gated(a, codes, sf, kept, kept_sf)
@@ -708,8 +719,8 @@ def swiglu_backward(d_a, kept, kept_sf, routing: Optional[Routing] = None, topk_
     kp = _whole(kept, "swiglu_backward", "kept", (R, 2, 32 * nb), torch.uint8)
     sp = _whole(kept_sf, "swiglu_backward", "kept_sf", (R, 2, nb), torch.uint8)
     pool = _pool("swiglu_backward", routing, topk_w, R)
-    d_h = _result(stream, (R, 2 * I), d_a.dtype, d_a.device)
-    d_w = None if topk_w is None else _result(stream, (routing.T, routing.K), torch.float32, d_a.device)
+    d_h = _result_rows(stream, R, 2 * I, d_a.dtype, d_a)
+    d_w = None if topk_w is None else _result_rows(stream, routing.T, routing.K, torch.float32, d_a)
     _check(lib().mm_moe_swiglu_backward(d_a.data_ptr(), code, _pitch(d_a), kp, sp, R, I, *pool, d_h.data_ptr(),
                                         None if d_w is None else d_w.data_ptr(), _stream(stream)),
            "mm_moe_swiglu_backward")
@@ -759,10 +770,14 @@ def weight_grad(d_y, codes, sf, C: int, routing: Optional[Routing] = None, by_to
     need = T if by_token else R
     if x_rows != need:
         _bad("weight_grad", f"x has {x_rows} rows, not {need}")
-    out = _result(stream, (N, C) if routing is None else (E, N, C), dtype, d_y.device)
-    scratch_bytes = _grad_scratch(d_y.data_ptr(), _pitch(d_y), R, N, sp, C, T, K, E, by_token)
-    scratch = _new(stream, scratch_bytes, torch.uint8, d_y.device) if scratch_bytes else None
-    _check(lib().mm_moe_weight_grad(d_y.data_ptr(), _pitch(d_y), R, N, cp, sp, C, T, K, E, block_m,
+    if routing is None:
+        out = _result_rows(stream, N, C, dtype, d_y)
+    else:
+        out = _result(stream, (E, N, C), dtype, d_y.device)
+    dp, pitch = d_y.data_ptr(), _pitch(d_y)
+    scratch_bytes = _grad_scratch(dp, pitch, R, N, sp, C, T, K, E, by_token)
+    scratch = _result_1d(stream, scratch_bytes, torch.uint8, d_y) if scratch_bytes else None
+    _check(lib().mm_moe_weight_grad(dp, pitch, R, N, cp, sp, C, T, K, E, block_m,
                                     None if routing is None else routing._cnt, src, blk, by_token, _DTYPES[dtype],
                                     out.data_ptr(), None if scratch is None else scratch.data_ptr(), scratch_bytes, 0, 0,
                                     _stream(stream)),
