@@ -42,8 +42,7 @@
 namespace mm {
 namespace {
 
-constexpr int kStages = 4;                       // of operands
-constexpr int kRaw = 6;                          // of codes
+constexpr int kRaw = 6;                          // stages of codes
 constexpr int kRowsPerStage = 64;
 constexpr int kTile = 256;                       // columns of d_y (M) and of x (N) of a pair; 128 of each in a CTA
 constexpr int kEpiWarps = 4, kConvertWarps = 12;
@@ -63,18 +62,23 @@ constexpr int kMostParts = 16;
 constexpr int kSplitPairs = 76;                  // CTA pairs that parts are made for; the scratch does not depend on the device
 constexpr int kBoxBytes = 32 * 128;              // 32 rows of 128 bytes of results
 
+// kDecoded: x comes in bf16. A stage then takes 1700 cycles from its copies' issue to their landing, and six of them are
+// what covers that (four: 800 cycles a stage); without the ring of codes there is room.
+template <bool kDecoded>
 struct Smem {
+  static constexpr int kStages = kDecoded ? 6 : 4;               // of operands
+  static constexpr int kBoxes = kDecoded ? 1 : 2;                // of results, of an epilogue warp
   static constexpr int a = 0;
   static constexpr int b = a + kStages * kHalfBytes;
   static constexpr int raw = b + kStages * kHalfBytes;
-  static constexpr int raw_sf = raw + kRaw * kRawBytes;
-  static constexpr int out = (raw_sf + kRaw * kRawSf + 1023) / 1024 * 1024;      // two boxes of results of each epilogue warp
-  static constexpr int bars = out + kEpiWarps * 2 * kBoxBytes;
+  static constexpr int raw_sf = raw + (kDecoded ? 0 : kRaw * kRawBytes);
+  static constexpr int out = (raw_sf + (kDecoded ? 0 : kRaw * kRawSf) + 1023) / 1024 * 1024;
+  static constexpr int bars = out + kEpiWarps * kBoxes * kBoxBytes;
   static constexpr int nbars = 4 * kStages + 2 * kRaw + 5;       // full_a, full_b, full, empty, raw_full, raw_empty, ...
   static constexpr int meta = bars + nbars * 8 + 16;             // blk_off[E + 1], cnt[E]
   static int total(int E) { return meta + (2 * E + 1) * 4 + 1024; }
+  static_assert(meta + (2 * kMaxE + 1) * 4 + 1024 <= 232448, "shared memory");
 };
-static_assert(Smem::meta + (2 * kMaxE + 1) * 4 + 1024 <= 232448, "shared memory");
 
 enum : int {
   kSiteEmpty = 181, kSiteFullA = 182, kSiteFull = 183, kSiteTmemEmpty = 184, kSiteTmemFull = 185, kSiteDrainCopies = 186,
@@ -263,10 +267,12 @@ struct Maps {
 template <typename T, bool kTma, bool kDecoded>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_grad_kernel(const __grid_constant__ Maps maps, const Args args) {
+  using Smem = Smem<kDecoded>;
+  constexpr int kStages = Smem::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + Smem::bars);   // this CTA's d_y has landed
-  uint64_t* full_b = full_a + kStages;           // this CTA's x has been decoded
+  uint64_t* full_b = full_a + kStages;           // this CTA's x has been decoded, or has landed in bf16
   uint64_t* full = full_b + kStages;             // leader: both CTAs' operands are there
   uint64_t* empty = full + kStages;              // the stage's MMAs have completed
   uint64_t* raw_full = empty + kStages;          // codes and scales of a stage are there
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full_a[i], 1);
-      mbar_init(&full_b[i], kConvertWarps / kGroups);        // (not used where x comes in bf16)
+      mbar_init(&full_b[i], kDecoded ? 1 : kConvertWarps / kGroups);
       mbar_init(&full[i], 2);
       mbar_init(&empty[i], 1);
     }
@@ -318,9 +324,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // accumulators of a task's n stages
   auto segments = [](int n) { return sizeof(T) == 4 ? (n + kSegment - 1) / kSegment : 1; };
 
-  if (warp == kTmaWarp) {
-    // ------------------------------------------------------------------ d_y (and x in bf16) by TMA
+  if (warp == kTmaWarp || (kDecoded && warp == kCodesWarp)) {
+    // ------------------------------------------------------------------ d_y by TMA, and x in bf16 by another warp: a copy
+    // takes its thread 150 cycles
     if (lane == 0) {
+      const bool is_x = kDecoded && warp == kCodesWarp;
+      const CUtensorMap* map = is_x ? &maps.codes : &maps.d_y;
+      uint64_t* landed = is_x ? full_b : full_a;
+      uint8_t* to = smem + (is_x ? Smem::b : Smem::a);
       const uint64_t pol = policy_evict_normal();
       Cursor at(first, stride, ntasks);
       Ring<kStages> ring;
@@ -328,21 +339,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (at.next(args, s_blk, s_cnt)) {
         const int s = ring.s;
         if (*s_abort || !mbar_wait(&empty[s], ring.phase ^ 1, st, s_abort, kSiteEmpty)) break;
-        mbar_arrive_expect_tx(&full_a[s], kDecoded ? 2 * kHalfBytes : kHalfBytes);
-        const int row = at.t.row0 + at.t.ks * kRowsPerStage, half = static_cast<int>(rank) * 128;
-        auto load = [&](uint8_t* d, const CUtensorMap* m, int c) {
-          tma_load_2d(d, m, &full_a[s], c, row, pol);
-          tma_load_2d(d + kChunkBytes, m, &full_a[s], c + 64, row, pol);
-        };
-        load(smem + Smem::a + s * kHalfBytes, &maps.d_y, at.t.n0 + half);
-        if (kDecoded) load(smem + Smem::b + s * kHalfBytes, &maps.codes, at.t.c0 + half);
+        mbar_arrive_expect_tx(&landed[s], kHalfBytes);
+        const int row = at.t.row0 + at.t.ks * kRowsPerStage;
+        const int col = (is_x ? at.t.c0 : at.t.n0) + static_cast<int>(rank) * 128;
+        tma_load_2d(to + s * kHalfBytes, map, &landed[s], col, row, pol);
+        tma_load_2d(to + s * kHalfBytes + kChunkBytes, map, &landed[s], col + 64, row, pol);
         ring.step();
         ++steps;
       }
 #pragma unroll 1
       for (int s = 0; s < kStages && s < steps; ++s) {
         const uint32_t last = ((steps - 1 - s) / kStages) & 1;   // its last phase
-        mbar_drain(&full_a[s], last, st, s_abort, kSiteDrainCopies);
+        mbar_drain(&landed[s], last, st, s_abort, kSiteDrainCopies);
         // the leader's last commit to this CTA's barrier has arrived before the CTA leaves
         if (!*s_abort) mbar_drain(&empty[s], last, st, s_abort, kSiteDrainEmpty);
       }
@@ -407,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (kDecoded && (warp == kCodesWarp || warp >= kConvert0)) {
-    // x comes in bf16
+  } else if (kDecoded && warp >= kConvert0) {
+    // nothing to decode
   } else if (warp == kCodesWarp) {
     // ------------------------------------------------------------------ codes by TMA, scales by loads
     const uint64_t pol = policy_evict_normal();
@@ -503,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       live = at.next(args, s_blk, s_cnt);
       if (!live && args.unreachable) break;
       if (!mbar_wait_warp(&full_a[s], ring.phase, st, s_abort, kSiteFullA) ||
-          (!kDecoded && !mbar_wait_warp(&full_b[s], ring.phase, st, s_abort, kSiteFullB)))
+          !mbar_wait_warp(&full_b[s], ring.phase, st, s_abort, kSiteFullB))
         break;
       if (rows < kRowsPerStage && (rows & 15)) {
         // the sum ends inside an MMA: whatever d_y's rows behind it hold becomes zero
@@ -530,8 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = t.n0 + static_cast<int>(rank) * 128 + quad * 32;
       const int64_t row = static_cast<int64_t>(t.slab) * args.N + n0;
       const int rows = args.N - n0;
-      const int nks = t.end - t.ks;
-      if (nks == 0) {                            // an expert without rows, or without any for this part
+      const int nks = t.end - t.ks;              // 0: an expert without rows, or without any for this part
+      if (!kTma && nks == 0) {
         for (int r = 0; r < 32 && r < rows; ++r) {
           T* p = reinterpret_cast<T*>(args.out + (row + r) * args.out_pitch);
           for (int c = t.c0 + half + lane; c < min(args.C, t.c0 + half + kShare); c += 32) p[c] = from_float<T>(0.f);
@@ -539,11 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       bool ok = true;
-      for (int seg = 0; seg < segments(nks) && ok; ++seg, ++it) {
+      for (int seg = 0; seg < max(segments(nks), 1) && ok; ++seg) {
         const int buf = it & 1;
-        ok = mbar_wait_warp(&tfull[buf], (it >> 1) & 1, st, s_abort, kSiteTmemFull);
+        ok = nks == 0 || mbar_wait_warp(&tfull[buf], (it >> 1) & 1, st, s_abort, kSiteTmemFull);
         if (!ok) break;
         tc_fence_after();
+        it += nks != 0;
         auto release = [&] {
           tc_fence_before();
           __syncwarp();
@@ -556,7 +565,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < kShare; c += kBox) {
             uint32_t w[32];
-            if constexpr (sizeof(T) == 4) {
+            if (nks == 0) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) w[j] = 0;
+            } else if constexpr (sizeof(T) == 4) {
               tmem_ld_32x32b_x32(src0 + c, w);
               tmem_ld_wait();
             } else {
@@ -569,12 +581,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 16; ++j) w[16 * h + j] = pack2<T>(v[2 * j], v[2 * j + 1]);
               }
             }
-            if (c + kBox == kShare) release();
+            if (nks != 0 && c + kBox == kShare) release();
             const int col = t.c0 + half + c;
             if (rows <= 0 || col >= args.C) continue;
-            uint8_t* box = smem + Smem::out + (warp * 2 + (box_turn & 1)) * kBoxBytes;
+            uint8_t* box = smem + Smem::out + (warp * Smem::kBoxes + box_turn % Smem::kBoxes) * kBoxBytes;
             ++box_turn;
-            if (lane == 0) tma_store_read<1>();  // the box before the last one's is free
+            if (lane == 0) tma_store_read<Smem::kBoxes - 1>();     // its last results have left it
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -736,15 +748,15 @@ cudaError_t launch(const Args& a, Maps& maps, cudaStream_t s) {
   }
   auto kernel = tma ? weight_grad_kernel<T, true, kDecoded> : weight_grad_kernel<T, false, kDecoded>;
   const void* fn = reinterpret_cast<const void*>(kernel);
-  if (cudaError_t e = configure_kernel(fn, 0, Smem::total(kMaxE))) return e;
+  if (cudaError_t e = configure_kernel(fn, 0, Smem<kDecoded>::total(kMaxE))) return e;
   int most = 0;
-  if (cudaError_t e = max_pair_clusters(fn, kThreads, Smem::total(kMaxE), &most)) return e;
+  if (cudaError_t e = max_pair_clusters(fn, kThreads, Smem<kDecoded>::total(kMaxE), &most)) return e;
   if (most < 1) return cudaErrorInvalidConfiguration;
   const int pairs = a.tasks * a.parts;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (pairs < most ? pairs : most)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Smem::total(a.cnt ? a.E : 0);
+  cfg.dynamicSmemBytes = Smem<kDecoded>::total(a.cnt ? a.E : 0);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -85,6 +85,21 @@ def test_routed_decoded_first(ops, by_token):
     check(ops, d_y.bfloat16(), x, r, by_token)
 
 
+@pytest.mark.parametrize("N,C", [(1024, 2560), (1024, 2561), (2048, 1537)])
+def test_long_sums_of_many_tiles(ops, N, C):
+    """33 stages in one task: fp32 results are sums of three accumulators."""
+    check(ops, whole(N, 2100, N).bfloat16(), whole(C, 2100, C))
+
+
+def test_many_experts_without_rows(ops):
+    r = ops.sort_tokens(torch.tensor([[5], [200], [5]], dtype=torch.int32, device="cuda"), 256)
+    for C in (520, 519):
+        got = check(ops, whole(1, r.rows, 300).bfloat16(), whole(2, 3, C), r, True)
+        dead = torch.ones(256, dtype=torch.bool, device="cuda")
+        dead[[5, 200]] = False
+        assert not got[dead].any() and got[5].any() and got[200].any()
+
+
 def test_dense_random_values(ops):
     """Scales of every size, sums of 20000 rows."""
     x = randn(1, 20000, 96) * torch.exp2(torch.arange(96).remainder(17) - 8.0)
