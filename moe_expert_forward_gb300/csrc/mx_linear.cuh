@@ -122,9 +122,7 @@ __device__ __forceinline__ void transpose32(uint32_t (&w)[32], int lane) {
 // 128-byte lines of 8 rows instead of 32 bytes of 32 rows (8192x7168x4096: 87 us, 90 without).
 // Otherwise the warp transposes 32 words and stores one row at a time, consecutive lanes consecutive words, as words
 // where rows are 4-byte aligned (8192x4096x4095 bf16: 309 us with a row per lane).
-//
-// kAdd (fp32): added to what is there, which the same lane stored.
-template <typename T, int kCols, bool kLines, bool kAdd = false, typename F>
+template <typename T, int kCols, bool kLines, typename F>
 __device__ __forceinline__ void store_accumulator(uint32_t col, char* out, int64_t pitch, int rows, int cols,
                                                   int lane, F release) {
   // 64 columns as 32 words of two 16-bit elements
@@ -206,18 +204,7 @@ __device__ __forceinline__ void store_accumulator(uint32_t col, char* out, int64
         if (lane < rows) {
           float* p = reinterpret_cast<float*>(out + lane * pitch) + c;
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if constexpr (kAdd)
-#pragma unroll
-              for (int j = 0; j < 8; j += 4) {
-                const float4 o = *reinterpret_cast<const float4*>(p + i + j);
-                v[i + j] = __float_as_uint(__uint_as_float(v[i + j]) + o.x);
-                v[i + j + 1] = __float_as_uint(__uint_as_float(v[i + j + 1]) + o.y);
-                v[i + j + 2] = __float_as_uint(__uint_as_float(v[i + j + 2]) + o.z);
-                v[i + j + 3] = __float_as_uint(__uint_as_float(v[i + j + 3]) + o.w);
-              }
-            st_global_v8(p + i, v + i);
-          }
+          for (int i = 0; i < 32; i += 8) st_global_v8(p + i, v + i);
         }
       } else if (cols > c) {
         transpose32(v, lane);
@@ -225,10 +212,7 @@ __device__ __forceinline__ void store_accumulator(uint32_t col, char* out, int64
         if (c + lane < cols) {
 #pragma unroll
           for (int r = 0; r < 32; ++r, q += pitch)
-            if (r < rows) {
-              float* p = reinterpret_cast<float*>(q);
-              *p = kAdd ? *p + __uint_as_float(v[r]) : __uint_as_float(v[r]);
-            }
+            if (r < rows) *reinterpret_cast<uint32_t*>(q) = v[r];
         }
       }
     }

@@ -529,7 +529,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    constexpr int kCols = 64;                    // columns of a warp at a time
     constexpr int kShare = kTile / (kEpiWarps / 4);              // columns of a warp
     const int quad = warp & 3, half = (warp >> 2) * kShare;
     int it = 0, box_turn = 0;
@@ -539,13 +538,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t row = static_cast<int64_t>(t.slab) * args.N + n0;
       const int rows = args.N - n0;
       const int nks = t.end - t.ks;              // 0: an expert without rows, or without any for this part
-      if (!kTma && nks == 0) {
-        for (int r = 0; r < 32 && r < rows; ++r) {
-          T* p = reinterpret_cast<T*>(args.out + (row + r) * args.out_pitch);
-          for (int c = t.c0 + half + lane; c < min(args.C, t.c0 + half + kShare); c += 32) p[c] = from_float<T>(0.f);
-        }
-        continue;
-      }
       bool ok = true;
       for (int seg = 0; seg < max(segments(nks), 1) && ok; ++seg) {
         const int buf = it & 1;
@@ -559,58 +551,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_leader(map_shared(&tempty[buf], 0));
         };
         const uint32_t src0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTile + half;
-        if constexpr (kTma) {
-          constexpr int kBox = 128 / sizeof(T);  // columns of a box
-          if (seg > 0 && lane == 0) tma_stored();          // what the boxes are added to
+        constexpr int kBox = 128 / sizeof(T);    // columns of a box
+        if (kTma && seg > 0 && lane == 0) tma_stored();    // what the boxes are added to
 #pragma unroll 1
-          for (int c = 0; c < kShare; c += kBox) {
-            uint32_t w[32];
-            if (nks == 0) {
+        for (int c = 0; c < kShare; c += kBox) {
+          uint32_t w[32];
+          if (nks == 0) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) w[j] = 0;
-            } else if constexpr (sizeof(T) == 4) {
-              tmem_ld_32x32b_x32(src0 + c, w);
+            for (int j = 0; j < 32; ++j) w[j] = 0;
+          } else if constexpr (sizeof(T) == 4) {
+            tmem_ld_32x32b_x32(src0 + c, w);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(src0 + c + 32 * h, v);
               tmem_ld_wait();
-            } else {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(src0 + c + 32 * h, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) w[16 * h + j] = pack2<T>(v[2 * j], v[2 * j + 1]);
-              }
+              for (int j = 0; j < 16; ++j) w[16 * h + j] = pack2<T>(v[2 * j], v[2 * j + 1]);
             }
-            if (nks != 0 && c + kBox == kShare) release();
-            const int col = t.c0 + half + c;
-            if (rows <= 0 || col >= args.C) continue;
-            uint8_t* box = smem + Smem::out + (warp * Smem::kBoxes + box_turn % Smem::kBoxes) * kBoxBytes;
-            ++box_turn;
-            if (lane == 0) tma_store_read<Smem::kBoxes - 1>();     // its last results have left it
-            __syncwarp();
+          }
+          if (nks != 0 && c + kBox == kShare) release();
+          const int col = t.c0 + half + c;
+          if (rows <= 0 || col >= args.C) continue;
+          uint8_t* box = smem + Smem::out + (warp * Smem::kBoxes + box_turn % Smem::kBoxes) * kBoxBytes;
+          ++box_turn;
+          if (kTma && lane == 0) tma_store_read<Smem::kBoxes - 1>();       // its last results have left it
+          __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          if constexpr (kTma) {
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
               if (sizeof(T) == 4 && seg > 0) tma_store_box<true>(&maps.out, box, col, n0, t.slab);
               else tma_store_box<false>(&maps.out, box, col, n0, t.slab);
             }
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < kShare; c += kCols) {
-            const int col = t.c0 + half + c;
-            char* dst = args.out + row * args.out_pitch + col * static_cast<int64_t>(sizeof(T));
-            auto last = [&] {
-              if (c + kCols == kShare) release();
-            };
-            if (sizeof(T) == 4 && seg > 0)
-              store_accumulator<T, kCols, false, sizeof(T) == 4>(src0 + c, dst, args.out_pitch, rows, args.C - col, lane, last);
-            else
-              store_accumulator<T, kCols, false>(src0 + c, dst, args.out_pitch, rows, args.C - col, lane, last);
+          } else {
+            // row by row, consecutive lanes consecutive words
+            __syncwarp();
+            const int left = args.C - col - lane * (4 / static_cast<int>(sizeof(T)));      // columns from this lane's on
+            char* q = args.out + row * args.out_pitch + col * static_cast<int64_t>(sizeof(T)) + lane * 4;
+#pragma unroll 4
+            for (int r = 0; r < 32; ++r, q += args.out_pitch) {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+              if (r >= rows || left <= 0) continue;
+              if constexpr (sizeof(T) == 4) {
+                float* p = reinterpret_cast<float*>(q);
+                *p = seg > 0 ? *p + __uint_as_float(v) : __uint_as_float(v);
+              } else if (left >= 2 && (reinterpret_cast<uintptr_t>(q) & 3) == 0) {
+                *reinterpret_cast<uint32_t*>(q) = v;
+              } else {
+                reinterpret_cast<uint16_t*>(q)[0] = static_cast<uint16_t>(v);
+                if (left >= 2) reinterpret_cast<uint16_t*>(q)[1] = static_cast<uint16_t>(v >> 16);
+              }
+            }
+            __syncwarp();
           }
         }
       }
