@@ -625,10 +625,10 @@ int mm_moe_swiglu_backward(const void* d_a, int dtype, int64_t d_stride, const v
  *          Other rows are not part of any sum, whatever they hold.
  *   out    [E, N, C] (dense: [N, C]) contiguous of `dtype` (fp32 or bf16), fully overwritten;
  *          zero for an expert without rows
- *   scratch  mm_moe_weight_grad_scratch_size bytes, 16-byte aligned: with by_token x's rows
- *          at their pool rows, and copies of d_y and of sf where their rows do not start on 16-byte
- *          and 4-byte boundaries, and partial sums where few columns share many rows (K = E = 0:
- *          dense); often none (0 bytes, null allowed)
+ *   scratch  mm_moe_weight_grad_scratch_size bytes, 32-byte aligned: x in bf16 with by_token or
+ *          N > 1024, copies of d_y and of sf where their rows do not start on 16-byte and 4-byte
+ *          boundaries, and partial sums where few columns share many rows (K = E = 0: dense); none
+ *          otherwise (0 bytes, null allowed)
  * A device wait past timeout_ms (0: 2000) leaves out undefined and is reported by
  * mm_moe_ops_status.  debug_flags: 0; bit 0 leaves one stage of each CTA unloaded, so that its
  * wait runs out. */
@@ -640,9 +640,9 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
                        size_t scratch_bytes, unsigned timeout_ms, int debug_flags, void* stream);
 
 /* Waits for `stream` and returns MM_MOE_ERR_TIMEOUT if a device wait of mm_moe_mx_product,
- * mm_moe_mx_linear, mm_moe_weight_grad, mm_moe_rms_norm or its gradients has run out on the current device, on any stream, since the last
- * time this returned it; else MM_MOE_OK (calls on other streams that are still running
- * are not waited for).  `where` (may be null) gets the site of the first
+ * mm_moe_mx_linear, mm_moe_weight_grad, mm_moe_rms_norm or its gradients has run out on
+ * the current device, on any stream, since the last time this returned it; else MM_MOE_OK
+ * (calls on other streams that are still running are not waited for).  `where` (may be null) gets the site of the first
  * such wait.  The record is the library's: it outlives the calls' status words and
  * workspaces.  Not to be called while `stream` is being captured. */
 int mm_moe_ops_status(void* stream, int* where);

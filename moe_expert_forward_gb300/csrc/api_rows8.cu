@@ -165,7 +165,7 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
     return MM_MOE_ERR_INVALID_ARG;
   const int64_t terms = terms_of(rows, T, K, cnt ? E : 0);
   const size_t need = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0, E, terms);
-  if (need && (!scratch || !aligned(scratch, 16))) return MM_MOE_ERR_INVALID_ARG;
+  if (need && (!scratch || !aligned(scratch, 32))) return MM_MOE_ERR_INVALID_ARG;
   if (scratch_bytes < need) return MM_MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -24,10 +24,10 @@
 // accumulator were 3.7e-6 off (rounding to nearest: 3.6e-7).
 //
 // Codes come by TMA too, their scales by 4-byte asynchronous copies, into a ring of their own: converters that load
-// for themselves keep the SM's loads in flight at their limit, and wait for it (1000 cycles a stage and more).  Where
-// x's rows are tokens, a kernel before this one copies them to their pool rows (TMA's own gather, four rows an
-// instruction, took 1900 cycles a stage).  Rows of d_y, or of scales, that start on no 16-byte, or 4-byte, boundary are
-// copied first too.  With many tiles of N that kernel decodes x instead, and the product takes both operands by TMA.
+// for themselves keep the SM's loads in flight at their limit, and wait for it (1000 cycles a stage and more).  With
+// many tiles of N, and where x's rows are tokens (TMA's own gather, four rows an instruction, took 1900 cycles a stage), a
+// kernel before this one decodes x into bf16 rows, and the product takes both operands by TMA.  Rows of d_y, or of scales,
+// that start on no 16-byte, or 4-byte, boundary are copied first.
 //
 // The loops of all roles have to fit the instruction cache together: none is unrolled over its ring (unrolled, a third
 // of the fetches missed and a stage took 1500 cycles).
@@ -48,7 +48,8 @@ constexpr int kTile = 256;                       // columns of d_y (M) and of x 
 constexpr int kEpiWarps = 4, kConvertWarps = 12;
 constexpr int kMmaWarp = kEpiWarps, kTmaWarp = kMmaWarp + 1, kCodesWarp = kTmaWarp + 1, kHandWarp = kCodesWarp + 1,
               kConvert0 = kHandWarp + 1;
-constexpr int kThreads = 32 * (kConvert0 + kConvertWarps);
+template <bool kDecoded>
+constexpr int kThreads = 32 * (kConvert0 + (kDecoded ? 0 : kConvertWarps));
 constexpr int kAtom = 1024;                      // 8 rows of 64 columns
 constexpr int kChunkBytes = kRowsPerStage * 128; // 64 columns of a stage
 constexpr int kHalfBytes = 2 * kChunkBytes;      // 128 columns: one CTA's share of an operand
@@ -76,8 +77,8 @@ struct Smem {
   static constexpr int bars = out + kEpiWarps * kBoxes * kBoxBytes;
   static constexpr int nbars = 4 * kStages + 2 * kRaw + 5;       // full_a, full_b, full, empty, raw_full, raw_empty, ...
   static constexpr int meta = bars + nbars * 8 + 16;             // blk_off[E + 1], cnt[E]
-  static int total(int E) { return meta + (2 * E + 1) * 4 + 1024; }
-  static_assert(meta + (2 * kMaxE + 1) * 4 + 1024 <= 232448, "shared memory");
+  __host__ __device__ static constexpr int total(int E) { return meta + (2 * E + 1) * 4 + 1024; }
+  static_assert(bars % 8 == 0 && meta + (2 * kMaxE + 1) * 4 + 1024 <= 232448, "shared memory");
 };
 
 enum : int {
@@ -197,6 +198,18 @@ template <int kLeft>
 __device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory"); }
 __device__ __forceinline__ void tma_stored() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// Waits for tensor memory loads; the registers that they fill are the wait's results, so that no use moves before it.
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
+
 // One lane of a whole warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -265,7 +278,7 @@ struct Maps {
 
 // kTma: out's rows are 16-byte aligned, and results leave by TMA. kDecoded: x comes in bf16.
 template <typename T, bool kTma, bool kDecoded>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<kDecoded>, 1)
     weight_grad_kernel(const __grid_constant__ Maps maps, const Args args) {
   using Smem = Smem<kDecoded>;
   constexpr int kStages = Smem::kStages;
@@ -311,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kMmaWarp) tmem_alloc_pair(s_tmem, 512);
   if (args.cnt) {
-    for (int i = threadIdx.x; i <= args.E; i += kThreads) s_blk[i] = args.blk_off[i];
-    for (int i = threadIdx.x; i < args.E; i += kThreads) s_cnt[i] = args.cnt[i];
+    for (int i = threadIdx.x; i <= args.E; i += blockDim.x) s_blk[i] = args.blk_off[i];
+    for (int i = threadIdx.x; i < args.E; i += blockDim.x) s_cnt[i] = args.cnt[i];
   }
   tc_fence_before();
   __syncthreads();
@@ -415,8 +428,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (kDecoded && warp >= kConvert0) {
-    // nothing to decode
   } else if (warp == kCodesWarp) {
     // ------------------------------------------------------------------ codes by TMA, scales by loads
     const uint64_t pol = policy_evict_normal();
@@ -553,26 +564,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t src0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTile + half;
         constexpr int kBox = 128 / sizeof(T);    // columns of a box
         if (kTma && seg > 0 && lane == 0) tma_stored();    // what the boxes are added to
+        uint32_t v[kBox];                        // a box's accumulators (kDecoded, which has the registers for it: the
+                                                 // next one's are on their way while one is stored)
+        auto fetch = [&](int c) {
+#pragma unroll
+          for (int h = 0; h < kBox; h += 32) tmem_ld_32x32b_x32(src0 + c + h, *reinterpret_cast<uint32_t(*)[32]>(v + h));
+        };
+        if (kDecoded && nks != 0) fetch(0);
 #pragma unroll 1
         for (int c = 0; c < kShare; c += kBox) {
           uint32_t w[32];
           if (nks == 0) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) w[j] = 0;
-          } else if constexpr (sizeof(T) == 4) {
-            tmem_ld_32x32b_x32(src0 + c, w);
-            tmem_ld_wait();
           } else {
+            if (!kDecoded) fetch(c);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t v[32];
-              tmem_ld_32x32b_x32(src0 + c + 32 * h, v);
-              tmem_ld_wait();
+            for (int h = 0; h < kBox; h += 32) tmem_loaded(*reinterpret_cast<uint32_t(*)[32]>(v + h));
 #pragma unroll
-              for (int j = 0; j < 16; ++j) w[16 * h + j] = pack2<T>(v[2 * j], v[2 * j + 1]);
-            }
+            for (int j = 0; j < 32; ++j)
+              w[j] = sizeof(T) == 4 ? v[j] : pack2<T>(v[(2 * j) % kBox], v[(2 * j + 1) % kBox]);
+            if (c + kBox == kShare) release();
+            else if (kDecoded) fetch(c + kBox);
           }
-          if (nks != 0 && c + kBox == kShare) release();
           const int col = t.c0 + half + c;
           if (rows <= 0 || col >= args.C) continue;
           uint8_t* box = smem + Smem::out + (warp * Smem::kBoxes + box_turn % Smem::kBoxes) * kBoxBytes;
@@ -627,26 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Rows of x in token order into the pool rows that hold a pair of theirs, a warp a row: `pieces` of 16 bytes of codes, and
-// the scales as whole words.
 constexpr int kCopyThreads = 256;
-__global__ void __launch_bounds__(kCopyThreads)
-    gather_rows_kernel(const uint4* __restrict__ codes, int pieces, const uint8_t* __restrict__ sf, int blocks,
-                       const int32_t* __restrict__ src, const int32_t* __restrict__ blk_off, int E, int block_m, int K,
-                       int64_t rows, uint4* __restrict__ out, uint32_t* __restrict__ out_sf) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * (kCopyThreads / 32) + (threadIdx.x >> 5);
-  if (r >= rows || r >= static_cast<int64_t>(__ldg(blk_off + E)) * block_m) return;
-  const int pair = __ldg(src + r);
-  if (pair < 0) return;                          // padding: no sum reads it
-  const int64_t t = pair / K;
-  const int words = (blocks + 3) / 4;
-  for (int i = lane; i < words; i += 32)
-    out_sf[r * words + i] = load16_any(sf + t * blocks + 4 * i, min(4, blocks - 4 * i)).x;
-#pragma unroll 4
-  for (int i = lane; i < pieces; i += 32) out[r * pieces + i] = __ldg(codes + t * pieces + i);
-}
-
 // The rows of x that the sums take in bf16, a warp a row: a pool row's token's (by_token), or its own; zeros where it holds
 // no pair (its 16 rows may be an MMA's). Without a routing every row is its own.
 __global__ void __launch_bounds__(kCopyThreads)
@@ -749,12 +744,12 @@ cudaError_t launch(const Args& a, Maps& maps, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kernel);
   if (cudaError_t e = configure_kernel(fn, 0, Smem<kDecoded>::total(kMaxE))) return e;
   int most = 0;
-  if (cudaError_t e = max_pair_clusters(fn, kThreads, Smem<kDecoded>::total(kMaxE), &most)) return e;
+  if (cudaError_t e = max_pair_clusters(fn, kThreads<kDecoded>, Smem<kDecoded>::total(kMaxE), &most)) return e;
   if (most < 1) return cudaErrorInvalidConfiguration;
   const int pairs = a.tasks * a.parts;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (pairs < most ? pairs : most)));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<kDecoded>);
   cfg.dynamicSmemBytes = Smem<kDecoded>::total(a.cnt ? a.E : 0);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -773,25 +768,27 @@ int parts_of(int64_t tasks, int64_t terms) {
 }
 int sums_pitch(int C) { return (C + 3) / 4 * 4; }
 
-// Whether x is decoded into bf16 rows before the product, and not by its converters: with many tiles of N each of which
-// would decode the same codes. 8192 rows, C = 4096, first / by converters, us: N 512 67 / 51, 1024 77 / 66, 2048 121 / 120,
-// 4096 215 / 239; 64 experts of 384 rows, 4096 x 4096, 768 / 872.
-constexpr int kDecodeTiles = 8;
-bool decodes_first(int N) { return N > (kDecodeTiles - 1) * kTile; }
+// Whether x is decoded into bf16 rows before the product, and not by its converters: where more than 4 tiles of N would
+// decode the same codes (8192 rows, C = 4096, first / by converters, us: N 256 61 / 42, 512 63 / 50, 1024 70 / 70, 1280
+// 105 / 120, 1792 105 / 124, 4096 184 / 249), and where x's rows are tokens, which some kernel has to bring to their pool
+// rows anyhow (copied as codes and left to the converters: 8 experts of 1024 rows, N 256 45 us for 48, 512 63 for 59; 64 of
+// 384, C = 2048, N 256 123 for 72, 1408 215 for 142).
+constexpr int kDecodeTiles = 4;
+bool decodes_first(int N, bool by_token) { return by_token || N > kDecodeTiles * kTile; }
 
-// What a call keeps in its scratch: copies of d_y, of the codes and of the scales, and parts' sums. Bytes, 0: none.
+// What a call keeps in its scratch, in this order: x in bf16 (rows of 64 bytes' multiples, stored 32 bytes at a time), a
+// copy of d_y, one of the scales, and parts' sums. Bytes, 0: none.
 struct Copies {
-  size_t d_y, codes, sf, sums;                   // (codes: x in bf16 where it is decoded first)
+  size_t x, d_y, sf, sums;
 };
 Copies copies_of(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C, bool by_token, int E,
                  int64_t terms) {
   const int blocks = blocks8(C, MM_MOE_VARIANT_MX);
   Copies c{0, 0, 0, 0};
   if (reinterpret_cast<uintptr_t>(d_y) % 16 || d_stride % 8) c.d_y = static_cast<size_t>(rows) * ((N + 7) / 8) * 16;
-  if (decodes_first(N)) c.codes = static_cast<size_t>(rows) * blocks * kMxBlock * 2;
-  else if (by_token) c.codes = static_cast<size_t>(rows) * blocks * kMxBlock;
-  if (decodes_first(N)) c.sf = 0;
-  else if (by_token || reinterpret_cast<uintptr_t>(sf) % 4 || blocks % 4) c.sf = (static_cast<size_t>(rows) * ((blocks + 3) / 4) * 4 + 15) / 16 * 16;
+  if (decodes_first(N, by_token)) c.x = static_cast<size_t>(rows) * blocks * kMxBlock * 2;
+  else if (reinterpret_cast<uintptr_t>(sf) % 4 || blocks % 4)
+    c.sf = (static_cast<size_t>(rows) * ((blocks + 3) / 4) * 4 + 15) / 16 * 16;
   const int parts = parts_of(weight_grad_tasks(E, N, C), terms);
   if (parts > 1) c.sums = static_cast<size_t>(parts) * E * N * sums_pitch(C) * sizeof(float);
   return c;
@@ -806,7 +803,7 @@ int64_t weight_grad_tasks(int E, int N, int C) {
 size_t weight_grad_scratch_bytes(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C,
                                  bool by_token, int E, int64_t terms) {
   const Copies c = copies_of(d_y, d_stride, rows, N, sf, C, by_token, E, terms);
-  return c.d_y + c.codes + c.sf + c.sums;
+  return c.x + c.d_y + c.sf + c.sums;
 }
 
 cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
@@ -824,32 +821,27 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
   a.unreachable = p.unreachable;
   a.timeout_ns = p.timeout_ns;
   const int blocks = blocks8(p.C, MM_MOE_VARIANT_MX);
-  const bool by_token = p.by_token, decoded = decodes_first(p.N);
-  const Copies copies = copies_of(p.d_y, p.d_stride, p.rows, p.N, p.sf, p.C, by_token, p.E, p.terms);
+  const bool decoded = decodes_first(p.N, p.by_token);
+  const Copies copies = copies_of(p.d_y, p.d_stride, p.rows, p.N, p.sf, p.C, p.by_token, p.E, p.terms);
   const void *d_y = p.d_y, *codes = p.codes, *sf = p.sf;
   uint64_t pitch = static_cast<uint64_t>(p.d_stride) * 2;
   char* to = static_cast<char*>(p.scratch);
+  if (decoded) {
+    const unsigned per = kCopyThreads / 32, grid = static_cast<unsigned>((p.rows + per - 1) / per);
+    decode_rows_kernel<<<grid, kCopyThreads, 0, s>>>(reinterpret_cast<const uint4*>(p.codes), blocks * kMxBlock / 16, p.sf,
+                                                     blocks, p.src, p.blk_off, p.E, p.block_m, p.K, p.by_token, p.rows,
+                                                     reinterpret_cast<uint4*>(to));
+    if (cudaError_t e = cudaGetLastError()) return e;
+    codes = to;
+    to += copies.x;
+  }
   if (copies.d_y) {
     if (cudaError_t e = align_rows<uint4>(p.d_y, p.d_stride * 2, p.rows, p.N * 2, to, s)) return e;
     d_y = to;
     pitch = static_cast<uint64_t>((p.N + 7) / 8) * 16;
     to += copies.d_y;
   }
-  const unsigned per = kCopyThreads / 32, grid = static_cast<unsigned>((p.rows + per - 1) / per);
-  const uint4* x = reinterpret_cast<const uint4*>(p.codes);
-  const int pieces = blocks * kMxBlock / 16;
-  if (decoded)
-    decode_rows_kernel<<<grid, kCopyThreads, 0, s>>>(x, pieces, p.sf, blocks, p.src, p.blk_off, p.E, p.block_m, p.K, by_token,
-                                                     p.rows, reinterpret_cast<uint4*>(to));
-  else if (by_token)
-    gather_rows_kernel<<<grid, kCopyThreads, 0, s>>>(x, pieces, p.sf, blocks, p.src, p.blk_off, p.E, p.block_m, p.K, p.rows,
-                                                     reinterpret_cast<uint4*>(to),
-                                                     reinterpret_cast<uint32_t*>(to + copies.codes));
-  if (copies.codes) {
-    if (cudaError_t e = cudaGetLastError()) return e;
-    codes = to;
-    sf = to + copies.codes;
-  } else if (copies.sf) {
+  if (copies.sf) {
     if (cudaError_t e = align_rows<uint32_t>(p.sf, blocks, p.rows, blocks, to, s)) return e;
     sf = to;
   }
@@ -871,7 +863,7 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
   };
   if (a.parts == 1) return p.dtype == MM_MOE_DTYPE_F32 ? go(float{}) : go(__nv_bfloat16{});
   const int pitch_c = sums_pitch(p.C);
-  float* sums = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + copies.d_y + copies.codes + copies.sf);
+  float* sums = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + copies.x + copies.d_y + copies.sf);
   a.out = reinterpret_cast<char*>(sums);
   a.out_pitch = static_cast<int64_t>(pitch_c) * sizeof(float);
   if (cudaError_t e = go(float{})) return e;

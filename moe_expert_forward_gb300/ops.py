@@ -727,18 +727,17 @@ def swiglu_backward(d_a, kept, kept_sf, routing: Optional[Routing] = None, topk_
     return d_h, d_w
 
 
-GRAD_TILE, GRAD_STAGE, GRAD_PAIRS, GRAD_PARTS, GRAD_DECODE = 256, 64, 76, 16, 8     # mm_moe_weight_grad_scratch_size's rule
+GRAD_TILE, GRAD_STAGE, GRAD_PAIRS, GRAD_PARTS, GRAD_DECODE = 256, 64, 76, 16, 4     # mm_moe_weight_grad_scratch_size's rule
 
 
 def _grad_scratch(d_y: int, pitch: int, rows: int, N: int, sf: int, C: int, T: int, K: int, E: int, by_token: bool) -> int:
-    """x in bf16 for many tiles of N, else the tokens' rows at their pool rows; copies of rows that are not 16-byte, or of
-    scales that are not 4-byte, aligned; and partial sums (E = 0: dense)."""
+    """x in bf16 for tokens' rows or many tiles of N; copies of rows that are not 16-byte, or of scales that are not 4-byte,
+    aligned; and partial sums (E = 0: dense)."""
     blocks = -(-C // 32)
     n = 0 if d_y % 16 == 0 and pitch % 8 == 0 else rows * -(-N // 8) * 16
-    if N > (GRAD_DECODE - 1) * GRAD_TILE:
+    if by_token or N > GRAD_DECODE * GRAD_TILE:
         n += rows * 64 * blocks
-    elif by_token or sf % 4 or blocks % 4:
-        n += rows * 32 * blocks if by_token else 0
+    elif sf % 4 or blocks % 4:
         n += -(-rows * -(-blocks // 4) * 4 // 16) * 16
     tasks = max(E, 1) * -(-N // GRAD_TILE) * -(-C // GRAD_TILE)
     stages = -(-(T * K // E if E else rows) // GRAD_STAGE)

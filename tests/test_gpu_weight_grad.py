@@ -63,7 +63,7 @@ def test_dense_widths(ops, N, C):
     check(ops, whole(N, 150, N).bfloat16(), whole(C, 150, C))
 
 
-@pytest.mark.parametrize("rows,N,C", [(1, 1800, 40), (70, 2048, 96), (200, 1793, 300), (17, 2304, 33)])
+@pytest.mark.parametrize("rows,N,C", [(1, 1800, 40), (70, 2048, 96), (200, 1793, 300), (17, 2304, 33), (33, 1024, 64), (33, 1025, 64)])
 def test_dense_decoded_first(ops, rows, N, C):
     check(ops, whole(N, rows, N).bfloat16(), whole(C, rows, C))
 

@@ -95,7 +95,8 @@ def test_weight_grad(M):
     need = M.mm_moe_weight_grad_scratch_size(A, 65, n, 64, A, 64, 4, 2, 4, 0)
     assert need == 16 * 8 * n + 4 * n and M.mm_moe_weight_grad_scratch_size(A, 64, n, 64, A, 128, 4, 2, 4, 0) == 0
     assert g(ds=65, scr=A, n_scr=need - 1) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL
-    assert g(tok=1, scr=A, n_scr=(64 + 4) * n - 1) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL
+    assert g(tok=1, scr=A, n_scr=2 * 64 * n - 1) == M.MM_MOE_ERR_WORKSPACE_TOO_SMALL
+    assert g(tok=1, scr=A + 16, n_scr=2 * 64 * n) == M.MM_MOE_ERR_INVALID_ARG          # stored 32 bytes at a time
     # the router's gradient: 16 tiles, four parts of each
     assert M.mm_moe_weight_grad_scratch_size(A, 256, 8192, 256, A, 4096, 0, 0, 0, 0) == 4 * 256 * 4096 * 4
     for bad in ((A, 63, n, 64, A, 64, 4, 2, 4, 0), (A, 64, -1, 64, A, 64, 4, 2, 4, 0), (A, 64, n, 0, A, 64, 4, 2, 4, 0),
