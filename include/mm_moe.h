@@ -411,8 +411,9 @@ int mm_moe_ep_barrier_ranks(void* const* peer_flags, int N, uint32_t epoch, unsi
 
 /* ------------------------------------------------------------------------
  * Operators around the expert layer: the router's top-k, tokens sorted by
- * expert and back, 4-bit quantisation and product; then rows in 8 bits.  Each enqueues its kernels
- * on `stream`; none allocates or synchronises.  Element types of rows: */
+ * expert and back, 4-bit quantisation and product; then rows in 8 bits.  Each
+ * enqueues its kernels on `stream`; none allocates or synchronises.  Element
+ * types of rows: */
 #define MM_MOE_DTYPE_F32 0
 #define MM_MOE_DTYPE_BF16 1
 #define MM_MOE_DTYPE_F16 2
@@ -554,7 +555,7 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
  * A row's last block is filled up with zeros; codes round to nearest, ties to the even
  * code, and are 16-byte aligned.  A block with a NaN or an infinity gets zero codes and
  * a scale of NaN (MX: byte 255), and everything computed from it is NaN; codes 0x7F and
- * 0xFF do not occur. */
+ * 0xFF do not occur.  Results of these calls overlap no operand. */
 int mm_moe_rows_quantize(const void* x, int dtype, int64_t row_stride, int64_t R, int C, int variant, void* codes,
                          void* sf, void* stream);
 
@@ -573,7 +574,8 @@ int mm_moe_rows_dequantize(const void* codes, const void* sf, int64_t R, int C, 
  *   y            [T, H] contiguous of `dtype`, or null
  *   codes, sf    y in 8 bits of `variant` (from the fp32 y), or both null
  *   rstd         what the gradients take
- * eps >= 0; H of any size (up to 16384 elements a row is read once).  A device wait of 2 s
+ * eps >= 0; H of any size (up to 16384 elements a row is read once).  The sum of squares is
+ * fp32: where it passes fp32's range rstd is 0.  A device wait of 2 s
  * that runs out (many long rows come by copies that are waited for) leaves the results
  * undefined and is reported by mm_moe_ops_status; the gradients' too. */
 int mm_moe_rms_norm(const void* x, int dtype, int64_t x_stride, const void* residual, int64_t residual_stride,
@@ -642,8 +644,8 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
 /* Waits for `stream` and returns MM_MOE_ERR_TIMEOUT if a device wait of mm_moe_mx_product,
  * mm_moe_mx_linear, mm_moe_weight_grad, mm_moe_rms_norm or its gradients has run out on
  * the current device, on any stream, since the last time this returned it; else MM_MOE_OK
- * (calls on other streams that are still running are not waited for).  `where` (may be null) gets the site of the first
- * such wait.  The record is the library's: it outlives the calls' status words and
+ * (calls on other streams that are still running are not waited for).  `where` (may be
+ * null) gets the site of the first such wait.  The record is the library's: it outlives the calls' status words and
  * workspaces.  Not to be called while `stream` is being captured. */
 int mm_moe_ops_status(void* stream, int* where);
 

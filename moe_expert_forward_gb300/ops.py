@@ -785,6 +785,6 @@ def weight_grad(d_y, codes, sf, C: int, routing: Optional[Routing] = None, by_to
 
 
 def sync_status(stream=None):
-    """Waits for `stream`; (code, where) of the first device wait of a product (weight_grad among them) that ran out on this device since the
-    last report, on any stream: MM_MOE_ERR_TIMEOUT and its site, or (0, 0)."""
+    """Waits for `stream`; (code, where) of the first device wait of a product, weight_grad, rms_norm or its gradients that
+    ran out on this device since the last report, on any stream: MM_MOE_ERR_TIMEOUT and its site, or (0, 0)."""
     return mm_moe_ops_status(_stream(stream))

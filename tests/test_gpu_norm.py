@@ -99,7 +99,7 @@ def test_tokens(ops, T, H):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("H", [512, 1024, 2064, 4096, 4112, 7168, 8192, 8208, 16384])
+@pytest.mark.parametrize("H", [512, 1024, 2032, 2048, 2064, 3584, 4096, 4112, 7168, 8192, 8208, 16384])
 @pytest.mark.parametrize("T", [305, 700])
 def test_many_long_rows(ops, T, H, dt):
     """Rows that come by copies into a ring, with and without a residual, weights of both types."""
