@@ -4,6 +4,8 @@
 // Bound by memory both ways: an element is read in its own type and written as one
 // byte and a 32nd, or the reverse.  A lane takes 16 elements, and a warp's lanes
 // follow each other through the rows.
+//
+// Measured: 65536x4096 bf16 into "mx" 124 us and back 118 (813 MB, 6.6 and 6.9 TB/s: 97 and 102 % of the copy rate).
 #include "rows8.cuh"
 
 namespace mm {
@@ -11,7 +13,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 2;            // groups of 16 elements a thread has in flight
 
 // The position of a thread in [rows][groups of 16], stepped by a fixed number of groups.
 struct Walk {
@@ -30,7 +31,8 @@ struct Walk {
 
 // step = gridDim * kThreads groups = d_row rows and d_group groups. A row's groups are those its codes fill, so that
 // blocks lie inside a warp.
-template <typename T, bool kVec>
+// kBatch: groups a thread has in flight.
+template <typename T, bool kVec, int kBatch>
 __global__ void __launch_bounds__(kThreads)
     quantize8_kernel(const T* __restrict__ x, int64_t stride, int64_t R, int C, const Out8 out, int d_row, int d_group) {
   Walk at(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, out.groups);
@@ -63,36 +65,26 @@ __global__ void __launch_bounds__(kThreads)
                        int d_group) {
   __shared__ alignas(16) T s_run[kVec ? 1 : kWarps * 512];
   T* run = kVec ? s_run : s_run + (threadIdx.x >> 5) * 512;
-  Walk at(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, groups);
-  while (__any_sync(0xffffffffu, at.r < R)) {
-    uint4 c[kBatch];
-    float s[kBatch];
-    T* d[kBatch];
-    int n[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      d[u] = out;
-      n[u] = 0;
-      c[u] = make_uint4(0, 0, 0, 0);
-      s[u] = 0.f;
-      if (at.r < R) {
-        c[u] = __ldg(reinterpret_cast<const uint4*>(in.codes) + at.r * in.groups + at.g);
-        s[u] = in.variant == MM_MOE_VARIANT_MX
-                   ? ue8m0_value(__ldg(static_cast<const uint8_t*>(in.sf) + at.r * in.blocks + (at.g >> 1)))
-                   : __ldg(static_cast<const float*>(in.sf) + at.r * in.blocks + (at.g >> 3));
-        d[u] = out + at.r * stride + at.g * 16;
-        n[u] = min(16, C - at.g * 16);
-      }
-      at.step(d_row, d_group, groups);
+  // a warp runs while any of its lanes has a row, so the shuffles see all of it
+  for (Walk at(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, groups); __any_sync(0xffffffffu, at.r < R);
+       at.step(d_row, d_group, groups)) {
+    uint4 c = make_uint4(0, 0, 0, 0);
+    float s = 0.f;
+    T* d = out;
+    int n = 0;
+    if (at.r < R) {
+      c = __ldg(reinterpret_cast<const uint4*>(in.codes) + at.r * in.groups + at.g);
+      s = in.variant == MM_MOE_VARIANT_MX
+              ? ue8m0_value(__ldg(static_cast<const uint8_t*>(in.sf) + at.r * in.blocks + (at.g >> 1)))
+              : __ldg(static_cast<const float*>(in.sf) + at.r * in.blocks + (at.g >> 3));
+      d = out + at.r * stride + at.g * 16;
+      n = min(16, C - at.g * 16);
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      float f[16];
-      decode16(c[u], s[u], f);
-      uint32_t w[Group<T>::kWords];
-      round16<T>(f, w);
-      store_groups<T, kVec>(d[u], n[u], w, run);
-    }
+    float f[16];
+    decode16(c, s, f);
+    uint32_t w[Group<T>::kWords];
+    round16<T>(f, w);
+    store_groups<T, kVec>(d, n, w, run);
   }
 }
 
@@ -107,16 +99,19 @@ int grid_for(int64_t threads) {
 cudaError_t launch_quantize8(const void* x, int dtype, int64_t stride, int64_t R, int C, int variant, void* codes,
                              void* sf, cudaStream_t s) {
   const Out8 o{variant, static_cast<uint8_t*>(codes), sf, groups8(C, variant), blocks8(C, variant)};
-  const int grid = grid_for((R * o.groups + kBatch - 1) / kBatch);
+  // Groups a thread: four of rows on 32-byte boundaries where they are more than 2^22, else one (65536x4096 bf16 132 us for
+  // 143 with one, 136 with two; 65536x4095 205 for 172; 33x1001 9.6 for 7.4).
+  const bool vec = whole_groups(x, stride * dtype_size(dtype), C);
+  const int batch = vec && R * o.groups > (int64_t(1) << 22) ? 4 : 1;
+  const int grid = grid_for((R * o.groups + batch - 1) / batch);
   const int64_t step = static_cast<int64_t>(grid) * kThreads;
   const int d_row = static_cast<int>(step / o.groups), d_group = static_cast<int>(step % o.groups);
   return with_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     const T* p = static_cast<const T*>(x);
-    if (whole_groups(x, stride * sizeof(T), C))
-      quantize8_kernel<T, true><<<grid, kThreads, 0, s>>>(p, stride, R, C, o, d_row, d_group);
-    else
-      quantize8_kernel<T, false><<<grid, kThreads, 0, s>>>(p, stride, R, C, o, d_row, d_group);
+    if (batch == 4) quantize8_kernel<T, true, 4><<<grid, kThreads, 0, s>>>(p, stride, R, C, o, d_row, d_group);
+    else if (vec) quantize8_kernel<T, true, 1><<<grid, kThreads, 0, s>>>(p, stride, R, C, o, d_row, d_group);
+    else quantize8_kernel<T, false, 1><<<grid, kThreads, 0, s>>>(p, stride, R, C, o, d_row, d_group);
     return cudaGetLastError();
   });
 }
@@ -126,7 +121,7 @@ cudaError_t launch_dequantize8(const void* codes, const void* sf, int64_t R, int
   const Out8 in{variant, static_cast<uint8_t*>(const_cast<void*>(codes)), const_cast<void*>(sf), groups8(C, variant),
                 blocks8(C, variant)};
   const int groups = (C + 15) / 16;
-  const int grid = grid_for((R * groups + kBatch - 1) / kBatch);
+  const int grid = grid_for(R * groups);
   const int64_t step = static_cast<int64_t>(grid) * kThreads;
   const int d_row = static_cast<int>(step / groups), d_group = static_cast<int>(step % groups);
   return with_dtype(dtype, [&](auto tag) {

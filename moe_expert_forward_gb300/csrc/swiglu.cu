@@ -9,12 +9,17 @@
 //
 // Memory bounds both (forward: 4 bytes an element of a read and 2 written in 16 bits,
 // and 2 1/16 where kept; back: 2 and 2 1/16 read, 4 written).  A CTA takes a few rows,
-// looks their pairs and weights up at once, and then has two independent groups of 16
-// columns a lane in flight; everything about an element stays in its lane but a block's
-// amax and the row's dot.
+// looks their pairs and weights up at once, and then a lane takes 16 columns at a time;
+// everything about an element stays in its lane but a block's amax and the row's dot.
+// Two groups a lane in flight changed nothing: four CTAs an SM have the loads in flight.
 //
 // 16-bit rows take the fast exponential and reciprocal (within 2^-20, under a
-// hundredth of the rounding of the result; without denormals, a third of the instructions); fp32 rows expf and the IEEE division.
+// hundredth of the rounding of the result; without denormals, a third of the instructions); fp32 rows expf and the IEEE
+// division.
+//
+// Measured: 13248 pool rows (2048 tokens, top-6) of 2048 columns in bf16, kept in 8 bits, 42 us forward and 44 back, 82 and
+// 78 % of the copy rate of 34.5 us each; 4093 rows of 2731 in fp16 30 and 33 (rows on no 32-byte boundary: shifted from and
+// into 16-byte granules).
 #include "rows8.cuh"
 
 namespace mm {
@@ -34,7 +39,6 @@ __device__ __forceinline__ float sigmoid(float g) {
 }
 
 constexpr int kMostRows = 64;        // of a CTA
-constexpr int kFlight = 1;           // groups of 16 columns a lane has in flight
 
 // The CTA's rows: their pairs (-1: padding, or past the end) and weights. Without a routing a row is its own pair.
 struct Rows {
@@ -64,81 +68,70 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows;
   look_up(s_rows, r, w, row0, rows);
   const int I = r.I, groups = kept.groups, items = rows * groups;
-  for (int i0 = threadIdx.x; i0 - static_cast<int>(threadIdx.x & 31) < items; i0 += kFlight * kThreads) {
-    Group<T> vg[kFlight], vu[kFlight];
-    int at[kFlight], gg[kFlight];
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int i = i0 + u * kThreads;
-      at[u] = i / groups;
-      gg[u] = i - at[u] * groups;
-      if (i < items && s_rows.pair[at[u]] >= 0 && gg[u] * 16 < I) {
-        const T* hr = h + (row0 + at[u]) * stride;
-        vg[u].template load<kVec>(hr, gg[u] * 16, I);
-        vu[u].template load<kVec>(hr + I, gg[u] * 16, I);
-      } else {
-        vg[u].clear();
-        vu[u].clear();
-      }
+  for (int i = threadIdx.x; i - static_cast<int>(threadIdx.x & 31) < items; i += kThreads) {
+    const int at = i / groups, g = i - at * groups;
+    const int64_t row = row0 + at;
+    const bool in = i < items && row < r.rows;
+    const bool live = in && s_rows.pair[at] >= 0;
+    Group<T> vg, vu;
+    if (live && g * 16 < I) {
+      const T* hr = h + row * stride;
+      vg.template load<kVec>(hr, g * 16, I);
+      vu.template load<kVec>(hr + I, g * 16, I);
+    } else {
+      vg.clear();
+      vu.clear();
     }
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      if (i0 + u * kThreads - static_cast<int>(threadIdx.x & 31) >= items) break;       // the whole warp
-      const int64_t row = row0 + at[u];
-      const int g = gg[u];
-      const bool in = i0 + u * kThreads < items && row < r.rows;
-      const bool live = in && s_rows.pair[at[u]] >= 0;
-      if (!__any_sync(0xffffffffu, live)) {      // padding: zeros, and the scale of zeros
-        const uint8_t zero = static_cast<uint8_t>(ue8m0_exponent_e4m3(0.f) + 127);
-        if (in && kept.codes) {
-          reinterpret_cast<uint4*>(kept.codes)[row * 2 * groups + g] = make_uint4(0, 0, 0, 0);
-          reinterpret_cast<uint4*>(kept.codes)[(row * 2 + 1) * groups + g] = make_uint4(0, 0, 0, 0);
-          static_cast<uint8_t*>(kept.sf)[(row * 2 + (g & 1)) * kept.blocks + (g >> 1)] = zero;
-        }
-        if (in && q.codes) {
-          reinterpret_cast<uint4*>(q.codes)[row * groups + g] = make_uint4(0, 0, 0, 0);
-          if ((g & 1) == 0) static_cast<uint8_t*>(q.sf)[row * q.blocks + (g >> 1)] = zero;
-        }
-        if (a) {
-          uint32_t o[Group<T>::kWords];
-#pragma unroll
-          for (int c = 0; c < Group<T>::kWords; ++c) o[c] = 0;
-          store_groups<T, kVec>(a + row * I + g * 16, in ? min(16, I - g * 16) : 0, o, run);
-        }
-        continue;
+    if (!__any_sync(0xffffffffu, live)) {        // padding: zeros, and the scale of zeros
+      const uint8_t zero = static_cast<uint8_t>(ue8m0_exponent_e4m3(0.f) + 127);
+      if (in && kept.codes) {
+        reinterpret_cast<uint4*>(kept.codes)[row * 2 * groups + g] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(kept.codes)[(row * 2 + 1) * groups + g] = make_uint4(0, 0, 0, 0);
+        static_cast<uint8_t*>(kept.sf)[(row * 2 + (g & 1)) * kept.blocks + (g >> 1)] = zero;
       }
-      float gate[16], up[16];
-      vg[u].floats(gate);
-      vu[u].floats(up);
-      if (kept.codes) {                          // gate and up as blocks of one row of both
-        store_mx(kept, row * 2, g, in, gate, vg[u].amax_bits());
-        store_mx(kept, row * 2 + 1, g, in, up, vu[u].amax_bits());
-      }
-      const float weight = live ? s_rows.w[at[u]] : 0.f;
-      float f[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) f[c] = 0.f;
-      if (live)
-#pragma unroll
-        for (int c = 0; c < 16; ++c) f[c] = gate[c] * sigmoid<T>(gate[c]) * up[c] * weight;
-      if (q.codes) {
-        float z[16];                             // past the row: zeros, also where the weight is not finite
-#pragma unroll
-        for (int c = 0; c < 16; ++c) z[c] = g * 16 + c < I ? f[c] : 0.f;
-        store_mx(q, row, g, in, z, amax_bits16(z));
+      if (in && q.codes) {
+        reinterpret_cast<uint4*>(q.codes)[row * groups + g] = make_uint4(0, 0, 0, 0);
+        if ((g & 1) == 0) static_cast<uint8_t*>(q.sf)[row * q.blocks + (g >> 1)] = zero;
       }
       if (a) {
         uint32_t o[Group<T>::kWords];
-        round16<T>(f, o);
+#pragma unroll
+        for (int c = 0; c < Group<T>::kWords; ++c) o[c] = 0;
         store_groups<T, kVec>(a + row * I + g * 16, in ? min(16, I - g * 16) : 0, o, run);
       }
+      continue;
+    }
+    float gate[16], up[16];
+    vg.floats(gate);
+    vu.floats(up);
+    if (kept.codes) {                            // gate and up as blocks of one row of both
+      store_mx(kept, row * 2, g, in, gate, vg.amax_bits());
+      store_mx(kept, row * 2 + 1, g, in, up, vu.amax_bits());
+    }
+    const float weight = live ? s_rows.w[at] : 0.f;
+    float f[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) f[c] = 0.f;
+    if (live)
+#pragma unroll
+      for (int c = 0; c < 16; ++c) f[c] = gate[c] * sigmoid<T>(gate[c]) * up[c] * weight;
+    if (q.codes) {
+      float z[16];                               // past the row: zeros, also where the weight is not finite
+#pragma unroll
+      for (int c = 0; c < 16; ++c) z[c] = g * 16 + c < I ? f[c] : 0.f;
+      store_mx(q, row, g, in, z, amax_bits16(z));
+    }
+    if (a) {
+      uint32_t o[Group<T>::kWords];
+      round16<T>(f, o);
+      store_groups<T, kVec>(a + row * I + g * 16, in ? min(16, I - g * 16) : 0, o, run);
     }
   }
 }
 
-// P threads a row; a group of threads has two of the CTA's rows in flight. Their dots meet in shared memory.
+// P threads a row. The dots of a row's warps meet in shared memory.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
     swiglu_backward_kernel(const SwigluRows r, int rows, const T* __restrict__ d_a, int64_t stride, const Out8 kept,
                            const float* __restrict__ w, T* __restrict__ d_h, float* __restrict__ d_w, int P) {
   __shared__ Rows s_rows;
@@ -154,72 +147,50 @@ __global__ void __launch_bounds__(kThreads, 4)
   look_up(s_rows, r, w, row0, rows);
   const int l = threadIdx.x % P, sub = threadIdx.x / P, subs = kThreads / P, I = r.I;
   const int groups = (I + 15) / 16;
-  for (int i0 = sub; i0 < rows; i0 += kFlight * subs) {
-    float dot[kFlight];
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) dot[u] = 0.f;
+  for (int i = sub; i < rows; i += subs) {
+    const int64_t row = row0 + i;
+    const bool live = s_rows.pair[i] >= 0;
+    const float weight = s_rows.w[i];
+    float dot = 0.f;
     for (int g = l; g - (l & 31) < groups; g += P) {
-      Group<T> vd[kFlight];
-      uint4 cg[kFlight], cu[kFlight];
-      uint32_t sg[kFlight], su[kFlight];
+      float og[16], ou[16];
+      if (live && g < groups) {
+        const uint4* codes = reinterpret_cast<const uint4*>(kept.codes) + row * 2 * kept.groups + g;
+        const uint8_t* sf = static_cast<const uint8_t*>(kept.sf) + row * 2 * kept.blocks + (g >> 1);
+        Group<T> vd;
+        vd.template load<kVec>(d_a + row * stride, g * 16, I);
+        const uint4 cg = __ldg(codes), cu = __ldg(codes + kept.groups);
+        const uint32_t sg = __ldg(sf), su = __ldg(sf + kept.blocks);
+        float gate[16], up[16], d[16];
+        decode16(cg, ue8m0_value(sg), gate);
+        decode16(cu, ue8m0_value(su), up);
+        vd.floats(d);
 #pragma unroll
-      for (int u = 0; u < kFlight; ++u) {
-        const int i = i0 + u * subs;
-        const bool live = i < rows && s_rows.pair[i] >= 0 && g < groups;
-        vd[u].clear();
-        cg[u] = cu[u] = make_uint4(0, 0, 0, 0);
-        sg[u] = su[u] = 0;
-        if (live) {
-          const int64_t row = row0 + i;
-          const uint4* codes = reinterpret_cast<const uint4*>(kept.codes) + row * 2 * kept.groups + g;
-          const uint8_t* sf = static_cast<const uint8_t*>(kept.sf) + row * 2 * kept.blocks + (g >> 1);
-          vd[u].template load<kVec>(d_a + row * stride, g * 16, I);
-          cg[u] = __ldg(codes);
-          cu[u] = __ldg(codes + kept.groups);
-          sg[u] = __ldg(sf);
-          su[u] = __ldg(sf + kept.blocks);
+        for (int c = 0; c < 16; ++c) {
+          const float s = sigmoid<T>(gate[c]);
+          const float silu = gate[c] * s;
+          if (kVec || g * 16 + c < I) dot = fmaf(d[c] * silu, up[c], dot);
+          const float dw = d[c] * weight;
+          og[c] = dw * up[c] * (s * (1.0f + gate[c] * (1.0f - s)));
+          ou[c] = dw * silu;
         }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) og[c] = ou[c] = 0.f;
       }
-#pragma unroll
-      for (int u = 0; u < kFlight; ++u) {
-        const int i = i0 + u * subs;
-        if (i >= rows) break;                    // the whole group of threads
-        float og[16], ou[16];
-        if (s_rows.pair[i] >= 0 && g < groups) {
-          const float weight = s_rows.w[i];
-          float gate[16], up[16], d[16];
-          decode16(cg[u], ue8m0_value(sg[u]), gate);
-          decode16(cu[u], ue8m0_value(su[u]), up);
-          vd[u].floats(d);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float s = sigmoid<T>(gate[c]);
-            const float silu = gate[c] * s;
-            if (kVec || g * 16 + c < I) dot[u] = fmaf(d[c] * silu, up[c], dot[u]);
-            const float dw = d[c] * weight;
-            og[c] = dw * up[c] * (s * (1.0f + gate[c] * (1.0f - s)));
-            ou[c] = dw * silu;
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) og[c] = ou[c] = 0.f;
-        }
-        uint32_t o[Group<T>::kWords];
-        T* at = d_h + (row0 + i) * 2 * I + g * 16;
-        const int n = row0 + i < r.rows ? min(16, I - g * 16) : 0;
-        round16<T>(og, o);
-        store_groups<T, kVec>(at, n, o, run);
-        round16<T>(ou, o);
-        store_groups<T, kVec>(at + I, n, o, run);
-      }
+      uint32_t o[Group<T>::kWords];
+      T* at = d_h + row * 2 * I + g * 16;
+      const int n = row < r.rows ? min(16, I - g * 16) : 0;
+      round16<T>(og, o);
+      store_groups<T, kVec>(at, n, o, run);
+      round16<T>(ou, o);
+      store_groups<T, kVec>(at + I, n, o, run);
     }
-    if (d_w)
+    if (d_w) {
 #pragma unroll
-      for (int u = 0; u < kFlight; ++u) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
-        if (i0 + u * subs < rows && (threadIdx.x & 31) == 0) s_dot[i0 + u * subs][l >> 5] = dot[u];
-      }
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if ((threadIdx.x & 31) == 0) s_dot[i][l >> 5] = dot;
+    }
   }
   if (!d_w) return;
   __syncthreads();
@@ -231,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 }
 
-// Rows of a CTA: about four groups of 16 columns a thread, fewer where that leaves SMs without a CTA.
+// Rows of a CTA: about four groups of 16 columns a thread, fewer where that leaves SMs without a CTA. (13248 rows of 2048
+// columns, forward / back with cold caches, us: four 45 / 46, eight 50 / 51, one 49 / 52; 1216 rows 11 / 12 with any.)
 int cta_rows(int64_t rows, int groups) {
   int64_t n = 4 * kThreads / groups;
   const int64_t spread = rows / (4 * dev_info().sms);
