@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
   __syncthreads();
   cluster_barrier();                             // every CTA's barriers exist before anything targets them
   tc_fence_after();
+  if (kDecoded) pdl_wait();                      // x has been decoded
   const uint32_t tmem = *s_tmem;
   const int ntasks = args.tasks * args.parts;
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
@@ -648,13 +649,14 @@ __global__ void __launch_bounds__(kCopyThreads)
     decode_rows_kernel(const uint4* __restrict__ codes, int pieces, const uint8_t* __restrict__ sf, int blocks,
                        const int32_t* __restrict__ src, const int32_t* __restrict__ blk_off, int E, int block_m, int K,
                        int by_token, int64_t rows, uint4* __restrict__ out) {
+  pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * (kCopyThreads / 32) + (threadIdx.x >> 5);
   if (r >= rows || (src && r >= static_cast<int64_t>(__ldg(blk_off + E)) * block_m)) return;
   const int pair = src ? __ldg(src + r) : 0;
   const int64_t t = by_token ? pair / K : r;
   uint4* o = out + r * pieces * 2;
-#pragma unroll 2
+#pragma unroll 4
   for (int i0 = 0; i0 < pieces; i0 += 32) {
     const int i = i0 + lane;
     uint4 c = make_uint4(0, 0, 0, 0);
@@ -752,11 +754,13 @@ cudaError_t launch(const Args& a, Maps& maps, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads<kDecoded>);
   cfg.dynamicSmemBytes = Smem<kDecoded>::total(a.cnt ? a.E : 0);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2; attr[0].val.clusterDim.y = 1; attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;         // the kernel before is one of this call
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = kDecoded ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
 
