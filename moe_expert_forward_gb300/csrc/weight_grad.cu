@@ -91,6 +91,7 @@ struct Args {
   int N, C, E, block_m;
   int NT, CT;                // tiles of N and of C
   int tasks, parts;          // E NT CT, and the parts of each
+  int whole;                 // (parts 1) tasks from this one on are taken in halves of 128 columns of x; else all
   int rows;                  // of d_y
   const uint32_t* sf;
   int sf_words;              // words from one row of scales to the next
@@ -107,6 +108,7 @@ struct Args {
 // N >> 3 in [22:17], M >> 4 in [28:24].
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                             (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
+constexpr uint32_t kIdescHalf = kIdesc - (static_cast<uint32_t>(kTile / 2 >> 3) << 17);
 
 __device__ __forceinline__ void tc_mma_f16_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                 uint32_t accumulate) {
@@ -137,6 +139,7 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar) {
 // A part of a task: the sum over stages [ks, end) of an expert's rows.
 struct Task {
   int slab, n0, c0;          // [part][expert] of out
+  int cols;                  // of x: kTile, or half of it
   int row0;                  // first row of the expert
   int rows;                  // its rows
   int ks, end;
@@ -145,12 +148,19 @@ __device__ __forceinline__ Task task_at(int i, const Args& a, const int* s_blk, 
   Task t;
   const int part = a.parts > 1 ? i / a.tasks : 0;
   i -= part * a.tasks;
+  t.cols = kTile;
+  int right = 0;
+  if (a.parts == 1 && i >= a.whole) {
+    t.cols = kTile / 2;
+    right = (i - a.whole) & 1;
+    i = a.whole + ((i - a.whole) >> 1);
+  }
   const int nt = i % a.NT;
   i /= a.NT;
   const int ct = i % a.CT, e = i / a.CT;
   t.slab = part * a.E + e;
   t.n0 = nt * kTile;
-  t.c0 = ct * kTile;
+  t.c0 = ct * kTile + right * (kTile / 2);
   t.row0 = a.cnt ? s_blk[e] * a.block_m : 0;
   t.rows = a.cnt ? max(0, min(s_cnt[e], a.rows - t.row0)) : a.rows;
   const int nks = (t.rows + kRowsPerStage - 1) / kRowsPerStage;
@@ -333,7 +343,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
   tc_fence_after();
   if (kDecoded) pdl_wait();                      // x has been decoded
   const uint32_t tmem = *s_tmem;
-  const int ntasks = args.tasks * args.parts;
+  const int ntasks = args.parts == 1 ? args.tasks + (args.tasks - args.whole) : args.tasks * args.parts;
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   // accumulators of a task's n stages
   auto segments = [](int n) { return sizeof(T) == 4 ? (n + kSegment - 1) / kSegment : 1; };
@@ -353,11 +363,12 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
       while (at.next(args, s_blk, s_cnt)) {
         const int s = ring.s;
         if (*s_abort || !mbar_wait(&empty[s], ring.phase ^ 1, st, s_abort, kSiteEmpty)) break;
-        mbar_arrive_expect_tx(&landed[s], kHalfBytes);
+        const int mine = is_x ? at.t.cols / 2 : 128;             // columns
+        mbar_arrive_expect_tx(&landed[s], mine * kRowsPerStage * 2);
         const int row = at.t.row0 + at.t.ks * kRowsPerStage;
-        const int col = (is_x ? at.t.c0 : at.t.n0) + static_cast<int>(rank) * 128;
+        const int col = (is_x ? at.t.c0 : at.t.n0) + static_cast<int>(rank) * mine;
         tma_load_2d(to + s * kHalfBytes, map, &landed[s], col, row, pol);
-        tma_load_2d(to + s * kHalfBytes + kChunkBytes, map, &landed[s], col + 64, row, pol);
+        if (mine == 128) tma_load_2d(to + s * kHalfBytes + kChunkBytes, map, &landed[s], col + 64, row, pol);
         ring.step();
         ++steps;
       }
@@ -381,7 +392,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
       const uint16_t both = 3;
       Cursor at(first, stride, ntasks);
       Ring<kStages> ring;
-      uint32_t acc = tmem;
+      uint32_t acc = tmem, idesc = kIdesc;
       int it = 0, left = 0, in_acc = 0, rows = 0;     // accumulators so far; of this one: stages left, stages in it; rows left
       bool live = at.next_task(args, s_blk, s_cnt);
       auto wait = [&](uint64_t* bar, uint32_t phase, int where) {
@@ -392,6 +403,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
       auto start = [&]() {                       // an accumulator
         const int buf = it & 1;
         acc = tmem + buf * kTile;
+        if (kDecoded) idesc = at.t.cols == kTile ? kIdesc : kIdescHalf;
         left = at.t.end - at.t.ks;
         if (sizeof(T) == 4) left = min(left, kSegment);
         in_acc = 0;
@@ -404,10 +416,10 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
         if (!wait(&full[s], ring.phase, kSiteFull)) break;
         const uint64_t da = da0 + ((s * kHalfBytes) >> 4), db = db0 + ((s * kHalfBytes) >> 4);
         if (issues) {
-          tc_mma_f16_pair(acc, da, db, kIdesc, in_acc);
+          tc_mma_f16_pair(acc, da, db, idesc, in_acc);
 #pragma unroll
           for (int k = 1; k < 4; ++k)            // 16 rows: two atoms
-            if (rows > 16 * k) tc_mma_f16_pair(acc, da + k * (2 * kAtom >> 4), db + k * (2 * kAtom >> 4), kIdesc, 1);
+            if (rows > 16 * k) tc_mma_f16_pair(acc, da + k * (2 * kAtom >> 4), db + k * (2 * kAtom >> 4), idesc, 1);
           tc_commit_both(&empty[s], both);
         }
         __syncwarp();
@@ -541,8 +553,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    constexpr int kShare = kTile / (kEpiWarps / 4);              // columns of a warp
-    const int quad = warp & 3, half = (warp >> 2) * kShare;
+    const int quad = warp & 3;                   // 32 of the CTA's rows of the tile
     int it = 0, box_turn = 0;
     for (int i = first; i < ntasks; i += stride) {
       const Task t = task_at(i, args, s_blk, s_cnt);
@@ -550,6 +561,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
       const int64_t row = static_cast<int64_t>(t.slab) * args.N + n0;
       const int rows = args.N - n0;
       const int nks = t.end - t.ks;              // 0: an expert without rows, or without any for this part
+      const int cols = kDecoded ? t.cols : kTile;
       bool ok = true;
       for (int seg = 0; seg < max(segments(nks), 1) && ok; ++seg) {
         const int buf = it & 1;
@@ -562,7 +574,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
           __syncwarp();
           if (lane == 0) arrive_leader(map_shared(&tempty[buf], 0));
         };
-        const uint32_t src0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTile + half;
+        const uint32_t src0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTile;
         constexpr int kBox = 128 / sizeof(T);    // columns of a box
         if (kTma && seg > 0 && lane == 0) tma_stored();    // what the boxes are added to
         uint32_t v[kBox];                        // a box's accumulators (kDecoded, which has the registers for it: the
@@ -573,7 +585,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
         };
         if (kDecoded && nks != 0) fetch(0);
 #pragma unroll 1
-        for (int c = 0; c < kShare; c += kBox) {
+        for (int c = 0; c < cols; c += kBox) {
           uint32_t w[32];
           if (nks == 0) {
 #pragma unroll
@@ -585,10 +597,10 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               w[j] = sizeof(T) == 4 ? v[j] : pack2<T>(v[(2 * j) % kBox], v[(2 * j + 1) % kBox]);
-            if (c + kBox == kShare) release();
+            if (c + kBox == cols) release();
             else if (kDecoded) fetch(c + kBox);
           }
-          const int col = t.c0 + half + c;
+          const int col = t.c0 + c;
           if (rows <= 0 || col >= args.C) continue;
           uint8_t* box = smem + Smem::out + (warp * Smem::kBoxes + box_turn % Smem::kBoxes) * kBoxBytes;
           ++box_turn;
@@ -731,7 +743,7 @@ cudaError_t add_parts(const float* sums, int parts, int64_t rows, int C, int pit
 
 // a.out and a.out_pitch: where the sums go, of T.
 template <typename T, bool kDecoded>
-cudaError_t launch(const Args& a, Maps& maps, cudaStream_t s) {
+cudaError_t launch(Args& a, Maps& maps, cudaStream_t s) {
   const bool tma = (reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(a.out_pitch)) % 16 == 0;
   if (tma) {
     const uint64_t dims[3] = {static_cast<uint64_t>(a.C), static_cast<uint64_t>(a.N),
@@ -748,7 +760,12 @@ cudaError_t launch(const Args& a, Maps& maps, cudaStream_t s) {
   int most = 0;
   if (cudaError_t e = max_pair_clusters(fn, kThreads<kDecoded>, Smem<kDecoded>::total(kMaxE), &most)) return e;
   if (most < 1) return cudaErrorInvalidConfiguration;
-  const int pairs = a.tasks * a.parts;
+  // The tasks past the last whole round are taken in halves where these fit a round (8192x4096x4096, 256 tasks on 76 pairs,
+  // 174 us for 177 with all whole; 2048x2560x2560 34 for 36). In parts, whose fp32 sums a kernel adds up, they took 2 us
+  // less at 8192 rows and 7 more at 4096.
+  const int rest = a.tasks % most, halves = kDecoded && a.parts == 1 && 2 * rest <= most ? rest : 0;
+  a.whole = a.tasks - halves;
+  const int pairs = a.tasks * a.parts + halves;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (pairs < most ? pairs : most)));
   cfg.blockDim = dim3(kThreads<kDecoded>);
@@ -764,7 +781,9 @@ cudaError_t launch(const Args& a, Maps& maps, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
 
-// Parts of a task's contraction of `terms` rows: as many as pairs of SMs have room for, of 8 stages at least.
+// Parts of a task's contraction of `terms` rows: as many as pairs of SMs have room for, of 8 stages at least. (N = 256, one
+// part / parts, cold caches, us: 8192 rows, C = 4096 69 / 37, C = 256 69 / 22; 65536 rows, C = 2048 451 / 87; 2048 rows, C =
+// 4096 27 / 23; 1024 rows 20 / 21.)
 int parts_of(int64_t tasks, int64_t terms) {
   const int64_t stages = (terms + kRowsPerStage - 1) / kRowsPerStage;
   const int64_t n = kSplitPairs / tasks < stages / 8 ? kSplitPairs / tasks : stages / 8;

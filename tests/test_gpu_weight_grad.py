@@ -91,6 +91,23 @@ def test_long_sums_of_many_tiles(ops, N, C):
     check(ops, whole(N, 2100, N).bfloat16(), whole(C, 2100, C))
 
 
+@pytest.mark.parametrize("rows", [1, 70, 1100])
+@pytest.mark.parametrize("N,C", [(2600, 1800), (2601, 1799), (5000, 950), (2048, 2560)])
+def test_last_tiles_in_halves(ops, rows, N, C):
+    """80 to 88 tiles: those past the last whole round of 76 pairs go in halves, some of them past C."""
+    check(ops, whole(N, rows, N).bfloat16(), whole(C, rows, C))
+
+
+def test_last_tiles_of_experts_in_halves(ops):
+    """96 tiles of four experts, the last of them without rows, then with most."""
+    for seed, dead in ((3, 3), (4, 1)):
+        idx = torch.randint(0, 3, (150, 1), generator=torch.Generator().manual_seed(seed))
+        r = ops.sort_tokens((idx + (idx >= dead).long()).int().cuda(), 4)
+        for by_token in (False, True):
+            x = whole(2, 150 if by_token else r.rows, 1000)
+            check(ops, whole(1, r.rows, 1400).bfloat16(), x, r, by_token)
+
+
 def test_many_experts_without_rows(ops):
     r = ops.sort_tokens(torch.tensor([[5], [200], [5]], dtype=torch.int32, device="cuda"), 256)
     for C in (520, 519):
