@@ -18,8 +18,8 @@
 // division.
 //
 // Measured: 13248 pool rows (2048 tokens, top-6) of 2048 columns in bf16, kept in 8 bits, 42 us forward and 44 back, 82 and
-// 78 % of the copy rate of 34.5 us each; 4093 rows of 2731 in fp16 30 and 33 (rows on no 32-byte boundary: shifted from and
-// into 16-byte granules).
+// 78 % of the copy rate of 34.5 us each; 4093 rows of 2731 in fp16 26 and 28 (rows on no 32-byte boundary: shifted from and
+// into 16-byte granules; 2736 columns 18 and 20).
 #include "rows8.cuh"
 
 namespace mm {
@@ -202,12 +202,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
     }
 }
 
-// Rows of a CTA: about four groups of 16 columns a thread, fewer where that leaves SMs without a CTA. (13248 rows of 2048
-// columns, forward / back with cold caches, us: four 45 / 46, eight 50 / 51, one 49 / 52; 1216 rows 11 / 12 with any.)
+// Rows of a CTA: about four groups of 16 columns a thread, as many as share the rows out evenly over whole rounds of four
+// CTAs an SM. (Forward / back with cold caches, us: 13248 rows of 2048 columns 45 / 46, by two or eight groups 46 / 47 and
+// 44 / 44; 4093 of 2731 in fp16 32 / 33, with four groups whatever the rounds 35 / 38; 3000 of 4096 24 / 24, 27 / 27.)
 int cta_rows(int64_t rows, int groups) {
-  int64_t n = 4 * kThreads / groups;
-  const int64_t spread = rows / (4 * dev_info().sms);
-  n = n < spread ? n : spread;
+  const int64_t slots = 4 * dev_info().sms, most = slots * 4 * kThreads / groups;          // rows of a round
+  const int64_t rounds = most > 0 ? (2 * rows + most) / (2 * most) : 1;
+  const int64_t ctas = slots * (rounds > 0 ? rounds : 1), n = (rows + ctas - 1) / ctas;
   return static_cast<int>(n < 1 ? 1 : n > kMostRows ? kMostRows : n);
 }
 
