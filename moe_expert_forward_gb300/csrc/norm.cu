@@ -49,18 +49,32 @@ struct NormArgs {
   int row_threads;
 };
 
-// The sum of v over the row_threads threads of a row, for each of them. All threads of the CTA take part.
-__device__ __forceinline__ float row_sum(float v, int row_threads, float* s_part) {
+// The sum of a row's groups of 16 columns, in every thread of the row: v[i] that of the thread's i-th group. Groups are
+// added up by 32 that follow each other, and those sums in order, so that a row's sum depends on its length alone, not on
+// the kernel and the threads that take it, nor on how many rows there are.
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N], float* s_part, int warps, int warp) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (row_threads == 32) return v;
-  const int warps = row_threads / 32, first = (threadIdx.x / row_threads) * warps;
-  __syncthreads();                               // the parts of the sum before this one have been read
-  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.f;
-  for (int i = 0; i < warps; ++i) v += s_part[first + i];
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if ((threadIdx.x & 31) == 0) s_part[i * warps + warp] = v[i];
+  }
+}
+__device__ __forceinline__ float sum_in_order(const float* s_part, int n) {
+  float v = s_part[0];
+  for (int i = 1; i < n; ++i) v += s_part[i];
   return v;
+}
+// All threads of the CTA take part; its rows have row_threads threads each.
+template <int N>
+__device__ __forceinline__ float row_sum(float (&v)[N], int row_threads, float* s_part) {
+  const int warps = row_threads / 32, row = threadIdx.x / row_threads;
+  __syncthreads();                               // the parts of the sum before this one have been read
+  warp_sums(v, s_part + row * warps * N, warps, (threadIdx.x >> 5) - row * warps);
+  if (row_threads == 32 && N == 1) return v[0];
+  __syncthreads();
+  return sum_in_order(s_part + row * warps * N, warps * N);
 }
 
 // Weights of columns c .. c+15, zeros past H.
@@ -80,8 +94,8 @@ __device__ __forceinline__ void load_weight(const void* w, bool w_f32, int c, in
 // G > 0: a row's G groups a thread are held in registers. G = 0: any length, read twice.
 template <typename T, bool kVec, int G>
 __global__ void __launch_bounds__(kMostThreads) rms_norm_kernel(const NormArgs a) {
-  __shared__ float s_part[kMostThreads / 32];
-  extern __shared__ __align__(16) unsigned char s_dyn[];
+  __shared__ float s_part[2 * kMostThreads / 32];
+  extern __shared__ __align__(128) unsigned char s_dyn[];
   T* run = reinterpret_cast<T*>(s_dyn) + (threadIdx.x >> 5) * 512;
   const int P = a.row_threads;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / P) + threadIdx.x / P;
@@ -140,7 +154,7 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_kernel(const NormArgs a
     }
   };
 
-  float s = 0.f;
+  float s[G > 0 ? G : 1] = {};
   Group<T> held[G > 0 ? G : 1];
   if constexpr (G > 0) {
 #pragma unroll
@@ -148,16 +162,15 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_kernel(const NormArgs a
       if (i * P + (l & ~31) < groups) take(i * P + l, true, held[i]);
       else held[i].clear();
 #pragma unroll
-    for (int i = 0; i < G; ++i) s += squares(held[i]);
+    for (int i = 0; i < G; ++i) s[i] = squares(held[i]);
   } else {
     for (int g = l; g - (l & 31) < groups; g += P) {
       Group<T> v;
       take(g, true, v);
-      s += squares(v);
+      s[0] += squares(v);
     }
   }
-  s = row_sum(s, P, s_part);
-  const float r = 1.0f / sqrtf(s / static_cast<float>(a.H) + a.eps);
+  const float r = 1.0f / sqrtf(row_sum(s, P, s_part) / static_cast<float>(a.H) + a.eps);
   if (live && l == 0) a.rstd[row] = r;
   if constexpr (G > 0) {
 #pragma unroll
@@ -201,17 +214,28 @@ __device__ __forceinline__ void back16(const float (&y)[16], const float (&h)[16
   }
 }
 
-// One CTA takes rows in a fixed stride; each group of row_threads threads sums d_weight's part of its own rows.
+// Brings the 16 elements from p on (their first 32-byte sectors) into L2.
+template <typename T>
+__device__ __forceinline__ void prefetch_group(const T* p) {
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p) + 32 * i));
+}
+
+// One CTA takes rows in a fixed stride; each group of row_threads threads sums d_weight's part of its own rows. The next
+// row is on its way into L2 meanwhile, and the weights stay in registers where a thread has one group of columns (cold
+// caches, without the two / with them, us: 8192 rows of 512 in fp32 50 / 27, 1024 in bf16 31 / 25, 1025 in fp16 61 / 48, 2049
+// in bf16 106 / 78; 4096 of 4097 112 / 85; 2954 of 6047 in fp32 138 / 120).
 template <typename T, bool kVec, int G>
 __global__ void __launch_bounds__(kMostThreads) rms_norm_backward_kernel(const NormBackArgs a) {
-  __shared__ float s_part[kMostThreads / 32];
-  extern __shared__ __align__(16) unsigned char s_dyn[];
+  __shared__ float s_part[2 * kMostThreads / 32];
+  extern __shared__ __align__(128) unsigned char s_dyn[];
   T* run = reinterpret_cast<T*>(s_dyn) + (threadIdx.x >> 5) * 512;
   const int P = a.row_threads, rows = blockDim.x / P;
   const int l = threadIdx.x % P;
   const int groups = ((a.H + 15) / 16 + 31) / 32 * 32;
   float* part = a.parts + static_cast<int64_t>(blockIdx.x) * a.pitch;
-  float acc[G > 0 ? G : 1][16];
+  float acc[G > 0 ? G : 1][16], w[16];           // G = 1: the weights of the thread's columns
+  if constexpr (G == 1) load_weight<T, kVec>(a.weight, a.w_f32, l * 16, a.H, w);
   if constexpr (G > 0) {
 #pragma unroll
     for (int i = 0; i < G; ++i)
@@ -237,20 +261,20 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_backward_kernel(const N
     };
     // sum over a group of g n
     auto dot = [&](int g, const Group<T>& vy, const Group<T>& vh) {
-      float y[16], n[16], w[16], s = 0.f;
+      float y[16], n[16], s = 0.f;
       vy.floats(y);
       vh.floats(n);
-      load_weight<T, kVec>(a.weight, a.w_f32, g * 16, a.H, w);
+      if (G != 1) load_weight<T, kVec>(a.weight, a.w_f32, g * 16, a.H, w);
 #pragma unroll
       for (int i = 0; i < 16; ++i) s = fmaf(y[i] * w[i], n[i] * r, s);
       return s;
     };
     auto finish = [&](int g, const Group<T>& vy, const Group<T>& vh, const Group<T>& vd, float mean, float (&sum)[16]) {
-      float y[16], n[16], w[16], d[16];
+      float y[16], n[16], d[16];
       vy.floats(y);
       vh.floats(n);
       vd.floats(d);
-      load_weight<T, kVec>(a.weight, a.w_f32, g * 16, a.H, w);
+      if (G != 1) load_weight<T, kVec>(a.weight, a.w_f32, g * 16, a.H, w);
       back16(y, n, w, r, mean, d, sum);
       uint32_t o[Group<T>::kWords];
       round16<T>(d, o);
@@ -258,6 +282,15 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_backward_kernel(const N
     };
     if constexpr (G > 0) {
       Group<T> vy[G], vh[G], vd[G];
+      const int64_t after = row + static_cast<int64_t>(gridDim.x) * rows;      // the row after this one
+      if (after < a.T)
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+          if ((i * P + l) * 16 < a.H) {
+            prefetch_group(static_cast<const T*>(a.d_y) + after * a.dy_stride + (i * P + l) * 16);
+            prefetch_group(static_cast<const T*>(a.h) + after * a.h_stride + (i * P + l) * 16);
+            if (a.d_h) prefetch_group(static_cast<const T*>(a.d_h) + after * a.dh_stride + (i * P + l) * 16);
+          }
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         load(dy, i * P + l, vy[i]);
@@ -265,20 +298,20 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_backward_kernel(const N
         if (a.d_h) load(dh, i * P + l, vd[i]);
         else vd[i].clear();
       }
-      float s = 0.f;
+      float s[G];
 #pragma unroll
-      for (int i = 0; i < G; ++i) s += dot(i * P + l, vy[i], vh[i]);
+      for (int i = 0; i < G; ++i) s[i] = dot(i * P + l, vy[i], vh[i]);
       const float mean = row_sum(s, P, s_part) / static_cast<float>(a.H);
 #pragma unroll
       for (int i = 0; i < G; ++i)
         if (i * P + (l & ~31) < groups) finish(i * P + l, vy[i], vh[i], vd[i], mean, acc[i]);
     } else {
-      float s = 0.f;
+      float s[1] = {};
       for (int g = l; g - (l & 31) < groups; g += P) {
         Group<T> vy, vh;
         load(dy, g, vy);
         load(h, g, vh);
-        s += dot(g, vy, vh);
+        s[0] += dot(g, vy, vh);
       }
       const float mean = row_sum(s, P, s_part) / static_cast<float>(a.H);
       for (int g = l; g - (l & 31) < groups; g += P) {
@@ -386,22 +419,20 @@ __device__ __forceinline__ void take16(Group<T>& v, const uint8_t* row, int g, i
     v.w[4 * q] = w.x; v.w[4 * q + 1] = w.y; v.w[4 * q + 2] = w.z; v.w[4 * q + 3] = w.w;
   }
 }
-// The sum of v over the CTA, in each of its threads; s_part alternates between two arrays, so that one barrier does.
-__device__ __forceinline__ float cta_sum(float v, float* s_part) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
+// The row_sum of a CTA's one row; s_part alternates between two arrays, so that one barrier does.
+template <int N>
+__device__ __forceinline__ float cta_sum(float (&v)[N], float* s_part) {
+  const int warps = static_cast<int>(blockDim.x) / 32;
+  warp_sums(v, s_part, warps, threadIdx.x >> 5);
   __syncthreads();
-  v = 0.f;
-  for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) v += s_part[i];
-  return v;
+  return sum_in_order(s_part, warps * N);
 }
 
 template <typename T, typename W, int G>
 __global__ void __launch_bounds__(kMostThreads)
     rms_norm_ring_kernel(const NormArgs a, int stages, int* report) {
   extern __shared__ __align__(128) unsigned char s_dyn[];
-  __shared__ float s_part[2][kMostThreads / 32];
+  __shared__ float s_part[2][G * kMostThreads / 32];
   const uint32_t row_bytes = a.H * static_cast<uint32_t>(sizeof(T));
   RowRing ring(s_dyn, stages, a.residual ? 2 : 1, row_bytes);
   const Status st{report, kTimeoutNs};
@@ -421,7 +452,7 @@ __global__ void __launch_bounds__(kMostThreads)
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, ring.step(), turn ^= 1) {
     const bool ok = ring.wait(st, kSiteForward);
     Group<T> h[G];
-    float s = 0.f;
+    float s[G] = {};
     if (ok) {
 #pragma unroll
       for (int i = 0; i < G; ++i) {
@@ -441,16 +472,16 @@ __global__ void __launch_bounds__(kMostThreads)
           h[i].floats(f);
         }
 #pragma unroll
-        for (int c = 0; c < 16; ++c) s = fmaf(f[c], f[c], s);
+        for (int c = 0; c < 16; ++c) s[i] = fmaf(f[c], f[c], s[i]);
       }
     }
-    s = cta_sum(s, s_part[turn]);                // and everyone has read the stage
+    const float sum = cta_sum(s, s_part[turn]);  // and everyone has read the stage
     if (*reinterpret_cast<volatile int*>(ring.abort)) break;
     if (l == 0 && next < a.T) {
       load(next);
       next += gridDim.x;
     }
-    const float r = 1.0f / sqrtf(s / static_cast<float>(a.H) + a.eps);
+    const float r = 1.0f / sqrtf(sum / static_cast<float>(a.H) + a.eps);
     if (l == 0) a.rstd[row] = r;
 #pragma unroll
     for (int i = 0; i < G; ++i) {
@@ -480,7 +511,7 @@ template <typename T, typename W, int G>
 __global__ void __launch_bounds__(kMostThreads)
     rms_norm_backward_ring_kernel(const NormBackArgs a, int stages, int* report) {
   extern __shared__ __align__(128) unsigned char s_dyn[];
-  __shared__ float s_part[2][kMostThreads / 32];
+  __shared__ float s_part[2][G * kMostThreads / 32];
   const uint32_t row_bytes = a.H * static_cast<uint32_t>(sizeof(T));
   RowRing ring(s_dyn, stages, a.d_h ? 3 : 2, row_bytes);
   const Status st{report, kTimeoutNs};
@@ -505,7 +536,7 @@ __global__ void __launch_bounds__(kMostThreads)
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, ring.step(), turn ^= 1) {
     const bool ok = ring.wait(st, kSiteBackward);
     const float r = __ldg(a.rstd + row);
-    float s = 0.f;
+    float s[G] = {};
     if (ok)
 #pragma unroll
       for (int i = 0; i < G; ++i) {
@@ -518,15 +549,15 @@ __global__ void __launch_bounds__(kMostThreads)
         v.floats(n);
         w[i].floats(q);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) s = fmaf(y[c] * q[c], n[c] * r, s);
+        for (int c = 0; c < 16; ++c) s[i] = fmaf(y[c] * q[c], n[c] * r, s[i]);
       }
-    s = cta_sum(s, s_part[turn]);                // and everyone is done with the row before
+    const float sum = cta_sum(s, s_part[turn]);  // and everyone is done with the row before
     if (*reinterpret_cast<volatile int*>(ring.abort)) break;
     if (l == 0 && row != blockIdx.x && next < a.T) {
       load(next);
       next += gridDim.x;
     }
-    const float mean = s / static_cast<float>(a.H);
+    const float mean = sum / static_cast<float>(a.H);
 #pragma unroll
     for (int i = 0; i < G; ++i) {
       const int g = i * static_cast<int>(blockDim.x) + l;
@@ -595,18 +626,19 @@ struct RingShape {
   int threads, G, stages, ctas;
 };
 // stages 0: not by a ring. 512 threads an SM in CTAs as small as hold a row (16384 elements at most) and two stages; a row
-// is then a CTA's for less time, and more of them are under way. From 2048 columns on, and more rows than two CTAs an SM
-// take at once. bf16 with a residual, cold caches, us, by a ring / by their threads (f8: with those codes):
-//   8192 rows of   1536       2048       2560       4096       7168       8192     16384 (4096 rows)
-//   forward      27 / 27    28 / 34    36 / 38    52 / 57   83 / 107   93 / 110   91 / 105
-//   f8           36 / 32    38 / 40    46 / 44    62 / 68   93 / 133  112 / 137  106 / 126
-//   back         43 / 44    48 / 48    50 / 67    57 / 76   93 / 149   99 / 156  111 / 156
-//   320 rows of 4096: 11.4 / 10.3, back 14.6 / 15.5; 1024: 14.2 / 14.6, back 19.1 / 21.6
+// is then a CTA's for less time, and more of them are under way. From 2048 columns on (the gradients: 3584), and more rows
+// than two CTAs an SM take at once. bf16 with a residual, cold caches, us, by a ring / by their threads (f8: with those
+// codes):
+//   8192 rows of   1536       2048       2560       3584       4096       7168       8192     16384 (4096 rows)
+//   forward      27 / 27    28 / 34    36 / 38    46 / 50    51 / 56   83 / 107   93 / 110   91 / 105
+//   f8           36 / 32    38 / 40    46 / 44    53 / 59    61 / 68   92 / 133  112 / 137  106 / 126
+//   back         43 / 33    48 / 36    50 / 47    54 / 55    57 / 57   93 / 109   99 / 115  111 / 145
+//   320 rows of 4096 11.4 / 10.3, 1024 rows 14.2 / 14.6
 // CTAs of 256 threads for 2560 columns: 42, f8 61; the gradients with 160 KB of ring: 5120 columns 81 us, with 200 KB 71.
-RingShape ring_for(int64_t T, int H, int elem, int arrays, bool vec, int least_threads, int bytes) {
+RingShape ring_for(int64_t T, int H, int elem, int arrays, bool vec, int least_groups, int least_threads, int bytes) {
   const int64_t stage = static_cast<int64_t>(arrays) * H * elem;
   const int groups = (H + 15) / 16;
-  if (vec && groups >= 128 && T > 2 * kNormSms)
+  if (vec && groups >= least_groups && T > 2 * kNormSms)
     for (int threads = least_threads; threads <= kMostThreads; threads *= 2) {
       const int per_sm = kMostThreads / threads, n = static_cast<int>(bytes / per_sm / stage);
       if (groups <= 2 * threads && n >= 2)
@@ -644,7 +676,7 @@ cudaError_t launch_rms_norm(const NormLaunch& n, cudaStream_t s) {
   const bool vec = whole_groups(n.x, n.x_stride * elem, n.H) && whole_groups(n.residual, n.residual_stride * elem, n.H) &&
                    whole_groups(n.h, pitch, n.H) && whole_groups(n.y, pitch, n.H) && whole_groups(n.weight, 0, n.H);
   const int arrays = n.residual ? 2 : 1;
-  const RingShape ring = ring_for(n.T, n.H, elem, arrays, vec, 128, kRingBytes);
+  const RingShape ring = ring_for(n.T, n.H, elem, arrays, vec, 128, 128, kRingBytes);
   if (ring.stages) {
     int* report = nullptr;
     if (cudaError_t e = mx_report(&report)) return e;
@@ -688,7 +720,7 @@ cudaError_t launch_rms_norm_backward(const NormBackLaunch& n, cudaStream_t s) {
                    whole_groups(n.d_h, n.d_h_stride * elem, n.H) && whole_groups(n.d_x, pitch, n.H) &&
                    whole_groups(n.weight, 0, n.H);
   const int arrays = n.d_h ? 3 : 2;
-  const RingShape ring = ring_for(n.T, n.H, elem, arrays, vec, 256, kBackRingBytes);   // as many CTAs as back_ctas at most
+  const RingShape ring = ring_for(n.T, n.H, elem, arrays, vec, 224, 256, kBackRingBytes);     // back_ctas at most
   int count = ring.ctas;
   cudaError_t e;
   if (ring.stages) {

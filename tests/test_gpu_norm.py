@@ -179,6 +179,24 @@ def test_repeats_are_bit_equal(ops):
         assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [520, 2048, 2064, 3584, 4096, 4112, 6000, 8192, 8208, 12000, 16384])
+def test_a_row_does_not_depend_on_the_batch(ops, dt, H):
+    """Bits of one row among few rows, among many, and in rows on other boundaries."""
+    x, r, dy = randn(1, 700, H, dt=dt).cuda(), randn(2, 700, H, dt=dt).cuda(), randn(3, 700, H, dt=dt).cuda()
+    w = randn(4, H, dt=dt).cuda()
+    n = ops.rms_norm(x, w, r, quant="mx")
+    dx, _ = ops.rms_norm_backward(dy, n.h, w, n.rstd, r)
+    some = slice(41, 44)
+    m = ops.rms_norm(x[some], w, r[some], quant="mx")
+    wide = [torch.empty(3, H + 5, dtype=t.dtype, device="cuda")[:, 3:H + 3].copy_(t[some]) for t in (x, r, dy)]
+    v = ops.rms_norm(wide[0], w, wide[1], quant="mx")
+    for k in (m, v):
+        assert all(torch.equal(a[some], b) for a, b in zip(n, k))
+    assert torch.equal(ops.rms_norm_backward(dy[some], m.h, w, m.rstd, r[some])[0], dx[some])
+    assert torch.equal(ops.rms_norm_backward(wide[2], m.h, w, m.rstd, wide[1])[0], dx[some])
+
+
 def test_offsets_past_32_bits(ops):
     T, H = 600_000, 4096
     x = torch.empty(T, H, device="cuda", dtype=torch.bfloat16)
