@@ -150,3 +150,23 @@ def test_rounding_of_f8_values(ops):
     for dt in DT:
         got = d64(ops.dequantize8(codes, sf, 256, DT[dt]))
         assert (np.abs(got - want) <= (HALF[dt] + 2.0 ** -24) * 1.01 * np.abs(want) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("quant", ["mx", "f8"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [1040, 1025])
+def test_many_rows_as_few(ops, quant, dt, C):
+    """More than 2^22 groups of 16 columns, where a thread takes several: the bits of the same rows in a small call."""
+    R = 65539
+    x = randn(1, R, C, dt=dt).cuda()
+    codes, sf = ops.quantize8(x, quant)
+    back = ops.dequantize8(codes, sf, C, x.dtype)
+    for at in (0, 1234, 32766, R - 5):
+        part = slice(at, at + 5)
+        c, s = ops.quantize8(x[part], quant)
+        assert torch.equal(codes[part], c) and torch.equal(sf[part], s)
+        assert torch.equal(back[part], ops.dequantize8(c, s, C, x.dtype))
+    # and each row once: the rows between the parts, by a call of a tenth of them at a time
+    for at in range(0, R, 6554):
+        part = slice(at, at + 6554)
+        assert torch.equal(codes[part], ops.quantize8(x[part], quant)[0])
