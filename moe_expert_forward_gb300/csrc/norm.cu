@@ -13,8 +13,8 @@
 //          flight through the sum and the stores. Weights stay in registers.
 //   rows   few rows, short ones, or rows on no 32-byte boundary: loaded by their threads.
 //          Rows longer than the threads hold are read twice.
-// Measured (bf16 with a residual, in a stream of calls, of the copy rate): forward 8192x4096 38 us (83 %), 8192x7168 with f8
-// codes 105 (88 %, of its 533 MB); gradients 45 us (88 %) and 4.5 for the sum of d_weight's parts.  One row of 4096 takes
+// Measured (bf16 with a residual, in a stream of calls, of the copy rate): forward 8192x4096 39 us (82 %), 8192x7168 with f8
+// codes 105 (88 %, of its 533 MB); gradients 46 us (87 %) and 4.5 for the sum of d_weight's parts.  One row of 4096 takes
 // 4 us, latency.
 // For d_weight a thread keeps the same columns of every row that its CTA takes, so the
 // sums over tokens stay in registers too; the CTAs' parts are added up, in order, by a

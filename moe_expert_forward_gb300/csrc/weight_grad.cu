@@ -668,19 +668,25 @@ __global__ void __launch_bounds__(kCopyThreads)
   const int pair = src ? __ldg(src + r) : 0;
   const int64_t t = by_token ? pair / K : r;
   uint4* o = out + r * pieces * 2;
-#pragma unroll 4
-  for (int i0 = 0; i0 < pieces; i0 += 32) {
-    const int i = i0 + lane;
-    uint4 c = make_uint4(0, 0, 0, 0);
-    uint32_t byte = kNoRow;
-    if (pair >= 0 && i < pieces) {
-      c = __ldg(codes + t * pieces + i);
-      byte = __ldg(sf + t * blocks + (i >> 1));
+  constexpr int kFlight = 4;                     // pieces a lane has on their way
+  for (int i0 = lane; i0 - lane < pieces; i0 += 32 * kFlight) {
+    uint4 c[kFlight];
+    uint32_t byte[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int i = i0 + 32 * u;
+      const bool in = pair >= 0 && i < pieces;
+      c[u] = in ? __ldg(codes + t * pieces + i) : make_uint4(0, 0, 0, 0);
+      byte[u] = in ? __ldg(sf + t * blocks + (i >> 1)) : kNoRow;
     }
-    uint32_t w[8];
-    if (__any_sync(0xffffffffu, is_large(byte))) to_bf16<true>(c, byte, w);
-    else to_bf16<false>(c, byte, w);
-    if (i < pieces) st_global_v8(reinterpret_cast<float*>(o + 2 * i), w);
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int i = i0 + 32 * u;
+      uint32_t w[8];
+      if (__any_sync(0xffffffffu, is_large(byte[u]))) to_bf16<true>(c[u], byte[u], w);
+      else to_bf16<false>(c[u], byte[u], w);
+      if (i < pieces) st_global_v8(reinterpret_cast<float*>(o + 2 * i), w);
+    }
   }
 }
 
