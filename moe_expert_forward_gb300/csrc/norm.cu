@@ -214,11 +214,13 @@ __device__ __forceinline__ void back16(const float (&y)[16], const float (&h)[16
   }
 }
 
-// Brings the 16 elements from p on (their first 32-byte sectors) into L2.
+// Brings up to 16 of the n elements from p on into L2, by addresses of theirs 32 bytes apart.
 template <typename T>
-__device__ __forceinline__ void prefetch_group(const T* p) {
-  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p) + 32 * i));
+__device__ __forceinline__ void prefetch_group(const T* p, int n) {
+  constexpr int kStep = 32 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < 16; i += kStep)
+    if (i < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
 }
 
 // One CTA takes rows in a fixed stride; each group of row_threads threads sums d_weight's part of its own rows. The next
@@ -285,12 +287,12 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_backward_kernel(const N
       const int64_t after = row + static_cast<int64_t>(gridDim.x) * rows;      // the row after this one
       if (after < a.T)
 #pragma unroll
-        for (int i = 0; i < G; ++i)
-          if ((i * P + l) * 16 < a.H) {
-            prefetch_group(static_cast<const T*>(a.d_y) + after * a.dy_stride + (i * P + l) * 16);
-            prefetch_group(static_cast<const T*>(a.h) + after * a.h_stride + (i * P + l) * 16);
-            if (a.d_h) prefetch_group(static_cast<const T*>(a.d_h) + after * a.dh_stride + (i * P + l) * 16);
-          }
+        for (int i = 0; i < G; ++i) {
+          const int c = (i * P + l) * 16;
+          prefetch_group(static_cast<const T*>(a.d_y) + after * a.dy_stride + c, a.H - c);
+          prefetch_group(static_cast<const T*>(a.h) + after * a.h_stride + c, a.H - c);
+          if (a.d_h) prefetch_group(static_cast<const T*>(a.d_h) + after * a.dh_stride + c, a.H - c);
+        }
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         load(dy, i * P + l, vy[i]);
