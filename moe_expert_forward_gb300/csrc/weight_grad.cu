@@ -60,6 +60,7 @@ constexpr int kRowStep = 8 * kConvertWarps / (2 * kGroups);      // between the 
 constexpr int kLaneRows = kRowsPerStage / kRowStep;
 constexpr int kSegment = 16;                     // stages of one fp32 accumulator
 constexpr int kMostParts = 16;
+constexpr int64_t kLongTerms = 1 << 18;
 constexpr int kSplitPairs = 76;                  // CTA pairs that parts are made for; the scratch does not depend on the device
 constexpr int kBoxBytes = 32 * 128;              // 32 rows of 128 bytes of results
 
@@ -789,11 +790,13 @@ cudaError_t launch(Args& a, Maps& maps, cudaStream_t s) {
 
 // Parts of a task's contraction of `terms` rows: as many as pairs of SMs have room for, of 8 stages at least. (N = 256, one
 // part / parts, cold caches, us: 8192 rows, C = 4096 69 / 37, C = 256 69 / 22; 65536 rows, C = 2048 451 / 87; 2048 rows, C =
-// 4096 27 / 23; 1024 rows 20 / 21.)
+// 4096 27 / 23; 1024 rows 20 / 21.) Past kLongTerms rows two at least: bf16 results come out of one accumulator only where
+// what it drops, 3.7e-6 of the sum in 8192 rows and growing with them, is a small part of their rounding.
 int parts_of(int64_t tasks, int64_t terms) {
   const int64_t stages = (terms + kRowsPerStage - 1) / kRowsPerStage;
   const int64_t n = kSplitPairs / tasks < stages / 8 ? kSplitPairs / tasks : stages / 8;
-  return static_cast<int>(n < 1 ? 1 : n > kMostParts ? kMostParts : n);
+  const int64_t least = terms > kLongTerms ? 2 : 1;
+  return static_cast<int>(n < least ? least : n > kMostParts ? kMostParts : n);
 }
 int sums_pitch(int C) { return (C + 3) / 4 * 4; }
 

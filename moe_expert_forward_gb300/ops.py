@@ -727,7 +727,8 @@ def swiglu_backward(d_a, kept, kept_sf, routing: Optional[Routing] = None, topk_
     return d_h, d_w
 
 
-GRAD_TILE, GRAD_STAGE, GRAD_PAIRS, GRAD_PARTS, GRAD_DECODE = 256, 64, 76, 16, 4     # mm_moe_weight_grad_scratch_size's rule
+# mm_moe_weight_grad_scratch_size's rule
+GRAD_TILE, GRAD_STAGE, GRAD_PAIRS, GRAD_PARTS, GRAD_DECODE, GRAD_LONG = 256, 64, 76, 16, 4, 1 << 18
 
 
 def _grad_scratch(d_y: int, pitch: int, rows: int, N: int, sf: int, C: int, T: int, K: int, E: int, by_token: bool) -> int:
@@ -740,8 +741,8 @@ def _grad_scratch(d_y: int, pitch: int, rows: int, N: int, sf: int, C: int, T: i
     elif sf % 4 or blocks % 4:
         n += -(-rows * -(-blocks // 4) * 4 // 16) * 16
     tasks = max(E, 1) * -(-N // GRAD_TILE) * -(-C // GRAD_TILE)
-    stages = -(-(T * K // E if E else rows) // GRAD_STAGE)
-    parts = min(GRAD_PAIRS // tasks, stages // 8, GRAD_PARTS)
+    terms = T * K // E if E else rows
+    parts = max(min(GRAD_PAIRS // tasks, -(-terms // GRAD_STAGE) // 8, GRAD_PARTS), 2 if terms > GRAD_LONG else 1)
     return n + (parts * max(E, 1) * N * -(-C // 4) * 16 if parts > 1 else 0)
 
 

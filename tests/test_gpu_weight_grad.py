@@ -123,6 +123,20 @@ def test_dense_random_values(ops):
     check(ops, randn(2, 20000, 72, dt="bf16"), x, exact=False)
 
 
+def test_bf16_results_of_very_long_sums(ops):
+    """270000 rows of one sign over 42 tiles: the sums of both result types are the same, and right."""
+    R, N, C = 270_000, 1792, 1536
+    g = torch.Generator(device="cuda").manual_seed(5)
+    d_y = torch.rand(R, N, device="cuda", generator=g).bfloat16()
+    codes, sf = ops.quantize8(torch.rand(R, C, device="cuda", generator=g))
+    got = ops.weight_grad(d_y, codes, sf, C, dtype=torch.float32)
+    assert torch.equal(ops.weight_grad(d_y, codes, sf, C), got.bfloat16())
+    xv = ops.dequantize8(codes, sf, C, torch.float32)[:, ::100].double()
+    want = d_y[:, ::100].double().t() @ xv
+    # 16 rows an MMA and 64 MMAs an accumulator, each dropping less than a step (2 U) of it; then 264 additions of U
+    assert ((got[::100, ::100].double() - want).abs() <= (64 * 16 * 2 + 266) * U * want).all()
+
+
 def test_scales_at_the_ends_of_their_range(ops):
     """Codes and scale bytes as a caller may hold them: 2^-127 to 2^127, subnormal codes, both zeros."""
     codes = torch.arange(256, dtype=torch.uint8)

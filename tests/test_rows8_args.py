@@ -112,9 +112,9 @@ def test_binding_sizes_agree_with_the_library(M):
         for H in (1, 16, 17, 512, 513, 1001, 1024, 1025, 4096, 7168, 8192, 8193, 16384, 16400, 100000):
             assert M.mm_moe_rms_norm_scratch_size(T, H) == ops._norm_scratch(T, H), (T, H)
     for at in (A, A + 2, A + 8, A + 16):
-        for pitch, N in ((64, 64), (64, 63), (65, 64), (72, 65), (1, 1), (8, 1)):
+        for pitch, N in ((64, 64), (64, 63), (65, 64), (72, 65), (1, 1), (8, 1), (5000, 4096), (5001, 5000)):
             for sf, C in ((A, 128), (A, 129), (A, 96), (A + 1, 256), (A + 4, 1024)):
-                for rows in (77, 5000, 100000):
+                for rows in (77, 5000, 100000, 1 << 18, (1 << 18) + 1):
                     for T, K, E, by_token in ((0, 0, 0, False), (2000, 2, 3, False), (2000, 2, 3, True), (50000, 6, 9, True)):
                         args = (at, pitch, rows, N, sf, C, T, K, E, by_token)
                         assert M.mm_moe_weight_grad_scratch_size(*args) == ops._grad_scratch(*args), args

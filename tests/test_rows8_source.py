@@ -25,5 +25,6 @@ def test_the_binding_has_the_kernels_constants():
     found = {n: int(re.search(rf"constexpr int [^;]*\b{n} = (\d+)", text).group(1))
              for n in ("kTile", "kRowsPerStage", "kSplitPairs", "kMostParts", "kDecodeTiles")}
     assert (ops.GRAD_TILE, ops.GRAD_STAGE, ops.GRAD_PAIRS, ops.GRAD_PARTS, ops.GRAD_DECODE) == tuple(found.values())
+    assert re.search(r"kLongTerms = 1 << (\d+)", text).group(1) == str(ops.GRAD_LONG.bit_length() - 1)
     sms = int(re.search(r"kNormSms = (\d+)", source("internal.h")).group(1))
     assert ops.NORM_CTAS == 2 * sms
