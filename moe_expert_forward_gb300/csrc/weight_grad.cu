@@ -619,11 +619,12 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
               else tma_store_box<false>(&maps.out, box, col, n0, t.slab);
             }
           } else {
-            // row by row, consecutive lanes consecutive words
+            // row by row, consecutive lanes consecutive words (44 experts of 3188x2181, unrolled by 4 / whole, us: fp32 618 /
+            // 510, bf16 554 / 476)
             __syncwarp();
             const int left = args.C - col - lane * (4 / static_cast<int>(sizeof(T)));      // columns from this lane's on
             char* q = args.out + row * args.out_pitch + col * static_cast<int64_t>(sizeof(T)) + lane * 4;
-#pragma unroll 4
+#pragma unroll
             for (int r = 0; r < 32; ++r, q += args.out_pitch) {
               const uint32_t v = *reinterpret_cast<const uint32_t*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
               if (r >= rows || left <= 0) continue;
