@@ -555,7 +555,8 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
  * A row's last block is filled up with zeros; codes round to nearest, ties to the even
  * code, and are 16-byte aligned.  A block with a NaN or an infinity gets zero codes and
  * a scale of NaN (MX: byte 255), and everything computed from it is NaN; codes 0x7F and
- * 0xFF do not occur.  Results of these calls overlap no operand. */
+ * 0xFF do not occur, and stand for NaN in the calls that read codes which another quantiser
+ * wrote.  Results of these calls overlap no operand. */
 int mm_moe_rows_quantize(const void* x, int dtype, int64_t row_stride, int64_t R, int C, int variant, void* codes,
                          void* sf, void* stream);
 

@@ -258,15 +258,21 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // 16 codes times 2^(byte - 127) as 16 bf16, exact where bf16 has the value; byte kNoRow: zeros.
 // A code's sign, exponent and fraction at bf16's bits 15 and 10 to 4 stand for the same value times 2^-120, bf16's larger
 // bias (subnormals too): the high byte is the sign and three bits of the exponent, the low one the other four bits.
-// kLarge: bytes of 135 (2^8) and up too, whose factor is past bf16's range and comes in two, and 255, NaN.
+// Codes of NaN (0x7F, 0xFF) would come out as +-480 that way: kRare also takes these, bytes of 135 (2^8) and up, whose factor
+// is past bf16's range and comes in two, and 255, NaN. is_rare: whether 16 codes and their byte need it.
 constexpr uint32_t kNoRow = 0u - 120u;
 __device__ __forceinline__ bool is_large(uint32_t byte) { return byte - 135u < 121u; }
-template <bool kLarge>
+// bit 7 of each byte: the code there is NaN
+__device__ __forceinline__ uint32_t nan_codes(uint32_t codes) { return ((codes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ bool is_rare(const uint4& c, uint32_t byte) {
+  return is_large(byte) || (nan_codes(c.x) | nan_codes(c.y) | nan_codes(c.z) | nan_codes(c.w)) != 0;
+}
+template <bool kRare>
 __device__ __forceinline__ void to_bf16(const uint4& c, uint32_t byte, uint32_t (&w)[8]) {
   const uint32_t in[4] = {c.x, c.y, c.z, c.w};
   // 2^(byte - 127) 2^120 has the exponent field byte + 120, twice in a word
   uint32_t p1 = (byte + 120u) * 0x00800080u, p2 = 0x3F803F80u;
-  if (kLarge && is_large(byte)) {
+  if (kRare && is_large(byte)) {
     p1 = byte == 255u ? 0x7FC07FC0u : 254u * 0x00800080u;
     p2 = (byte - 134u + 127u) * 0x00800080u;
   }
@@ -276,9 +282,10 @@ __device__ __forceinline__ void to_bf16(const uint4& c, uint32_t byte, uint32_t 
     const uint32_t low = (in[i] << 4) & 0xF0F0F0F0u;
     w[2 * i] = mul_bf16x2(__byte_perm(low, high, 0x5140), p1);
     w[2 * i + 1] = mul_bf16x2(__byte_perm(low, high, 0x7362), p1);
-    if (kLarge) {
-      w[2 * i] = mul_bf16x2(w[2 * i], p2);
-      w[2 * i + 1] = mul_bf16x2(w[2 * i + 1], p2);
+    if (kRare) {
+      const uint32_t nan = byte == kNoRow ? 0u : nan_codes(in[i]) >> 7;        // bits 0, 8, 16 and 24
+      w[2 * i] = mul_bf16x2(w[2 * i], p2) | (nan & 1u) * 0x7FC0u | (nan >> 8 & 1u) * 0x7FC00000u;
+      w[2 * i + 1] = mul_bf16x2(w[2 * i + 1], p2) | (nan >> 16 & 1u) * 0x7FC0u | (nan >> 24) * 0x7FC00000u;
     }
   }
 }
@@ -496,11 +503,11 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
           c[i] = *reinterpret_cast<const uint4*>(raw0 + raw.s * kRawBytes + i * kRowStep * 128);
           byte[i] = sf0[raw.s * kRawSf + i * kRowStep * 4];
         }
-        bool large = false;
+        bool rare = false;
 #pragma unroll
         for (int i = 0; i < kLaneRows; ++i) {
           if (my_row + kRowStep * i >= rows) byte[i] = kNoRow;
-          large = large || is_large(byte[i]);
+          rare = rare || is_rare(c[i], byte[i]);
         }
         if (!mbar_wait_warp(&empty[ring.s], ring.phase ^ 1, st, s_abort, kSiteEmpty)) break;
         auto decode = [&](auto tag) {
@@ -513,7 +520,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
             *reinterpret_cast<uint4*>(p + hi) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         };
-        if (__any_sync(0xffffffffu, large)) decode(std::true_type{});
+        if (__any_sync(0xffffffffu, rare)) decode(std::true_type{});
         else decode(std::false_type{});
         __syncwarp();
         if (lane == 0) {
@@ -685,7 +692,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     for (int u = 0; u < kFlight; ++u) {
       const int i = i0 + 32 * u;
       uint32_t w[8];
-      if (__any_sync(0xffffffffu, is_large(byte[u]))) to_bf16<true>(c[u], byte[u], w);
+      if (__any_sync(0xffffffffu, is_rare(c[u], byte[u]))) to_bf16<true>(c[u], byte[u], w);
       else to_bf16<false>(c[u], byte[u], w);
       if (i < pieces) st_global_v8(reinterpret_cast<float*>(o + 2 * i), w);
     }

@@ -275,3 +275,26 @@ def test_a_stage_that_never_comes(ops, monkeypatch, rows, N, C, routed):
     assert ops.sync_status() == (0, 0)
     monkeypatch.setattr(ops, "lib", lambda: real)
     assert torch.equal(ops.weight_grad(d_y, codes, sf, C, r), want) and ops.sync_status() == (0, 0)
+
+
+@pytest.mark.parametrize("N", [8, 1025])
+def test_codes_of_nan(ops, N):
+    """0x7F and 0xFF, which the quantiser does not write but a caller's tensor may hold: NaN, as dequantize8 has it, in
+    their own sums alone; none of it from rows that are no expert's."""
+    codes, sf = ops.quantize8(whole(1, 40, 70).cuda())
+    d_y = whole(2, 40, N).bfloat16().cuda()
+    clean = ops.weight_grad(d_y, codes, sf, 70, dtype=torch.float32)
+    for row, col, code in ((0, 0, 0x7F), (3, 17, 0xFF), (21, 38, 0x7F), (39, 69, 0xFF)):
+        codes[row, col] = code
+    bad = torch.isnan(ops.dequantize8(codes, sf, 70)).any(0)
+    assert bad.nonzero().flatten().tolist() == [0, 17, 38, 69]
+    got = ops.weight_grad(d_y, codes, sf, 70, dtype=torch.float32)
+    assert torch.isnan(got[:, bad]).all() and torch.equal(got[:, ~bad], clean[:, ~bad])
+    r = ops.sort_tokens(torch.tensor([[0], [1], [1]], dtype=torch.int32, device="cuda"), 3)
+    codes, sf = ops.quantize8(whole(3, r.rows, 70).cuda())
+    d_y = whole(4, r.rows, N).bfloat16().cuda()
+    want = ops.weight_grad(d_y, codes, sf, 70, r)
+    padding = torch.ones(r.rows, dtype=torch.bool, device="cuda")
+    padding[r.slot.flatten().long()] = False
+    codes[padding] = 0x7F
+    assert torch.equal(ops.weight_grad(d_y, codes, sf, 70, r), want)
