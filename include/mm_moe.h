@@ -630,8 +630,9 @@ int mm_moe_swiglu_backward(const void* d_a, int dtype, int64_t d_stride, const v
  *          zero for an expert without rows
  *   scratch  mm_moe_weight_grad_scratch_size bytes, 32-byte aligned: x in bf16 with by_token or
  *          N > 1024, copies of d_y and of sf where their rows do not start on 16-byte and 4-byte
- *          boundaries, and partial sums where few columns share many rows (K = E = 0: dense); none
- *          otherwise (0 bytes, null allowed)
+ *          boundaries, partial sums where few columns share many rows, and 20 MB at most where one sum
+ *          may have more than 16384 rows (T * K, or all dense ones; K = E = 0: dense); none otherwise
+ *          (0 bytes, null allowed)
  * A device wait past timeout_ms (0: 2000) leaves out undefined and is reported by
  * mm_moe_ops_status.  debug_flags: 0; bit 0 leaves one stage of each CTA unloaded, so that its
  * wait runs out. */

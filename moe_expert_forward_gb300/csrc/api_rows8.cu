@@ -23,6 +23,8 @@ bool rows_known(int dtype, int64_t rows, int cols) {
 }
 // rows of one sum of a weight gradient: all (E = 0: dense), or an expert's on average
 int64_t terms_of(int64_t rows, int T, int K, int E) { return E ? static_cast<int64_t>(T) * K / E : rows; }
+// and at most: one expert may take every pair
+int64_t longest_of(int64_t rows, int T, int K, int E) { return E ? static_cast<int64_t>(T) * K : rows; }
 // codes and scales of rows, both or neither
 bool held_ok(const void* codes, const void* sf, int variant) {
   if (!codes || !sf) return !codes && !sf;
@@ -145,7 +147,8 @@ int mm_moe_weight_grad_scratch_size(const void* d_y, int64_t d_stride, int64_t r
   if (!bytes || rows < 0 || rows > kMaxRows || N < 1 || N > kMaxCols || d_stride < N || C < 1 || C > kMaxCols || T < 0 ||
       K < 0 || K > kMaxK || E < 0 || E > kMaxE || !K != !E || (by_token && !E))
     return MM_MOE_ERR_INVALID_ARG;
-  *bytes = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0, E ? E : 1, terms_of(rows, T, K, E));
+  *bytes = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0, E ? E : 1, terms_of(rows, T, K, E),
+                                     longest_of(rows, T, K, E));
   return MM_MOE_OK;
 }
 
@@ -163,8 +166,8 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
   if (!out || !aligned(out, dtype_size(dtype))) return MM_MOE_ERR_INVALID_ARG;
   if (rows > 0 && !(cnt && T == 0) && (!d_y || !codes || !aligned(d_y, 2) || !held_ok(codes, sf, MM_MOE_VARIANT_MX)))
     return MM_MOE_ERR_INVALID_ARG;
-  const int64_t terms = terms_of(rows, T, K, cnt ? E : 0);
-  const size_t need = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0, E, terms);
+  const int64_t terms = terms_of(rows, T, K, cnt ? E : 0), longest = longest_of(rows, T, K, cnt ? E : 0);
+  const size_t need = weight_grad_scratch_bytes(d_y, d_stride, rows, N, sf, C, by_token != 0, E, terms, longest);
   if (need && (!scratch || !aligned(scratch, 32))) return MM_MOE_ERR_INVALID_ARG;
   if (scratch_bytes < need) return MM_MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!device_ok()) return MM_MOE_ERR_UNSUPPORTED;
@@ -173,7 +176,7 @@ int mm_moe_weight_grad(const void* d_y, int64_t d_stride, int64_t rows, int N, c
     return done(cudaMemsetAsync(out, 0, static_cast<size_t>(E) * N * C * dtype_size(dtype), s));
   const WeightGradLaunch p{d_y, d_stride, rows, N, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(sf),
                            C, cnt, blk_off, src, by_token != 0, K, E, block_m,
-                           terms, dtype, out, scratch,
+                           terms, longest, dtype, out, scratch,
                            static_cast<uint64_t>(timeout_ms ? timeout_ms : 2000) * 1000000ull, (debug_flags & 1) != 0};
   return done(launch_weight_grad(p, s));
 }

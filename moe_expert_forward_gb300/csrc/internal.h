@@ -293,6 +293,7 @@ struct WeightGradLaunch {
   bool by_token;             // x's rows are tokens
   int K, E, block_m;
   int64_t terms;             // rows of a sum, of an expert on average
+  int64_t longest;           // rows of a sum, at most
   int dtype;                 // of out: fp32 or bf16
   void* out;
   void* scratch;             // weight_grad_scratch_bytes
@@ -300,7 +301,7 @@ struct WeightGradLaunch {
   bool unreachable;
 };
 size_t weight_grad_scratch_bytes(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C,
-                                 bool by_token, int E, int64_t terms);
+                                 bool by_token, int E, int64_t terms, int64_t longest);
 int64_t weight_grad_tasks(int E, int N, int C);
 cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s);
 

@@ -19,9 +19,16 @@
 // scratch and are added up in order by a second kernel. (Clusters of 8 CTAs that add up in shared memory do not all fit
 // at once: 8192x256x4096 50 us.)
 //
-// fp32 results are sums of sums over 1024 rows (kSegment stages), added by the epilogue:
-// the MMA's accumulation drops bits below its accumulator's last, and 8192 rows in one
-// accumulator were 3.7e-6 off (rounding to nearest: 3.6e-7).
+// The MMA's accumulation drops bits below its accumulator's last: of random sign 8192 rows in
+// one accumulator are 3.7e-6 off (rounding to nearest: 3.6e-7), of one sign 4.5e-9 a row too
+// small, so that 2^18 rows lose a third of bf16's half step and 2^21 three whole ones.  fp32
+// results are sums of sums over 1024 rows (kSegment stages), added by the epilogue in memory;
+// bf16 results of more than 16384 rows (kLongSegment; what one accumulator of these drops is
+// 4 % of a half step at most) of sums over 16384, which the epilogue keeps in a tile of fp32
+// scratch of the pair's own. How many rows an expert has is known on the device alone, and one
+// may have all pairs, so the kernel that can do so (kLong) runs wherever there are more pairs,
+// or dense rows (bf16, cold caches, us, one accumulator / several: 65536x4096x4096 1298 / 1325,
+// 65536x1024x4096 404 / 440, 8 experts of 24576 rows and 2048x2048 993 / 1010).
 //
 // Codes come by TMA too, their scales by 4-byte asynchronous copies, into a ring of their own: converters that load
 // for themselves keep the SM's loads in flight at their limit, and wait for it (1000 cycles a stage and more).  With
@@ -58,11 +65,13 @@ constexpr int kRawSf = kRowsPerStage * 4;        // and their scales
 constexpr int kGroups = 3;                       // of converter warps, which take turns at the stages
 constexpr int kRowStep = 8 * kConvertWarps / (2 * kGroups);      // between the rows of a converter lane
 constexpr int kLaneRows = kRowsPerStage / kRowStep;
-constexpr int kSegment = 16;                     // stages of one fp32 accumulator
+constexpr int kSegment = 16;                     // stages of one accumulator, fp32 results
+constexpr int kLongSegment = 256;                // bf16 results
 constexpr int kMostParts = 16;
 constexpr int64_t kLongTerms = 1 << 18;
 constexpr int kSplitPairs = 76;                  // CTA pairs that parts are made for; the scratch does not depend on the device
 constexpr int kBoxBytes = 32 * 128;              // 32 rows of 128 bytes of results
+constexpr size_t kPairSums = size_t(kTile) * kTile * sizeof(float);      // a pair's tile
 
 // kDecoded: x comes in bf16. A stage then takes 1700 cycles from its copies' issue to their landing, and six of them are
 // what covers that (four: 800 cycles a stage); without the ring of codes there is room.
@@ -100,6 +109,7 @@ struct Args {
   const int* blk_off;
   char* out;
   int64_t out_pitch;         // bytes of a row of out; [parts][E][N] rows
+  float4* sums;              // kLong: kPairSums bytes a pair
   int unreachable;           // the CTA's last stage is not handed over
   int* report;
   uint64_t timeout_ns;
@@ -294,8 +304,9 @@ struct Maps {
   CUtensorMap d_y, codes, out;
 };
 
-// kTma: out's rows are 16-byte aligned, and results leave by TMA. kDecoded: x comes in bf16.
-template <typename T, bool kTma, bool kDecoded>
+// kTma: out's rows are 16-byte aligned, and results leave by TMA. kDecoded: x comes in bf16. kLong (bf16 results): a sum may
+// have more than one accumulator.
+template <typename T, bool kTma, bool kDecoded, bool kLong>
 __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
     weight_grad_kernel(const __grid_constant__ Maps maps, const Args args) {
   using Smem = Smem<kDecoded>;
@@ -353,8 +364,10 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
   const uint32_t tmem = *s_tmem;
   const int ntasks = args.parts == 1 ? args.tasks + (args.tasks - args.whole) : args.tasks * args.parts;
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-  // accumulators of a task's n stages
-  auto segments = [](int n) { return sizeof(T) == 4 ? (n + kSegment - 1) / kSegment : 1; };
+  static_assert(sizeof(T) == 2 || !kLong);
+  constexpr bool kSeveral = kLong || sizeof(T) == 4;
+  constexpr int kMost = sizeof(T) == 4 ? kSegment : kLongSegment;
+  auto segments = [](int n) { return kSeveral ? (n + kMost - 1) / kMost : 1; };      // accumulators of a task's n stages
 
   if (warp == kTmaWarp || (kDecoded && warp == kCodesWarp)) {
     // ------------------------------------------------------------------ d_y by TMA, and x in bf16 by another warp: a copy
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
         acc = tmem + buf * kTile;
         if (kDecoded) idesc = at.t.cols == kTile ? kIdesc : kIdescHalf;
         left = at.t.end - at.t.ks;
-        if (sizeof(T) == 4) left = min(left, kSegment);
+        if (kSeveral) left = min(left, kMost);
         in_acc = 0;
         rows = at.t.rows - at.t.ks * kRowsPerStage;
         live = !__any_sync(0xffffffffu, *s_abort) && wait(&tempty[buf], ((it >> 1) & 1) ^ 1, kSiteTmemEmpty);
@@ -571,7 +584,8 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
       const int nks = t.end - t.ks;              // 0: an expert without rows, or without any for this part
       const int cols = kDecoded ? t.cols : kTile;
       bool ok = true;
-      for (int seg = 0; seg < max(segments(nks), 1) && ok; ++seg) {
+      const int segs = max(segments(nks), 1);
+      for (int seg = 0; seg < segs && ok; ++seg) {
         const int buf = it & 1;
         ok = nks == 0 || mbar_wait_warp(&tfull[buf], (it >> 1) & 1, st, s_abort, kSiteTmemFull);
         if (!ok) break;
@@ -602,6 +616,21 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
             if (!kDecoded) fetch(c);
 #pragma unroll
             for (int h = 0; h < kBox; h += 32) tmem_loaded(*reinterpret_cast<uint32_t(*)[32]>(v + h));
+            if (kLong && segs > 1) {             // this lane's own sums so far
+              float4* sum = args.sums + ((blockIdx.x * kEpiWarps + warp) * (kTile / 4) + c / 4) * 32 + lane;
+#pragma unroll
+              for (int j = 0; j < kBox; j += 4) {
+                float4 f = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
+                                       __uint_as_float(v[j + 3]));
+                if (seg > 0) {
+                  const float4 g = sum[j * 8];
+                  f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
+                }
+                if (seg + 1 < segs) sum[j * 8] = f;
+                v[j] = __float_as_uint(f.x); v[j + 1] = __float_as_uint(f.y);
+                v[j + 2] = __float_as_uint(f.z); v[j + 3] = __float_as_uint(f.w);
+              }
+            }
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               w[j] = sizeof(T) == 4 ? v[j] : pack2<T>(v[(2 * j) % kBox], v[(2 * j + 1) % kBox]);
@@ -609,7 +638,7 @@ __global__ void __launch_bounds__(kThreads<kDecoded>, 1)
             else if (kDecoded) fetch(c + kBox);
           }
           const int col = t.c0 + c;
-          if (rows <= 0 || col >= args.C) continue;
+          if (rows <= 0 || col >= args.C || (kLong && seg + 1 < segs)) continue;
           uint8_t* box = smem + Smem::out + (warp * Smem::kBoxes + box_turn % Smem::kBoxes) * kBoxBytes;
           ++box_turn;
           if (kTma && lane == 0) tma_store_read<Smem::kBoxes - 1>();       // its last results have left it
@@ -757,7 +786,7 @@ cudaError_t add_parts(const float* sums, int parts, int64_t rows, int C, int pit
 }
 
 // a.out and a.out_pitch: where the sums go, of T.
-template <typename T, bool kDecoded>
+template <typename T, bool kDecoded, bool kLong = false>
 cudaError_t launch(Args& a, Maps& maps, cudaStream_t s) {
   const bool tma = (reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(a.out_pitch)) % 16 == 0;
   if (tma) {
@@ -769,12 +798,13 @@ cudaError_t launch(Args& a, Maps& maps, cudaStream_t s) {
                     dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  auto kernel = tma ? weight_grad_kernel<T, true, kDecoded> : weight_grad_kernel<T, false, kDecoded>;
+  auto kernel = tma ? weight_grad_kernel<T, true, kDecoded, kLong> : weight_grad_kernel<T, false, kDecoded, kLong>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   if (cudaError_t e = configure_kernel(fn, 0, Smem<kDecoded>::total(kMaxE))) return e;
   int most = 0;
   if (cudaError_t e = max_pair_clusters(fn, kThreads<kDecoded>, Smem<kDecoded>::total(kMaxE), &most)) return e;
   if (most < 1) return cudaErrorInvalidConfiguration;
+  if (kLong && most > kSplitPairs) most = kSplitPairs;           // what the scratch is for
   // The tasks past the last whole round are taken in halves where these fit a round (8192x4096x4096, 256 tasks on 76 pairs,
   // 174 us for 177 with all whole; 2048x2560x2560 34 for 36). In parts, whose fp32 sums a kernel adds up, they took 2 us
   // less at 8192 rows and 7 more at 4096.
@@ -798,8 +828,8 @@ cudaError_t launch(Args& a, Maps& maps, cudaStream_t s) {
 
 // Parts of a task's contraction of `terms` rows: as many as pairs of SMs have room for, of 8 stages at least. (N = 256, one
 // part / parts, cold caches, us: 8192 rows, C = 4096 69 / 37, C = 256 69 / 22; 65536 rows, C = 2048 451 / 87; 2048 rows, C =
-// 4096 27 / 23; 1024 rows 20 / 21.) Past kLongTerms rows two at least: bf16 results come out of one accumulator only where
-// what it drops, 3.7e-6 of the sum in 8192 rows and growing with them, is a small part of their rounding.
+// 4096 27 / 23; 1024 rows 20 / 21.) Past kLongTerms rows two at least: both types' results are then the same
+// fp32 sums.
 int parts_of(int64_t tasks, int64_t terms) {
   const int64_t stages = (terms + kRowsPerStage - 1) / kRowsPerStage;
   const int64_t n = kSplitPairs / tasks < stages / 8 ? kSplitPairs / tasks : stages / 8;
@@ -817,20 +847,23 @@ constexpr int kDecodeTiles = 4;
 bool decodes_first(int N, bool by_token) { return by_token || N > kDecodeTiles * kTile; }
 
 // What a call keeps in its scratch, in this order: x in bf16 (rows of 64 bytes' multiples, stored 32 bytes at a time), a
-// copy of d_y, one of the scales, and parts' sums. Bytes, 0: none.
+// copy of d_y, one of the scales, and the sums of parts or of a pair's accumulators. Bytes, 0: none. longest: rows of a sum,
+// at most (one expert may take them all).
 struct Copies {
   size_t x, d_y, sf, sums;
 };
 Copies copies_of(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C, bool by_token, int E,
-                 int64_t terms) {
+                 int64_t terms, int64_t longest) {
   const int blocks = blocks8(C, MM_MOE_VARIANT_MX);
   Copies c{0, 0, 0, 0};
   if (reinterpret_cast<uintptr_t>(d_y) % 16 || d_stride % 8) c.d_y = static_cast<size_t>(rows) * ((N + 7) / 8) * 16;
   if (decodes_first(N, by_token)) c.x = static_cast<size_t>(rows) * blocks * kMxBlock * 2;
   else if (reinterpret_cast<uintptr_t>(sf) % 4 || blocks % 4)
     c.sf = (static_cast<size_t>(rows) * ((blocks + 3) / 4) * 4 + 15) / 16 * 16;
-  const int parts = parts_of(weight_grad_tasks(E, N, C), terms);
+  const int64_t tasks = weight_grad_tasks(E, N, C);
+  const int parts = parts_of(tasks, terms);
   if (parts > 1) c.sums = static_cast<size_t>(parts) * E * N * sums_pitch(C) * sizeof(float);
+  else if (longest > kLongSegment * kRowsPerStage) c.sums = (2 * tasks < kSplitPairs ? 2 * tasks : kSplitPairs) * kPairSums;
   return c;
 }
 
@@ -841,8 +874,8 @@ int64_t weight_grad_tasks(int E, int N, int C) {
 }
 
 size_t weight_grad_scratch_bytes(const void* d_y, int64_t d_stride, int64_t rows, int N, const void* sf, int C,
-                                 bool by_token, int E, int64_t terms) {
-  const Copies c = copies_of(d_y, d_stride, rows, N, sf, C, by_token, E, terms);
+                                 bool by_token, int E, int64_t terms, int64_t longest) {
+  const Copies c = copies_of(d_y, d_stride, rows, N, sf, C, by_token, E, terms, longest);
   return c.x + c.d_y + c.sf + c.sums;
 }
 
@@ -862,7 +895,7 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
   a.timeout_ns = p.timeout_ns;
   const int blocks = blocks8(p.C, MM_MOE_VARIANT_MX);
   const bool decoded = decodes_first(p.N, p.by_token);
-  const Copies copies = copies_of(p.d_y, p.d_stride, p.rows, p.N, p.sf, p.C, p.by_token, p.E, p.terms);
+  const Copies copies = copies_of(p.d_y, p.d_stride, p.rows, p.N, p.sf, p.C, p.by_token, p.E, p.terms, p.longest);
   const void *d_y = p.d_y, *codes = p.codes, *sf = p.sf;
   uint64_t pitch = static_cast<uint64_t>(p.d_stride) * 2;
   char* to = static_cast<char*>(p.scratch);
@@ -901,9 +934,14 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
     using T = decltype(tag);
     return decoded ? launch<T, true>(a, maps, s) : launch<T, false>(a, maps, s);
   };
-  if (a.parts == 1) return p.dtype == MM_MOE_DTYPE_F32 ? go(float{}) : go(__nv_bfloat16{});
-  const int pitch_c = sums_pitch(p.C);
   float* sums = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + copies.x + copies.d_y + copies.sf);
+  if (a.parts == 1) {
+    if (p.dtype == MM_MOE_DTYPE_F32) return go(float{});
+    if (!copies.sums) return go(__nv_bfloat16{});
+    a.sums = reinterpret_cast<float4*>(sums);
+    return decoded ? launch<__nv_bfloat16, true, true>(a, maps, s) : launch<__nv_bfloat16, false, true>(a, maps, s);
+  }
+  const int pitch_c = sums_pitch(p.C);
   a.out = reinterpret_cast<char*>(sums);
   a.out_pitch = static_cast<int64_t>(pitch_c) * sizeof(float);
   if (cudaError_t e = go(float{})) return e;

@@ -729,11 +729,12 @@ def swiglu_backward(d_a, kept, kept_sf, routing: Optional[Routing] = None, topk_
 
 # mm_moe_weight_grad_scratch_size's rule
 GRAD_TILE, GRAD_STAGE, GRAD_PAIRS, GRAD_PARTS, GRAD_DECODE, GRAD_LONG = 256, 64, 76, 16, 4, 1 << 18
+GRAD_SEGMENT = 256
 
 
 def _grad_scratch(d_y: int, pitch: int, rows: int, N: int, sf: int, C: int, T: int, K: int, E: int, by_token: bool) -> int:
     """x in bf16 for tokens' rows or many tiles of N; copies of rows that are not 16-byte, or of scales that are not 4-byte,
-    aligned; and partial sums (E = 0: dense)."""
+    aligned; and partial sums, or those of a pair's accumulators (E = 0: dense)."""
     blocks = -(-C // 32)
     n = 0 if d_y % 16 == 0 and pitch % 8 == 0 else rows * -(-N // 8) * 16
     if by_token or N > GRAD_DECODE * GRAD_TILE:
@@ -743,7 +744,11 @@ def _grad_scratch(d_y: int, pitch: int, rows: int, N: int, sf: int, C: int, T: i
     tasks = max(E, 1) * -(-N // GRAD_TILE) * -(-C // GRAD_TILE)
     terms = T * K // E if E else rows
     parts = max(min(GRAD_PAIRS // tasks, -(-terms // GRAD_STAGE) // 8, GRAD_PARTS), 2 if terms > GRAD_LONG else 1)
-    return n + (parts * max(E, 1) * N * -(-C // 4) * 16 if parts > 1 else 0)
+    if parts > 1:
+        return n + parts * max(E, 1) * N * -(-C // 4) * 16
+    if (T * K if E else rows) > GRAD_SEGMENT * GRAD_STAGE:
+        n += min(2 * tasks, GRAD_PAIRS) * GRAD_TILE * GRAD_TILE * 4
+    return n
 
 
 def weight_grad(d_y, codes, sf, C: int, routing: Optional[Routing] = None, by_token: bool = False,

@@ -298,3 +298,64 @@ def test_codes_of_nan(ops, N):
     padding[r.slot.flatten().long()] = False
     codes[padding] = 0x7F
     assert torch.equal(ops.weight_grad(d_y, codes, sf, 70, r), want)
+
+
+def long_rows(n):
+    """n > 16384 values of d_y whose sum with x = 1 shows in fp32 and in bf16 whether an accumulator took more than its rows.
+    The first 16384 sum up to 2^24 + 2^16, half way between two bf16 values, each partial sum exact; of those behind, 16 (one
+    MMA's) make 1, half of the accumulator's last place there: dropped if they are added to it one MMA at a time, and exact in
+    sums of their own."""
+    v = torch.full((n,), 2.0 ** -4)
+    v[:16384] = 2.0 ** 10
+    v[:64] = 2.0 ** 11
+    return v, 2.0 ** 24 + 2.0 ** 16 + (n - 16384) / 16
+
+
+@pytest.mark.parametrize("N,C", [(1792, 1536), (1024, 2560), (1793, 1535), (1024, 2559)])
+def test_accumulators_of_long_dense_sums(ops, N, C):
+    """40 tiles and more, so that no sum is split into parts: x decoded first and by the converters, results by TMA and row
+    by row."""
+    v, total = long_rows(40_000)
+    d_y = v.cuda().bfloat16()[:, None].repeat(1, N)
+    codes, sf = ops.quantize8(torch.ones(len(v), C, device="cuda"))
+    for dtype in (torch.float32, torch.bfloat16):
+        got = ops.weight_grad(d_y, codes, sf, C, dtype=dtype)
+        assert torch.equal(got, torch.full_like(got, total)), dtype          # bf16: up from half way
+
+
+@pytest.mark.parametrize("by_token", [False, True])
+@pytest.mark.parametrize("K", [1, 2])
+def test_accumulators_of_an_expert_that_takes_nearly_all(ops, K, by_token):
+    """One of 64 experts has 40000 rows (K = 2: every token names it twice), two others a few, the average is 640 (1250)."""
+    T = 40_000 // K
+    idx = torch.full((T + 5, K), 7, dtype=torch.int32)
+    idx[T:] = torch.tensor([0, 0, 63, 0, 63], dtype=torch.int32)[:, None]
+    r = ops.sort_tokens(idx.cuda(), 64)
+    v, total = long_rows(T * K)
+    d_y = torch.full((r.rows, 72), float("nan"))
+    rows = torch.arange(T * K) + r.blk_off[7].item() * r.block_m
+    few = torch.ones(r.rows, dtype=torch.bool)
+    few[rows] = False
+    d_y[few & (r.src.cpu() >= 0)] = 2.0
+    d_y[rows] = v[:, None]
+    codes, sf = ops.quantize8(torch.ones(T + 5 if by_token else r.rows, 100, device="cuda"))
+    for dtype in (torch.float32, torch.bfloat16):
+        got = ops.weight_grad(d_y.bfloat16().cuda(), codes, sf, 100, r, by_token, dtype)
+        want = torch.zeros_like(got)
+        want[0], want[7], want[63] = 6.0 * K, total, 4.0 * K
+        assert torch.equal(got, want), dtype
+    assert ops.sync_status() == (0, 0)
+
+
+@pytest.mark.parametrize("N,C", [(2048, 2560), (1024, 5000)])
+def test_long_sums_of_one_sign(ops, N, C):
+    """20000 rows of values that round, 80 tiles, no parts: bf16 results from two accumulators, fp32 from 20."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    d_y = torch.rand(20_000, N, device="cuda", generator=g).bfloat16()
+    codes, sf = ops.quantize8(torch.rand(20_000, C, device="cuda", generator=g))
+    want = d_y[:, ::31].double().t() @ ops.dequantize8(codes, sf, C, torch.float32)[:, ::31].double()
+    # an MMA's 16 products and its accumulator lose less than a place (2 U) each: 64 MMAs an accumulator in fp32, 1024 in
+    # bf16; then the accumulators' additions and (bf16) the rounding
+    for dtype, off in ((torch.float32, (64 * 17 * 2 + 20) * U), (torch.bfloat16, (1024 * 17 * 2 + 2) * U + 2.0 ** -8)):
+        got = ops.weight_grad(d_y, codes, sf, C, dtype=dtype)[::31, ::31].double()
+        assert ((got - want).abs() <= off * want).all(), dtype

@@ -218,3 +218,15 @@ def test_tensors_that_require_grad_are_refused_where_a_gradient_would_be_lost(M,
     codes, sf = ops.quantize8(need)
     ops.rms_norm_backward(need, x, need_w, torch.ones(6))
     ops.weight_grad(torch.ones(6, 8, dtype=torch.bfloat16).requires_grad_(), codes, sf, 64)
+
+
+def test_scratch_of_long_sums(M):
+    """Tiles of fp32 sums, one a pair of CTAs, wherever one sum may pass 16384 rows: dense, or of one expert that takes every
+    pair; not where the sums are in parts."""
+    from moe_expert_forward_gb300 import ops
+    tile = 256 * 256 * 4
+    for rows, N, C, T, K, E, want in ((16384, 1024, 2560, 0, 0, 0, 0), (16385, 1024, 2560, 0, 0, 0, 76 * tile),
+                                      (17000, 256, 256, 2048, 8, 64, 0), (17000, 256, 256, 2049, 8, 64, 76 * tile),
+                                      (17000, 256, 256, 2049, 8, 39, 76 * tile), (20000, 8, 128, 20000, 1, 1, 16 * 8 * 128 * 4)):
+        args = (A, N, rows, N, A, C, T, K, E, 0)
+        assert M.mm_moe_weight_grad_scratch_size(*args) == ops._grad_scratch(*args) == want, args

@@ -28,3 +28,8 @@ def test_the_binding_has_the_kernels_constants():
     assert re.search(r"kLongTerms = 1 << (\d+)", text).group(1) == str(ops.GRAD_LONG.bit_length() - 1)
     sms = int(re.search(r"kNormSms = (\d+)", source("internal.h")).group(1))
     assert ops.NORM_CTAS == 2 * sms
+
+
+def test_the_binding_has_the_accumulators_rows():
+    from moe_expert_forward_gb300 import ops
+    assert re.search(r"kLongSegment = (\d+)", source("weight_grad.cu")).group(1) == str(ops.GRAD_SEGMENT)
