@@ -732,17 +732,18 @@ __global__ void __launch_bounds__(kCopyThreads)
 // of whole words: `pieces` a row and a thread each, of T.
 template <typename T>
 __global__ void __launch_bounds__(kCopyThreads)
-    align_rows_kernel(const char* __restrict__ x, int64_t pitch, int64_t rows, int bytes, int pieces, T* __restrict__ out) {
+    align_rows_kernel(const char* __restrict__ x, int64_t pitch, int64_t rows, int64_t bytes, int64_t pieces,
+                      T* __restrict__ out) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
   const int64_t r = i / pieces;
-  const int c = static_cast<int>(i - r * pieces) * static_cast<int>(sizeof(T));
+  const int64_t c = (i - r * pieces) * static_cast<int64_t>(sizeof(T)), left = bytes - c;
   if (r >= rows) return;
-  const uint4 v = load16_any(x + r * pitch + c, min(static_cast<int>(sizeof(T)), bytes - c));
+  const uint4 v = load16_any(x + r * pitch + c, left < static_cast<int64_t>(sizeof(T)) ? static_cast<int>(left) : sizeof(T));
   memcpy(out + i, &v, sizeof(T));                // past the row: columns that no tile stores
 }
 template <typename T>
-cudaError_t align_rows(const void* x, int64_t pitch, int64_t rows, int bytes, void* out, cudaStream_t s) {
-  const int pieces = (bytes + static_cast<int>(sizeof(T)) - 1) / static_cast<int>(sizeof(T));
+cudaError_t align_rows(const void* x, int64_t pitch, int64_t rows, int64_t bytes, void* out, cudaStream_t s) {
+  const int64_t pieces = (bytes + static_cast<int64_t>(sizeof(T)) - 1) / static_cast<int64_t>(sizeof(T));
   const int64_t all = rows * pieces;
   align_rows_kernel<T><<<static_cast<unsigned>((all + kCopyThreads - 1) / kCopyThreads), kCopyThreads, 0, s>>>(
       static_cast<const char*>(x), pitch, rows, bytes, pieces, static_cast<T*>(out));
@@ -909,7 +910,7 @@ cudaError_t launch_weight_grad(const WeightGradLaunch& p, cudaStream_t s) {
     to += copies.x;
   }
   if (copies.d_y) {
-    if (cudaError_t e = align_rows<uint4>(p.d_y, p.d_stride * 2, p.rows, p.N * 2, to, s)) return e;
+    if (cudaError_t e = align_rows<uint4>(p.d_y, p.d_stride * 2, p.rows, static_cast<int64_t>(p.N) * 2, to, s)) return e;
     d_y = to;
     pitch = static_cast<uint64_t>((p.N + 7) / 8) * 16;
     to += copies.d_y;

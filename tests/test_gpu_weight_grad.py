@@ -359,3 +359,12 @@ def test_long_sums_of_one_sign(ops, N, C):
     for dtype, off in ((torch.float32, (64 * 17 * 2 + 20) * U), (torch.bfloat16, (1024 * 17 * 2 + 2) * U + 2.0 ** -8)):
         got = ops.weight_grad(d_y, codes, sf, C, dtype=dtype)[::31, ::31].double()
         assert ((got - want).abs() <= off * want).all(), dtype
+
+
+@pytest.mark.parametrize("N", [(1 << 30) - 3, 1 << 30])
+def test_the_widest_d_y_on_no_boundary(ops, N):
+    """A row of 2 GB that is copied to 16-byte boundaries first: its bytes pass 31 bits."""
+    d_y = torch.empty(N + 1, dtype=torch.bfloat16, device="cuda").random_(-3, 4)[1:].view(1, N)
+    codes, sf = ops.quantize8(torch.full((1, 1), 2.0, device="cuda"))
+    got = ops.weight_grad(d_y, codes, sf, 1)
+    assert ops.sync_status() == (0, 0) and torch.equal(got, 2 * d_y.view(N, 1))
