@@ -541,7 +541,8 @@ def quantize8(x, quant: str = "mx", stream=None):
 
     quant="mx": codes [R, 32 ceil(C/32)], scales u8 [R, ceil(C/32)] (UE8M0); "f8": codes
     [R, 128 ceil(C/128)], scales fp32 [R, ceil(C/128)].  Where C is a multiple of 128 they
-    are the x and x_sf of the layer's variant of that name."""
+    are the x and x_sf of the layer's variant of that name.  "mx" rounds elements from
+    248 * 2^120 on to 2^128, which dequantize8 and weight_grad take as infinite."""
     code = _rows(x, "quantize8", "x")
     v = _format("quantize8", quant)
     R, C = x.shape
@@ -566,7 +567,7 @@ def _held_args(what: str, codes, sf, C: int, name: str = "codes"):
 
 
 def dequantize8(codes, sf, C: int, dtype=torch.bfloat16, stream=None):
-    """The values of quantize8's codes and scales (whose type tells the form): [R, C]."""
+    """The values of quantize8's codes and scales (whose type tells the form): [R, C], infinite past dtype's range."""
     R, v, cp, sp = _held_args("dequantize8", codes, sf, C)
     if dtype not in _DTYPES:
         _bad("dequantize8", f"dtype must be float32, bfloat16 or float16, got {dtype}")

@@ -170,3 +170,22 @@ def test_many_rows_as_few(ops, quant, dt, C):
     for at in range(0, R, 6554):
         part = slice(at, at + 6554)
         assert torch.equal(codes[part], ops.quantize8(x[part], quant)[0])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_the_largest_elements_round_to_infinity(ops, dt):
+    """248 * 2^120 is half way between the codes of 240 and 256, and the latter is even: 2^128, past both types."""
+    top = torch.finfo(DT[dt])
+    border = torch.tensor(248.0 * 2.0 ** 120, dtype=DT[dt])
+    below = torch.nextafter(border, torch.zeros((), dtype=DT[dt]))
+    x = torch.zeros(1, 64, dtype=DT[dt])
+    x[0, 0], x[0, 1], x[0, 32], x[0, 33] = border, top.min, below, -below
+    codes, sf = ops.quantize8(x.cuda())
+    inf, edge = float("inf"), 240.0 * 2.0 ** 120
+    want = torch.zeros(1, 64)
+    want[0, [0, 1, 32, 33]] = torch.tensor([inf, -inf, edge, -edge])
+    assert torch.equal(ops.dequantize8(codes, sf, 64, torch.float32).cpu(), want)
+    assert torch.equal(ops.dequantize8(codes, sf, 64).cpu(), want.bfloat16())
+    for N in (1, 1025):
+        got = ops.weight_grad(torch.ones(1, N, device="cuda", dtype=torch.bfloat16), codes, sf, 64, dtype=torch.float32)
+        assert torch.equal(got.cpu(), want.repeat(N, 1))
