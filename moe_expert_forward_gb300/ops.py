@@ -28,7 +28,7 @@ the caller's to order and to keep alive.
 Nothing here is recorded by autograd: the *_backward calls give the gradients, for
 example from a torch.autograd.Function.  So while grad mode is on, the calls whose
 result a gradient would flow through refuse tensors that require one; detach them,
-or call under torch.no_grad().
+or call under torch.no_grad().  The quantisers take them: their codes carry none.
 """
 from __future__ import annotations
 
