@@ -759,8 +759,11 @@ def weight_grad(d_y, codes, sf, C: int, routing: Optional[Routing] = None, by_to
     d_y bf16 [rows, N].  Dense: x [rows, C], the result [N, C].  With a routing: the rows
     are its pool's, every expert's own sum [E, N, C], zero for an expert without rows;
     padding takes no part, whatever it holds.  by_token: x [T, C] are the tokens' rows.
-    dtype: bfloat16 or float32.  A device wait that runs out leaves the result undefined
-    and is reported by sync_status."""
+    dtype: bfloat16 or float32.  During the call all rows of x are held in bf16 too where
+    by_token is given or N passes 1024: 2 C bytes a row of d_y (2 T K C and the padding),
+    beside copies of operands on no 16-byte boundary and partial sums
+    (mm_moe_weight_grad_scratch_size).  A device wait that runs out leaves the result
+    undefined and is reported by sync_status."""
     _rows(d_y, "weight_grad", "d_y", dtype=torch.bfloat16)
     R, N = d_y.shape
     if N < 1:
