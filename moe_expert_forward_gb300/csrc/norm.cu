@@ -13,9 +13,10 @@
 //          flight through the sum and the stores. Weights stay in registers.
 //   rows   few rows, short ones, or rows on no 32-byte boundary: loaded by their threads.
 //          Rows longer than the threads hold are read twice.
-// Measured (bf16 with a residual, in a stream of calls, of the copy rate): forward 8192x4096 39 us (82 %), 8192x7168 with f8
-// codes 105 (88 %, of its 533 MB); gradients 46 us (87 %) and 4.5 for the sum of d_weight's parts.  One row of 4096 takes
-// 4 us, latency.
+// Measured (with a residual or d_h, one of the calls of a graph over 400 MB of inputs, of the copy rate): forward 8192x4096
+// bf16 47 us (83 %), fp32 95 (83 %), 8192x7168 bf16 with f8 codes 88 (89 %); gradients 8192x4096 bf16 51 us with the sum of
+// d_weight's parts (77 %), fp32 100 (79 %).  By their threads, bf16 forward / back: 8192x1024 16 / 19 (61 and 51 %), 8192x2049
+// 44 / 73 (45 and 27 %).  One row of 4096 takes 3 us, latency.
 // For d_weight a thread keeps the same columns of every row that its CTA takes, so the
 // sums over tokens stay in registers too; the CTAs' parts are added up, in order, by a
 // second kernel.
