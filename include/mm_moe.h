@@ -556,13 +556,14 @@ int mm_moe_mx_linear(const void* x, int dtype, int64_t row_stride, int T, int C,
  * code, and are 16-byte aligned.  A block with a NaN or an infinity gets zero codes and
  * a scale of NaN (MX: byte 255), and everything computed from it is NaN; codes 0x7F and
  * 0xFF do not occur, and stand for NaN in the calls that read codes which another quantiser
- * wrote.  Results of these calls overlap no operand. */
+ * wrote.  MX rounds elements from 248 * 2^120 on to 2^128: infinite in the calls that read it.
+ * Results of these calls overlap no operand. */
 int mm_moe_rows_quantize(const void* x, int dtype, int64_t row_stride, int64_t R, int C, int variant, void* codes,
                          void* sf, void* stream);
 
 /* The values codes and scales stand for, rounded once: out [R, C] of `dtype` (bf16 and
- * fp32 hold those of MX exactly but 2^128, to which MX rounds elements from 248 * 2^120 on;
- * a value past the type's range is infinite), out_stride elements between rows. */
+ * fp32 hold those of MX exactly but 2^128; a value past the type's range is infinite),
+ * out_stride elements between rows. */
 int mm_moe_rows_dequantize(const void* codes, const void* sf, int64_t R, int C, int variant, int dtype, void* out,
                            int64_t out_stride, void* stream);
 
@@ -623,7 +624,7 @@ int mm_moe_swiglu_backward(const void* d_a, int dtype, int64_t d_stride, const v
 /* Weight gradients from rows kept in 8 bits (MX): out[e][n][c] = the sum over expert e's
  * rows r of d_y[r][n] * x[r][c], fp32 sums rounded once.
  *   d_y    bf16 [rows, N], d_stride elements between rows
- *   codes, sf  x [rows, C], or with by_token [T, C]: the tokens' own rows; a value of 2^128 is infinite here
+ *   codes, sf  x [rows, C], or with by_token [T, C]: the tokens' own rows
  *   cnt, src, blk_off  null: one dense sum over all rows (T, K, E, block_m are not read).  Else the
  *          routing whose pool the rows are: cnt[e] rows of expert e from row blk_off[e] * block_m on.
  *          Other rows are not part of any sum, whatever they hold.

@@ -20,11 +20,11 @@
 // at once: 8192x256x4096 50 us.)
 //
 // The MMA's accumulation drops bits below its accumulator's last: of random sign 8192 rows in
-// one accumulator are 3.7e-6 off (rounding to nearest: 3.6e-7), of one sign 4.5e-9 a row too
-// small, so that 2^18 rows lose a third of bf16's half step and 2^21 three whole ones.  fp32
+// one accumulator are 3.7e-6 off (rounding to nearest: 3.6e-7), of one sign up to 6e-9 a row
+// too small: 2^18 rows lost 1.2e-3, a third of bf16's half step and more, and 2^21 1.2e-2.  fp32
 // results are sums of sums over 1024 rows (kSegment stages), added by the epilogue in memory;
 // bf16 results of more than 16384 rows (kLongSegment; what one accumulator of these drops is
-// 4 % of a half step at most) of sums over 16384, which the epilogue keeps in a tile of fp32
+// 5 % of a half step at most) of sums over 16384, which the epilogue keeps in a tile of fp32
 // scratch of the pair's own. How many rows an expert has is known on the device alone, and one
 // may have all pairs, so the kernel that can do so (kLong) runs wherever there are more pairs,
 // or dense rows (bf16, cold caches, us, one accumulator / several: 65536x4096x4096 1298 / 1325,

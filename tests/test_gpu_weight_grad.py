@@ -368,3 +368,62 @@ def test_the_widest_d_y_on_no_boundary(ops, N):
     codes, sf = ops.quantize8(torch.full((1, 1), 2.0, device="cuda"))
     got = ops.weight_grad(d_y, codes, sf, 1)
     assert ops.sync_status() == (0, 0) and torch.equal(got, 2 * d_y.view(N, 1))
+
+
+def test_long_sums_on_two_streams_and_in_graphs(ops):
+    """Each call's sums of several accumulators are its own: at once on two streams, captured and replayed with new inputs,
+    and from rows of d_y on no boundary."""
+    v, total = long_rows(20_000)
+    wide = v.cuda().bfloat16()[:, None].repeat(1, 2050)
+    codes, sf = ops.quantize8(torch.ones(len(v), 2560, device="cuda"))
+    calls = [(wide[:, 1:1025], total), (2 * wide[:, :2048], 2 * total)]
+    want = [torch.full((d.shape[1], 2560), t, device="cuda").bfloat16() for d, t in calls]
+    for _ in range(3):
+        streams = [torch.cuda.Stream() for _ in calls]
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(2_000_000)
+        got = [ops.weight_grad(d, codes, sf, 2560, stream=s) for (d, _), s in zip(calls, streams)]
+        for s in streams:
+            s.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    graphs = []
+    for d, _ in calls:
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = ops.weight_grad(d, codes, sf, 2560)
+        graphs.append((g, out))
+    for scale in (1, 4):
+        wide.copy_(scale * v[:, None])
+        calls[1][0].copy_(2 * wide[:, :2048])
+        for (g, out), w in zip(graphs, want):
+            out.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, scale * w)
+    assert ops.sync_status() == (0, 0)
+
+
+@pytest.mark.parametrize("N", [1024, 2048])
+def test_a_stage_that_never_comes_in_a_long_sum(ops, monkeypatch, N):
+    import moe_expert_forward_gb300 as M
+    real = M.lib()
+
+    class Short:
+        def __getattr__(self, name):
+            return getattr(real, name)
+
+        def mm_moe_weight_grad(self, *a):
+            return real.mm_moe_weight_grad(*a[:19], 50, 1, a[21])
+    d_y = torch.ones(20_000, N, device="cuda", dtype=torch.bfloat16)
+    codes, sf = ops.quantize8(torch.ones(20_000, 2560, device="cuda"))
+    want = ops.weight_grad(d_y, codes, sf, 2560)
+    assert (want == torch.tensor(20_000.0).bfloat16().item()).all() and ops.sync_status() == (0, 0)
+    monkeypatch.setattr(ops, "lib", lambda: Short())
+    ops.weight_grad(d_y, codes, sf, 2560)
+    code, where = ops.sync_status()
+    assert code == M.MM_MOE_ERR_TIMEOUT and 181 <= where <= 191
+    monkeypatch.setattr(ops, "lib", lambda: real)
+    assert torch.equal(ops.weight_grad(d_y, codes, sf, 2560), want) and ops.sync_status() == (0, 0)
